@@ -367,6 +367,131 @@ FP4Q_API fp4_status_t fp4_gemm_ex(const uint8_t* a_packed, const uint8_t* b_pack
                                   int32_t* status, fp4q_stream_t stream);
 
 /*
+ * The NVFP4 key/value cache: attention's keys and values held in this
+ * library's own 4-bit blocks (E2M1 codes, one E4M3 scale per 16 channels of a
+ * head of a token), in pages.  Per page and key/value head:
+ *
+ *   k_packed, v_packed  [num_pages, num_kv_heads, page_size, head_dim/2] bytes, channel 2j in
+ *                       the low nibble of byte j;
+ *   k_sf                [num_pages, num_kv_heads, page_size, head_dim/16] bytes;
+ *   v_sf                [num_pages, num_kv_heads, head_dim/16, page_size] bytes: the scales of
+ *                       consecutive tokens lie side by side, because the product with V runs
+ *                       over tokens.
+ *
+ * Slot number = page * page_size + place in the page.  Every buffer is dense
+ * and 16-byte aligned; page_size is a multiple of 16, head_dim 64 or 128.
+ * k_global_scale, v_global_scale: DEVICE pointers to one positive finite fp32
+ * each, or NULL for 1, with the meaning of fp4_quantize's global_scale (blocks
+ * hold value * scale; the readers divide by it).
+ * A slot that was never written may hold any bytes as long as no sequence
+ * counts it; a counted slot holds what fp4_kv_append_nvfp4 writes (scale
+ * bytes that are finite).
+ */
+typedef struct {
+  uint8_t* k_packed;
+  uint8_t* k_sf;
+  uint8_t* v_packed;
+  uint8_t* v_sf;
+  const float* k_global_scale;
+  const float* v_global_scale;
+  int64_t num_pages;
+  int64_t page_size;
+  int64_t num_kv_heads;
+  int64_t head_dim;
+} fp4_kv_cache_t;
+
+/*
+ * fp4_kv_append_nvfp4 - rotates the queries and keys of T tokens by their
+ * positions, quantizes keys and values and stores them in the tokens' slots.
+ *
+ *   q, q_stride        [T, Hq, head_dim] dtype, q_stride elements between tokens (0: dense);
+ *                      NULL with Hq = 0 when there is nothing to rotate but the keys.
+ *   out_q, out_q_stride  the rotated queries, rounded once to dtype; may be q itself (same
+ *                      stride).  NULL exactly when q is NULL.
+ *   k, k_stride, v, v_stride  [T, num_kv_heads, head_dim] dtype, e.g. column slices of one
+ *                      fused projection's output.
+ *   positions          [T] int64, each token's row of cos_sin.  A token whose position is
+ *                      outside [0, max_position) is left out altogether: no out_q row, nothing
+ *                      appended.
+ *   cos_sin            [max_position, rot_dim] fp32: rot_dim/2 cosines, then rot_dim/2 sines.
+ *   rot_dim            channels of each head that are rotated, a multiple of 32, at most
+ *                      head_dim; 0: no rotation (positions, cos_sin NULL; q is then copied).
+ *                      Channels x1, x2 of a pair become rn(rn(x1 cos) - rn(x2 sin)) and
+ *                      rn(rn(x2 cos) + rn(x1 sin)) in fp32; keys are quantized from these.
+ *   interleaved        0: pair i is channels i and i + rot_dim/2; 1: channels 2i and 2i + 1.
+ *   slots              [T] int64.  A slot outside [0, num_pages * page_size) appends nothing
+ *                      (padding tokens: -1).  The slots of one call have to differ: where two
+ *                      tokens name the same one it is left holding blocks of either.
+ *   pdl                as in fp4_add_rmsnorm_quant_ex.
+ * Codes and scales are those of fp4_quantize (NVFP4) on the rotated keys and on
+ * the values.  q, k, v and out_q rows start on 32-byte boundaries (strides
+ * multiples of 16); positions and slots are 8-byte aligned.  Nothing that is
+ * written may overlap anything else the call reads or writes, out_q = q excepted.
+ */
+FP4Q_API fp4_status_t fp4_kv_append_nvfp4(const void* q, int64_t q_stride, void* out_q,
+                                          int64_t out_q_stride, const void* k, int64_t k_stride,
+                                          const void* v, int64_t v_stride,
+                                          const int64_t* positions, const float* cos_sin,
+                                          int64_t max_position, int64_t rot_dim, int interleaved,
+                                          const int64_t* slots, int64_t T, int64_t Hq,
+                                          fp4_dtype_t dtype, const fp4_kv_cache_t* cache, int pdl,
+                                          fp4q_stream_t stream);
+
+/*
+ * fp4_kv_gather_nvfp4 - reads the tokens of T slots back: out_k, out_v
+ * [T, num_kv_heads, head_dim] dtype, dense, 32-byte aligned (either may be
+ * NULL), code * scale / global scale in fp32, rounded once to dtype (exact
+ * without a global scale).  A slot outside the cache leaves its rows as they
+ * were.  Slots may repeat.
+ */
+FP4Q_API fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int64_t* slots,
+                                          int64_t T, fp4_dtype_t dtype, void* out_k, void* out_v,
+                                          int pdl, fp4q_stream_t stream);
+
+/*
+ * fp4_attention_nvfp4 - attention over the cached sequences of a batch:
+ *
+ *   out = softmax(sm_scale * q k^T) v,   lse = log(sum(exp(sm_scale * q k^T)))
+ *
+ * per query row and head, keys and values taken from the cache as code * scale
+ * / global scale.  Query head h reads key/value head h / (Hq / num_kv_heads).
+ *
+ *   q, q_stride     [T, Hq, head_dim] dtype (rotated, e.g. out_q above), rows 32-byte aligned.
+ *   block_tables    [B, max_pages] int32: the pages of each sequence in order.  Keys of a page
+ *                   whose number is outside [0, num_pages) are masked.
+ *   seq_lens        [B] int32: cached tokens of each sequence, this call's own among them
+ *                   (taken as clamped to [0, max_pages * page_size]).
+ *   cu_seqlens_q    [B + 1] int32, ascending: sequence b's query rows are cu[b] .. cu[b+1]-1.
+ *                   NULL: one row per sequence (T == B).  Rows outside [cu[0], cu[B]) are
+ *                   left as they were.
+ *   causal          nonzero: row i of a sequence's n_q rows sees its first len - n_q + i + 1
+ *                   keys; zero: all of them (cross attention to an encoder's states).
+ *   sm_scale        > 0, finite.
+ *   out             [T, Hq, head_dim] dtype, dense, 32-byte aligned.  A row that sees no key is
+ *                   0, with lse -inf.
+ *   lse             [T, Hq] fp32 (natural logarithm), or NULL.
+ *   workspace       at least fp4_attention_workspace_bytes(...) bytes, 16-byte aligned, any
+ *                   contents; two calls that may run at the same time need one each.
+ *   status, pdl     as in fp4_add_rmsnorm_quant_ex.
+ * Lengths and tables are read on the device, so a captured call follows them.
+ * Accumulators, maxima and sums are fp32.  Nothing that is written may overlap
+ * anything else the call reads or writes.
+ */
+FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
+                                          const fp4_kv_cache_t* cache, const int32_t* block_tables,
+                                          int64_t max_pages, const int32_t* seq_lens,
+                                          const int32_t* cu_seqlens_q, int64_t B, int64_t T,
+                                          int64_t Hq, fp4_dtype_t dtype, float sm_scale, int causal,
+                                          void* out, float* lse, void* workspace,
+                                          int64_t workspace_bytes, int32_t* status, int pdl,
+                                          fp4q_stream_t stream);
+
+/* Bytes of workspace fp4_attention_nvfp4 needs for these sizes on the current
+ * device (152 SMs taken when none is visible); 0 or more, -1 on bad arguments. */
+FP4Q_API int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
+                                               int64_t head_dim);
+
+/*
  * fp4_read_device_status - synchronises `stream`, then copies the device
  * status word back and returns it as a status: FP4_OK (0) or FP4_ERR_TIMEOUT;
  * FP4_ERR_INVALID_ARG for a NULL or misaligned pointer or a value that is no

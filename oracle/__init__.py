@@ -47,3 +47,4 @@ from .add_rmsnorm_quant import (  # noqa: F401
     block_size,
 )
 from .gemm import GemmResult, gelu, gemm_bf16, gemm_gelu_nvfp4  # noqa: F401
+from . import kv_cache  # noqa: F401

@@ -18,6 +18,10 @@ Around it: ``quantize_fp4`` (the same block quantization of x itself, FlashRT
 E2M1 operands and their tiled scales in, bf16 or NVFP4 out, NVFP4 or MXFP4
 operands, any K that is a multiple of 32), with ``fp4_gemm_variant`` and
 ``fp4_launch_shape`` reporting the launches the library would make.
+The paged key/value cache holds attention's keys and values in the same NVFP4
+blocks: ``kv_cache_nvfp4`` makes one, ``kv_append_nvfp4`` rotates queries and keys
+and stores the tokens, ``kv_gather_nvfp4`` reads slots back and
+``attention_nvfp4`` attends over the cached sequences of a batch.
 Kernels that wait on asynchronous copies bound every wait; a call given a
 device ``status`` word learns of a wait that ran out (``read_device_status``).
 """
@@ -40,19 +44,29 @@ from ._binding import (  # noqa: F401
     FP4_EPI_GELU_BF16,
     FP4_EPI_GELU_NVFP4,
     Fp4Error,
+    KVCacheStruct,
+    NVFP4KVCache,
     add_rmsnorm_fp4quant,
+    attention_nvfp4,
     dequant,
     gemm_nvfp4_bf16,
     gemm_nvfp4_gelu,
     fp4_add_rmsnorm_quant,
     fp4_add_rmsnorm_quant_ex,
     fp4_add_rmsnorm_quant_gs,
+    fp4_attention_nvfp4,
+    fp4_attention_workspace_bytes,
     fp4_dequant,
     fp4_gemm_mxfp4_bf16,
     fp4_gemm_nvfp4_gelu_bf16,
     fp4_gemm_nvfp4_gelu_nvfp4,
     fp4_gemm_nvfp4_bf16,
     fp4_gemm_ex,
+    fp4_kv_append_nvfp4,
+    fp4_kv_gather_nvfp4,
+    kv_append_nvfp4,
+    kv_cache_nvfp4,
+    kv_gather_nvfp4,
     fp4_read_device_status,
     read_device_status,
     fp4_quantize,

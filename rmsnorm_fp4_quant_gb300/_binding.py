@@ -4,7 +4,7 @@ from __future__ import annotations
 import contextlib
 import ctypes
 import os
-from typing import Optional, Tuple
+from typing import NamedTuple, Optional, Tuple
 
 from .build import DEBUG_LIBPATH, LIBPATH
 
@@ -31,6 +31,26 @@ class Fp4Error(RuntimeError):
             msg += f", cudaError {fp4_last_cuda_error()}"
         super().__init__(msg)
         self.status = status
+
+
+class KVCacheStruct(ctypes.Structure):
+    """fp4_kv_cache_t of include/fp4q.h: raw addresses (None = NULL) and sizes."""
+    _fields_ = [("k_packed", ctypes.c_void_p), ("k_sf", ctypes.c_void_p),
+                ("v_packed", ctypes.c_void_p), ("v_sf", ctypes.c_void_p),
+                ("k_global_scale", ctypes.c_void_p), ("v_global_scale", ctypes.c_void_p),
+                ("num_pages", ctypes.c_int64), ("page_size", ctypes.c_int64),
+                ("num_kv_heads", ctypes.c_int64), ("head_dim", ctypes.c_int64)]
+
+
+class NVFP4KVCache(NamedTuple):
+    """The four uint8 buffers of a paged NVFP4 key/value cache (include/fp4q.h,
+    fp4_kv_cache_t): codes [pages, kv_heads, page_size, head_dim/2], the keys' scales
+    [pages, kv_heads, page_size, head_dim/16], the values' [pages, kv_heads,
+    head_dim/16, page_size].  The calls below take any sequence of the four."""
+    k_packed: object
+    k_sf: object
+    v_packed: object
+    v_sf: object
 
 
 def lib_path() -> str:
@@ -113,6 +133,17 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_gemm_ex.restype = ci
     L.fp4_read_device_status.argtypes = [vp, vp]
     L.fp4_read_device_status.restype = ci
+    cp = ctypes.POINTER(KVCacheStruct)
+    L.fp4_kv_append_nvfp4.argtypes = [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, i64, i64, ci, vp,
+                                      i64, i64, ci, cp, ci, vp]
+    L.fp4_kv_append_nvfp4.restype = ci
+    L.fp4_kv_gather_nvfp4.argtypes = [cp, vp, i64, ci, vp, vp, ci, vp]
+    L.fp4_kv_gather_nvfp4.restype = ci
+    L.fp4_attention_nvfp4.argtypes = [vp, i64, cp, vp, i64, vp, vp, i64, i64, i64, ci,
+                                      ctypes.c_float, ci, vp, vp, vp, i64, vp, ci, vp]
+    L.fp4_attention_nvfp4.restype = ci
+    L.fp4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    L.fp4_attention_workspace_bytes.restype = i64
     L.fp4_debug_build.argtypes = []
     L.fp4_debug_build.restype = ci
     L.fp4_debug_configure.argtypes = [i64, i64, ci, ci, ci, vp]
@@ -209,6 +240,41 @@ def fp4_gemm_ex(a_packed_ptr: int, b_packed_ptr: int, sfa_ptr: int, sfb_ptr: int
                              bias_ptr or None, residual_ptr or None, M, N, K, out_ptr or None,
                              out_packed_ptr or None, out_sf_ptr or None, variant, pdl,
                              status_ptr or None, stream or None)
+
+
+def fp4_kv_append_nvfp4(q_ptr: int, q_stride: int, out_q_ptr: int, out_q_stride: int, k_ptr: int,
+                        k_stride: int, v_ptr: int, v_stride: int, positions_ptr: int,
+                        cos_sin_ptr: int, max_position: int, rot_dim: int, interleaved: int,
+                        slots_ptr: int, T: int, Hq: int, dtype: int, cache: KVCacheStruct,
+                        pdl: int, stream: int) -> int:
+    return lib().fp4_kv_append_nvfp4(q_ptr or None, q_stride, out_q_ptr or None, out_q_stride,
+                                     k_ptr or None, k_stride, v_ptr or None, v_stride,
+                                     positions_ptr or None, cos_sin_ptr or None, max_position,
+                                     rot_dim, interleaved, slots_ptr or None, T, Hq, dtype, cache,
+                                     pdl, stream or None)
+
+
+def fp4_kv_gather_nvfp4(cache: KVCacheStruct, slots_ptr: int, T: int, dtype: int, out_k_ptr: int,
+                        out_v_ptr: int, pdl: int, stream: int) -> int:
+    return lib().fp4_kv_gather_nvfp4(cache, slots_ptr or None, T, dtype, out_k_ptr or None,
+                                     out_v_ptr or None, pdl, stream or None)
+
+
+def fp4_attention_nvfp4(q_ptr: int, q_stride: int, cache: KVCacheStruct, block_tables_ptr: int,
+                        max_pages: int, seq_lens_ptr: int, cu_seqlens_q_ptr: int, B: int, T: int,
+                        Hq: int, dtype: int, sm_scale: float, causal: int, out_ptr: int,
+                        lse_ptr: int, workspace_ptr: int, workspace_bytes: int, status_ptr: int,
+                        pdl: int, stream: int) -> int:
+    return lib().fp4_attention_nvfp4(q_ptr or None, q_stride, cache, block_tables_ptr or None,
+                                     max_pages, seq_lens_ptr or None, cu_seqlens_q_ptr or None, B,
+                                     T, Hq, dtype, sm_scale, causal, out_ptr or None,
+                                     lse_ptr or None, workspace_ptr or None, workspace_bytes,
+                                     status_ptr or None, pdl, stream or None)
+
+
+def fp4_attention_workspace_bytes(B: int, T: int, Hq: int, num_kv_heads: int,
+                                  head_dim: int) -> int:
+    return lib().fp4_attention_workspace_bytes(B, T, Hq, num_kv_heads, head_dim)
 
 
 def fp4_read_device_status(status_ptr: int, stream: int) -> int:
@@ -540,3 +606,229 @@ def gemm_nvfp4_gelu(a_packed, b_packed, sfa, sfb, alpha: float = 1.0, bias=None,
     if st != 0:
         raise Fp4Error(st, "fp4_gemm_nvfp4_gelu_nvfp4")
     return packed, sf
+
+
+# ---------------------------------------------------------------------------
+# the paged NVFP4 key/value cache
+# ---------------------------------------------------------------------------
+def kv_cache_nvfp4(num_pages: int, page_size: int, num_kv_heads: int, head_dim: int,
+                   device=None) -> NVFP4KVCache:
+    """A cache of zeros (every slot reads as 0) on `device` (default: the current one)."""
+    torch = _torch()
+    if page_size <= 0 or page_size % 16 or head_dim not in (64, 128):
+        raise ValueError("page_size must be a multiple of 16 and head_dim 64 or 128")
+    dev = torch.device("cuda") if device is None else torch.device(device)
+
+    def zeros(*shape):
+        return torch.zeros(num_pages, num_kv_heads, *shape, dtype=torch.uint8, device=dev)
+    return NVFP4KVCache(zeros(page_size, head_dim // 2), zeros(page_size, head_dim // 16),
+                        zeros(page_size, head_dim // 2), zeros(head_dim // 16, page_size))
+
+
+def _kv_struct(cache, k_global_scale, v_global_scale) -> KVCacheStruct:
+    torch = _torch()
+    kp, ks, vp, vs = cache
+    for name, t in (("k_packed", kp), ("k_sf", ks), ("v_packed", vp), ("v_sf", vs)):
+        if t.dtype != torch.uint8 or t.dim() != 4:
+            raise ValueError(f"cache {name} must be uint8 with four dimensions")
+        _check_cuda(t, f"cache {name}")
+        if t.device != kp.device:
+            raise ValueError("the cache's buffers must be on one device")
+    pages, heads, page, half = kp.shape
+    if (vp.shape != kp.shape or ks.shape != (pages, heads, page, half // 8) or half % 8
+            or vs.shape != (pages, heads, half // 8, page)):
+        raise ValueError("cache buffers must be [pages, kv_heads, page_size, head_dim/2], "
+                         "[pages, kv_heads, page_size, head_dim/16], [pages, kv_heads, page_size, "
+                         "head_dim/2] and [pages, kv_heads, head_dim/16, page_size]")
+    return KVCacheStruct(kp.data_ptr(), ks.data_ptr(), vp.data_ptr(), vs.data_ptr(),
+                         _gs_ptr(k_global_scale) or None, _gs_ptr(v_global_scale) or None,
+                         pages, page, heads, 2 * half)
+
+
+def _kv_device(cache, *tensors):
+    """Every tensor on the cache's device, which has to be the current one (the
+    launch goes to a stream of the current device)."""
+    torch = _torch()
+    dev = cache[0].device
+    if dev.index != torch.cuda.current_device():
+        raise ValueError(f"the cache is on {dev}, which is not the current device")
+    for name, t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"{name} must be on the cache's device")
+
+
+def _head_rows(t, name, heads, dim):
+    """Elements between tokens of a (T, heads, dim) tensor whose heads are dense."""
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
+        raise ValueError(f"{name} must be (T, {heads}, {dim})")
+    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+        raise ValueError(f"{name} must have dense heads")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _on(stream):
+    """What is allocated inside belongs to the stream the kernels run on."""
+    return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+
+
+def _index(t, name, dtype, shape):
+    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    return t.data_ptr()
+
+
+def kv_append_nvfp4(cache, k, v, slots, q=None, positions=None, cos_sin=None,
+                    interleaved: bool = False, k_global_scale=None, v_global_scale=None,
+                    out_q=None, pdl: bool = False, stream=None):
+    """Rotates q and k of T tokens by their positions, quantizes k and v to NVFP4
+    and stores them in the cache's slots; returns the rotated q (None without q).
+
+    k, v: (T, kv_heads, head_dim), q: (T, heads, head_dim), bf16 or fp16, dense
+    heads, any token stride that is a multiple of 16 elements (column slices of a
+    fused projection's output).  slots: (T,) int64, page * page_size + place in
+    the page, all different; one outside the cache (padding: -1) appends nothing.
+    cos_sin: (positions, rot_dim) fp32, rot_dim/2 cosines then as many sines, with
+    positions (T,) int64 naming each token's row; without it nothing is rotated
+    (q is then copied).  A token whose position is outside the table is left out:
+    neither its slot nor its row of out_q is written.  interleaved: pairs are
+    channels 2i and 2i + 1 instead of i and i + rot_dim/2.  out_q: may be q itself."""
+    torch = _torch()
+    struct = _kv_struct(cache, k_global_scale, v_global_scale)
+    heads, dim = struct.num_kv_heads, struct.head_dim
+    _kv_device(cache, ("k", k), ("v", v), ("slots", slots), ("q", q), ("positions", positions),
+               ("cos_sin", cos_sin), ("out_q", out_q), ("k_global_scale", k_global_scale),
+               ("v_global_scale", v_global_scale))
+    ks, vs = _head_rows(k, "k", heads, dim), _head_rows(v, "v", heads, dim)
+    T = k.shape[0]
+    dt = _dtype_code(k)
+    if v.dtype != k.dtype or v.shape[0] != T:
+        raise ValueError("k and v must have the same shape and dtype")
+    hq = qs = oqs = 0
+    if q is not None:
+        hq = q.shape[1]
+        qs = _head_rows(q, "q", hq, dim)
+        if q.shape[0] != T or q.dtype != k.dtype:
+            raise ValueError("q must have k's dtype and number of tokens")
+        if out_q is None:
+            with _on(stream):
+                out_q = torch.empty(T, hq, dim, dtype=q.dtype, device=q.device)
+        oqs = _head_rows(out_q, "out_q", hq, dim)
+        if out_q.shape[0] != T or out_q.dtype != q.dtype:
+            raise ValueError("out_q must have q's shape and dtype")
+    elif out_q is not None:
+        raise ValueError("out_q without q")
+    rot = table = pos = rows = 0
+    if cos_sin is not None:
+        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
+            raise ValueError("cos_sin must be a contiguous float32 (positions, rot_dim) tensor")
+        if positions is None:
+            raise ValueError("cos_sin needs positions")
+        rows, rot = cos_sin.shape
+        table, pos = cos_sin.data_ptr(), _index(positions, "positions", torch.int64, (T,))
+    elif positions is not None:
+        raise ValueError("positions without cos_sin")
+    st = fp4_kv_append_nvfp4(q.data_ptr() if hq else 0, qs, out_q.data_ptr() if hq else 0, oqs,
+                             k.data_ptr(), ks, v.data_ptr(), vs, pos, table, rows, rot,
+                             1 if interleaved else 0, _index(slots, "slots", torch.int64, (T,)), T,
+                             hq, dt, struct, 1 if pdl else 0, _stream_handle(stream))
+    if st != 0:
+        raise Fp4Error(st, "fp4_kv_append_nvfp4")
+    return out_q
+
+
+def kv_gather_nvfp4(cache, slots, dtype=None, k_global_scale=None, v_global_scale=None,
+                    out_k=None, out_v=None, pdl: bool = False, stream=None):
+    """(k, v) of the given slots, (T, kv_heads, head_dim) in `dtype` (default bf16, or
+    that of out_k / out_v); a slot outside the cache leaves its rows of out_k and
+    out_v as they were."""
+    torch = _torch()
+    struct = _kv_struct(cache, k_global_scale, v_global_scale)
+    _kv_device(cache, ("slots", slots), ("out_k", out_k), ("out_v", out_v),
+               ("k_global_scale", k_global_scale), ("v_global_scale", v_global_scale))
+    if dtype is None:
+        dtype = out_k.dtype if out_k is not None else out_v.dtype if out_v is not None \
+            else torch.bfloat16
+    shape = (slots.shape[0], struct.num_kv_heads, struct.head_dim)
+    with _on(stream):
+        if out_k is None:
+            out_k = torch.empty(shape, dtype=dtype, device=slots.device)
+        if out_v is None:
+            out_v = torch.empty(shape, dtype=dtype, device=slots.device)
+    for name, t in (("out_k", out_k), ("out_v", out_v)):
+        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    st = fp4_kv_gather_nvfp4(struct, _index(slots, "slots", torch.int64, (shape[0],)), shape[0],
+                             _dtype_code(out_k), out_k.data_ptr(), out_v.data_ptr(),
+                             1 if pdl else 0, _stream_handle(stream))
+    if st != 0:
+        raise Fp4Error(st, "fp4_kv_gather_nvfp4")
+    return out_k, out_v
+
+
+def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal: bool = True,
+                    sm_scale: Optional[float] = None, k_global_scale=None, v_global_scale=None,
+                    out=None, return_lse: bool = False, lse=None, workspace=None, status=None,
+                    pdl: bool = False, stream=None):
+    """softmax(sm_scale * q k^T) v over the cached tokens of every sequence.
+
+    q: (T, heads, head_dim) bf16 or fp16, heads a multiple of the cache's kv_heads.
+    block_tables: (B, max_pages) int32, the pages of each sequence in order; keys of
+    a page outside the cache are masked.  seq_lens: (B,) int32, cached tokens of
+    each sequence, the call's own included.  cu_seqlens_q: (B + 1,) int32, sequence
+    b's rows of q are cu[b] .. cu[b + 1] - 1; without it q has one row per sequence.
+    causal: the last row of a sequence sees all its keys, the row before it one
+    less, and so on; else every row sees all of them.  sm_scale: default
+    head_dim ** -0.5.  A row that sees no key gives 0 and lse -inf; rows of no
+    sequence are left as they were.  Returns out, or (out, lse) with return_lse
+    (lse (T, heads) fp32, natural logarithm).  workspace: optional uint8 tensor of
+    fp4_attention_workspace_bytes bytes, for one call at a time."""
+    torch = _torch()
+    struct = _kv_struct(cache, k_global_scale, v_global_scale)
+    _kv_device(cache, ("q", q), ("block_tables", block_tables), ("seq_lens", seq_lens),
+               ("cu_seqlens_q", cu_seqlens_q), ("out", out), ("lse", lse),
+               ("workspace", workspace), ("status", status), ("k_global_scale", k_global_scale),
+               ("v_global_scale", v_global_scale))
+    if q.dim() != 3:
+        raise ValueError("q must be (T, heads, head_dim)")
+    T, hq, dim = q.shape
+    qs = _head_rows(q, "q", hq, struct.head_dim)
+    if hq % struct.num_kv_heads:
+        raise ValueError("the number of query heads must be a multiple of the cache's kv_heads")
+    if block_tables.dim() != 2:
+        raise ValueError("block_tables must be (B, max_pages)")
+    B, max_pages = block_tables.shape
+    tables = _index(block_tables, "block_tables", torch.int32, (B, max_pages))
+    lens = _index(seq_lens, "seq_lens", torch.int32, (B,))
+    cu = 0
+    if cu_seqlens_q is not None:
+        cu = _index(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+    elif T != B:
+        raise ValueError("q must have one row per sequence without cu_seqlens_q")
+    with _on(stream):
+        if out is None:
+            out = torch.empty(T, hq, dim, dtype=q.dtype, device=q.device)
+        if return_lse and lse is None:
+            lse = torch.empty(T, hq, dtype=torch.float32, device=q.device)
+        if workspace is None:
+            need = fp4_attention_workspace_bytes(B, T, hq, struct.num_kv_heads, dim)
+            if need > 0:
+                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
+    if out.dtype != q.dtype or tuple(out.shape) != (T, hq, dim) or not out.is_contiguous():
+        raise ValueError("out must be contiguous with q's shape and dtype")
+    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, hq)
+                            or not lse.is_contiguous()):
+        raise ValueError("lse must be a contiguous float32 (T, heads) tensor")
+    if workspace is not None:
+        _check_cuda(workspace, "workspace")
+    st = fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
+                             _dtype_code(q),
+                             float(sm_scale) if sm_scale is not None else float(dim) ** -0.5,
+                             1 if causal else 0, out.data_ptr(),
+                             lse.data_ptr() if lse is not None else 0,
+                             workspace.data_ptr() if workspace is not None else 0,
+                             workspace.numel() * workspace.element_size()
+                             if workspace is not None else 0,
+                             _status_ptr(status), 1 if pdl else 0, _stream_handle(stream))
+    if st != 0:
+        raise Fp4Error(st, "fp4_attention_nvfp4")
+    return (out, lse) if return_lse else out

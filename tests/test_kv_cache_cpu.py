@@ -1,0 +1,159 @@
+"""Host-side refusals of the key/value cache entry points (no GPU): every call
+below fails its checks before anything is launched or read."""
+import ctypes
+
+import pytest
+
+import rmsnorm_fp4_quant_gb300 as fq
+from rmsnorm_fp4_quant_gb300 import build as fbuild
+
+A = 0x7F0000000000
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    fbuild.build()
+    return fq.lib()
+
+
+def at(i):
+    return A + (i << 34)
+
+
+def cache(**kw):
+    d = dict(k_packed=at(0), k_sf=at(1), v_packed=at(2), v_sf=at(3), k_global_scale=None,
+             v_global_scale=None, num_pages=64, page_size=16, num_kv_heads=2, head_dim=128)
+    d.update(kw)
+    return fq.KVCacheStruct(**d)
+
+
+CACHE_REFUSALS = [
+    (dict(k_packed=0), 1), (dict(k_sf=0), 1), (dict(v_packed=0), 1), (dict(v_sf=0), 1),
+    (dict(num_pages=-1), 1), (dict(page_size=0), 1), (dict(num_kv_heads=0), 1),
+    (dict(head_dim=96), 2), (dict(head_dim=32), 2), (dict(page_size=24), 2), (dict(head_dim=0), 1),
+    (dict(num_pages=1 << 31), 2), (dict(num_kv_heads=5000), 2),
+    (dict(k_packed=at(0) + 8), 3), (dict(v_sf=at(3) + 4), 3), (dict(k_global_scale=at(9) + 2), 3),
+]
+
+
+def append(c=None, **kw):
+    a = dict(q=at(4), qs=0, oq=at(5), oqs=0, k=at(6), ks=0, v=at(7), vs=0, pos=at(8), cs=at(9),
+             maxp=1024, rot=128, inter=0, slots=at(10), T=5, Hq=4, dt=0)
+    a.update(kw)
+    return fq.fp4_kv_append_nvfp4(a["q"], a["qs"], a["oq"], a["oqs"], a["k"], a["ks"], a["v"],
+                                  a["vs"], a["pos"], a["cs"], a["maxp"], a["rot"], a["inter"],
+                                  a["slots"], a["T"], a["Hq"], a["dt"], c or cache(), 0, 0)
+
+
+@pytest.mark.parametrize("kw,status", CACHE_REFUSALS)
+def test_append_refuses_bad_caches(kw, status):
+    assert append(cache(**kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dt=2), 1), (dict(T=-1), 1), (dict(Hq=-1), 1), (dict(inter=2), 1), (dict(rot=-32), 1),
+    (dict(maxp=-1), 1), (dict(rot=48), 2), (dict(rot=160), 2), (dict(Hq=5000), 2), (dict(T=1 << 31), 2),
+    (dict(q=0), 1), (dict(oq=0), 1), (dict(q=0, oq=0), 1), (dict(Hq=0), 1),
+    (dict(k=0), 1), (dict(v=0), 1), (dict(slots=0), 1), (dict(pos=0), 1), (dict(cs=0), 1),
+    (dict(qs=500), 1), (dict(ks=250), 1), (dict(vs=128), 1), (dict(oqs=256), 1),
+    (dict(q=at(4) + 16), 3), (dict(k=at(6) + 2), 3), (dict(v=at(7) + 8), 3), (dict(oq=at(5) + 4), 3),
+    (dict(qs=520), 3), (dict(ks=264), 3), (dict(slots=at(10) + 4), 3), (dict(pos=at(8) + 4), 3),
+    (dict(cs=at(9) + 8), 3),
+    (dict(oq=at(4) + 64), 1),                        # out_q shifted against q
+    (dict(oq=at(4), oqs=528), 1),                    # q itself with another stride
+    (dict(oq=at(6)), 1),                             # out_q over k
+    (dict(oq=at(0) + 4096), 1),                      # out_q inside the cache
+    (dict(k=at(2) + 32), 1),                         # k inside the cache
+    (dict(slots=at(1) + 64), 1), (dict(pos=at(3) + 8), 1), (dict(cs=at(0)), 1),
+    (dict(oq=at(10)), 1),
+    (dict(q=at(6) + 256, qs=768, oq=at(6) + 256, oqs=768, k=at(6), ks=768), 1),   # columns shared
+    (dict(T=0, q=0, oq=0, Hq=0, k=0, v=0, slots=0), 0),
+])
+def test_append_refusals(kw, status):
+    assert append(**kw) == status
+
+
+def test_append_refuses_shared_cache_buffers():
+    assert append(cache(v_packed=at(0) + 64)) == 1
+    assert append(cache(k_sf=at(2))) == 1
+
+
+@pytest.mark.parametrize("kw,status", CACHE_REFUSALS)
+def test_gather_refuses_bad_caches(kw, status):
+    assert fq.fp4_kv_gather_nvfp4(cache(**kw), at(10), 5, 0, at(4), at(5), 0, 0) == status
+
+
+@pytest.mark.parametrize("args,status", [
+    ((at(10), -1, 0, at(4), at(5)), 1), ((at(10), 5, 2, at(4), at(5)), 1), ((0, 5, 0, at(4), at(5)), 1),
+    ((at(10) + 4, 5, 0, at(4), at(5)), 3), ((at(10), 5, 0, at(4) + 16, at(5)), 3),
+    ((at(10), 5, 0, at(4), at(4) + 32), 1), ((at(10), 5, 0, at(2), at(5)), 1),
+    ((at(10), 5, 0, at(4), at(10)), 1), ((at(10), 1 << 31, 0, at(4), at(5)), 2),
+    ((0, 0, 0, 0, 0), 0), ((at(10), 5, 0, 0, 0), 0),
+])
+def test_gather_refusals(args, status):
+    assert fq.fp4_kv_gather_nvfp4(cache(), *args, 0, 0) == status
+
+
+def attention(c=None, **kw):
+    a = dict(q=at(4), qs=0, tab=at(6), pages=8, lens=at(7), cu=0, B=5, T=5, Hq=4, dt=0, scale=0.1,
+             causal=1, out=at(5), lse=at(8), ws=at(11), wsb=1 << 33, st=0)
+    a.update(kw)
+    return fq.fp4_attention_nvfp4(a["q"], a["qs"], c or cache(), a["tab"], a["pages"], a["lens"],
+                                  a["cu"], a["B"], a["T"], a["Hq"], a["dt"], a["scale"],
+                                  a["causal"], a["out"], a["lse"], a["ws"], a["wsb"], a["st"], 0, 0)
+
+
+@pytest.mark.parametrize("kw,status", CACHE_REFUSALS)
+def test_attention_refuses_bad_caches(kw, status):
+    assert attention(cache(**kw)) == status
+
+
+@pytest.mark.parametrize("kw,status", [
+    (dict(dt=3), 1), (dict(B=-1), 1), (dict(T=-1), 1), (dict(Hq=0), 1), (dict(Hq=3), 1),
+    (dict(pages=-1), 1), (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=float("nan")), 1),
+    (dict(scale=float("inf")), 1), (dict(qs=500), 1), (dict(T=6), 1), (dict(B=4), 1),
+    (dict(pages=1 << 30), 2), (dict(Hq=5000), 2), (dict(T=1 << 31, B=1 << 31), 2),
+    (dict(q=0), 1), (dict(out=0), 1), (dict(lens=0), 1), (dict(tab=0), 1),
+    (dict(q=at(4) + 16), 3), (dict(qs=520), 3), (dict(out=at(5) + 8), 3), (dict(lse=at(8) + 2), 3),
+    (dict(tab=at(6) + 2), 3), (dict(lens=at(7) + 1), 3), (dict(cu=at(9) + 2), 3), (dict(st=at(9) + 2), 3),
+    (dict(out=at(4)), 1), (dict(out=at(0) + 64), 1), (dict(lse=at(5) + 64), 1), (dict(lse=at(4)), 1),
+    (dict(out=at(6)), 1), (dict(out=at(7)), 1), (dict(cu=at(5)), 1), (dict(st=at(5)), 1),
+    (dict(st=at(7)), 1), (dict(lse=at(3)), 1),
+    (dict(T=0, B=0, q=0, out=0), 0),
+])
+def test_attention_refusals(kw, status):
+    assert attention(**kw) == status
+
+
+def test_workspace_sizes():
+    f = fq.fp4_attention_workspace_bytes
+    assert f(4, 4, 8, 2, 128) >= 0
+    for bad in [(-1, 4, 8, 2, 128), (4, -1, 8, 2, 128), (4, 4, 0, 2, 128), (4, 4, 8, 3, 128),
+                (4, 4, 8, 2, 96), (4, 4, 8, 0, 128)]:
+        assert f(*bad) == -1
+    need = f(5, 5, 4, 2, 128)
+    if need:
+        assert attention(wsb=need - 1) == 1 and attention(ws=0) == 1 and attention(ws=at(11) + 8) == 3
+        assert attention(ws=at(5)) == 1 and attention(ws=at(0)) == 1
+
+
+def test_the_struct_matches_the_header():
+    assert ctypes.sizeof(fq.KVCacheStruct) == 6 * ctypes.sizeof(ctypes.c_void_p) + 4 * 8
+
+
+def test_tensor_calls_refuse_cpu_tensors_and_bad_shapes():
+    import torch
+    u8 = lambda *s: torch.zeros(*s, dtype=torch.uint8)  # noqa: E731
+    c = (u8(4, 2, 16, 64), u8(4, 2, 16, 8), u8(4, 2, 16, 64), u8(4, 2, 8, 16))
+    k = torch.zeros(3, 2, 128, dtype=torch.bfloat16)
+    slots = torch.zeros(3, dtype=torch.int64)
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.kv_append_nvfp4(c, k, k, slots)
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.kv_gather_nvfp4(c, slots)
+    with pytest.raises(ValueError, match="CUDA"):
+        fq.attention_nvfp4(k, c, torch.zeros(3, 1, dtype=torch.int32), torch.zeros(3, dtype=torch.int32))
+    with pytest.raises(ValueError):
+        fq.kv_cache_nvfp4(4, 24, 2, 128, device="cpu")
+    with pytest.raises(ValueError):
+        fq.kv_cache_nvfp4(4, 16, 2, 96, device="cpu")

@@ -1,0 +1,560 @@
+"""The NVFP4 key/value cache on the GPU against the oracle: append (rotation,
+quantization, placement), gather, attention, and a chain of them.
+
+Attention's tolerance, from the kernels' roundings (h = half a step of the
+output type, n = keys of the row, w = sum of p |v|, L = largest sum of |scale q k|):
+  * a logit is an fp32 sum of D exact products: off by at most e_s = D * 2^-23 * L,
+    and by 2^-22 * L more for the factor 2^x is taken with; p is off by the factor
+    exp(e_s), and so is the sum of the p: 2 e_s * w in the output;
+  * each p is rounded to 11 bits for the product with v: 2^-11 * w;
+  * the fp32 sums over n keys: n * 2^-23 * w, twice (numerator and denominator);
+  * the output's rounding: h * |out|.
+lse: e_s + n * 2^-23 + 2^-22 * (|lse| + 1).
+"""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+import rmsnorm_fp4_quant_gb300 as fq
+from oracle import kv_cache as okv
+from rmsnorm_fp4_quant_gb300 import build as fbuild
+
+pytestmark = pytest.mark.gpu
+
+DT = {"bf16": torch.bfloat16, "fp16": torch.float16}
+HALF_STEP = {"bf16": 2.0 ** -8, "fp16": 2.0 ** -11}
+
+
+@pytest.fixture(scope="module", autouse=True)
+def library():
+    fbuild.build()
+    fq.lib()
+
+
+def gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def rope_table(n, rot):
+    freq = 10000.0 ** (-torch.arange(0, rot, 2, dtype=torch.float64) / rot)
+    a = torch.arange(n, dtype=torch.float64)[:, None] * freq
+    return torch.cat((a.cos(), a.sin()), -1).float()
+
+
+def random_cache(pages, heads, page, D, seed):
+    """Any bytes: what earlier sequences left behind."""
+    g = gen(seed)
+    r = lambda *s: torch.randint(0, 256, (pages, heads, *s), dtype=torch.uint8, generator=g)  # noqa: E731
+    return [r(page, D // 2), r(page, D // 16), r(page, D // 2), r(D // 16, page)]
+
+
+def to_np(cache):
+    return [t.cpu().numpy().copy() for t in cache]
+
+
+# ---------------------------------------------------------------------------
+# append and gather
+# ---------------------------------------------------------------------------
+APPEND = [
+    # T, Hq, Hkv, D, page, rot, interleaved, dtype
+    (1, 12, 2, 128, 16, 128, False, "bf16"),
+    (1, 0, 1, 64, 16, 64, False, "fp16"),
+    (7, 5, 1, 64, 48, 32, True, "bf16"),
+    (41, 40, 8, 128, 16, 64, True, "fp16"),
+    (130, 3, 3, 128, 64, 128, True, "bf16"),
+    (33, 1, 24, 64, 32, 64, False, "fp16"),
+    (65, 0, 7, 128, 16, 0, False, "bf16"),
+    (1031, 9, 3, 64, 128, 32, False, "bf16"),
+    (515, 14, 2, 128, 48, 96, False, "fp16"),
+    (515, 14, 2, 128, 48, 96, True, "bf16"),
+]
+
+
+def append_inputs(T, Hq, Hkv, D, rot, dtype, seed, positions=4096):
+    g = gen(seed)
+    qkv = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g) * 1.7
+    qkv[:, ::29] *= 20
+    if T > 3:
+        qkv[2] = 0                                   # a token of zeros: scale and codes 0
+        qkv[3] *= 1e-4                               # blocks that quantize to nothing
+    qkv = qkv.to(DT[dtype])
+    pos = torch.randint(0, positions, (T,), generator=g)
+    return qkv, pos, rope_table(positions, rot) if rot else None
+
+
+def split(qkv, Hq, Hkv, D):
+    q, k, v = qkv.split((Hq * D, Hkv * D, Hkv * D), -1)
+    return (q.unflatten(-1, (Hq, D)) if Hq else None, k.unflatten(-1, (Hkv, D)), v.unflatten(-1, (Hkv, D)))
+
+
+def f32(t):
+    return None if t is None else t.float().numpy()
+
+
+@pytest.mark.parametrize("T,Hq,Hkv,D,page,rot,inter,dtype", APPEND)
+@pytest.mark.parametrize("scales", [None, (2.5, 0.3125)])
+def test_append_and_gather(T, Hq, Hkv, D, page, rot, inter, dtype, scales):
+    qkv, pos, table = append_inputs(T, Hq, Hkv, D, rot, dtype, seed=T + D)
+    pages = T // page + 3
+    cache = random_cache(pages, Hkv, page, D, seed=5)
+    slots = torch.randperm(pages * page, generator=gen(9))[:T]
+    if T > 6:
+        slots[1], slots[4], slots[5] = -1, pages * page, -(1 << 40)      # append nothing
+        if rot:
+            pos[0], pos[6] = -1, 4096                                    # tokens left out
+    want = to_np(cache)
+    q, k, v = split(qkv, Hq, Hkv, D)
+    kg, vg = scales or (1.0, 1.0)
+    rq, here = okv.append(want, f32(k), f32(v), slots.numpy(), pos.numpy(),
+                          table.numpy() if rot else None, inter, kg, vg, f32(q)) if rot else \
+        okv.append(want, f32(k), f32(v), slots.numpy(), k_gs=kg, v_gs=vg, q=f32(q))
+    dev = [t.cuda() for t in cache]
+    dq, dk, dv = split(qkv.cuda(), Hq, Hkv, D)
+    gs = [torch.tensor([s], device="cuda") if scales else None for s in (kg, vg)]
+    out_q = torch.full((T, Hq, D), 77.0, dtype=DT[dtype], device="cuda") if Hq else None
+    got = fq.kv_append_nvfp4(dev, dk, dv, slots.cuda(), q=dq, positions=pos.cuda() if rot else None,
+                             cos_sin=table.cuda() if rot else None, interleaved=inter,
+                             k_global_scale=gs[0], v_global_scale=gs[1], out_q=out_q)
+    torch.cuda.synchronize()
+    for name, a, b in zip(("k_packed", "k_sf", "v_packed", "v_sf"), to_np(dev), want):
+        assert np.array_equal(a, b), name
+    if Hq:
+        exp = torch.from_numpy(rq).to(DT[dtype])
+        exp[torch.from_numpy(~here)] = 77.0
+        assert torch.equal(got.cpu(), exp)
+    # the slots read back: exact without a global scale
+    valid = (slots >= 0) & (slots < pages * page)
+    ok = slots[valid & torch.from_numpy(here)]
+    gk, gv = okv.gather(want, ok.numpy(), kg, vg)
+    rk, rv = fq.kv_gather_nvfp4(dev, ok.cuda(), dtype=DT[dtype], k_global_scale=gs[0], v_global_scale=gs[1])
+    for a, b in ((rk, gk), (rv, gv)):
+        a = a.double().cpu().numpy()
+        if scales is None:
+            assert np.array_equal(a, b)
+        else:      # a division in 32 bits, then one rounding (values below the type's normals: absolute)
+            assert np.all(np.abs(a - b) <= (HALF_STEP[dtype] + 2.0 ** -22) * np.abs(b) + 2.0 ** -25)
+
+
+def test_append_equals_quantize_fp4():
+    T, H, D, page = 64, 4, 128, 16
+    k = (torch.randn(T, H, D, generator=gen(0)) * 3).bfloat16().cuda()
+    v = (torch.randn(T, H, D, generator=gen(1)) * 3).bfloat16().cuda()
+    c = fq.kv_cache_nvfp4(T // page, page, H, D)
+    fq.kv_append_nvfp4(c, k, v, torch.arange(T, device="cuda"))
+    for x, packed, sf in ((k, c.k_packed, c.k_sf), (v, c.v_packed, c.v_sf.transpose(-1, -2))):
+        pk, s = fq.quantize_fp4(x.reshape(T * H, D), sf_layout="rowmajor")
+        assert torch.equal(packed.transpose(1, 2).reshape(T * H, -1), pk)
+        assert torch.equal(sf.transpose(1, 2).reshape(T * H, -1), s)
+
+
+def test_append_in_place_and_views():
+    """q rotated inside the fused projection's output; k and v beside it stay."""
+    T, Hq, Hkv, D = 19, 4, 2, 64
+    qkv, pos, table = append_inputs(T, Hq, Hkv, D, 64, "bf16", seed=3)
+    dev = qkv.cuda()
+    q, k, v = split(dev, Hq, Hkv, D)
+    c = fq.kv_cache_nvfp4(4, 16, Hkv, D)
+    out = fq.kv_append_nvfp4(c, k, v, torch.arange(T, device="cuda"), q=q, positions=pos.cuda(),
+                             cos_sin=table.cuda(), out_q=q)
+    assert out.data_ptr() == dev.data_ptr()
+    want = okv.rotate(f32(split(qkv, Hq, Hkv, D)[0]), pos.numpy(), table.numpy(), False)
+    assert torch.equal(q.cpu(), torch.from_numpy(want).bfloat16())
+    assert torch.equal(dev[:, Hq * D:].cpu(), qkv[:, Hq * D:])
+    with pytest.raises(fq.Fp4Error):           # out_q over k's columns
+        fq.kv_append_nvfp4(c, k, v, torch.arange(T, device="cuda"), q=q, positions=pos.cuda(),
+                           cos_sin=table.cuda(), out_q=dev[:, D:(Hq + 1) * D].unflatten(-1, (Hq, D)))
+
+
+def test_gather_leaves_rows_of_slots_outside_and_repeats():
+    c = [t.cuda() for t in random_cache(3, 2, 16, 64, seed=1)]
+    c[1] &= 0x3F
+    c[3] &= 0x3F
+    slots = torch.tensor([5, -1, 47, 48, 5, 1 << 50], device="cuda")
+    out_k = torch.full((6, 2, 64), 3.0, dtype=torch.float16, device="cuda")
+    out_v = torch.full_like(out_k, 4.0)
+    fq.kv_gather_nvfp4(c, slots, out_k=out_k, out_v=out_v)
+    gk, gv = okv.gather(to_np(c), [5, 47, 5])
+    live = torch.tensor([0, 2, 4])
+    assert np.array_equal(out_k.cpu()[live].double().numpy(), gk)
+    assert np.array_equal(out_v.cpu()[live].double().numpy(), gv)
+    dead = torch.tensor([1, 3, 5])
+    assert torch.all(out_k.cpu()[dead] == 3) and torch.all(out_v.cpu()[dead] == 4)
+
+
+def test_append_infinities_and_nan_stay_in_their_blocks():
+    T, H, D = 4, 1, 64
+    k = torch.ones(T, H, D)
+    k[1, 0, 3], k[2, 0, 17], k[3, 0, 40] = float("inf"), float("-inf"), float("nan")
+    c = fq.kv_cache_nvfp4(1, 16, H, D)
+    fq.kv_append_nvfp4(c, k.bfloat16().cuda(), k.bfloat16().cuda(), torch.arange(T, device="cuda"))
+    gk, _ = fq.kv_gather_nvfp4(c, torch.arange(T, device="cuda"))
+    gk = gk.float().cpu()
+    assert torch.isfinite(gk).all()            # the format has no infinities: they saturate
+    one = gk[0, 0, 0]
+    for t, blk in ((1, 0), (2, 1), (3, 2)):
+        for b in range(4):
+            if b != blk:
+                assert torch.all(gk[t, 0, 16 * b:16 * b + 16] == one)
+
+
+# ---------------------------------------------------------------------------
+# attention
+# ---------------------------------------------------------------------------
+def fill_sequences(lens, Hkv, D, page, seed, extra_pages=3, bad=()):
+    """A cache of garbage with `lens` tokens written for each sequence by the oracle;
+    (cache, tables).  bad: (sequence, page index, number) entries put into the tables
+    afterwards."""
+    g = gen(seed)
+    used = [max(0, -(-n // page)) for n in lens]
+    pages = sum(used) + extra_pages
+    cache = to_np(random_cache(pages, Hkv, page, D, seed + 1))
+    cache[1][:, :, ::3] = 0x7F                       # scales that are no numbers, too
+    cache[3][:, :, :, 1::3] = 0xFF
+    order = torch.randperm(pages, generator=g).numpy()
+    tables = np.full((len(lens), max(used + [1]) + 1), -7, np.int64)
+    at = 0
+    for b, n in enumerate(lens):
+        tables[b, :used[b]] = order[at:at + used[b]]
+        at += used[b]
+        j = np.arange(n)
+        slots = tables[b][j // page] * page + j % page if n else j
+        k = torch.randn(n, Hkv, D, generator=g).numpy()
+        k[..., 3::17] *= 3
+        if n:
+            okv.append(cache, k, torch.randn(n, Hkv, D, generator=g).numpy(), slots)
+    for b, i, number in bad:
+        tables[b, i] = number
+    return cache, tables
+
+
+def check_attention(q, cache, tables, lens, cu, causal, dtype, sm_scale=None, kg=1.0, vg=1.0, **kw):
+    """Runs the call and compares every row with the oracle; returns (out, lse)."""
+    T, Hq, D = q.shape
+    scale = D ** -0.5 if sm_scale is None else sm_scale
+    ref = okv.attention(q.double().numpy(), cache, tables, lens, cu, causal, scale, kg, vg)
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    out = torch.full((T, Hq, D), 5.0, dtype=DT[dtype], device="cuda")
+    lse = torch.full((T, Hq), 6.0, device="cuda")
+    gs = dict(k_global_scale=torch.tensor([kg], device="cuda") if kg != 1 else None,
+              v_global_scale=torch.tensor([vg], device="cuda") if vg != 1 else None)
+    fq.attention_nvfp4(q.cuda(), dev, torch.from_numpy(tables.astype(np.int32)).cuda(),
+                       torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                       None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                       causal=causal, sm_scale=sm_scale, out=out, return_lse=True, lse=lse, **gs, **kw)
+    torch.cuda.synchronize()
+    compare_attention(out, lse, ref, D, dtype)
+    return out, lse
+
+
+def compare_attention(out, lse, ref, D, dtype):
+    o, s = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    assert np.all(o[~ref.rows] == 5.0) and np.all(s[~ref.rows] == 6.0)      # rows of no sequence
+    o, s = o[ref.rows], s[ref.rows]
+    n = ref.keys[ref.rows][:, None]
+    e_s = (D * 2.0 ** -23 + 2.0 ** -22) * ref.logit[ref.rows]
+    tol = HALF_STEP[dtype] * np.abs(ref.out[ref.rows]) + \
+        (2.0 ** -11 + 2 * e_s + n * 2.0 ** -22)[..., None] * ref.weight[ref.rows] + 2.0 ** -24
+    err = np.abs(o - ref.out[ref.rows])
+    assert np.all(np.isfinite(o))
+    assert np.all(err <= tol), (err / tol).max()
+    empty = np.broadcast_to(n == 0, s.shape)
+    assert np.all(np.isneginf(s[empty])) and np.all(o[empty] == 0)
+    want = ref.lse[ref.rows][~empty]
+    ltol = (e_s + n * 2.0 ** -23)[~empty] + 2.0 ** -22 * (np.abs(want) + 1)
+    assert np.all(np.abs(s[~empty] - want) <= ltol), (np.abs(s[~empty] - want) / ltol).max()
+
+
+def queries(T, Hq, D, dtype, seed, size=1.5):
+    return (torch.randn(T, Hq, D, generator=gen(seed)) * size).to(DT[dtype])
+
+
+EDGE_LENS = [1, 2, 15, 16, 17, 31, 33, 63, 64, 65, 127, 128, 129, 255, 257, 0, 511, 700]
+
+
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [
+    (12, 2, 128, 16, "bf16"), (4, 4, 64, 48, "fp16"), (7, 1, 128, 64, "fp16"), (6, 2, 64, 16, "bf16"),
+    (8, 1, 128, 32, "bf16"), (10, 1, 64, 128, "fp16"), (17, 1, 128, 16, "bf16"), (40, 8, 128, 48, "fp16"),
+    (33, 1, 64, 16, "bf16"),
+])
+def test_decode_lengths(Hq, Hkv, D, page, dtype):
+    cache, tables = fill_sequences(EDGE_LENS, Hkv, D, page, seed=Hq)
+    check_attention(queries(len(EDGE_LENS), Hq, D, dtype, 3), cache, tables, EDGE_LENS, None, True, dtype)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page,dtype", [
+    ([5000], 4, 1, 128, 16, "bf16"), ([4097, 3, 0, 2050], 12, 2, 64, 64, "fp16"),
+    ([9001, 1], 8, 2, 128, 128, "bf16"), ([12345], 1, 1, 64, 48, "fp16"),
+])
+def test_decode_long(lens, Hq, Hkv, D, page, dtype):
+    cache, tables = fill_sequences(lens, Hkv, D, page, seed=2)
+    check_attention(queries(len(lens), Hq, D, dtype, 4), cache, tables, lens, None, True, dtype)
+
+
+def test_decode_many_sequences():
+    lens = [(i * 37) % 90 for i in range(700)]
+    cache, tables = fill_sequences(lens, 1, 64, 16, seed=2)
+    check_attention(queries(700, 2, 64, "bf16", 4), cache, tables, lens, None, True, "bf16")
+
+
+VARLEN = [
+    # lens, q lengths (rows before, between and behind them belong to nobody)
+    ([40, 17, 0, 129, 64, 5], [1, 17, 3, 2, 0, 9]),
+    ([300], [300]),
+    ([301, 129], [129, 129]),
+    ([700, 20, 33], [65, 1, 40]),
+    ([128], [128]),
+    ([1, 1, 1], [1, 5, 1]),
+]
+
+
+@pytest.mark.parametrize("lens,q_lens", VARLEN)
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [
+    (8, 2, 128, 16, "bf16"), (3, 3, 64, 48, "fp16"), (5, 1, 128, 64, "fp16"), (24, 8, 64, 32, "bf16")])
+def test_varlen(lens, q_lens, causal, Hq, Hkv, D, page, dtype):
+    cu = np.cumsum([2] + q_lens).tolist()                 # two rows in front of the first sequence
+    T = cu[-1] + 3                                        # and three behind the last
+    cache, tables = fill_sequences(lens, Hkv, D, page, seed=11)
+    check_attention(queries(T, Hq, D, dtype, 6), cache, tables, lens, cu, causal, dtype)
+
+
+@pytest.mark.parametrize("q_lens", [None, [1, 40, 150]])
+@pytest.mark.parametrize("D", [64, 128])
+def test_bad_pages_are_masked(q_lens, D):
+    lens = [200, 100, 160]
+    cache, tables = fill_sequences(lens, 2, D, 16, seed=21,
+                                   bad=[(0, 2, -1), (0, 12, 10 ** 6), (2, 0, 2 ** 31 - 1), (2, 9, -2 ** 31)]
+                                   + [(1, i, -1) for i in range(7)])        # sequence 1 sees nothing
+    cu = None if q_lens is None else np.cumsum([0] + q_lens).tolist()
+    T = 3 if cu is None else cu[-1]
+    check_attention(queries(T, 4, D, "bf16", 2), cache, tables, lens, cu, True, "bf16")
+
+
+@pytest.mark.parametrize("varlen", [False, True])
+def test_lengths_beyond_the_table_are_clamped(varlen):
+    cache, tables = fill_sequences([64, 64], 1, 64, 16, seed=1)
+    tables = tables[:, :4]
+    cu = [0, 20, 40] if varlen else None
+    T = 40 if varlen else 2
+    check_attention(queries(T, 4, 64, "fp16", 1), cache, np.ascontiguousarray(tables), [1000, 64], cu, False, "fp16")
+    check_attention(queries(T, 4, 64, "fp16", 1), cache, np.ascontiguousarray(tables), [-5, 64], cu, False, "fp16")
+
+
+@pytest.mark.parametrize("dtype,size", [("bf16", 1e-3), ("bf16", 60.0), ("fp16", 60.0), ("bf16", 1e6), ("fp16", 300.0),
+                                        ("bf16", 0.0)])
+@pytest.mark.parametrize("varlen", [False, True])
+def test_query_sizes(dtype, size, varlen):
+    lens = [90, 300]
+    cache, tables = fill_sequences(lens, 2, 128, 16, seed=31)
+    cu = [0, 30, 170] if varlen else None
+    check_attention(queries(170 if varlen else 2, 4, 128, dtype, 8, size), cache, tables, lens, cu, True, dtype)
+
+
+@pytest.mark.parametrize("varlen", [False, True])
+def test_global_scales_and_softmax_scale(varlen):
+    lens = [90, 300]
+    cache, tables = fill_sequences(lens, 2, 128, 16, seed=31)
+    cu = [0, 30, 170] if varlen else None
+    check_attention(queries(170 if varlen else 2, 4, 128, "fp16", 8), cache, tables, lens, cu, True, "fp16",
+                    sm_scale=0.21, kg=1.75, vg=0.4)
+
+
+@pytest.mark.parametrize("varlen", [False, True])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_bad_query_row_stays_alone(varlen, bad):
+    lens = [90, 300]
+    cache, tables = fill_sequences(lens, 2, 64, 16, seed=31)
+    cu = [0, 30, 170] if varlen else None
+    T = 170 if varlen else 2
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+    q = queries(T, 4, 64, "bf16", 8).cuda()
+    a = fq.attention_nvfp4(q, dev, tab, sl, cud)
+    q2 = q.clone()
+    q2[T // 2, 1, 5] = bad
+    b = fq.attention_nvfp4(q2, dev, tab, sl, cud)
+    same = torch.ones(T, 4, dtype=torch.bool)
+    same[T // 2, 1] = False
+    assert torch.equal(a.cpu()[same], b.cpu()[same])
+    assert torch.isnan(b[T // 2, 1]).all()
+
+
+@pytest.mark.parametrize("varlen", [False, True])
+def test_strided_queries_graphs_streams_and_repeats(varlen):
+    """A column slice of a wider matrix as q; the same bits on repeats, on another
+    stream and from a captured graph, which follows the lengths; two graphs."""
+    lens = [90, 300, 40]
+    Hq, D = 4, 128
+    cache, tables = fill_sequences(lens, 2, D, 16, seed=31)
+    cu = [0, 30, 170, 180] if varlen else None
+    T = 180 if varlen else 3
+    wide = torch.randn(T, (Hq + 3) * D, generator=gen(0)).bfloat16().cuda()
+    q = wide[:, D:(Hq + 1) * D].unflatten(-1, (Hq, D))
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cud = None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda")
+
+    def call(**kw):
+        return fq.attention_nvfp4(q, dev, tab, sl, cud, return_lse=True, **kw)
+    a, la = call()
+    assert torch.equal(a, fq.attention_nvfp4(q.contiguous(), dev, tab, sl, cud))
+    for _ in range(3):
+        b, lb = call()
+        assert torch.equal(a, b) and torch.equal(la, lb)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    b, lb = call(stream=side)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(a, b) and torch.equal(la, lb)
+    torch.cuda.synchronize()
+    g1, g2 = torch.cuda.CUDAGraph(), torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g1):
+        o1, l1 = call()
+    with torch.cuda.graph(g2):
+        o2, l2 = call()
+    for t in (o1, l1, o2, l2):
+        t.fill_(9)
+    g1.replay()
+    g2.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(o1, a) and torch.equal(o2, a) and torch.equal(l1, la) and torch.equal(l2, la)
+    sl.copy_(torch.tensor([10, 299, 0], dtype=torch.int32))
+    g1.replay()
+    torch.cuda.synchronize()
+    c, lc = call()
+    assert torch.equal(o1, c) and torch.equal(l1, lc)
+    assert not torch.equal(c, a)
+
+
+def test_offsets_beyond_32_bits():
+    """Pages behind 4 GiB of codes."""
+    pages, Hkv, page, D = 70000, 8, 128, 128
+    kp = torch.empty(pages, Hkv, page, D // 2, dtype=torch.uint8, device="cuda")
+    assert kp.numel() > 1 << 32
+    vp = torch.empty_like(kp)
+    ks = torch.empty(pages, Hkv, page, D // 16, dtype=torch.uint8, device="cuda")
+    vs = torch.empty(pages, Hkv, D // 16, page, dtype=torch.uint8, device="cuda")
+    c = (kp, ks, vp, vs)
+    T = 300
+    k, v = torch.randn(2, T, Hkv, D, generator=gen(0)).bfloat16().cuda()
+    tab = torch.tensor([[69999, 3, 68001]], dtype=torch.int32, device="cuda")
+    j = torch.arange(T, device="cuda")
+    slots = tab[0].long()[j // page] * page + j % page
+    fq.kv_append_nvfp4(c, k, v, slots)
+    small = fq.kv_cache_nvfp4(3, page, Hkv, D)
+    fq.kv_append_nvfp4(small, k, v, j)
+    for a, b in zip(fq.kv_gather_nvfp4(c, slots), fq.kv_gather_nvfp4(small, j)):
+        assert torch.equal(a, b)
+    sl = torch.tensor([T], dtype=torch.int32, device="cuda")
+    tab2 = torch.arange(3, dtype=torch.int32, device="cuda")[None]
+    q = queries(200, 16, D, "bf16", 1).cuda()
+    cu = torch.tensor([0, 200], dtype=torch.int32, device="cuda")
+    assert torch.equal(fq.attention_nvfp4(q, c, tab, sl, cu), fq.attention_nvfp4(q, small, tab2, sl, cu))
+    assert torch.equal(fq.attention_nvfp4(q[:1], c, tab, sl), fq.attention_nvfp4(q[:1], small, tab2, sl))
+
+
+# ---------------------------------------------------------------------------
+# together, as a serving step uses them
+# ---------------------------------------------------------------------------
+@pytest.mark.parametrize("pdl", [False, True])
+@pytest.mark.parametrize("D,Hq,Hkv", [(128, 8, 2), (64, 6, 3)])
+def test_prefill_then_decode_steps(pdl, D, Hq, Hkv):
+    """A prompt, then single tokens: append, attention, the output quantized for the
+    next product and multiplied; every attention row against the oracle on the oracle's
+    own cache bytes, which the GPU's equal."""
+    dtype, page, prompt, steps, B = "bf16", 16, 37, 5, 2
+    pages = 16
+    table = rope_table(256, D)
+    dev = fq.kv_cache_nvfp4(pages, page, Hkv, D)
+    ref = to_np(dev)
+    tables = np.arange(pages, dtype=np.int64)[::-1].reshape(B, -1).copy()
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    g = gen(77)
+    wmat = torch.randn(64, Hq * D, generator=g).bfloat16().cuda()
+    wp, wsf = fq.quantize_fp4(wmat)
+    lens = [0] * B
+    for step in range(1 + steps):
+        new = [prompt, prompt - 9] if step == 0 else [1] * B
+        cu = np.cumsum([0] + new)
+        T = int(cu[-1])
+        qkv = torch.randn(T, (Hq + 2 * Hkv) * D, generator=g).bfloat16()
+        pos = torch.cat([torch.arange(lens[b], lens[b] + new[b]) for b in range(B)])
+        slots = torch.cat([torch.from_numpy(tables[b])[torch.arange(lens[b], lens[b] + new[b]) // page] * page
+                           + torch.arange(lens[b], lens[b] + new[b]) % page for b in range(B)])
+        q, k, v = split(qkv, Hq, Hkv, D)
+        rq, _ = okv.append(ref, f32(k), f32(v), slots.numpy(), pos.numpy(), table.numpy(), False, q=f32(q))
+        lens = [lens[b] + new[b] for b in range(B)]
+        dq, dk, dv = split(qkv.cuda(), Hq, Hkv, D)
+        oq = fq.kv_append_nvfp4(dev, dk, dv, slots.cuda(), q=dq, positions=pos.cuda(), cos_sin=table.cuda(), pdl=pdl)
+        out, lse = fq.attention_nvfp4(oq, dev, tab, torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                      None if step else torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                      return_lse=True, pdl=pdl)
+        pk, sf = fq.quantize_fp4(out.reshape(T, Hq * D), pdl=pdl)
+        y = fq.gemm_nvfp4_bf16(pk, wp, sf, wsf, pdl=pdl)
+        torch.cuda.synchronize()
+        for a, b in zip(to_np(dev), ref):
+            assert np.array_equal(a, b)
+        q16 = torch.from_numpy(rq).bfloat16()
+        assert torch.equal(oq.cpu(), q16)
+        r = okv.attention(q16.double().numpy(), ref, tables, lens, cu, True, D ** -0.5)
+        compare_attention(out, lse, r, D, dtype)
+        a = fq.dequant(pk, sf, T, Hq * D, sf_layout="swizzled").double()
+        b = fq.dequant(wp, wsf, 64, Hq * D, sf_layout="swizzled").double()
+        exact = a @ b.T
+        bound = a.abs() @ b.abs().T
+        assert torch.all((y.double() - exact).abs() <= 2.0 ** -8 * exact.abs() + 2.0 ** -22 * Hq * D * bound)
+
+
+def test_cross_attention_to_encoder_states():
+    """Keys and values of an encoder appended without rotation; every decoder row sees all of them."""
+    Hq, Hkv, D, page = 6, 6, 64, 16
+    enc = [50, 77]
+    cache, tables = fill_sequences(enc, Hkv, D, page, seed=5)
+    check_attention(queries(9, Hq, D, "fp16", 5), cache, tables, enc, [0, 5, 9], False, "fp16")
+
+
+def test_status_word_is_left_alone():
+    cache, tables = fill_sequences([90, 300], 2, 128, 16, seed=31)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    for cu, T in ((None, 2), ([0, 30, 170], 170)):
+        check_attention(queries(T, 4, 128, "bf16", 8), cache, tables, [90, 300], cu, True, "bf16", status=status)
+        assert fq.read_device_status(status) == fq.FP4_OK
+
+
+def test_debug_build_finds_no_access_out_of_bounds():
+    fbuild.build(debug=True)
+    L = fq.debug_lib()
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    assert L.fp4_debug_configure(2_000_000_000, 0, 0, -1, -1, bad.data_ptr()) == 0
+    try:
+        with fq.using_library(L):
+            for args in APPEND[:8]:
+                test_append_and_gather(*args, None)
+            test_decode_lengths(12, 2, 128, 48, "bf16")
+            test_decode_lengths(4, 4, 64, 16, "fp16")
+            test_decode_long([4097, 3, 0, 2050], 12, 2, 64, 64, "fp16")
+            for lens, q_lens in VARLEN:
+                test_varlen(lens, q_lens, True, 8, 2, 128, 16, "bf16")
+                test_varlen(lens, q_lens, False, 3, 3, 64, 48, "fp16")
+            test_bad_pages_are_masked([1, 40, 150], 128)
+            torch.cuda.synchronize()
+            assert bad.item() == 0
+            # with every extent one byte shorter the checks see the last accesses
+            assert L.fp4_debug_configure(2_000_000_000, 1, 0, -1, -1, bad.data_ptr()) == 0
+            c = fq.kv_cache_nvfp4(1, 16, 1, 64)
+            k = torch.zeros(16, 1, 64, dtype=torch.bfloat16, device="cuda")
+            slots = torch.arange(16, device="cuda")
+            fq.kv_append_nvfp4(c, k, k, slots)
+            torch.cuda.synchronize()
+            n1 = bad.item()
+            assert n1 > 0
+            fq.kv_gather_nvfp4(c, slots)
+            torch.cuda.synchronize()
+            assert bad.item() > n1
+    finally:
+        L.fp4_debug_configure(2_000_000_000, 0, 0, -1, -1, None)
