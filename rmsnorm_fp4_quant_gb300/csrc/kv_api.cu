@@ -208,9 +208,10 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   if (q_stride == 0) q_stride = Hq * D;
   if (q_stride < Hq * D) return FP4_ERR_INVALID_ARG;
   if (!cu_seqlens_q && B != T) return FP4_ERR_INVALID_ARG;
-  // key positions are 32-bit numbers in the kernels, and so are row tiles
-  if (Hq > kMaxHeads || B > INT32_MAX / 2 || T > INT32_MAX / 2 ||
-      max_pages > INT32_MAX / 2 / cache->page_size || T * Hq > (int64_t{1} << 33))
+  // keys of a sequence and rows of a key/value head are 32-bit numbers in the
+  // kernels, and so are the grids over rows and sequences times heads
+  if (Hq > kMaxHeads || B > INT32_MAX / 2 || T > INT32_MAX / 2 || B * Hkv > INT32_MAX / 2 ||
+      T * Hq > INT32_MAX || max_pages > INT32_MAX / 2 / cache->page_size)
     return FP4_ERR_UNSUPPORTED_SHAPE;
   if (B == 0 || T == 0) return FP4_OK;
   if (!q || !out || !seq_lens || (max_pages && !block_tables)) return FP4_ERR_INVALID_ARG;

@@ -1,0 +1,634 @@
+// kv_decode.cuh - attention of few query rows per sequence over the paged NVFP4
+// cache: the cache's bytes are read once and bound the time.
+//
+// An item is (sequence, key/value head, tile of 8 * NT query rows), the rows
+// being the sequence's query tokens times the heads that share the key/value
+// head.  Products are taken transposed, keys and channels in the 16 rows of
+// mma.m16n8k16 and query rows in its 8 columns, so 4 to 8 heads of a group fill
+// the tile that 16 rows would leave half empty:
+//     S^T [16 keys x 8 rows]      = K [16 x D] * Q^T      (D / 16 steps)
+//     O^T [D channels x 8 rows]  += V^T [D x 16 keys] * P^T
+// Both contractions may run over their index in any order, so a lane takes
+// its operands where they lie: of K, D/4 consecutive channels of two keys (one
+// load each), and of V, D/8 consecutive channels of four consecutive keys;
+// codes become fp16 pairs byte by byte in registers (for V the nibbles of two
+// keys are first interleaved), and one multiplication by the block scales
+// makes them exact values.  P^T comes from S^T by an 8x8 transposition.
+//
+// Work split.  Every item is cut into units of 64 keys, the units of all items
+// are numbered in order, and CTA c of G takes units [c W / G, (c+1) W / G): the
+// CTAs get the same number of keys whatever the lengths are, and each item is
+// shared by consecutive CTAs.  Lengths are read on the device.  An item that
+// one CTA has whole is finished there; else each CTA leaves its part (O, the
+// reference r and the sum l, fp32) in the workspace and a second, small
+// kernel joins the parts in order.
+//
+// A CTA is 4 warps, each with its own 16 keys of a unit, its own r, l and O, and
+// its own ring of NST tiles in shared memory that cp.async fills NST - 1 tiles
+// ahead (a tile: 16 keys' codes and scales, 18 D bytes); no barrier in the loop.
+// At the end of an item's segment the four are joined in shared memory.
+#pragma once
+
+#include "kv_attention_common.cuh"
+
+namespace fp4q {
+
+constexpr int kDecWarps = 4;
+constexpr int kDecThreads = 32 * kDecWarps;
+constexpr int kDecUnit = 16 * kDecWarps;       // keys of a unit
+constexpr int kDecStages = 4;
+constexpr int kDecMinUnits = 4;                // a CTA's share is at least this long
+
+template <int D, int NT>
+struct DecodeShape {
+  static constexpr int kRows = 8 * NT;
+  static constexpr int kTile = 18 * D;         // bytes of 16 keys: K codes, V codes, K scales, V scales
+  static constexpr int kV = 8 * D, kKs = 16 * D, kVs = 17 * D;
+  static constexpr int kMergeStride = D + 8;   // floats per row in the merge buffer
+  static constexpr int kRing = kDecWarps * kDecStages * kTile;
+  static constexpr int kMerge = kDecWarps * kRows * kMergeStride * 4;
+  static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kCtas = NT == 1 ? 4 : 3;   // resident per SM
+  static constexpr int kPart = kRows * (D + 2);   // floats of one part in the workspace
+};
+
+// Workspace: 2 G parts, then one {first CTA, parts} pair per item.
+__host__ __device__ inline int64_t decode_row_slots(int64_t B, int64_t T, int group, int rows) {
+  return T * group / rows + B;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> __device__ __forceinline__ void cp_async_wait() {
+  asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
+}
+__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds16(uint32_t a) {
+  uint16_t v;
+  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
+  return v;
+}
+__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+template <int W> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[W]) {
+  if constexpr (W == 4)
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+  else if constexpr (W == 2)
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+  else
+    w[0] = lds32(a);
+}
+__device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                          uint32_t a3, uint32_t b0, uint32_t b1) {
+  asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+      "{%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t x) {
+  uint32_t y;
+  asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+  return y;
+}
+
+// Places of the 16-byte pieces of a tile's K and V codes: rows (keys) are D/2
+// bytes.  Chosen so that the lanes of one load (K: keys {0,1,4,5,...}, four
+// pieces each; V: keys {i, 4+i, 8+i, 12+i}, every piece) fall on different banks.
+template <int D> __device__ __forceinline__ int k_place(int row, int piece) {
+  if (D == 128) return row * 64 + piece * 16;
+  const int slot = (row & 9) | ((row & 2) << 1) | ((row & 4) >> 1);
+  return slot * 32 + piece * 16;
+}
+template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
+  if (D == 128) return (row ^ ((row >> 2) & 1)) * 64 + ((piece ^ (row >> 2)) & 3) * 16;
+  return ((row >> 2) | ((row & 3) << 2)) * 32 + piece * 16;
+}
+
+// What one CTA's walk over the units needs to know of the sequence it is in.
+struct DecodeWalk {
+  int b;             // sequence
+  int64_t base;      // its first unit
+  int tiles;         // units per item
+  int row_tiles;     // row tiles
+  KvSeq s;
+};
+template <int ROWS>
+__device__ __forceinline__ int64_t decode_units(const KvAttentionParams& p, int b, DecodeWalk& w) {
+  w.s = kv_sequence(p, b);
+  w.b = b;
+  // a sequence without keys still has a unit: its rows are written as 0
+  w.tiles = max(1, (w.s.len + kDecUnit - 1) / kDecUnit);
+  w.row_tiles = (w.s.n_q * p.group + ROWS - 1) / ROWS;
+  return static_cast<int64_t>(w.tiles) * w.row_tiles * p.c.heads;
+}
+
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kDecThreads, DecodeShape<D, NT>::kCtas)
+kv_decode_kernel(const KvAttentionParams p) {
+  using S = DecodeShape<D, NT>;
+  constexpr int ROWS = S::kRows;
+  constexpr int KW = D / 32;          // words of K a lane takes of one key
+  constexpr int VW = D / 64;          // words of V a lane takes of one key
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ int64_t scan_tot[kDecThreads / 32];
+  __shared__ int64_t start_base;
+  __shared__ int start_b;
+  __shared__ float merge_r[kDecWarps][ROWS], merge_l[kDecWarps][ROWS];
+
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int g = lane >> 2, t = lane & 3;
+  griddep_wait();
+  griddep_launch_dependents();
+
+  // total units, and the sequence that holds this CTA's first one: each thread
+  // sums a run of consecutive sequences
+  const int run = (p.B + kDecThreads - 1) / kDecThreads;
+  const int b_lo = min(tid * run, p.B), b_hi = min(b_lo + run, p.B);
+  int64_t mine = 0;
+  DecodeWalk w;
+  for (int b = b_lo; b < b_hi; ++b) mine += decode_units<ROWS>(p, b, w);
+  int64_t incl = mine;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int64_t up = __shfl_up_sync(kFullMask, incl, o);
+    if (lane >= o) incl += up;
+  }
+  if (lane == 31) scan_tot[warp] = incl;
+  __syncthreads();
+  int64_t before = incl - mine, total = 0;
+#pragma unroll
+  for (int i = 0; i < kDecThreads / 32; ++i) {
+    if (i < warp) before += scan_tot[i];
+    total += scan_tot[i];
+  }
+  int64_t G = (total + kDecMinUnits - 1) / kDecMinUnits;
+  if (G > static_cast<int64_t>(gridDim.x)) G = gridDim.x;
+  const int64_t cta = blockIdx.x;
+  if (cta >= G) return;
+  int64_t u = cta * total / G;
+  const int64_t u_end = (cta + 1) * total / G;
+  if (u >= before && u < before + mine) {       // exactly one thread
+    int64_t base = before;
+    int b = b_lo;
+    for (;;) {
+      const int64_t n = decode_units<ROWS>(p, b, w);
+      if (u < base + n) break;
+      base += n;
+      ++b;
+    }
+    start_b = b;
+    start_base = base;
+  }
+  __syncthreads();
+  int64_t units = decode_units<ROWS>(p, start_b, w);
+  w.base = start_base;
+
+  const uint32_t ring = smem_addr(smem) + warp * kDecStages * S::kTile;
+  const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
+  const float vgs = p.c.v_gs ? __ldg(p.c.v_gs) : 1.0f;
+  const int row_k = 4 * (g >> 1) + (g & 1);     // key of tile row g; row g + 8 is key row_k + 2
+
+  while (u < u_end) {
+    while (u >= w.base + units) {               // the next sequence that has units
+      w.base += units;
+      units = decode_units<ROWS>(p, w.b + 1, w);
+    }
+    const int item = static_cast<int>((u - w.base) / w.tiles);
+    const int tile0 = static_cast<int>(u - w.base - static_cast<int64_t>(item) * w.tiles);
+    const int kvh = item / w.row_tiles, rt = item - kvh * w.row_tiles;
+    const int n_units = static_cast<int>(min(static_cast<int64_t>(w.tiles - tile0), u_end - u));
+    const int rows = w.s.n_q * p.group;         // of the whole sequence
+    const int r0 = rt * ROWS;
+
+    // --- the item's queries, as the B operand: lane (g, t) holds channels
+    // D/4 * t ... of row g of each 8-row tile
+    uint32_t qf[NT][D / 16][2];
+    float fac[NT][2], ref[NT][2], sum[NT][2];
+    int lim[NT][2];                             // keys that columns 2t, 2t + 1 see
+    int lim_lo, lim_hi;                         // smallest and largest over the tile's rows
+    const int off = w.s.len - w.s.n_q;          // last visible key of token i: off + i
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = r0 + 8 * n + g;
+      const bool ok = r < rows;
+      const int tok = r / p.group, hq = kvh * p.group + r - tok * p.group;
+      const T* src = static_cast<const T*>(p.q) +
+                     static_cast<int64_t>(w.s.q0 + (ok ? tok : 0)) * p.q_stride +
+                     static_cast<int64_t>(ok ? hq : 0) * D + t * (D / 4);
+      Chunk c[D / 64];
+      float top = 0.0f;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        c[i] = Chunk{};
+        if (ok && FP4Q_IN_RANGE(p, src + 16 * i, 32, p.q, 2LL * ((p.T - 1) * p.q_stride + p.Hq * D)))
+          c[i] = ld_cached_ro(src + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 x = Pair<T>::to_f32(c[i].u[j]);
+          top = max_abs3(top, x.x, x.y);
+          nan |= x.x != x.x || x.y != x.y;
+        }
+      }
+      if (nan) top = INFINITY;                  // no scaling: the row is NaN whatever is done
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      const int k = q_exponent(top);
+      const float up = pow2(k);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 x = Pair<T>::to_f32(c[i].u[j]);
+          qf[n][4 * i + j / 2][j & 1] = pack_f16x2(x.x * up, x.y * up);
+        }
+      const float f = p.sm_scale * kLog2e / kgs * pow2(-k);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fac[n][e] = __shfl_sync(kFullMask, f, (2 * t + e) * 4);
+        ref[n][e] = kRefStart;
+        sum[n][e] = 0.0f;
+        const int rc = r0 + 8 * n + 2 * t + e;
+        lim[n][e] = p.causal && rc < rows ? min(w.s.len, off + rc / p.group + 1) : w.s.len;
+      }
+    }
+    {
+      const int last = min(r0 + ROWS, rows) - 1;
+      lim_lo = p.causal ? off + r0 / p.group + 1 : w.s.len;
+      lim_hi = p.causal ? off + last / p.group + 1 : w.s.len;
+    }
+
+    float acc[NT][D / 16][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
+
+    // --- the ring: tile x of this warp is keys key0(x) ... + 15
+    const int first_key = tile0 * kDecUnit + warp * 16;
+    const int32_t* table = p.tables + static_cast<int64_t>(w.b) * p.max_pages;
+    int pg = -1, in_pg = 0, pg_next = -1, in_pg_next = 0;
+    auto look_up = [&](int x, int& page, int& in_page) {     // tile x + lane
+      const int key = first_key + (x + lane) * kDecUnit;
+      page = -1;
+      if (x + lane < n_units && key < lim_hi) {
+        const int idx = key / p.c.page_size;
+        in_page = key - idx * p.c.page_size;
+        if (FP4Q_IN_RANGE(p, table + idx, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(table + idx);
+        if (page >= p.c.num_pages) page = -1;
+      }
+    };
+    look_up(0, pg, in_pg);
+    look_up(32, pg_next, in_pg_next);
+    uint32_t valid = 0;                          // bit i: the tile issued i tiles ago holds keys
+    auto issue = [&](int x) {
+      if ((x & 31) == 0 && x) {
+        pg = pg_next;
+        in_pg = in_pg_next;
+        look_up(x + 32, pg_next, in_pg_next);
+      }
+      const int page = __shfl_sync(kFullMask, pg, x & 31);
+      const int at = __shfl_sync(kFullMask, in_pg, x & 31);
+      valid = valid << 1 | (page >= 0 ? 1u : 0u);
+      if (page >= 0) {
+        const uint32_t dst = ring + (x % kDecStages) * S::kTile;
+        const int64_t ph = static_cast<int64_t>(page) * p.c.heads + kvh;
+        const int64_t row = ph * p.c.page_size + at;
+        const uint8_t* kc = p.c.k_packed + row * (D / 2);
+        const uint8_t* vc = p.c.v_packed + row * (D / 2);
+#pragma unroll
+        for (int i = 0; i < D / 64; ++i) {
+          const int c = lane + 32 * i;           // 16-byte piece of the 16 keys
+          const int r = c / (D / 32), piece = c % (D / 32);
+          if (FP4Q_IN_RANGE(p, kc + c * 16, 16, p.c.k_packed, kv_packed_extent(p.c)))
+            cp_async16(dst + k_place<D>(r, piece), kc + c * 16);
+          if (FP4Q_IN_RANGE(p, vc + c * 16, 16, p.c.v_packed, kv_packed_extent(p.c)))
+            cp_async16(dst + S::kV + v_place<D>(r, piece), vc + c * 16);
+        }
+        if (lane < D / 16) {
+          const uint8_t* s = p.c.k_sf + row * (D / 16) + lane * 16;
+          if (FP4Q_IN_RANGE(p, s, 16, p.c.k_sf, kv_sf_extent(p.c))) cp_async16(dst + S::kKs + lane * 16, s);
+        } else if (lane < D / 8) {
+          const int blk = lane - D / 16;
+          const uint8_t* s = p.c.v_sf + (ph * (D / 16) + blk) * p.c.page_size + at;
+          if (FP4Q_IN_RANGE(p, s, 16, p.c.v_sf, kv_sf_extent(p.c))) cp_async16(dst + S::kVs + blk * 16, s);
+        }
+      }
+      cp_async_commit();
+    };
+    for (int x = 0; x < kDecStages - 1; ++x) issue(x);
+
+    for (int x = 0; x < n_units; ++x) {
+      cp_async_wait<kDecStages - 2>();
+      __syncwarp();                              // the tile is here for every lane, tile x - 1 read
+      const bool here = valid >> (kDecStages - 2) & 1u;
+      issue(x + kDecStages - 1);
+      if (!here) continue;
+      const uint32_t st = ring + (x % kDecStages) * S::kTile;
+      const int key0 = first_key + x * kDecUnit;
+
+      // S^T = K Q^T
+      float s[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
+      {
+        uint32_t ka[KW], kb[KW], sa[2], sb[2];
+        lds_words<KW>(st + k_place<D>(row_k, KW * t / 4) + (KW * t % 4) * 4, ka);
+        lds_words<KW>(st + k_place<D>(row_k + 2, KW * t / 4) + (KW * t % 4) * 4, kb);
+        if constexpr (D == 128) {                // two blocks per lane
+          const uint32_t fa = e4m3x2_to_f16x2(lds16(st + S::kKs + row_k * 8 + 2 * t));
+          const uint32_t fb = e4m3x2_to_f16x2(lds16(st + S::kKs + (row_k + 2) * 8 + 2 * t));
+          sa[0] = __byte_perm(fa, 0, 0x1010);
+          sa[1] = __byte_perm(fa, 0, 0x3232);
+          sb[0] = __byte_perm(fb, 0, 0x1010);
+          sb[1] = __byte_perm(fb, 0, 0x3232);
+        } else {
+          const uint32_t ba = lds8(st + S::kKs + row_k * 4 + t), bb = lds8(st + S::kKs + (row_k + 2) * 4 + t);
+          sa[0] = sa[1] = e4m3x2_to_f16x2(ba | ba << 8);
+          sb[0] = sb[1] = e4m3x2_to_f16x2(bb | bb << 8);
+        }
+#pragma unroll
+        for (int i = 0; i < KW; ++i) {
+          uint32_t ha[4], hb[4];
+          e2m1x8_to_f16x2(ka[i], ha);
+          e2m1x8_to_f16x2(kb[i], hb);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            ha[e] = mul_f16x2(ha[e], sa[i / 2]);
+            hb[e] = mul_f16x2(hb[e], sb[i / 2]);
+          }
+#pragma unroll
+          for (int n = 0; n < NT; ++n) {
+            mma_16816(s[n], ha[0], hb[0], ha[1], hb[1], qf[n][2 * i][0], qf[n][2 * i][1]);
+            mma_16816(s[n], ha[2], hb[2], ha[3], hb[3], qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+          }
+        }
+      }
+
+      // logits as exponents of 2; keys a row does not see become -inf
+      const bool whole = key0 + 16 <= lim_lo;
+      bool over = false;
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] *= fac[n][e & 1];
+          if (!whole && key0 + row_k + (e & 2) >= lim[n][e & 1]) s[n][e] = -INFINITY;
+          over |= s[n][e] > ref[n][e & 1] + kRefSlack;
+        }
+      if (__any_sync(kFullMask, over)) {         // rare after the first tiles
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float m = fmaxf(s[n][e], s[n][e + 2]);
+            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
+            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
+            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
+            const float r = fmaxf(ref[n][e], m - kRefBelow);
+            const float f = ex2(ref[n][e] - r);
+            ref[n][e] = r;
+            sum[n][e] *= f;
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) {
+              acc[n][i][e] *= f;
+              acc[n][i][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t pb[NT][2];
+#pragma unroll
+      for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          s[n][e] = ex2(s[n][e] - ref[n][e & 1]);
+          sum[n][e & 1] += s[n][e];
+        }
+        pb[n][0] = transpose8x8(pack_f16x2(s[n][0], s[n][1]));
+        pb[n][1] = transpose8x8(pack_f16x2(s[n][2], s[n][3]));
+      }
+
+      // O^T += V^T P^T: keys 4t .. 4t + 3 of the tile
+      {
+        uint32_t sv = lds32(st + S::kVs + (D == 128 ? g : g / 2) * 16 + 4 * t);
+        if (key0 + 16 > w.s.len) {               // slots behind the end may hold no numbers
+          const int left = w.s.len - key0 - 4 * t;
+          sv = left <= 0 ? 0u : left >= 4 ? sv : sv & (0xffffffffu >> (32 - 8 * left));
+        }
+        const uint32_t s01 = e4m3x2_to_f16x2(sv), s23 = e4m3x2_to_f16x2(sv >> 16);
+        uint32_t v[4][VW];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int word = VW * g;               // of the key's D/8 words
+          lds_words<VW>(st + S::kV + v_place<D>(4 * t + i, word / 4) + (word % 4) * 4, v[i]);
+        }
+#pragma unroll
+        for (int i = 0; i < VW; ++i) {
+          uint32_t e01[4], o01[4], e23[4], o23[4];
+          e2m1x8_to_f16x2((v[0][i] & 0x0f0f0f0fu) | (v[1][i] << 4 & 0xf0f0f0f0u), e01);
+          e2m1x8_to_f16x2((v[0][i] >> 4 & 0x0f0f0f0fu) | (v[1][i] & 0xf0f0f0f0u), o01);
+          e2m1x8_to_f16x2((v[2][i] & 0x0f0f0f0fu) | (v[3][i] << 4 & 0xf0f0f0f0u), e23);
+          e2m1x8_to_f16x2((v[2][i] >> 4 & 0x0f0f0f0fu) | (v[3][i] & 0xf0f0f0f0u), o23);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {          // channels D/8 g + 8 i + 2 j and the next
+            const uint32_t a0 = mul_f16x2(e01[j], s01), a1 = mul_f16x2(o01[j], s01);
+            const uint32_t a2 = mul_f16x2(e23[j], s23), a3 = mul_f16x2(o23[j], s23);
+#pragma unroll
+            for (int n = 0; n < NT; ++n) mma_16816(acc[n][4 * i + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+          }
+        }
+      }
+    }
+    cp_async_wait<0>();
+
+    // --- join the four warps
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        sum[n][e] += __shfl_xor_sync(kFullMask, sum[n][e], 4);
+        sum[n][e] += __shfl_xor_sync(kFullMask, sum[n][e], 8);
+        sum[n][e] += __shfl_xor_sync(kFullMask, sum[n][e], 16);
+        if (g == 0) {
+          merge_r[warp][8 * n + 2 * t + e] = ref[n][e];
+          merge_l[warp][8 * n + 2 * t + e] = sum[n][e];
+        }
+      }
+    __syncthreads();                             // every warp is done with its ring
+    float* mo = reinterpret_cast<float*>(smem) + warp * ROWS * S::kMergeStride;
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = 8 * n + 2 * t + e;
+        float top = merge_r[0][r];
+#pragma unroll
+        for (int i = 1; i < kDecWarps; ++i) top = fmaxf(top, merge_r[i][r]);
+        const float f = ex2(ref[n][e] - top);
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i)         // channels D/8 g + 2 i, + 1 at 16 i + 2 g, + 1
+          *reinterpret_cast<float2*>(mo + r * S::kMergeStride + 16 * i + 2 * g) =
+              make_float2(acc[n][i][e] * f, acc[n][i][e + 2] * f);
+      }
+    __syncthreads();
+    const bool whole_item = n_units == w.tiles;
+    // a part that begins the item is this CTA's last, one that does not its first
+    float* part = p.ws + (2 * cta + (tile0 == 0 ? 1 : 0)) * S::kPart;
+    const float* m0 = reinterpret_cast<const float*>(smem);
+    for (int x = tid; x < ROWS * (D / 8); x += kDecThreads) {
+      const int r = x / (D / 8), d0 = (x % (D / 8)) * 8;
+      float top = merge_r[0][r];
+#pragma unroll
+      for (int i = 1; i < kDecWarps; ++i) top = fmaxf(top, merge_r[i][r]);
+      float l = 0.0f;
+#pragma unroll
+      for (int i = 0; i < kDecWarps; ++i) l += merge_l[i][r] * ex2(merge_r[i][r] - top);
+      float o[8];
+#pragma unroll
+      for (int j = 0; j < 8; j += 2) {
+        const int d = d0 + j, gg = d / (D / 8), i = (d % (D / 8)) / 2;
+        float2 a = make_float2(0.0f, 0.0f);
+#pragma unroll
+        for (int k = 0; k < kDecWarps; ++k) {
+          const float2 y = *reinterpret_cast<const float2*>(m0 + (k * ROWS + r) * S::kMergeStride +
+                                                            16 * i + 2 * gg);
+          a.x += y.x;
+          a.y += y.y;
+        }
+        o[j] = a.x;
+        o[j + 1] = a.y;
+      }
+      const int row = r0 + r;
+      if (row >= rows) continue;
+      if (whole_item) {
+        const int tok = row / p.group;
+        const int64_t at = static_cast<int64_t>(w.s.q0 + tok) * p.Hq + kvh * p.group + row - tok * p.group;
+        const float inv = l > 0.0f ? 1.0f / (l * vgs) : l == 0.0f ? 0.0f : l;   // NaN stays
+        T* dst = static_cast<T*>(p.out) + at * D + d0;
+        if (FP4Q_IN_RANGE(p, dst, 16, p.out, 2LL * p.T * p.Hq * D))
+          *reinterpret_cast<uint4*>(dst) = make_uint4(
+              Pair<T>::from_f32(o[0] * inv, o[1] * inv), Pair<T>::from_f32(o[2] * inv, o[3] * inv),
+              Pair<T>::from_f32(o[4] * inv, o[5] * inv), Pair<T>::from_f32(o[6] * inv, o[7] * inv));
+        if (d0 == 0 && p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * p.T * p.Hq))
+          p.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (top + log2f(l));
+      } else {
+        float4* po = reinterpret_cast<float4*>(part + r * D + d0);
+        po[0] = make_float4(o[0], o[1], o[2], o[3]);
+        po[1] = make_float4(o[4], o[5], o[6], o[7]);
+        if (d0 == 0) *reinterpret_cast<float2*>(part + ROWS * D + 2 * r) = make_float2(top, l);
+      }
+    }
+    if (tid == 0 && tile0 == 0) {
+      // where the joining kernel finds the item's parts
+      const int64_t slot = (static_cast<int64_t>(w.s.q0) * p.group / ROWS + w.b + rt) * p.c.heads + kvh;
+      const int64_t last = u + w.tiles - 1;      // its last unit
+      const int n = static_cast<int>(((last + 1) * G - 1) / total - cta) + 1;
+      int* desc = reinterpret_cast<int*>(p.ws + 2 * static_cast<int64_t>(gridDim.x) * S::kPart) + 2 * slot;
+      desc[0] = static_cast<int>(cta);
+      desc[1] = n;
+    }
+    u += n_units;
+    __syncthreads();                             // the merge buffer becomes the ring again
+  }
+}
+
+// Joins the parts of the items that several CTAs shared: block = (item, row),
+// D / 4 lanes per part, parts taken in turn by the block's groups of lanes and
+// summed in order.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(128) kv_decode_join_kernel(const KvAttentionParams p, int ctas) {
+  using S = DecodeShape<D, NT>;
+  constexpr int ROWS = S::kRows;
+  constexpr int LANES = D / 4, GROUPS = 128 / LANES;
+  __shared__ float red[4];
+  __shared__ float4 o_part[GROUPS][LANES];
+  __shared__ float l_part[GROUPS];
+  const int tid = threadIdx.x;
+  const int64_t slot = blockIdx.x;
+  const int kvh = static_cast<int>(slot % p.c.heads), r = blockIdx.y;
+  const int64_t rs = slot / p.c.heads;
+  griddep_wait();
+  griddep_launch_dependents();
+  // the last sequence whose slots begin at or before rs
+  auto slots_from = [&](int b) {
+    const int64_t q0 = p.cu ? min(max(p.cu[b], 0), static_cast<int>(p.T)) : b;
+    return q0 * p.group / ROWS + b;
+  };
+  int b = 0, hi = p.B - 1;
+  while (b < hi) {
+    const int mid = (b + hi + 1) / 2;
+    if (slots_from(mid) <= rs) b = mid; else hi = mid - 1;
+  }
+  const int64_t rt = rs - slots_from(b);
+  const KvSeq s = kv_sequence(p, b);
+  const int rows = s.n_q * p.group;
+  if (rt < 0 || rt * ROWS + r >= rows) return;
+  const int row = static_cast<int>(rt) * ROWS + r;
+  const int* desc = reinterpret_cast<const int*>(p.ws + 2 * static_cast<int64_t>(ctas) * S::kPart) + 2 * slot;
+  const int c0 = desc[0], n = desc[1];
+  if (n <= 1 || c0 < 0 || n > ctas - c0) return;
+  // part i: the last of CTA c0 for i = 0, the first of CTA c0 + i else
+  auto part = [&](int i) { return p.ws + (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * S::kPart; };
+  float top = kRefStart;
+  for (int i = tid; i < n; i += 128) top = fmaxf(top, part(i)[ROWS * D + 2 * r]);
+#pragma unroll
+  for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
+  if ((tid & 31) == 0) red[tid >> 5] = top;
+  __syncthreads();
+  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  const int grp = tid / LANES, ln = tid % LANES;
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f;
+#pragma unroll 4
+  for (int i = grp; i < n; i += GROUPS) {
+    const float* q = part(i);
+    const float2 rl = *reinterpret_cast<const float2*>(q + ROWS * D + 2 * r);
+    const float4 x = *reinterpret_cast<const float4*>(q + r * D + 4 * ln);
+    const float f = ex2(rl.x - top);
+    o.x += x.x * f;
+    o.y += x.y * f;
+    o.z += x.z * f;
+    o.w += x.w * f;
+    l += rl.y * f;
+  }
+  o_part[grp][ln] = o;
+  if (ln == 0) l_part[grp] = l;
+  __syncthreads();
+  if (grp) return;
+  l = l_part[0];
+#pragma unroll
+  for (int i = 1; i < GROUPS; ++i) {
+    const float4 x = o_part[i][ln];
+    o.x += x.x;
+    o.y += x.y;
+    o.z += x.z;
+    o.w += x.w;
+    l += l_part[i];
+  }
+  const float vgs = p.c.v_gs ? __ldg(p.c.v_gs) : 1.0f;
+  const float inv = l > 0.0f ? 1.0f / (l * vgs) : l == 0.0f ? 0.0f : l;
+  const int tok = row / p.group;
+  const int64_t at = static_cast<int64_t>(s.q0 + tok) * p.Hq + kvh * p.group + row - tok * p.group;
+  T* dst = static_cast<T*>(p.out) + at * D + 4 * ln;
+  if (FP4Q_IN_RANGE(p, dst, 8, p.out, 2LL * p.T * p.Hq * D))
+    *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::from_f32(o.x * inv, o.y * inv),
+                                                Pair<T>::from_f32(o.z * inv, o.w * inv));
+  if (ln == 0 && p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * p.T * p.Hq))
+    p.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (top + log2f(l));
+}
+
+}  // namespace fp4q
