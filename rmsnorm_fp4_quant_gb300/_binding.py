@@ -625,45 +625,64 @@ def kv_cache_nvfp4(num_pages: int, page_size: int, num_kv_heads: int, head_dim: 
                         zeros(page_size, head_dim // 2), zeros(head_dim // 16, page_size))
 
 
-def _kv_struct(cache, k_global_scale, v_global_scale) -> KVCacheStruct:
-    torch = _torch()
+# These calls are short enough on the device that the checks count: attributes are
+# read once, devices compared by number, and the library is called directly.
+def _kv_struct(cache, k_global_scale, v_global_scale):
+    """(fp4_kv_cache_t, device number) of a cache whose buffers have been checked."""
+    u8 = _torch().uint8
     kp, ks, vp, vs = cache
-    for name, t in (("k_packed", kp), ("k_sf", ks), ("v_packed", vp), ("v_sf", vs)):
-        if t.dtype != torch.uint8 or t.dim() != 4:
-            raise ValueError(f"cache {name} must be uint8 with four dimensions")
-        _check_cuda(t, f"cache {name}")
-        if t.device != kp.device:
-            raise ValueError("the cache's buffers must be on one device")
-    pages, heads, page, half = kp.shape
-    if (vp.shape != kp.shape or ks.shape != (pages, heads, page, half // 8) or half % 8
+    shape = kp.shape
+    dev = kp.get_device()
+    if dev < 0:
+        raise ValueError("the cache must be CUDA tensors (the library has no CPU path)")
+    if len(shape) != 4:
+        raise ValueError("cache buffers must have four dimensions")
+    pages, heads, page, half = shape
+    if (vp.shape != shape or ks.shape != (pages, heads, page, half // 8) or half % 8
             or vs.shape != (pages, heads, half // 8, page)):
         raise ValueError("cache buffers must be [pages, kv_heads, page_size, head_dim/2], "
                          "[pages, kv_heads, page_size, head_dim/16], [pages, kv_heads, page_size, "
                          "head_dim/2] and [pages, kv_heads, head_dim/16, page_size]")
-    return KVCacheStruct(kp.data_ptr(), ks.data_ptr(), vp.data_ptr(), vs.data_ptr(),
-                         _gs_ptr(k_global_scale) or None, _gs_ptr(v_global_scale) or None,
-                         pages, page, heads, 2 * half)
+    for t in (kp, ks, vp, vs):
+        if t.dtype is not u8 or not t.is_contiguous() or t.get_device() != dev:
+            raise ValueError("cache buffers must be contiguous uint8 tensors on one device")
+    if dev != _torch().cuda.current_device():
+        raise ValueError(f"the cache is on cuda:{dev}, which is not the current device")
+    kg = vg = None
+    if k_global_scale is not None:
+        _same_device(dev, "k_global_scale", k_global_scale)
+        kg = _gs_ptr(k_global_scale)
+    if v_global_scale is not None:
+        _same_device(dev, "v_global_scale", v_global_scale)
+        vg = _gs_ptr(v_global_scale)
+    return KVCacheStruct(kp.data_ptr(), ks.data_ptr(), vp.data_ptr(), vs.data_ptr(), kg, vg,
+                         pages, page, heads, 2 * half), dev
 
 
-def _kv_device(cache, *tensors):
-    """Every tensor on the cache's device, which has to be the current one (the
-    launch goes to a stream of the current device)."""
-    torch = _torch()
-    dev = cache[0].device
-    if dev.index != torch.cuda.current_device():
-        raise ValueError(f"the cache is on {dev}, which is not the current device")
-    for name, t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"{name} must be on the cache's device")
+def _same_device(dev, name, t):
+    if t.get_device() != dev:
+        raise ValueError(f"{name} must be on the cache's device (CUDA)")
 
 
-def _head_rows(t, name, heads, dim):
+def _head_rows(t, name, dev, T, heads, dim, dtype):
     """Elements between tokens of a (T, heads, dim) tensor whose heads are dense."""
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != dim:
-        raise ValueError(f"{name} must be (T, {heads}, {dim})")
-    if t.stride(2) != 1 or (heads > 1 and t.stride(1) != dim):
+    _same_device(dev, name, t)
+    if t.shape != (T, heads, dim) or t.dtype is not dtype:
+        raise ValueError(f"{name} must be ({T}, {heads}, {dim}) {dtype}")
+    tok, head, one = t.stride()
+    if one != 1 or (heads > 1 and head != dim):
         raise ValueError(f"{name} must have dense heads")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    if T > 1 and tok < heads * dim:
+        raise ValueError(f"{name} must have tokens that do not overlap")
+    return tok if T > 1 else heads * dim
+
+
+def _dense_ptr(t, name, dev, dtype, shape):
+    """Address of a contiguous tensor of the given type and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
+    _same_device(dev, name, t)
+    return t.data_ptr()
 
 
 def _on(stream):
@@ -671,10 +690,12 @@ def _on(stream):
     return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
 
 
-def _index(t, name, dtype, shape):
-    if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-    return t.data_ptr()
+def _kv_stream(stream, dev) -> int:
+    torch = _torch()
+    if stream is not None:
+        return stream.cuda_stream
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without a Stream object
+    return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
 def kv_append_nvfp4(cache, k, v, slots, q=None, positions=None, cos_sin=None,
@@ -693,44 +714,39 @@ def kv_append_nvfp4(cache, k, v, slots, q=None, positions=None, cos_sin=None,
     neither its slot nor its row of out_q is written.  interleaved: pairs are
     channels 2i and 2i + 1 instead of i and i + rot_dim/2.  out_q: may be q itself."""
     torch = _torch()
-    struct = _kv_struct(cache, k_global_scale, v_global_scale)
+    struct, dev = _kv_struct(cache, k_global_scale, v_global_scale)
     heads, dim = struct.num_kv_heads, struct.head_dim
-    _kv_device(cache, ("k", k), ("v", v), ("slots", slots), ("q", q), ("positions", positions),
-               ("cos_sin", cos_sin), ("out_q", out_q), ("k_global_scale", k_global_scale),
-               ("v_global_scale", v_global_scale))
-    ks, vs = _head_rows(k, "k", heads, dim), _head_rows(v, "v", heads, dim)
-    T = k.shape[0]
+    T, dtype = k.shape[0], k.dtype
     dt = _dtype_code(k)
-    if v.dtype != k.dtype or v.shape[0] != T:
-        raise ValueError("k and v must have the same shape and dtype")
-    hq = qs = oqs = 0
+    ks = _head_rows(k, "k", dev, T, heads, dim, dtype)
+    vs = _head_rows(v, "v", dev, T, heads, dim, dtype)
+    hq = qs = oqs = qp = oqp = 0
     if q is not None:
         hq = q.shape[1]
-        qs = _head_rows(q, "q", hq, dim)
-        if q.shape[0] != T or q.dtype != k.dtype:
-            raise ValueError("q must have k's dtype and number of tokens")
+        qs = _head_rows(q, "q", dev, T, hq, dim, dtype)
         if out_q is None:
             with _on(stream):
-                out_q = torch.empty(T, hq, dim, dtype=q.dtype, device=q.device)
-        oqs = _head_rows(out_q, "out_q", hq, dim)
-        if out_q.shape[0] != T or out_q.dtype != q.dtype:
-            raise ValueError("out_q must have q's shape and dtype")
+                out_q = torch.empty(T, hq, dim, dtype=dtype, device=q.device)
+        oqs = _head_rows(out_q, "out_q", dev, T, hq, dim, dtype)
+        if hq:
+            qp, oqp = q.data_ptr(), out_q.data_ptr()
     elif out_q is not None:
         raise ValueError("out_q without q")
     rot = table = pos = rows = 0
     if cos_sin is not None:
-        if cos_sin.dtype != torch.float32 or cos_sin.dim() != 2 or not cos_sin.is_contiguous():
-            raise ValueError("cos_sin must be a contiguous float32 (positions, rot_dim) tensor")
         if positions is None:
             raise ValueError("cos_sin needs positions")
+        if cos_sin.dim() != 2:
+            raise ValueError("cos_sin must be (positions, rot_dim)")
         rows, rot = cos_sin.shape
-        table, pos = cos_sin.data_ptr(), _index(positions, "positions", torch.int64, (T,))
+        table = _dense_ptr(cos_sin, "cos_sin", dev, torch.float32, (rows, rot))
+        pos = _dense_ptr(positions, "positions", dev, torch.int64, (T,))
     elif positions is not None:
         raise ValueError("positions without cos_sin")
-    st = fp4_kv_append_nvfp4(q.data_ptr() if hq else 0, qs, out_q.data_ptr() if hq else 0, oqs,
-                             k.data_ptr(), ks, v.data_ptr(), vs, pos, table, rows, rot,
-                             1 if interleaved else 0, _index(slots, "slots", torch.int64, (T,)), T,
-                             hq, dt, struct, 1 if pdl else 0, _stream_handle(stream))
+    st = lib().fp4_kv_append_nvfp4(qp, qs, oqp, oqs, k.data_ptr(), ks, v.data_ptr(), vs, pos, table,
+                                   rows, rot, 1 if interleaved else 0,
+                                   _dense_ptr(slots, "slots", dev, torch.int64, (T,)), T, hq, dt,
+                                   struct, 1 if pdl else 0, _kv_stream(stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_kv_append_nvfp4")
     return out_q
@@ -742,24 +758,22 @@ def kv_gather_nvfp4(cache, slots, dtype=None, k_global_scale=None, v_global_scal
     that of out_k / out_v); a slot outside the cache leaves its rows of out_k and
     out_v as they were."""
     torch = _torch()
-    struct = _kv_struct(cache, k_global_scale, v_global_scale)
-    _kv_device(cache, ("slots", slots), ("out_k", out_k), ("out_v", out_v),
-               ("k_global_scale", k_global_scale), ("v_global_scale", v_global_scale))
+    struct, dev = _kv_struct(cache, k_global_scale, v_global_scale)
     if dtype is None:
         dtype = out_k.dtype if out_k is not None else out_v.dtype if out_v is not None \
             else torch.bfloat16
-    shape = (slots.shape[0], struct.num_kv_heads, struct.head_dim)
-    with _on(stream):
-        if out_k is None:
-            out_k = torch.empty(shape, dtype=dtype, device=slots.device)
-        if out_v is None:
-            out_v = torch.empty(shape, dtype=dtype, device=slots.device)
-    for name, t in (("out_k", out_k), ("out_v", out_v)):
-        if t.dtype != dtype or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}")
-    st = fp4_kv_gather_nvfp4(struct, _index(slots, "slots", torch.int64, (shape[0],)), shape[0],
-                             _dtype_code(out_k), out_k.data_ptr(), out_v.data_ptr(),
-                             1 if pdl else 0, _stream_handle(stream))
+    T = slots.shape[0]
+    shape = (T, struct.num_kv_heads, struct.head_dim)
+    if out_k is None or out_v is None:
+        with _on(stream):
+            if out_k is None:
+                out_k = torch.empty(shape, dtype=dtype, device=slots.device)
+            if out_v is None:
+                out_v = torch.empty(shape, dtype=dtype, device=slots.device)
+    st = lib().fp4_kv_gather_nvfp4(struct, _dense_ptr(slots, "slots", dev, torch.int64, (T,)), T,
+                                   _dtype_code(out_k), _dense_ptr(out_k, "out_k", dev, dtype, shape),
+                                   _dense_ptr(out_v, "out_v", dev, dtype, shape),
+                                   1 if pdl else 0, _kv_stream(stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_kv_gather_nvfp4")
     return out_k, out_v
@@ -783,52 +797,51 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     (lse (T, heads) fp32, natural logarithm).  workspace: optional uint8 tensor of
     fp4_attention_workspace_bytes bytes, for one call at a time."""
     torch = _torch()
-    struct = _kv_struct(cache, k_global_scale, v_global_scale)
-    _kv_device(cache, ("q", q), ("block_tables", block_tables), ("seq_lens", seq_lens),
-               ("cu_seqlens_q", cu_seqlens_q), ("out", out), ("lse", lse),
-               ("workspace", workspace), ("status", status), ("k_global_scale", k_global_scale),
-               ("v_global_scale", v_global_scale))
-    if q.dim() != 3:
+    struct, dev = _kv_struct(cache, k_global_scale, v_global_scale)
+    shape, dtype = q.shape, q.dtype
+    if len(shape) != 3:
         raise ValueError("q must be (T, heads, head_dim)")
-    T, hq, dim = q.shape
-    qs = _head_rows(q, "q", hq, struct.head_dim)
-    if hq % struct.num_kv_heads:
+    T, hq, dim = shape
+    qs = _head_rows(q, "q", dev, T, hq, struct.head_dim, dtype)
+    heads = struct.num_kv_heads
+    if hq % heads:
         raise ValueError("the number of query heads must be a multiple of the cache's kv_heads")
+    i32 = torch.int32
     if block_tables.dim() != 2:
         raise ValueError("block_tables must be (B, max_pages)")
     B, max_pages = block_tables.shape
-    tables = _index(block_tables, "block_tables", torch.int32, (B, max_pages))
-    lens = _index(seq_lens, "seq_lens", torch.int32, (B,))
+    tables = _dense_ptr(block_tables, "block_tables", dev, i32, (B, max_pages))
+    lens = _dense_ptr(seq_lens, "seq_lens", dev, i32, (B,))
     cu = 0
     if cu_seqlens_q is not None:
-        cu = _index(cu_seqlens_q, "cu_seqlens_q", torch.int32, (B + 1,))
+        cu = _dense_ptr(cu_seqlens_q, "cu_seqlens_q", dev, i32, (B + 1,))
     elif T != B:
         raise ValueError("q must have one row per sequence without cu_seqlens_q")
-    with _on(stream):
-        if out is None:
-            out = torch.empty(T, hq, dim, dtype=q.dtype, device=q.device)
-        if return_lse and lse is None:
-            lse = torch.empty(T, hq, dtype=torch.float32, device=q.device)
-        if workspace is None:
-            need = fp4_attention_workspace_bytes(B, T, hq, struct.num_kv_heads, dim)
-            if need > 0:
-                workspace = torch.empty(need, dtype=torch.uint8, device=q.device)
-    if out.dtype != q.dtype or tuple(out.shape) != (T, hq, dim) or not out.is_contiguous():
-        raise ValueError("out must be contiguous with q's shape and dtype")
-    if lse is not None and (lse.dtype != torch.float32 or tuple(lse.shape) != (T, hq)
-                            or not lse.is_contiguous()):
-        raise ValueError("lse must be a contiguous float32 (T, heads) tensor")
-    if workspace is not None:
+    L = lib()
+    if workspace is None:
+        size = max(L.fp4_attention_workspace_bytes(B, T, hq, heads, dim), 0)
+    else:
         _check_cuda(workspace, "workspace")
-    st = fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
-                             _dtype_code(q),
-                             float(sm_scale) if sm_scale is not None else float(dim) ** -0.5,
-                             1 if causal else 0, out.data_ptr(),
-                             lse.data_ptr() if lse is not None else 0,
-                             workspace.data_ptr() if workspace is not None else 0,
-                             workspace.numel() * workspace.element_size()
-                             if workspace is not None else 0,
-                             _status_ptr(status), 1 if pdl else 0, _stream_handle(stream))
+        _same_device(dev, "workspace", workspace)
+        size = workspace.numel() * workspace.element_size()
+    if out is None or workspace is None or (return_lse and lse is None):
+        with _on(stream):
+            if out is None:
+                out = torch.empty(shape, dtype=dtype, device=q.device)
+            if return_lse and lse is None:
+                lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+            if workspace is None:
+                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+    if status is not None:
+        _same_device(dev, "status", status)
+    st = L.fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
+                               _dtype_code(q),
+                               float(sm_scale) if sm_scale is not None else dim ** -0.5,
+                               1 if causal else 0, _dense_ptr(out, "out", dev, dtype, shape),
+                               _dense_ptr(lse, "lse", dev, torch.float32, (T, hq))
+                               if lse is not None else 0,
+                               workspace.data_ptr(), size,
+                               _status_ptr(status), 1 if pdl else 0, _kv_stream(stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_attention_nvfp4")
     return (out, lse) if return_lse else out

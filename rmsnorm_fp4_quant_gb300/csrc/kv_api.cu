@@ -53,8 +53,9 @@ fp4_status_t check_cache_sizes(const fp4_kv_cache_t* c) {
     return FP4_ERR_INVALID_ARG;
   if (c->head_dim != 64 && c->head_dim != 128) return FP4_ERR_UNSUPPORTED_SHAPE;
   if (c->page_size % 16 || c->page_size > (1 << 20) || c->num_kv_heads > kMaxHeads ||
-      c->num_pages > INT32_MAX)
-    return FP4_ERR_UNSUPPORTED_SHAPE;
+      c->num_pages > INT32_MAX ||
+      c->num_pages * c->page_size > (int64_t{UINT32_MAX} - 1) / c->num_kv_heads)
+    return FP4_ERR_UNSUPPORTED_SHAPE;   // the kernels number slots times heads in 32 bits
   return FP4_OK;
 }
 fp4_status_t check_cache_buffers(const fp4_kv_cache_t* c) {

@@ -38,6 +38,10 @@ constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecUnit = 16 * kDecWarps;       // keys of a unit
 constexpr int kDecStages = 4;
 constexpr int kDecMinUnits = 4;                // a CTA's share is at least this long
+// What an item costs besides its keys (its queries, the ring's first tiles, the
+// join), in units: the CTAs' shares are even in these too.  Without it the one CTA
+// that has all the shortest sequences works on long after the others.
+constexpr int kDecItemCost = 2;
 
 template <int D, int NT>
 struct DecodeShape {
@@ -118,7 +122,8 @@ template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
 struct DecodeWalk {
   int b;             // sequence
   int64_t base;      // its first unit
-  int tiles;         // units per item
+  int tiles;         // units of keys per item
+  int cost;          // kDecItemCost + tiles: places per item in the numbering
   int row_tiles;     // row tiles
   KvSeq s;
 };
@@ -128,8 +133,9 @@ __device__ __forceinline__ int64_t decode_units(const KvAttentionParams& p, int 
   w.b = b;
   // a sequence without keys still has a unit: its rows are written as 0
   w.tiles = max(1, (w.s.len + kDecUnit - 1) / kDecUnit);
+  w.cost = w.tiles + kDecItemCost;
   w.row_tiles = (w.s.n_q * p.group + ROWS - 1) / ROWS;
-  return static_cast<int64_t>(w.tiles) * w.row_tiles * p.c.heads;
+  return static_cast<int64_t>(w.cost) * w.row_tiles * p.c.heads;
 }
 
 template <typename T, int D, int NT>
@@ -197,16 +203,34 @@ kv_decode_kernel(const KvAttentionParams p) {
   const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
   const float vgs = p.c.v_gs ? __ldg(p.c.v_gs) : 1.0f;
   const int row_k = 4 * (g >> 1) + (g & 1);     // key of tile row g; row g + 8 is key row_k + 2
+  // what a lane copies of a tile: 16-byte pieces of K and V codes, 32 pieces (512
+  // bytes of the source) apart, and one piece of the scales (D/16 lanes K, D/16 V:
+  // a block's 16 scales, which lie page_size apart per block and not per key)
+  constexpr int kPieces = D / 32;               // per key
+  const uint8_t* const k_lane = p.c.k_packed + lane * 16;
+  const uint8_t* const v_lane = p.c.v_packed + lane * 16;
+  const uint32_t k_dst = k_place<D>(lane / kPieces, lane % kPieces);
+  const uint32_t v_dst = S::kV + v_place<D>(lane / kPieces, lane % kPieces);
+  constexpr int kRows1 = 32 / kPieces;          // keys between a lane's two pieces (D = 128)
+  const uint32_t k_dst1 = D == 128 ? k_place<D>(lane / kPieces + kRows1, lane % kPieces) - k_dst : 0;
+  const uint32_t v_dst1 = D == 128 ? S::kV + v_place<D>(lane / kPieces + kRows1, lane % kPieces) - v_dst : 0;
+  const uint8_t* const s_lane = lane < D / 16 ? p.c.k_sf + lane * 16
+                                              : p.c.v_sf + static_cast<int64_t>(lane - D / 16) * p.c.page_size;
+  const int s_back = lane < D / 16 ? 0 : D / 16 - 1;
 
   while (u < u_end) {
     while (u >= w.base + units) {               // the next sequence that has units
       w.base += units;
       units = decode_units<ROWS>(p, w.b + 1, w);
     }
-    const int item = static_cast<int>((u - w.base) / w.tiles);
-    const int tile0 = static_cast<int>(u - w.base - static_cast<int64_t>(item) * w.tiles);
+    const int item = static_cast<int>((u - w.base) / w.cost);
+    const int64_t item_base = w.base + static_cast<int64_t>(item) * w.cost;
     const int kvh = item / w.row_tiles, rt = item - kvh * w.row_tiles;
-    const int n_units = static_cast<int>(min(static_cast<int64_t>(w.tiles - tile0), u_end - u));
+    const int tile0 = max(0, static_cast<int>(u - item_base) - kDecItemCost);
+    const int tile1 = static_cast<int>(min(static_cast<int64_t>(w.cost), u_end - item_base)) - kDecItemCost;
+    u = item_base + w.cost;                     // the next item, or beyond this share
+    const int n_units = tile1 - tile0;
+    if (n_units <= 0) continue;                 // the share ends in the item's own cost
     const int rows = w.s.n_q * p.group;         // of the whole sequence
     const int r0 = rt * ROWS;
 
@@ -279,52 +303,50 @@ kv_decode_kernel(const KvAttentionParams p) {
     // --- the ring: tile x of this warp is keys key0(x) ... + 15
     const int first_key = tile0 * kDecUnit + warp * 16;
     const int32_t* table = p.tables + static_cast<int64_t>(w.b) * p.max_pages;
-    int pg = -1, in_pg = 0, pg_next = -1, in_pg_next = 0;
-    auto look_up = [&](int x, int& page, int& in_page) {     // tile x + lane
+    // a row number counts slots of all pages and heads and fits 32 bits
+    constexpr uint32_t kNoRow = 0xffffffffu;
+    uint32_t row_of = kNoRow, row_next = kNoRow;
+    int at_of = 0, at_next = 0;
+    auto look_up = [&](int x, uint32_t& row, int& at) {      // tile x + lane
       const int key = first_key + (x + lane) * kDecUnit;
-      page = -1;
+      row = kNoRow;
       if (x + lane < n_units && key < lim_hi) {
         const int idx = key / p.c.page_size;
-        in_page = key - idx * p.c.page_size;
+        int page = -1;
         if (FP4Q_IN_RANGE(p, table + idx, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(table + idx);
-        if (page >= p.c.num_pages) page = -1;
+        if (page >= 0 && page < p.c.num_pages) {
+          at = key - idx * p.c.page_size;
+          row = (static_cast<uint32_t>(page) * p.c.heads + kvh) * p.c.page_size + at;
+        }
       }
     };
-    look_up(0, pg, in_pg);
-    look_up(32, pg_next, in_pg_next);
+    look_up(0, row_of, at_of);
+    look_up(32, row_next, at_next);
     uint32_t valid = 0;                          // bit i: the tile issued i tiles ago holds keys
     auto issue = [&](int x) {
       if ((x & 31) == 0 && x) {
-        pg = pg_next;
-        in_pg = in_pg_next;
-        look_up(x + 32, pg_next, in_pg_next);
+        row_of = row_next;
+        at_of = at_next;
+        look_up(x + 32, row_next, at_next);
       }
-      const int page = __shfl_sync(kFullMask, pg, x & 31);
-      const int at = __shfl_sync(kFullMask, in_pg, x & 31);
-      valid = valid << 1 | (page >= 0 ? 1u : 0u);
-      if (page >= 0) {
-        const uint32_t dst = ring + (x % kDecStages) * S::kTile;
-        const int64_t ph = static_cast<int64_t>(page) * p.c.heads + kvh;
-        const int64_t row = ph * p.c.page_size + at;
-        const uint8_t* kc = p.c.k_packed + row * (D / 2);
-        const uint8_t* vc = p.c.v_packed + row * (D / 2);
+      const uint32_t row = __shfl_sync(kFullMask, row_of, x & 31);
+      const uint32_t at = __shfl_sync(kFullMask, at_of, x & 31);
+      valid <<= 1;
+      if (row != kNoRow) {
+        valid |= 1;
+        const uint32_t dst = ring + (x & (kDecStages - 1)) * S::kTile;
+        const uint8_t* kc = k_lane + static_cast<uint64_t>(row) * (D / 2);
+        const uint8_t* vc = v_lane + static_cast<uint64_t>(row) * (D / 2);
+        const uint8_t* sc = s_lane + static_cast<uint64_t>(row) * (D / 16) - static_cast<uint64_t>(at) * s_back;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
-          const int c = lane + 32 * i;           // 16-byte piece of the 16 keys
-          const int r = c / (D / 32), piece = c % (D / 32);
-          if (FP4Q_IN_RANGE(p, kc + c * 16, 16, p.c.k_packed, kv_packed_extent(p.c)))
-            cp_async16(dst + k_place<D>(r, piece), kc + c * 16);
-          if (FP4Q_IN_RANGE(p, vc + c * 16, 16, p.c.v_packed, kv_packed_extent(p.c)))
-            cp_async16(dst + S::kV + v_place<D>(r, piece), vc + c * 16);
+          if (FP4Q_IN_RANGE(p, kc + 512 * i, 16, p.c.k_packed, kv_packed_extent(p.c)))
+            cp_async16(dst + k_dst + (i ? k_dst1 : 0), kc + 512 * i);
+          if (FP4Q_IN_RANGE(p, vc + 512 * i, 16, p.c.v_packed, kv_packed_extent(p.c)))
+            cp_async16(dst + v_dst + (i ? v_dst1 : 0), vc + 512 * i);
         }
-        if (lane < D / 16) {
-          const uint8_t* s = p.c.k_sf + row * (D / 16) + lane * 16;
-          if (FP4Q_IN_RANGE(p, s, 16, p.c.k_sf, kv_sf_extent(p.c))) cp_async16(dst + S::kKs + lane * 16, s);
-        } else if (lane < D / 8) {
-          const int blk = lane - D / 16;
-          const uint8_t* s = p.c.v_sf + (ph * (D / 16) + blk) * p.c.page_size + at;
-          if (FP4Q_IN_RANGE(p, s, 16, p.c.v_sf, kv_sf_extent(p.c))) cp_async16(dst + S::kVs + blk * 16, s);
-        }
+        if (lane < D / 8 && FP4Q_IN_RANGE(p, sc, 16, lane < D / 16 ? p.c.k_sf : p.c.v_sf, kv_sf_extent(p.c)))
+          cp_async16(dst + S::kKs + lane * 16, sc);
       }
       cp_async_commit();
     };
@@ -336,7 +358,7 @@ kv_decode_kernel(const KvAttentionParams p) {
       const bool here = valid >> (kDecStages - 2) & 1u;
       issue(x + kDecStages - 1);
       if (!here) continue;
-      const uint32_t st = ring + (x % kDecStages) * S::kTile;
+      const uint32_t st = ring + (x & (kDecStages - 1)) * S::kTile;
       const int key0 = first_key + x * kDecUnit;
 
       // S^T = K Q^T
@@ -379,17 +401,24 @@ kv_decode_kernel(const KvAttentionParams p) {
         }
       }
 
-      // logits as exponents of 2; keys a row does not see become -inf
-      const bool whole = key0 + 16 <= lim_lo;
+      // exponents of 2 against the reference; keys that a row does not see get -inf
+      float y[NT][4];
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[n][e] = fmaf(s[n][e], fac[n][e & 1], -ref[n][e & 1]);
+      if (key0 + 16 > lim_lo) {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            if (key0 + row_k + (e & 2) >= lim[n][e & 1]) y[n][e] = s[n][e] = -INFINITY;
+      }
       bool over = false;
 #pragma unroll
       for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          s[n][e] *= fac[n][e & 1];
-          if (!whole && key0 + row_k + (e & 2) >= lim[n][e & 1]) s[n][e] = -INFINITY;
-          over |= s[n][e] > ref[n][e & 1] + kRefSlack;
-        }
+        for (int e = 0; e < 4; ++e) over |= y[n][e] > kRefSlack;
       if (__any_sync(kFullMask, over)) {         // rare after the first tiles
 #pragma unroll
         for (int n = 0; n < NT; ++n)
@@ -398,7 +427,7 @@ kv_decode_kernel(const KvAttentionParams p) {
             float m = fmaxf(s[n][e], s[n][e + 2]);
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
+            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16)) * fac[n][e];
             const float r = fmaxf(ref[n][e], m - kRefBelow);
             const float f = ex2(ref[n][e] - r);
             ref[n][e] = r;
@@ -408,6 +437,8 @@ kv_decode_kernel(const KvAttentionParams p) {
               acc[n][i][e] *= f;
               acc[n][i][e + 2] *= f;
             }
+            y[n][e] = s[n][e] == -INFINITY ? -INFINITY : fmaf(s[n][e], fac[n][e], -r);
+            y[n][e + 2] = s[n][e + 2] == -INFINITY ? -INFINITY : fmaf(s[n][e + 2], fac[n][e], -r);
           }
       }
       uint32_t pb[NT][2];
@@ -415,11 +446,11 @@ kv_decode_kernel(const KvAttentionParams p) {
       for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
-          s[n][e] = ex2(s[n][e] - ref[n][e & 1]);
-          sum[n][e & 1] += s[n][e];
+          y[n][e] = ex2(y[n][e]);
+          sum[n][e & 1] += y[n][e];
         }
-        pb[n][0] = transpose8x8(pack_f16x2(s[n][0], s[n][1]));
-        pb[n][1] = transpose8x8(pack_f16x2(s[n][2], s[n][3]));
+        pb[n][0] = transpose8x8(pack_f16x2(y[n][0], y[n][1]));
+        pb[n][1] = transpose8x8(pack_f16x2(y[n][2], y[n][3]));
       }
 
       // O^T += V^T P^T: keys 4t .. 4t + 3 of the tile
@@ -535,13 +566,12 @@ kv_decode_kernel(const KvAttentionParams p) {
     if (tid == 0 && tile0 == 0) {
       // where the joining kernel finds the item's parts
       const int64_t slot = (static_cast<int64_t>(w.s.q0) * p.group / ROWS + w.b + rt) * p.c.heads + kvh;
-      const int64_t last = u + w.tiles - 1;      // its last unit
+      const int64_t last = item_base + w.cost - 1;
       const int n = static_cast<int>(((last + 1) * G - 1) / total - cta) + 1;
       int* desc = reinterpret_cast<int*>(p.ws + 2 * static_cast<int64_t>(gridDim.x) * S::kPart) + 2 * slot;
       desc[0] = static_cast<int>(cta);
       desc[1] = n;
     }
-    u += n_units;
     __syncthreads();                             // the merge buffer becomes the ring again
   }
 }

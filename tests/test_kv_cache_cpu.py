@@ -31,7 +31,7 @@ CACHE_REFUSALS = [
     (dict(k_packed=0), 1), (dict(k_sf=0), 1), (dict(v_packed=0), 1), (dict(v_sf=0), 1),
     (dict(num_pages=-1), 1), (dict(page_size=0), 1), (dict(num_kv_heads=0), 1),
     (dict(head_dim=96), 2), (dict(head_dim=32), 2), (dict(page_size=24), 2), (dict(head_dim=0), 1),
-    (dict(num_pages=1 << 31), 2), (dict(num_kv_heads=5000), 2),
+    (dict(num_pages=1 << 31), 2), (dict(num_kv_heads=5000), 2), (dict(num_pages=1 << 27), 2),
     (dict(k_packed=at(0) + 8), 3), (dict(v_sf=at(3) + 4), 3), (dict(k_global_scale=at(9) + 2), 3),
 ]
 
