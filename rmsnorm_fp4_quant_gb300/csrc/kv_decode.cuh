@@ -24,8 +24,8 @@
 // kernel joins the parts in order.
 //
 // A CTA is 4 warps, each with its own 16 keys of a unit, its own r, l and O, and
-// its own ring of NST tiles in shared memory that cp.async fills NST - 1 tiles
-// ahead (a tile: 16 keys' codes and scales, 18 D bytes); no barrier in the loop.
+// its own ring of tiles in shared memory that cp.async fills ahead (a tile: 16
+// keys' codes and scales, 18 D bytes); no barrier in the loop.
 // At the end of an item's segment the four are joined in shared memory.
 #pragma once
 
@@ -37,11 +37,11 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecUnit = 16 * kDecWarps;       // keys of a unit
 constexpr int kDecStages = 4;
-constexpr int kDecMinUnits = 4;                // a CTA's share is at least this long
+constexpr int kDecMinUnits = 2;                // a CTA's share is at least this long
 // What an item costs besides its keys (its queries, the ring's first tiles, the
 // join), in units: the CTAs' shares are even in these too.  Without it the one CTA
 // that has all the shortest sequences works on long after the others.
-constexpr int kDecItemCost = 2;
+constexpr int kDecItemCost = 4;
 
 template <int D, int NT>
 struct DecodeShape {
@@ -53,6 +53,9 @@ struct DecodeShape {
   static constexpr int kMerge = kDecWarps * kRows * kMergeStride * 4;
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
   static constexpr int kCtas = NT == 1 ? 4 : 3;   // resident per SM
+  // Tiles a warp takes per step.  Two share the loop's, the addresses' and the
+  // maximum's instructions and fill each other's waits; 16 rows have no registers for it.
+  static constexpr int kStep = NT == 1 ? 2 : 1;
   static constexpr int kPart = kRows * (D + 2);   // floats of one part in the workspace
 };
 
@@ -118,6 +121,13 @@ template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
   return ((row >> 2) | ((row & 3) << 2)) * 32 + piece * 16;
 }
 
+// Bytes of two keys' codes: the low nibbles of lo, the high nibbles of hi.
+__device__ __forceinline__ uint32_t low_nibbles_of(uint32_t lo, uint32_t hi) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xe4;" : "=r"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+
 // What one CTA's walk over the units needs to know of the sequence it is in.
 struct DecodeWalk {
   int b;             // sequence
@@ -145,6 +155,9 @@ kv_decode_kernel(const KvAttentionParams p) {
   constexpr int ROWS = S::kRows;
   constexpr int KW = D / 32;          // words of K a lane takes of one key
   constexpr int VW = D / 64;          // words of V a lane takes of one key
+  constexpr int TP = S::kStep;
+  constexpr int AHEAD = kDecStages / TP - 1;     // steps whose tiles are on their way
+  constexpr int kNoKey = INT32_MAX - 64;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int64_t scan_tot[kDecThreads / 32];
   __shared__ int64_t start_base;
@@ -217,6 +230,15 @@ kv_decode_kernel(const KvAttentionParams p) {
   const uint8_t* const s_lane = lane < D / 16 ? p.c.k_sf + lane * 16
                                               : p.c.v_sf + static_cast<int64_t>(lane - D / 16) * p.c.page_size;
   const int s_back = lane < D / 16 ? 0 : D / 16 - 1;
+  // what it reads of a tile for the products
+  const uint32_t k_src = k_place<D>(row_k, KW * t / 4) + (KW * t % 4) * 4;
+  const uint32_t k_src2 = k_place<D>(row_k + 2, KW * t / 4) + (KW * t % 4) * 4;
+  const uint32_t ks_src = S::kKs + row_k * (D / 16) + t * (D / 64);
+  const uint32_t vs_src = S::kVs + (D == 128 ? g : g / 2) * 16 + 4 * t;
+  uint32_t v_src[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+    v_src[i] = S::kV + v_place<D>(4 * t + i, VW * g / 4) + (VW * g % 4) * 4;
 
   while (u < u_end) {
     while (u >= w.base + units) {               // the next sequence that has units
@@ -348,38 +370,51 @@ kv_decode_kernel(const KvAttentionParams p) {
         if (lane < D / 8 && FP4Q_IN_RANGE(p, sc, 16, lane < D / 16 ? p.c.k_sf : p.c.v_sf, kv_sf_extent(p.c)))
           cp_async16(dst + S::kKs + lane * 16, sc);
       }
+    };
+    auto issue_step = [&](int step) {
+#pragma unroll
+      for (int j = 0; j < TP; ++j) issue(step * TP + j);
       cp_async_commit();
     };
-    for (int x = 0; x < kDecStages - 1; ++x) issue(x);
+#pragma unroll
+    for (int i = 0; i < AHEAD; ++i) issue_step(i);
 
-    for (int x = 0; x < n_units; ++x) {
-      cp_async_wait<kDecStages - 2>();
-      __syncwarp();                              // the tile is here for every lane, tile x - 1 read
-      const bool here = valid >> (kDecStages - 2) & 1u;
-      issue(x + kDecStages - 1);
+    const int steps = (n_units + TP - 1) / TP;
+    for (int step = 0; step < steps; ++step) {
+      cp_async_wait<AHEAD - 1>();
+      __syncwarp();                              // the step's tiles are here for every lane, the last one's read
+      const uint32_t here = valid >> (TP * (AHEAD - 1)) & ((1u << TP) - 1);   // bit TP - 1: the first tile
+      issue_step(step + AHEAD);
       if (!here) continue;
-      const uint32_t st = ring + (x & (kDecStages - 1)) * S::kTile;
-      const int key0 = first_key + x * kDecUnit;
+      uint32_t st[TP];
+      int key0[TP];                              // a tile without keys lies behind every limit
+#pragma unroll
+      for (int j = 0; j < TP; ++j) {
+        const int x = step * TP + j;
+        st[j] = ring + (x & (kDecStages - 1)) * S::kTile;
+        key0[j] = here >> (TP - 1 - j) & 1u ? first_key + x * kDecUnit : kNoKey;
+      }
 
       // S^T = K Q^T
-      float s[NT][4];
+      float s[TP][NT][4];
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+      for (int j = 0; j < TP; ++j) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) s[n][e] = 0.0f;
-      {
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) s[j][n][e] = 0.0f;
         uint32_t ka[KW], kb[KW], sa[2], sb[2];
-        lds_words<KW>(st + k_place<D>(row_k, KW * t / 4) + (KW * t % 4) * 4, ka);
-        lds_words<KW>(st + k_place<D>(row_k + 2, KW * t / 4) + (KW * t % 4) * 4, kb);
+        lds_words<KW>(st[j] + k_src, ka);
+        lds_words<KW>(st[j] + k_src2, kb);
         if constexpr (D == 128) {                // two blocks per lane
-          const uint32_t fa = e4m3x2_to_f16x2(lds16(st + S::kKs + row_k * 8 + 2 * t));
-          const uint32_t fb = e4m3x2_to_f16x2(lds16(st + S::kKs + (row_k + 2) * 8 + 2 * t));
+          const uint32_t fa = e4m3x2_to_f16x2(lds16(st[j] + ks_src));
+          const uint32_t fb = e4m3x2_to_f16x2(lds16(st[j] + ks_src + 16));
           sa[0] = __byte_perm(fa, 0, 0x1010);
           sa[1] = __byte_perm(fa, 0, 0x3232);
           sb[0] = __byte_perm(fb, 0, 0x1010);
           sb[1] = __byte_perm(fb, 0, 0x3232);
         } else {
-          const uint32_t ba = lds8(st + S::kKs + row_k * 4 + t), bb = lds8(st + S::kKs + (row_k + 2) * 4 + t);
+          const uint32_t ba = lds8(st[j] + ks_src), bb = lds8(st[j] + ks_src + 8);
           sa[0] = sa[1] = e4m3x2_to_f16x2(ba | ba << 8);
           sb[0] = sb[1] = e4m3x2_to_f16x2(bb | bb << 8);
         }
@@ -395,36 +430,45 @@ kv_decode_kernel(const KvAttentionParams p) {
           }
 #pragma unroll
           for (int n = 0; n < NT; ++n) {
-            mma_16816(s[n], ha[0], hb[0], ha[1], hb[1], qf[n][2 * i][0], qf[n][2 * i][1]);
-            mma_16816(s[n], ha[2], hb[2], ha[3], hb[3], qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
+            mma_16816(s[j][n], ha[0], hb[0], ha[1], hb[1], qf[n][2 * i][0], qf[n][2 * i][1]);
+            mma_16816(s[j][n], ha[2], hb[2], ha[3], hb[3], qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
           }
         }
       }
 
       // exponents of 2 against the reference; keys that a row does not see get -inf
-      float y[NT][4];
+      float y[TP][NT][4];
+      bool over = false, edge = false;
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) y[n][e] = fmaf(s[n][e], fac[n][e & 1], -ref[n][e & 1]);
-      if (key0 + 16 > lim_lo) {
+      for (int j = 0; j < TP; ++j) {
+        edge |= key0[j] > lim_lo - 16;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e)
-            if (key0 + row_k + (e & 2) >= lim[n][e & 1]) y[n][e] = s[n][e] = -INFINITY;
+          for (int e = 0; e < 4; ++e) y[j][n][e] = fmaf(s[j][n][e], fac[n][e & 1], -ref[n][e & 1]);
       }
-      bool over = false;
+      if (edge) {
 #pragma unroll
-      for (int n = 0; n < NT; ++n)
+        for (int j = 0; j < TP; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) over |= y[n][e] > kRefSlack;
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0[j] + row_k + (e & 2) >= lim[n][e & 1]) y[j][n][e] = s[j][n][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int j = 0; j < TP; ++j)
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) over |= y[j][n][e] > kRefSlack;
       if (__any_sync(kFullMask, over)) {         // rare after the first tiles
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(s[n][e], s[n][e + 2]);
+            float m = fmaxf(s[0][n][e], s[0][n][e + 2]);
+            if (TP == 2) m = fmaxf(m, fmaxf(s[TP - 1][n][e], s[TP - 1][n][e + 2]));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16)) * fac[n][e];
@@ -437,49 +481,53 @@ kv_decode_kernel(const KvAttentionParams p) {
               acc[n][i][e] *= f;
               acc[n][i][e + 2] *= f;
             }
-            y[n][e] = s[n][e] == -INFINITY ? -INFINITY : fmaf(s[n][e], fac[n][e], -r);
-            y[n][e + 2] = s[n][e + 2] == -INFINITY ? -INFINITY : fmaf(s[n][e + 2], fac[n][e], -r);
+#pragma unroll
+            for (int j = 0; j < TP; ++j)
+#pragma unroll
+              for (int k = e; k < 4; k += 2)
+                y[j][n][k] = s[j][n][k] == -INFINITY ? -INFINITY : fmaf(s[j][n][k], fac[n][e], -r);
           }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[TP][NT][2];
 #pragma unroll
-      for (int n = 0; n < NT; ++n) {
+      for (int j = 0; j < TP; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          y[n][e] = ex2(y[n][e]);
-          sum[n][e & 1] += y[n][e];
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+          for (int e = 0; e < 4; ++e) {
+            y[j][n][e] = ex2(y[j][n][e]);
+            sum[n][e & 1] += y[j][n][e];
+          }
+          pb[j][n][0] = transpose8x8(pack_f16x2(y[j][n][0], y[j][n][1]));
+          pb[j][n][1] = transpose8x8(pack_f16x2(y[j][n][2], y[j][n][3]));
         }
-        pb[n][0] = transpose8x8(pack_f16x2(y[n][0], y[n][1]));
-        pb[n][1] = transpose8x8(pack_f16x2(y[n][2], y[n][3]));
-      }
 
-      // O^T += V^T P^T: keys 4t .. 4t + 3 of the tile
-      {
-        uint32_t sv = lds32(st + S::kVs + (D == 128 ? g : g / 2) * 16 + 4 * t);
-        if (key0 + 16 > w.s.len) {               // slots behind the end may hold no numbers
-          const int left = w.s.len - key0 - 4 * t;
+      // O^T += V^T P^T: keys 4t .. 4t + 3 of each tile
+#pragma unroll
+      for (int j = 0; j < TP; ++j) {
+        uint32_t sv = lds32(st[j] + vs_src);
+        if (edge && key0[j] > w.s.len - 16) {    // slots behind the end may hold no numbers
+          const int left = w.s.len - key0[j] - 4 * t;
           sv = left <= 0 ? 0u : left >= 4 ? sv : sv & (0xffffffffu >> (32 - 8 * left));
         }
         const uint32_t s01 = e4m3x2_to_f16x2(sv), s23 = e4m3x2_to_f16x2(sv >> 16);
         uint32_t v[4][VW];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int word = VW * g;               // of the key's D/8 words
-          lds_words<VW>(st + S::kV + v_place<D>(4 * t + i, word / 4) + (word % 4) * 4, v[i]);
-        }
+        for (int i = 0; i < 4; ++i) lds_words<VW>(st[j] + v_src[i], v[i]);
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
           uint32_t e01[4], o01[4], e23[4], o23[4];
-          e2m1x8_to_f16x2((v[0][i] & 0x0f0f0f0fu) | (v[1][i] << 4 & 0xf0f0f0f0u), e01);
-          e2m1x8_to_f16x2((v[0][i] >> 4 & 0x0f0f0f0fu) | (v[1][i] & 0xf0f0f0f0u), o01);
-          e2m1x8_to_f16x2((v[2][i] & 0x0f0f0f0fu) | (v[3][i] << 4 & 0xf0f0f0f0u), e23);
-          e2m1x8_to_f16x2((v[2][i] >> 4 & 0x0f0f0f0fu) | (v[3][i] & 0xf0f0f0f0u), o23);
+          e2m1x8_to_f16x2(low_nibbles_of(v[0][i], v[1][i] << 4), e01);
+          e2m1x8_to_f16x2(low_nibbles_of(v[0][i] >> 4, v[1][i]), o01);
+          e2m1x8_to_f16x2(low_nibbles_of(v[2][i], v[3][i] << 4), e23);
+          e2m1x8_to_f16x2(low_nibbles_of(v[2][i] >> 4, v[3][i]), o23);
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {          // channels D/8 g + 8 i + 2 j and the next
-            const uint32_t a0 = mul_f16x2(e01[j], s01), a1 = mul_f16x2(o01[j], s01);
-            const uint32_t a2 = mul_f16x2(e23[j], s23), a3 = mul_f16x2(o23[j], s23);
+          for (int c = 0; c < 4; ++c) {          // channels D/8 g + 8 i + 2 c and the next
+            const uint32_t a0 = mul_f16x2(e01[c], s01), a1 = mul_f16x2(o01[c], s01);
+            const uint32_t a2 = mul_f16x2(e23[c], s23), a3 = mul_f16x2(o23[c], s23);
 #pragma unroll
-            for (int n = 0; n < NT; ++n) mma_16816(acc[n][4 * i + j], a0, a1, a2, a3, pb[n][0], pb[n][1]);
+            for (int n = 0; n < NT; ++n)
+              mma_16816(acc[n][4 * i + c], a0, a1, a2, a3, pb[j][n][0], pb[j][n][1]);
           }
         }
       }
