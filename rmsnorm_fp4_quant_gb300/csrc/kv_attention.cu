@@ -1,8 +1,11 @@
 // kv_attention.cu - attention over the paged NVFP4 key/value cache: choice of
 // kernel and launch.
 
+#include <mutex>
+
 #include "fp4q_launch.h"
 #include "kv_decode.cuh"
+#include "kv_prefill.cuh"
 
 namespace fp4q {
 namespace {
@@ -36,8 +39,63 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<T, D, NT>, p, ctas);
 }
 
+// Rows of a key/value head per sequence (on average: the lengths are on the
+// device) from which on the 256-row items are used.
+constexpr int kPrefillRows = 64;
+bool use_prefill(int64_t B, int64_t T, int group) { return T * group >= kPrefillRows * B; }
+
+// Ranges of keys that an item is cut into: so many that every SM gets two CTAs.
+int prefill_splits(int sms, int64_t B, int64_t T, int group, int heads) {
+  const int64_t items = prefill_row_slots(B, T, group) * heads;
+  const int64_t s = (2 * sms + items - 1) / items;
+  return static_cast<int>(s < 8 ? s : 8);
+}
+
+template <typename T, int D>
+cudaError_t launch_prefill(const KvAttentionParams& p, int pdl, cudaStream_t stream) {
+  using S = PrefillShape<D>;
+  {
+    // a per-device function attribute, set once
+    static bool done[64] = {};
+    static std::mutex mu;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+    std::lock_guard<std::mutex> lock(mu);
+    if (!done[dev]) {
+      e = cudaFuncSetAttribute(kv_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
+      if (e != cudaSuccess) return e;
+      done[dev] = true;
+    }
+  }
+  int splits = prefill_splits(sm_count_current_device(), p.B, p.T, p.group, p.c.heads);
+  const int64_t keys = p.max_pages * p.c.page_size;
+  while (splits > 1 && keys < 512LL * splits) --splits;   // a split has at least four steps
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(static_cast<unsigned>(prefill_row_slots(p.B, p.T, p.group) * p.c.heads),
+                     static_cast<unsigned>(splits));
+  cfg.blockDim = dim3(kPreThreads);
+  cfg.dynamicSmemBytes = S::kSmem;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = pdl ? 1 : 0;
+  const cudaError_t e = cudaLaunchKernelEx(&cfg, kv_prefill_kernel<T, D>, p, splits);
+  if (e != cudaSuccess || splits == 1) return e;
+  cfg.gridDim = dim3(static_cast<unsigned>((p.T * p.Hq * (D / 4) + 255) / 256));
+  cfg.blockDim = dim3(256);
+  cfg.dynamicSmemBytes = 0;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<T, D>, p, splits);
+}
+
 template <typename T>
 cudaError_t launch_type(const KvAttentionParams& p, int pdl, cudaStream_t stream) {
+  if (use_prefill(p.B, p.T, p.group))
+    return p.c.D == 128 ? launch_prefill<T, 128>(p, pdl, stream) : launch_prefill<T, 64>(p, pdl, stream);
   const int nt = decode_tiles(p.B, p.T, p.group);
   if (p.c.D == 128)
     return nt == 1 ? launch_decode<T, 128, 1>(p, pdl, stream) : launch_decode<T, 128, 2>(p, pdl, stream);
@@ -55,6 +113,10 @@ int64_t decode_workspace(int sms, int64_t B, int64_t T, int group, int heads) {
 int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads, int D) {
   const int group = Hq / heads;
   if (B == 0 || T == 0) return 0;
+  if (use_prefill(B, T, group)) {
+    const int64_t splits = prefill_splits(sms, B, T, group, heads);
+    return splits > 1 ? splits * T * Hq * (D + 2) * 4 : 0;
+  }
   const int nt = decode_tiles(B, T, group);
   if (D == 128)
     return nt == 1 ? decode_workspace<128, 1>(sms, B, T, group, heads)

@@ -80,6 +80,13 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return d;
 }
 
+// Bytes of two keys' codes: the low nibbles of lo, the high nibbles of hi.
+__device__ __forceinline__ uint32_t low_nibbles_of(uint32_t lo, uint32_t hi) {
+  uint32_t d;
+  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xe4;" : "=r"(d) : "r"(lo), "r"(hi));
+  return d;
+}
+
 // k with 2^k * m in [2^14, 2^15) for m > 0 (held to where 2^k and 2^-k are
 // normal numbers); 0 for zero, infinity and NaN.
 __device__ __forceinline__ int q_exponent(float m) {

@@ -121,13 +121,6 @@ template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
   return ((row >> 2) | ((row & 3) << 2)) * 32 + piece * 16;
 }
 
-// Bytes of two keys' codes: the low nibbles of lo, the high nibbles of hi.
-__device__ __forceinline__ uint32_t low_nibbles_of(uint32_t lo, uint32_t hi) {
-  uint32_t d;
-  asm("lop3.b32 %0, %1, %2, 0x0f0f0f0f, 0xe4;" : "=r"(d) : "r"(lo), "r"(hi));
-  return d;
-}
-
 // What one CTA's walk over the units needs to know of the sequence it is in.
 struct DecodeWalk {
   int b;             // sequence

@@ -1,0 +1,588 @@
+// kv_prefill.cuh - attention of many query rows per sequence over the paged
+// NVFP4 cache, on the 5th-generation tensor cores: the products bound the time.
+//
+// A CTA has one (sequence, key/value head, 256 query rows, range of keys); the
+// rows are the sequence's query tokens times the heads that share the key/value
+// head, as two tiles of 128.  Keys are taken 128 at a time:
+//     S [128 x 128] = Q K^T        (A, B from shared memory, D / 16 steps)
+//     O [128 x D]  += P V          (A = P from tensor memory, B = V^T from shared memory)
+// per tile, all operands fp16 (exact for K and V, see kv_attention_common.cuh),
+// accumulators fp32 in tensor memory: S of both tiles (256 columns; the fp16 P
+// takes the place of its S) and O of both (2 D columns).
+//
+//   warps 0-3, 4-7   softmax of tile 0, 1: one row per thread, so a row's maximum
+//                    and sum never leave the thread.  S is read twice (maximum,
+//                    then weights), P written back.  O is rescaled in place, by the
+//                    same threads, in the rare step in which a row's reference
+//                    moves; when S of a step is there the product before it has
+//                    ended, so nothing else touches O then.
+//   warps 8-11       key and value tiles: codes and scales from the cache to
+//                    registers one tile ahead, to fp16 in registers, to shared
+//                    memory in the 128-byte-swizzled K-major form (V transposed: a
+//                    thread takes 8 keys' codes of D / 8 channels, whose nibbles
+//                    interleave to pairs of keys), two stages of each.  One
+//                    conversion serves 256 rows.
+//   warp 12          one thread issues the products: P0 V, Q0 K' (next keys), P1 V,
+//                    Q1 K': while one tile's softmax runs the other's products do.
+//
+// Why these sizes: 128 x 128 tiles read 128 bytes of shared memory per clock at
+// the tensor cores' full rate, no less would; two tiles per CTA fill tensor
+// memory (512 columns at D = 128) and share every conversion.
+//
+// Every wait is bounded.  A role whose wait runs out stops and the others' waits
+// run out after it; the rows not finished by then are written as NaN, the status
+// word (if any) set, and tensor memory freed once the products issued so far have
+// ended.
+#pragma once
+
+#include "kv_attention_common.cuh"
+#include "tcgen05.cuh"
+
+namespace fp4q {
+
+constexpr int kPreRows = 256;            // query rows of an item, two tiles of 128
+constexpr int kPreKeys = 128;            // keys of a step
+constexpr int kPreThreads = 13 * 32;
+constexpr uint32_t kPreTmemCols = 512;
+
+template <int D>
+struct PrefillShape {
+  static constexpr int kTile = 128 * D * 2;                // bytes of one fp16 tile
+  static constexpr int kQ = 0, kK = 2 * kTile, kV = 4 * kTile;
+  static constexpr int kBars = 6 * kTile;                  // after two tiles of Q, two stages of K, of V
+  static constexpr int kSmem = 1024 + 6 * kTile + 256;     // 1 KiB of alignment slack
+};
+
+__host__ __device__ inline int64_t prefill_row_slots(int64_t B, int64_t T, int group) {
+  return T * group / kPreRows + B;
+}
+
+enum PrefillBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9,
+                  kBarP = 11, kBarO = 13, kBarDrain = 15, kBarCount = 16 };
+
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+__device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+  asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+
+// Row numbers (and places in the page) of the eight 16-key groups of the tile
+// that begins at key0, one per lane 0-7; kNoRow without a page.
+constexpr uint32_t kPreNoRow = 0xffffffffu;
+__device__ __forceinline__ void prefill_rows(const KvAttentionParams& p, int b, int kvh, int key0, int len,
+                                             int lane, uint32_t& row, uint32_t& at) {
+  const int key = key0 + 16 * lane;
+  row = kPreNoRow;
+  at = 0;
+  if (lane < 8 && key < len) {
+    const int idx = key / p.c.page_size;
+    const int32_t* entry = p.tables + static_cast<int64_t>(b) * p.max_pages + idx;
+    int page = -1;
+    if (FP4Q_IN_RANGE(p, entry, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(entry);
+    if (page >= 0 && page < p.c.num_pages) {
+      at = key - idx * p.c.page_size;
+      row = (static_cast<uint32_t>(page) * p.c.heads + kvh) * p.c.page_size + at;
+    }
+  }
+}
+
+// The codes and scales that a thread of warps 8-11 takes of one key tile.
+template <int D>
+struct PrefillRaw {
+  static constexpr int KP = D / 32;      // 16-byte pieces of a key's codes
+  static constexpr int VW = D / 64;      // words of a key's codes that a thread takes for V
+  uint4 k[KP];
+  uint32_t ks[KP];                       // scale bytes of a piece's two blocks
+  uint32_t v[8][VW];
+  uint2 vs;
+};
+
+template <int D>
+__device__ __forceinline__ void prefill_load(const KvAttentionParams& p, uint32_t row_of, uint32_t at_of,
+                                             int key0, int len, int pw, int lane, PrefillRaw<D>& r) {
+  constexpr int KP = PrefillRaw<D>::KP, VW = PrefillRaw<D>::VW;
+  // K: piece lane / KEYS of key i * 4 KEYS + pw * KEYS + lane % KEYS; eight neighbouring
+  // lanes hold eight keys, whose swizzled places lie in different banks
+  constexpr int KEYS = 32 / KP;
+#pragma unroll
+  for (int i = 0; i < KP; ++i) {
+    const int key = i * 4 * KEYS + pw * KEYS + lane % KEYS, piece = lane / KEYS;
+    const uint32_t base = __shfl_sync(kFullMask, row_of, key >> 4);
+    r.k[i] = make_uint4(0, 0, 0, 0);
+    r.ks[i] = 0;
+    if (base != kPreNoRow) {
+      const uint64_t row = static_cast<uint64_t>(base) + (key & 15);
+      const uint8_t* src = p.c.k_packed + row * (D / 2) + piece * 16;
+      const uint8_t* sf = p.c.k_sf + row * (D / 16) + piece * 2;
+      if (FP4Q_IN_RANGE(p, src, 16, p.c.k_packed, kv_packed_extent(p.c)))
+        r.k[i] = __ldg(reinterpret_cast<const uint4*>(src));
+      if (FP4Q_IN_RANGE(p, sf, 2, p.c.k_sf, kv_sf_extent(p.c)))
+        r.ks[i] = __ldg(reinterpret_cast<const unsigned short*>(sf));
+    }
+  }
+  // V: the 8 keys of group lane % 8 of half pw % 2, channels D/8 * (4 (pw / 2) + lane / 8) ...
+  const int first = (pw & 1) * 64 + (lane & 7) * 8, dw = (pw >> 1) * 4 + (lane >> 3);
+  const uint32_t base = __shfl_sync(kFullMask, row_of, first >> 4);
+  const uint32_t at = __shfl_sync(kFullMask, at_of, first >> 4);
+  r.vs = make_uint2(0, 0);
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+#pragma unroll
+    for (int w = 0; w < VW; ++w) r.v[i][w] = 0;
+  if (base != kPreNoRow) {
+    const uint64_t row = static_cast<uint64_t>(base) + (first & 15);
+    const uint8_t* src = p.c.v_packed + row * (D / 2) + dw * (4 * VW);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      if (!FP4Q_IN_RANGE(p, src + i * (D / 2), 4 * VW, p.c.v_packed, kv_packed_extent(p.c))) continue;
+      if constexpr (VW == 2) {
+        const uint2 x = __ldg(reinterpret_cast<const uint2*>(src + i * (D / 2)));
+        r.v[i][0] = x.x;
+        r.v[i][1] = x.y;
+      } else {
+        r.v[i][0] = __ldg(reinterpret_cast<const uint32_t*>(src + i * (D / 2)));
+      }
+    }
+    const uint64_t in_page = at + (first & 15);
+    const uint8_t* sf = p.c.v_sf + (row - in_page) * (D / 16) +
+                        static_cast<uint64_t>(dw * VW / 2) * p.c.page_size + in_page;
+    if (FP4Q_IN_RANGE(p, sf, 8, p.c.v_sf, kv_sf_extent(p.c))) r.vs = __ldg(reinterpret_cast<const uint2*>(sf));
+    const int left = len - (key0 + first);             // slots behind the end may hold no numbers
+    if (left < 8) {
+      r.vs.x = left <= 0 ? 0u : left >= 4 ? r.vs.x : r.vs.x & (0xffffffffu >> (32 - 8 * left));
+      r.vs.y = left <= 4 ? 0u : r.vs.y & (0xffffffffu >> (64 - 8 * left));
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void prefill_store_k(const PrefillRaw<D>& r, uint32_t dst, int pw, int lane) {
+  constexpr int KP = PrefillRaw<D>::KP, KEYS = 32 / KP;
+#pragma unroll
+  for (int i = 0; i < KP; ++i) {
+    const int key = i * 4 * KEYS + pw * KEYS + lane % KEYS, piece = lane / KEYS;
+    const uint32_t sf = e4m3x2_to_f16x2(r.ks[i]);
+    const uint32_t s0 = __byte_perm(sf, 0, 0x1010), s1 = __byte_perm(sf, 0, 0x3232);
+    const uint32_t row = dst + (piece >> 1) * 16384 + key * 128;
+    const uint32_t words[4] = {r.k[i].x, r.k[i].y, r.k[i].z, r.k[i].w};
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      uint32_t h[4];
+      e2m1x8_to_f16x2(words[w], h);
+      const uint32_t s = w < 2 ? s0 : s1;
+      sts128(row + ((((piece & 1) * 4 + w) ^ (key & 7)) << 4), mul_f16x2(h[0], s), mul_f16x2(h[1], s),
+             mul_f16x2(h[2], s), mul_f16x2(h[3], s));
+    }
+  }
+}
+
+template <int D>
+__device__ __forceinline__ void prefill_store_v(const PrefillRaw<D>& r, uint32_t dst, int pw, int lane) {
+  constexpr int VW = PrefillRaw<D>::VW;
+  const int kg = lane & 7, dw = (pw >> 1) * 4 + (lane >> 3);
+  const uint32_t base = dst + (pw & 1) * (D * 128);
+  uint32_t sc[4];
+  sc[0] = e4m3x2_to_f16x2(r.vs.x);
+  sc[1] = e4m3x2_to_f16x2(r.vs.x >> 16);
+  sc[2] = e4m3x2_to_f16x2(r.vs.y);
+  sc[3] = e4m3x2_to_f16x2(r.vs.y >> 16);
+#pragma unroll
+  for (int w = 0; w < VW; ++w) {
+    uint32_t lo[4][4], hi[4][4];                      // [pair of keys][channel pair]
+#pragma unroll
+    for (int kp = 0; kp < 4; ++kp) {
+      e2m1x8_to_f16x2(low_nibbles_of(r.v[2 * kp][w], r.v[2 * kp + 1][w] << 4), lo[kp]);
+      e2m1x8_to_f16x2(low_nibbles_of(r.v[2 * kp][w] >> 4, r.v[2 * kp + 1][w]), hi[kp]);
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+      const int d = dw * (8 * VW) + 8 * w + 2 * c;
+      sts128(base + d * 128 + ((kg ^ (d & 7)) << 4), mul_f16x2(lo[0][c], sc[0]), mul_f16x2(lo[1][c], sc[1]),
+             mul_f16x2(lo[2][c], sc[2]), mul_f16x2(lo[3][c], sc[3]));
+      sts128(base + (d + 1) * 128 + ((kg ^ ((d + 1) & 7)) << 4), mul_f16x2(hi[0][c], sc[0]),
+             mul_f16x2(hi[1][c], sc[1]), mul_f16x2(hi[2][c], sc[2]), mul_f16x2(hi[3][c], sc[3]));
+    }
+  }
+}
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAttentionParams p, int splits) {
+  using S = PrefillShape<D>;
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ uint32_t tmem_slot;
+  const uint32_t smem0 = (smem_addr(smem_raw) + 1023u) & ~1023u;
+  uint8_t* const smem = smem_raw + (smem0 - smem_addr(smem_raw));
+  uint64_t* const bars = reinterpret_cast<uint64_t*>(smem + S::kBars);
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+  griddep_wait();
+  // the item: row slots are counted from the last, which sees the most keys
+  const int kvh = static_cast<int>(blockIdx.x % p.c.heads);
+  const int64_t rs = prefill_row_slots(p.B, p.T, p.group) - 1 - blockIdx.x / p.c.heads;
+  auto slots_from = [&](int b) {
+    const int64_t q0 = p.cu ? min(max(p.cu[b], 0), static_cast<int>(p.T)) : b;
+    return q0 * p.group / kPreRows + b;
+  };
+  int b = 0, b_hi = p.B - 1;
+  while (b < b_hi) {
+    const int mid = (b + b_hi + 1) / 2;
+    if (slots_from(mid) <= rs) b = mid; else b_hi = mid - 1;
+  }
+  const int64_t rt = rs - slots_from(b);
+  const KvSeq seq = kv_sequence(p, b);
+  const int rows = seq.n_q * p.group;
+  if (rt < 0 || rt * kPreRows >= rows) return;
+  const int r0 = static_cast<int>(rt) * kPreRows;
+  const int off = seq.len - seq.n_q;
+  // steps of 128 keys: this split's share of what the last row sees, and how many of
+  // them each tile's last row sees
+  auto limit_of = [&](int r) { return p.causal ? min(seq.len, off + r / p.group + 1) : seq.len; };
+  const int last0 = min(r0 + 128, rows) - 1, last1 = min(r0 + 256, rows) - 1;
+  const int all = (max(0, limit_of(last1)) + kPreKeys - 1) / kPreKeys;
+  const int per = (all + splits - 1) / splits;
+  const int t0 = min(all, static_cast<int>(blockIdx.y) * per), t1 = min(all, t0 + per);
+  const int all0 = (max(0, limit_of(last0)) + kPreKeys - 1) / kPreKeys;
+  const int n[2] = {max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
+  const int steps = max(n[0], n[1]);
+
+  if (warp == 12) tmem_alloc(&tmem_slot, kPreTmemCols);
+  if (tid == 0) {
+    mbar_init(&bars[kBarQ], 256);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(&bars[kBarKFull + i], 128);
+      mbar_init(&bars[kBarKEmpty + i], 1);
+      mbar_init(&bars[kBarVFull + i], 128);
+      mbar_init(&bars[kBarVEmpty + i], 1);
+      mbar_init(&bars[kBarS + i], 1);
+      mbar_init(&bars[kBarP + i], 128);
+      mbar_init(&bars[kBarO + i], 1);
+    }
+    mbar_init(&bars[kBarDrain], 1);
+    mbar_init_fence();
+  }
+  tc_fence_before_sync();
+  __syncthreads();
+  tc_fence_after_sync();
+  griddep_launch_dependents();
+  const uint32_t tmem = tmem_slot;
+  const long long wait_limit = FP4Q_WAIT_LIMIT(p);
+
+  if (warp < 8) {
+    // --- softmax: one row per thread
+    const int tile = warp >> 2, r_in = (warp & 3) * 32 + lane;
+    const int r = r0 + tile * 128 + r_in;
+    const bool ok = r < rows;
+    const int tok = r / p.group, hq = kvh * p.group + r - tok * p.group;
+    const int64_t at = static_cast<int64_t>(seq.q0 + tok) * p.Hq + hq;     // row of out and lse
+    float fac;
+    {
+      const T* src = static_cast<const T*>(p.q) + static_cast<int64_t>(seq.q0 + (ok ? tok : 0)) * p.q_stride +
+                     static_cast<int64_t>(ok ? hq : 0) * D;
+      Chunk c[D / 16];
+      float top = 0.0f;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        c[i] = Chunk{};
+        if (ok && FP4Q_IN_RANGE(p, src + 16 * i, 32, p.q, 2LL * ((p.T - 1) * p.q_stride + p.Hq * D)))
+          c[i] = ld_cached_ro(src + 16 * i);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 x = Pair<T>::to_f32(c[i].u[j]);
+          top = max_abs3(top, x.x, x.y);
+          nan |= x.x != x.x || x.y != x.y;
+        }
+      }
+      if (nan) top = INFINITY;
+      const int k = q_exponent(top);
+      const float up = pow2(k);
+      const uint32_t dst = smem0 + S::kQ + tile * S::kTile + r_in * 128;
+#pragma unroll
+      for (int i = 0; i < D / 8; ++i) {          // 16 bytes: 8 channels
+        uint32_t h[4];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const float2 x = Pair<T>::to_f32(c[i / 2].u[(i & 1) * 4 + j]);
+          h[j] = pack_f16x2(x.x * up, x.y * up);
+        }
+        sts128(dst + (i >> 3) * 16384 + (((i & 7) ^ (r_in & 7)) << 4), h[0], h[1], h[2], h[3]);
+      }
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kBarQ]);
+      const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
+      fac = p.sm_scale * kLog2e / kgs * pow2(-k);
+    }
+    const uint32_t ts = tmem + tile * 128 + ((warp & 3) * 32 << 16);
+    const uint32_t to = tmem + 256 + tile * D + ((warp & 3) * 32 << 16);
+    const int lim = ok ? limit_of(r) : 0;
+    int lim_lo = ok ? lim : INT32_MAX;           // smallest of the warp's rows
+    lim_lo = __reduce_min_sync(kFullMask, lim_lo);
+    float ref = kRefStart, sum = 0.0f;
+    bool alive = true;
+    uint32_t row_of, at_of;                      // pages of the step's keys, for the bad ones
+    prefill_rows(p, b, kvh, t0 * kPreKeys, seq.len, lane, row_of, at_of);
+    for (int j = 0; j < n[tile]; ++j) {
+      const int key0 = (t0 + j) * kPreKeys;
+      const uint32_t have = __ballot_sync(kFullMask, row_of != kPreNoRow);
+      prefill_rows(p, b, kvh, key0 + kPreKeys, seq.len, lane, row_of, at_of);
+      if (!__all_sync(kFullMask, mbar_wait_bounded(&bars[kBarS + tile], j & 1, wait_limit))) {
+        alive = false;
+        break;
+      }
+      tc_fence_after_sync();
+      const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu;
+      float m = -INFINITY;
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32];
+        tmem_load_32cols(ts + 32 * c, x);
+        if (edge) {
+#pragma unroll
+          for (int i = 0; i < 32; ++i)
+            if (key0 + 32 * c + i < lim && (have >> (2 * c + i / 16) & 1u)) m = fmaxf(m, __uint_as_float(x[i]));
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+        }
+      }
+      bool moved = false;
+      float f = 1.0f;
+      if (m > -INFINITY && m * fac > ref + kRefSlack) {
+        const float to_ref = m * fac - kRefBelow;
+        f = ex2(ref - to_ref);
+        ref = to_ref;
+        sum *= f;
+        moved = true;
+      }
+      if (j > 0 && __any_sync(kFullMask, moved)) {
+#pragma unroll
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t x[32];
+          tmem_load_32cols(to + 32 * c, x);
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+          tmem_store_32cols(to + 32 * c, x);
+        }
+      }
+      const float2 fac2 = make_float2(fac, fac), ref2 = make_float2(-ref, -ref);
+      float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        uint32_t x[32], h[16];
+        tmem_load_32cols(ts + 32 * c, x);
+#pragma unroll
+        for (int i = 0; i < 32; i += 2) {
+          float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, ref2);
+          if (edge) {
+            const bool page = have >> (2 * c + i / 16) & 1u;
+            if (!page || key0 + 32 * c + i >= lim) y.x = -INFINITY;
+            if (!page || key0 + 32 * c + i + 1 >= lim) y.y = -INFINITY;
+          }
+          y.x = ex2(y.x);
+          y.y = ex2(y.y);
+          sum2 = __fadd2_rn(sum2, y);
+          h[i / 2] = pack_f16x2(y.x, y.y);
+        }
+        tmem_store_16cols(ts + 16 * c, h);       // over columns already read
+      }
+      sum += sum2.x + sum2.y;
+      tmem_store_wait();
+      tc_fence_before_sync();
+      mbar_arrive(&bars[kBarP + tile]);
+    }
+    // --- the row's result
+    if (alive && n[tile] > 0) {
+      alive = __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarO + tile], 0, wait_limit));
+      tc_fence_after_sync();
+    }
+    if (!alive) {
+      sum = __uint_as_float(0x7fc00000u);
+      if (p.status) atomicExch(p.status, kStatusTimeout);
+    }
+    const float vgs = p.c.v_gs ? __ldg(p.c.v_gs) : 1.0f;
+    const bool parts = splits > 1;
+    const float scale = parts ? 1.0f : sum > 0.0f ? 1.0f / (sum * vgs) : sum == 0.0f ? 0.0f : sum;
+    const int64_t total = p.T * p.Hq;
+    const int64_t pr = blockIdx.y * total + at;  // row of the partial results
+    if (alive && n[tile] == 0) {                 // no key for any row of the tile
+      if (ok && !parts) {
+#pragma unroll
+        for (int i = 0; i < D / 16; ++i) {
+          T* dst = static_cast<T*>(p.out) + at * D + 16 * i;
+          if (FP4Q_IN_RANGE(p, dst, 32, p.out, 2LL * total * D)) st_stream(dst, Chunk{});
+        }
+      }
+    } else {
+#pragma unroll
+      for (int c = 0; c < D / 32; ++c) {
+        uint32_t x[32];
+        if (alive) {
+          tmem_load_32cols(to + 32 * c, x);
+        } else {
+#pragma unroll
+          for (int i = 0; i < 32; ++i) x[i] = 0x7fc00000u;
+        }
+        if (ok && parts) {
+          float* dst = p.ws + pr * D + 32 * c;
+#pragma unroll
+          for (int i = 0; i < 32; i += 4)
+            *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+        } else if (ok) {
+#pragma unroll
+          for (int i = 0; i < 2; ++i) {
+            Chunk o;
+#pragma unroll
+            for (int k = 0; k < 8; ++k)
+              o.u[k] = Pair<T>::from_f32(__uint_as_float(x[16 * i + 2 * k]) * scale,
+                                         __uint_as_float(x[16 * i + 2 * k + 1]) * scale);
+            T* dst = static_cast<T*>(p.out) + at * D + 32 * c + 16 * i;
+            if (FP4Q_IN_RANGE(p, dst, 32, p.out, 2LL * total * D)) st_stream(dst, o);
+          }
+        }
+        __syncwarp();
+      }
+    }
+    if (ok) {
+      if (parts)
+        *reinterpret_cast<float2*>(p.ws + splits * total * D + 2 * pr) = make_float2(ref, sum);
+      else if (p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * total))
+        p.lse[at] = sum == 0.0f ? -INFINITY : kLn2 * (ref + log2f(sum));
+    }
+    tc_fence_before_sync();
+  } else if (warp < 12) {
+    // --- key and value tiles
+    const int pw = warp - 8;
+    uint32_t row_of, at_of, row_next, at_next;
+    PrefillRaw<D> raw;
+    prefill_rows(p, b, kvh, t0 * kPreKeys, seq.len, lane, row_of, at_of);
+    prefill_rows(p, b, kvh, (t0 + 1) * kPreKeys, seq.len, lane, row_next, at_next);
+    if (steps > 0) prefill_load<D>(p, row_of, at_of, t0 * kPreKeys, seq.len, pw, lane, raw);
+    for (int j = 0; j < steps; ++j) {
+      const int s = j & 1;
+      const uint32_t parity = ((j >> 1) & 1) ^ 1;    // of the use before
+      if (j >= 2 && !mbar_wait_bounded(&bars[kBarKEmpty + s], parity, wait_limit)) break;
+      prefill_store_k<D>(raw, smem0 + S::kK + s * S::kTile, pw, lane);
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kBarKFull + s]);
+      if (j >= 2 && !mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit)) break;
+      prefill_store_v<D>(raw, smem0 + S::kV + s * S::kTile, pw, lane);
+      fence_proxy_async_smem();
+      mbar_arrive(&bars[kBarVFull + s]);
+      if (j + 1 < steps) {
+        row_of = row_next;
+        at_of = at_next;
+        prefill_rows(p, b, kvh, (t0 + j + 2) * kPreKeys, seq.len, lane, row_next, at_next);
+        prefill_load<D>(p, row_of, at_of, (t0 + j + 1) * kPreKeys, seq.len, pw, lane, raw);
+      }
+    }
+  } else if (lane == 0 && steps > 0) {
+    // --- products
+    constexpr uint32_t kIdescS = idesc_f16(128, 128), kIdescO = idesc_f16(128, D);
+    auto q_k = [&](int tile, int s) {
+#pragma unroll
+      for (int k = 0; k < D / 16; ++k) {
+        const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
+        mma_f16_ss(tmem + tile * 128, smem_desc(smem0 + S::kQ + tile * S::kTile + o, 0, 1024, kSwizzle128B),
+                   smem_desc(smem0 + S::kK + s * S::kTile + o, 0, 1024, kSwizzle128B), kIdescS, k > 0);
+      }
+      tc_commit(&bars[kBarS + tile]);
+    };
+    auto p_v = [&](int tile, int s, bool first) {
+#pragma unroll
+      for (int k = 0; k < kPreKeys / 16; ++k) {
+        const uint32_t o = (k >> 2) * (D * 128) + (k & 3) * 32;
+        mma_f16_ts(tmem + 256 + tile * D, tmem + tile * 128 + 8 * k,
+                   smem_desc(smem0 + S::kV + s * S::kTile + o, 0, 1024, kSwizzle128B), kIdescO,
+                   !(first && k == 0));
+      }
+    };
+    bool alive = mbar_wait_bounded(&bars[kBarQ], 0, wait_limit) &&
+                 mbar_wait_bounded(&bars[kBarKFull], 0, wait_limit);
+    if (alive) {
+      tc_fence_after_sync();
+      for (int tile = 0; tile < 2; ++tile)
+        if (n[tile] > 0) q_k(tile, 0);
+      tc_commit(&bars[kBarKEmpty]);
+    }
+    for (int j = 0; j < steps && alive; ++j) {
+      const int s = j & 1;
+      alive = mbar_wait_bounded(&bars[kBarVFull + s], (j >> 1) & 1, wait_limit);
+      if (alive && j + 1 < steps)
+        alive = mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit);
+      for (int tile = 0; tile < 2 && alive; ++tile) {
+        if (j >= n[tile]) continue;
+        alive = mbar_wait_bounded(&bars[kBarP + tile], j & 1, wait_limit);
+        if (!alive) break;
+        tc_fence_after_sync();
+        p_v(tile, s, j == 0);
+        if (j + 1 < n[tile])
+          q_k(tile, s ^ 1);
+        else
+          tc_commit(&bars[kBarO + tile]);
+      }
+      if (alive) {
+        tc_commit(&bars[kBarVEmpty + s]);
+        if (j + 1 < steps) tc_commit(&bars[kBarKEmpty + (s ^ 1)]);
+      }
+    }
+    tc_commit(&bars[kBarDrain]);                 // nothing may run when tensor memory is freed
+    mbar_wait_bounded(&bars[kBarDrain], 0);
+  }
+  __syncthreads();
+  tc_fence_after_sync();
+  if (warp == 12) tmem_dealloc(tmem, kPreTmemCols);
+}
+
+// Joins the splits of every row: one group of D / 4 lanes per row.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttentionParams p, int splits) {
+  constexpr int LANES = D / 4;
+  griddep_wait();
+  griddep_launch_dependents();
+  const int64_t total = p.T * p.Hq;
+  const int64_t at = (static_cast<int64_t>(blockIdx.x) * 256 + threadIdx.x) / LANES;
+  const int ln = threadIdx.x % LANES;
+  if (at >= total) return;
+  // rows of no sequence are left as they were
+  const int64_t t = at / p.Hq;
+  bool mine = true;
+  if (p.cu) {
+    int b = 0, hi = p.B - 1;
+    while (b < hi) {
+      const int mid = (b + hi + 1) / 2;
+      if (p.cu[mid] <= t) b = mid; else hi = mid - 1;
+    }
+    // of several sequences that begin at one row all but the last are empty
+    const KvSeq s = kv_sequence(p, b);
+    mine = t >= s.q0 && t < s.q0 + s.n_q;
+  }
+  if (!mine) return;
+  float top = kRefStart;
+  for (int i = 0; i < splits; ++i) top = fmaxf(top, p.ws[splits * total * D + 2 * (i * total + at)]);
+  float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  float l = 0.0f;
+  for (int i = 0; i < splits; ++i) {
+    const float2 rl = *reinterpret_cast<const float2*>(p.ws + splits * total * D + 2 * (i * total + at));
+    if (rl.y == 0.0f) continue;                  // saw no key: its O was not written
+    const float4 x = *reinterpret_cast<const float4*>(p.ws + (i * total + at) * D + 4 * ln);
+    const float f = ex2(rl.x - top);
+    o.x += x.x * f;
+    o.y += x.y * f;
+    o.z += x.z * f;
+    o.w += x.w * f;
+    l += rl.y * f;
+  }
+  const float vgs = p.c.v_gs ? __ldg(p.c.v_gs) : 1.0f;
+  const float inv = l > 0.0f ? 1.0f / (l * vgs) : l == 0.0f ? 0.0f : l;
+  T* dst = static_cast<T*>(p.out) + at * D + 4 * ln;
+  if (FP4Q_IN_RANGE(p, dst, 8, p.out, 2LL * total * D))
+    *reinterpret_cast<uint2*>(dst) = make_uint2(Pair<T>::from_f32(o.x * inv, o.y * inv),
+                                                Pair<T>::from_f32(o.z * inv, o.w * inv));
+  if (ln == 0 && p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * total))
+    p.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (top + log2f(l));
+}
+
+}  // namespace fp4q
