@@ -10,19 +10,18 @@
 // accumulators fp32 in tensor memory: S of both tiles (256 columns; the fp16 P
 // takes the place of its S) and O of both (2 D columns).
 //
-//   warps 0-3, 4-7   softmax of tile 0, 1: one row per thread, so a row's maximum
-//                    and sum never leave the thread.  S is read twice (maximum,
-//                    then weights), P written back.  O is rescaled in place, by the
-//                    same threads, in the rare step in which a row's reference
-//                    moves; when S of a step is there the product before it has
-//                    ended, so nothing else touches O then.
+//   warps 0-3, 4-7   softmax of tile 0, 1: one row per thread, so a row's sum never
+//                    leaves the thread.  S is read once, P written back over it.
+//                    O is rescaled in place, by the same threads, in the rare step
+//                    in which a row's reference moves; when S of a step is there the
+//                    product before it has ended, so nothing else touches O then.
 //   warps 8-11       key and value tiles: codes and scales from the cache to
 //                    registers one tile ahead, to fp16 in registers, to shared
 //                    memory in the 128-byte-swizzled K-major form (V transposed: a
 //                    thread takes 8 keys' codes of D / 8 channels, whose nibbles
 //                    interleave to pairs of keys), two stages of each.  One
 //                    conversion serves 256 rows.
-//   warp 12          one thread issues the products: P0 V, Q0 K' (next keys), P1 V,
+//   warps 12-15      one thread of warp 12 issues the products: P0 V, Q0 K' (next keys), P1 V,
 //                    Q1 K': while one tile's softmax runs the other's products do.
 //
 // Why these sizes: 128 x 128 tiles read 128 bytes of shared memory per clock at
@@ -42,7 +41,15 @@ namespace fp4q {
 
 constexpr int kPreRows = 256;            // query rows of an item, two tiles of 128
 constexpr int kPreKeys = 128;            // keys of a step
-constexpr int kPreThreads = 13 * 32;
+constexpr int kPreThreads = 16 * 32;
+// Registers per thread of the three kinds of warpgroups: 2 x 128 x 160 + 128 x 128 +
+// 128 x 64 = 65536, what 512 threads of 128 are launched with.
+constexpr int kPreSoftmaxRegs = 160, kPreIssueRegs = 64;
+// A row's weights of one step are taken against the reference of the steps before;
+// only if their sum passes this is the maximum looked for and the reference moved to
+// kRefBelow below it (which leaves the sum at 128 * 2^6 at most).  Weights then stay
+// below 2^14, far from fp16's end, and the usual step needs no maximum at all.
+constexpr float kPreMostSum = 16384.0f;
 constexpr uint32_t kPreTmemCols = 512;
 
 template <int D>
@@ -208,6 +215,62 @@ __device__ __forceinline__ void prefill_store_v(const PrefillRaw<D>& r, uint32_t
   }
 }
 
+// One row's weights of a step: S from tensor memory, 32 columns being read while 32
+// are worked on, p = 2^(fac s - ref) in fp32 summed and in fp16 packed.  Keys that the
+// row does not see, and keys of 16-key groups without a page (bits of `have`), get 0.
+template <bool EDGE>
+__device__ __forceinline__ float2 prefill_weights_32(const uint32_t (&x)[32], int c, int key0, int lim,
+                                                     uint32_t have, float2 fac2, float2 ref2, float2 sum2,
+                                                     uint32_t (&h)[64]) {
+#pragma unroll
+  for (int i = 0; i < 32; i += 2) {
+    float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, ref2);
+    if (EDGE) {
+      const bool page = have >> (2 * c + i / 16) & 1u;
+      if (!page || key0 + 32 * c + i >= lim) y.x = -INFINITY;
+      if (!page || key0 + 32 * c + i + 1 >= lim) y.y = -INFINITY;
+    }
+    y.x = ex2(y.x);
+    y.y = ex2(y.y);
+    sum2 = __fadd2_rn(sum2, y);
+    h[16 * c + i / 2] = pack_f16x2(y.x, y.y);
+  }
+  return sum2;
+}
+__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim, uint32_t have, bool edge,
+                                                 float fac, float ref, uint32_t (&h)[64]) {
+  const float2 fac2 = make_float2(fac, fac), ref2 = make_float2(-ref, -ref);
+  float2 sum2 = make_float2(0.0f, 0.0f);
+  uint32_t a[32], b[32];
+  tmem_load_32cols(ts, a);
+#pragma unroll
+  for (int c = 0; c < 4; c += 2) {
+    tmem_load_32cols_async(ts + 32 * c + 32, b);
+    sum2 = edge ? prefill_weights_32<true>(a, c, key0, lim, have, fac2, ref2, sum2, h)
+                : prefill_weights_32<false>(a, c, key0, lim, have, fac2, ref2, sum2, h);
+    tmem_load_wait(b);
+    if (c == 0) tmem_load_32cols_async(ts + 64, a);
+    sum2 = edge ? prefill_weights_32<true>(b, c + 1, key0, lim, have, fac2, ref2, sum2, h)
+                : prefill_weights_32<false>(b, c + 1, key0, lim, have, fac2, ref2, sum2, h);
+    if (c == 0) tmem_load_wait(a);
+  }
+  return sum2.x + sum2.y;
+}
+// The largest product of a row with a key that it sees.
+__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, uint32_t have, bool edge) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 4; ++c) {
+    uint32_t x[32];
+    tmem_load_32cols(ts + 32 * c, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i)
+      if (!edge || (key0 + 32 * c + i < lim && (have >> (2 * c + i / 16) & 1u)))
+        m = fmaxf(m, __uint_as_float(x[i]));
+  }
+  return m;
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAttentionParams p, int splits) {
   using S = PrefillShape<D>;
@@ -272,6 +335,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
 
   if (warp < 8) {
     // --- softmax: one row per thread
+    registers_up<kPreSoftmaxRegs>();
     const int tile = warp >> 2, r_in = (warp & 3) * 32 + lane;
     const int r = r0 + tile * 128 + r_in;
     const bool ok = r < rows;
@@ -334,61 +398,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       }
       tc_fence_after_sync();
       const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu;
-      float m = -INFINITY;
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32];
-        tmem_load_32cols(ts + 32 * c, x);
-        if (edge) {
-#pragma unroll
-          for (int i = 0; i < 32; ++i)
-            if (key0 + 32 * c + i < lim && (have >> (2 * c + i / 16) & 1u)) m = fmaxf(m, __uint_as_float(x[i]));
-        } else {
-#pragma unroll
-          for (int i = 0; i < 32; i += 2) m = max3(m, __uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+      uint32_t h[64];
+      float step_sum = prefill_weights(ts, key0, lim, have, edge, fac, ref, h);
+      const bool moved = !(step_sum <= kPreMostSum);
+      if (__any_sync(kFullMask, moved)) {          // rare after the first steps
+        const float m = prefill_maximum(ts, key0, lim, have, edge);
+        float f = 1.0f;
+        if (moved && m > -INFINITY) {
+          const float to_ref = fmaxf(ref, m * fac - kRefBelow);
+          f = ex2(ref - to_ref);
+          ref = to_ref;
+          sum *= f;
         }
-      }
-      bool moved = false;
-      float f = 1.0f;
-      if (m > -INFINITY && m * fac > ref + kRefSlack) {
-        const float to_ref = m * fac - kRefBelow;
-        f = ex2(ref - to_ref);
-        ref = to_ref;
-        sum *= f;
-        moved = true;
-      }
-      if (j > 0 && __any_sync(kFullMask, moved)) {
+        if (j > 0) {
+#pragma unroll 1
+          for (int c = 0; c < D / 32; ++c) {
+            uint32_t x[32];
+            tmem_load_32cols(to + 32 * c, x);
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c) {
-          uint32_t x[32];
-          tmem_load_32cols(to + 32 * c, x);
-#pragma unroll
-          for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-          tmem_store_32cols(to + 32 * c, x);
-        }
-      }
-      const float2 fac2 = make_float2(fac, fac), ref2 = make_float2(-ref, -ref);
-      float2 sum2 = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int c = 0; c < 4; ++c) {
-        uint32_t x[32], h[16];
-        tmem_load_32cols(ts + 32 * c, x);
-#pragma unroll
-        for (int i = 0; i < 32; i += 2) {
-          float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, ref2);
-          if (edge) {
-            const bool page = have >> (2 * c + i / 16) & 1u;
-            if (!page || key0 + 32 * c + i >= lim) y.x = -INFINITY;
-            if (!page || key0 + 32 * c + i + 1 >= lim) y.y = -INFINITY;
+            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+            tmem_store_32cols(to + 32 * c, x);
           }
-          y.x = ex2(y.x);
-          y.y = ex2(y.y);
-          sum2 = __fadd2_rn(sum2, y);
-          h[i / 2] = pack_f16x2(y.x, y.y);
         }
-        tmem_store_16cols(ts + 16 * c, h);       // over columns already read
+        step_sum = prefill_weights(ts, key0, lim, have, edge, fac, ref, h);
       }
-      sum += sum2.x + sum2.y;
+      sum += step_sum;
+#pragma unroll
+      for (int c = 0; c < 2; ++c) {                // P over S, all of which has been read
+        uint32_t w[32];
+#pragma unroll
+        for (int i = 0; i < 32; ++i) w[i] = h[32 * c + i];
+        tmem_store_32cols(ts + 32 * c, w);
+      }
       tmem_store_wait();
       tc_fence_before_sync();
       mbar_arrive(&bars[kBarP + tile]);
@@ -455,30 +496,38 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   } else if (warp < 12) {
     // --- key and value tiles
     const int pw = warp - 8;
-    uint32_t row_of, at_of, row_next, at_next;
-    PrefillRaw<D> raw;
+    uint32_t row_of, at_of;
+    PrefillRaw<D> raw[2];                          // loaded one step before it is converted
     prefill_rows(p, b, kvh, t0 * kPreKeys, seq.len, lane, row_of, at_of);
-    prefill_rows(p, b, kvh, (t0 + 1) * kPreKeys, seq.len, lane, row_next, at_next);
-    if (steps > 0) prefill_load<D>(p, row_of, at_of, t0 * kPreKeys, seq.len, pw, lane, raw);
-    for (int j = 0; j < steps; ++j) {
-      const int s = j & 1;
-      const uint32_t parity = ((j >> 1) & 1) ^ 1;    // of the use before
-      if (j >= 2 && !mbar_wait_bounded(&bars[kBarKEmpty + s], parity, wait_limit)) break;
-      prefill_store_k<D>(raw, smem0 + S::kK + s * S::kTile, pw, lane);
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kBarKFull + s]);
-      if (j >= 2 && !mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit)) break;
-      prefill_store_v<D>(raw, smem0 + S::kV + s * S::kTile, pw, lane);
-      fence_proxy_async_smem();
-      mbar_arrive(&bars[kBarVFull + s]);
-      if (j + 1 < steps) {
-        row_of = row_next;
-        at_of = at_next;
-        prefill_rows(p, b, kvh, (t0 + j + 2) * kPreKeys, seq.len, lane, row_next, at_next);
-        prefill_load<D>(p, row_of, at_of, (t0 + j + 1) * kPreKeys, seq.len, pw, lane, raw);
+    if (steps > 0) prefill_load<D>(p, row_of, at_of, t0 * kPreKeys, seq.len, pw, lane, raw[0]);
+    prefill_rows(p, b, kvh, (t0 + 1) * kPreKeys, seq.len, lane, row_of, at_of);
+    bool alive = true;
+    for (int j0 = 0; j0 < steps && alive; j0 += 2) {
+#pragma unroll
+      for (int s = 0; s < 2; ++s) {
+        const int j = j0 + s;
+        if (j >= steps || !alive) break;
+        if (j + 1 < steps) {
+          prefill_load<D>(p, row_of, at_of, (t0 + j + 1) * kPreKeys, seq.len, pw, lane, raw[s ^ 1]);
+          prefill_rows(p, b, kvh, (t0 + j + 2) * kPreKeys, seq.len, lane, row_of, at_of);
+        }
+        const uint32_t parity = ((j >> 1) & 1) ^ 1;    // of the use before
+        alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarKEmpty + s], parity, wait_limit));
+        if (!alive) break;
+        prefill_store_k<D>(raw[s], smem0 + S::kK + s * S::kTile, pw, lane);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kBarKFull + s]);
+        alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit));
+        if (!alive) break;
+        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, pw, lane);
+        fence_proxy_async_smem();
+        mbar_arrive(&bars[kBarVFull + s]);
       }
     }
-  } else if (lane == 0 && steps > 0) {
+  } else {
+    registers_down<kPreIssueRegs>();
+  }
+  if (warp == 12 && lane == 0 && steps > 0) {
     // --- products
     constexpr uint32_t kIdescS = idesc_f16(128, 128), kIdescO = idesc_f16(128, D);
     auto q_k = [&](int tile, int s) {
