@@ -67,10 +67,10 @@ __host__ __device__ inline int64_t prefill_row_slots(int64_t B, int64_t T, int g
 enum PrefillBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9,
                   kBarP = 11, kBarO = 13, kBarDrain = 15, kBarCount = 16 };
 
-__device__ __forceinline__ float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
+// The warp's arrival, once all its lanes have come here.
+__device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
+  __syncwarp();
+  if (lane == 0) mbar_arrive(bar);
 }
 __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
   asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" :: "r"(a), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -79,6 +79,13 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // Row numbers (and places in the page) of the eight 16-key groups of the tile
 // that begins at key0, one per lane 0-7; kNoRow without a page.
 constexpr uint32_t kPreNoRow = 0xffffffffu;
+__device__ __forceinline__ uint32_t prefill_row(const KvAttentionParams& p, int b, int kvh, int idx, int at) {
+  const int32_t* entry = p.tables + static_cast<int64_t>(b) * p.max_pages + idx;
+  int page = -1;
+  if (FP4Q_IN_RANGE(p, entry, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(entry);
+  return page >= 0 && page < p.c.num_pages ? (static_cast<uint32_t>(page) * p.c.heads + kvh) * p.c.page_size + at
+                                           : kPreNoRow;
+}
 __device__ __forceinline__ void prefill_rows(const KvAttentionParams& p, int b, int kvh, int key0, int len,
                                              int lane, uint32_t& row, uint32_t& at) {
   const int key = key0 + 16 * lane;
@@ -86,13 +93,8 @@ __device__ __forceinline__ void prefill_rows(const KvAttentionParams& p, int b, 
   at = 0;
   if (lane < 8 && key < len) {
     const int idx = key / p.c.page_size;
-    const int32_t* entry = p.tables + static_cast<int64_t>(b) * p.max_pages + idx;
-    int page = -1;
-    if (FP4Q_IN_RANGE(p, entry, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(entry);
-    if (page >= 0 && page < p.c.num_pages) {
-      at = key - idx * p.c.page_size;
-      row = (static_cast<uint32_t>(page) * p.c.heads + kvh) * p.c.page_size + at;
-    }
+    at = key - idx * p.c.page_size;
+    row = prefill_row(p, b, kvh, idx, at);
   }
 }
 
@@ -215,44 +217,44 @@ __device__ __forceinline__ void prefill_store_v(const PrefillRaw<D>& r, uint32_t
   }
 }
 
-// One row's weights of a step: S from tensor memory, 32 columns being read while 32
+// One row's weights of a step: S from tensor memory, 16 columns being read while 16
 // are worked on, p = 2^(fac s - ref) in fp32 summed and in fp16 packed.  Keys that the
 // row does not see, and keys of 16-key groups without a page (bits of `have`), get 0.
 template <bool EDGE>
-__device__ __forceinline__ float2 prefill_weights_32(const uint32_t (&x)[32], int c, int key0, int lim,
+__device__ __forceinline__ float2 prefill_weights_16(const uint32_t (&x)[16], int c, int key0, int lim,
                                                      uint32_t have, float2 fac2, float2 ref2, float2 sum2,
                                                      uint32_t (&h)[64]) {
 #pragma unroll
-  for (int i = 0; i < 32; i += 2) {
+  for (int i = 0; i < 16; i += 2) {
     float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, ref2);
     if (EDGE) {
-      const bool page = have >> (2 * c + i / 16) & 1u;
-      if (!page || key0 + 32 * c + i >= lim) y.x = -INFINITY;
-      if (!page || key0 + 32 * c + i + 1 >= lim) y.y = -INFINITY;
+      const bool page = have >> c & 1u;
+      if (!page || key0 + 16 * c + i >= lim) y.x = -INFINITY;
+      if (!page || key0 + 16 * c + i + 1 >= lim) y.y = -INFINITY;
     }
     y.x = ex2(y.x);
     y.y = ex2(y.y);
     sum2 = __fadd2_rn(sum2, y);
-    h[16 * c + i / 2] = pack_f16x2(y.x, y.y);
+    h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
   }
   return sum2;
 }
-__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim, uint32_t have, bool edge,
-                                                 float fac, float ref, uint32_t (&h)[64]) {
+template <bool EDGE>
+__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim, uint32_t have, float fac,
+                                                 float ref, uint32_t (&h)[64]) {
   const float2 fac2 = make_float2(fac, fac), ref2 = make_float2(-ref, -ref);
   float2 sum2 = make_float2(0.0f, 0.0f);
-  uint32_t a[32], b[32];
-  tmem_load_32cols(ts, a);
+  uint32_t a[16], b[16];
+  tmem_load_16cols_async(ts, a);
+  tmem_load_wait(a);
 #pragma unroll
-  for (int c = 0; c < 4; c += 2) {
-    tmem_load_32cols_async(ts + 32 * c + 32, b);
-    sum2 = edge ? prefill_weights_32<true>(a, c, key0, lim, have, fac2, ref2, sum2, h)
-                : prefill_weights_32<false>(a, c, key0, lim, have, fac2, ref2, sum2, h);
+  for (int c = 0; c < 8; c += 2) {
+    tmem_load_16cols_async(ts + 16 * c + 16, b);
+    sum2 = prefill_weights_16<EDGE>(a, c, key0, lim, have, fac2, ref2, sum2, h);
     tmem_load_wait(b);
-    if (c == 0) tmem_load_32cols_async(ts + 64, a);
-    sum2 = edge ? prefill_weights_32<true>(b, c + 1, key0, lim, have, fac2, ref2, sum2, h)
-                : prefill_weights_32<false>(b, c + 1, key0, lim, have, fac2, ref2, sum2, h);
-    if (c == 0) tmem_load_wait(a);
+    if (c < 6) tmem_load_16cols_async(ts + 16 * c + 32, a);
+    sum2 = prefill_weights_16<EDGE>(b, c + 1, key0, lim, have, fac2, ref2, sum2, h);
+    if (c < 6) tmem_load_wait(a);
   }
   return sum2.x + sum2.y;
 }
@@ -313,21 +315,34 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
 
   if (warp == 12) tmem_alloc(&tmem_slot, kPreTmemCols);
   if (tid == 0) {
-    mbar_init(&bars[kBarQ], 256);
+    // one arrival per warp of the writers, one commit of the products
+    mbar_init(&bars[kBarQ], 8);
     for (int i = 0; i < 2; ++i) {
-      mbar_init(&bars[kBarKFull + i], 128);
+      mbar_init(&bars[kBarKFull + i], 4);
       mbar_init(&bars[kBarKEmpty + i], 1);
-      mbar_init(&bars[kBarVFull + i], 128);
+      mbar_init(&bars[kBarVFull + i], 4);
       mbar_init(&bars[kBarVEmpty + i], 1);
       mbar_init(&bars[kBarS + i], 1);
-      mbar_init(&bars[kBarP + i], 128);
+      mbar_init(&bars[kBarP + i], 4);
       mbar_init(&bars[kBarO + i], 1);
     }
     mbar_init(&bars[kBarDrain], 1);
     mbar_init_fence();
   }
+  // whether a page of these keys is outside the cache: only then are the steps' pages
+  // looked at by the softmax too
+  bool bad = false;
+  {
+    const int32_t* table = p.tables + static_cast<int64_t>(b) * p.max_pages;
+    const int end = min(t1 * kPreKeys, seq.len);
+    for (int i = t0 * kPreKeys / p.c.page_size + tid; static_cast<int64_t>(i) * p.c.page_size < end; i += kPreThreads) {
+      if (!FP4Q_IN_RANGE(p, table + i, 4, p.tables, 4LL * p.B * p.max_pages)) continue;
+      const int page = __ldg(table + i);
+      bad |= page < 0 || page >= p.c.num_pages;
+    }
+  }
   tc_fence_before_sync();
-  __syncthreads();
+  const bool bad_pages = __syncthreads_or(bad);
   tc_fence_after_sync();
   griddep_launch_dependents();
   const uint32_t tmem = tmem_slot;
@@ -375,7 +390,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         sts128(dst + (i >> 3) * 16384 + (((i & 7) ^ (r_in & 7)) << 4), h[0], h[1], h[2], h[3]);
       }
       fence_proxy_async_smem();
-      mbar_arrive(&bars[kBarQ]);
+      warp_arrive(&bars[kBarQ], lane);
       const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
       fac = p.sm_scale * kLog2e / kgs * pow2(-k);
     }
@@ -386,12 +401,14 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     lim_lo = __reduce_min_sync(kFullMask, lim_lo);
     float ref = kRefStart, sum = 0.0f;
     bool alive = true;
-    uint32_t row_of, at_of;                      // pages of the step's keys, for the bad ones
-    prefill_rows(p, b, kvh, t0 * kPreKeys, seq.len, lane, row_of, at_of);
     for (int j = 0; j < n[tile]; ++j) {
       const int key0 = (t0 + j) * kPreKeys;
-      const uint32_t have = __ballot_sync(kFullMask, row_of != kPreNoRow);
-      prefill_rows(p, b, kvh, key0 + kPreKeys, seq.len, lane, row_of, at_of);
+      uint32_t have = 0xffu;                       // 16-key groups that have a page
+      if (bad_pages) {
+        uint32_t row_of, at_of;
+        prefill_rows(p, b, kvh, key0, seq.len, lane, row_of, at_of);
+        have = __ballot_sync(kFullMask, row_of != kPreNoRow);
+      }
       if (!__all_sync(kFullMask, mbar_wait_bounded(&bars[kBarS + tile], j & 1, wait_limit))) {
         alive = false;
         break;
@@ -399,7 +416,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       tc_fence_after_sync();
       const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu;
       uint32_t h[64];
-      float step_sum = prefill_weights(ts, key0, lim, have, edge, fac, ref, h);
+      float step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, fac, ref, h)
+                            : prefill_weights<false>(ts, key0, lim, have, fac, ref, h);
       const bool moved = !(step_sum <= kPreMostSum);
       if (__any_sync(kFullMask, moved)) {          // rare after the first steps
         const float m = prefill_maximum(ts, key0, lim, have, edge);
@@ -420,7 +438,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
             tmem_store_32cols(to + 32 * c, x);
           }
         }
-        step_sum = prefill_weights(ts, key0, lim, have, edge, fac, ref, h);
+        step_sum = prefill_weights<true>(ts, key0, edge ? lim : INT32_MAX, have, fac, ref, h);
       }
       sum += step_sum;
 #pragma unroll
@@ -432,7 +450,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       }
       tmem_store_wait();
       tc_fence_before_sync();
-      mbar_arrive(&bars[kBarP + tile]);
+      warp_arrive(&bars[kBarP + tile], lane);
     }
     // --- the row's result
     if (alive && n[tile] > 0) {
@@ -496,11 +514,27 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   } else if (warp < 12) {
     // --- key and value tiles
     const int pw = warp - 8;
+    // group `lane` (of 8) of the step after the one whose row is in row_of: page idx, place at;
+    // a step of 128 keys is page_q pages and page_r places
+    const int page_q = kPreKeys / p.c.page_size, page_r = kPreKeys - page_q * p.c.page_size;
+    int key = t0 * kPreKeys + 16 * (lane & 7);
+    int idx = key / p.c.page_size, at = key - idx * p.c.page_size;
     uint32_t row_of, at_of;
+    auto next_rows = [&]() {
+      at_of = at;
+      row_of = key < seq.len ? prefill_row(p, b, kvh, idx, at) : kPreNoRow;
+      key += kPreKeys;
+      idx += page_q;
+      at += page_r;
+      if (at >= p.c.page_size) {
+        at -= p.c.page_size;
+        ++idx;
+      }
+    };
     PrefillRaw<D> raw[2];                          // loaded one step before it is converted
-    prefill_rows(p, b, kvh, t0 * kPreKeys, seq.len, lane, row_of, at_of);
+    next_rows();
     if (steps > 0) prefill_load<D>(p, row_of, at_of, t0 * kPreKeys, seq.len, pw, lane, raw[0]);
-    prefill_rows(p, b, kvh, (t0 + 1) * kPreKeys, seq.len, lane, row_of, at_of);
+    next_rows();
     bool alive = true;
     for (int j0 = 0; j0 < steps && alive; j0 += 2) {
 #pragma unroll
@@ -509,19 +543,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         if (j >= steps || !alive) break;
         if (j + 1 < steps) {
           prefill_load<D>(p, row_of, at_of, (t0 + j + 1) * kPreKeys, seq.len, pw, lane, raw[s ^ 1]);
-          prefill_rows(p, b, kvh, (t0 + j + 2) * kPreKeys, seq.len, lane, row_of, at_of);
+          next_rows();
         }
         const uint32_t parity = ((j >> 1) & 1) ^ 1;    // of the use before
         alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarKEmpty + s], parity, wait_limit));
         if (!alive) break;
         prefill_store_k<D>(raw[s], smem0 + S::kK + s * S::kTile, pw, lane);
         fence_proxy_async_smem();
-        mbar_arrive(&bars[kBarKFull + s]);
+        warp_arrive(&bars[kBarKFull + s], lane);
         alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit));
         if (!alive) break;
         prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, pw, lane);
         fence_proxy_async_smem();
-        mbar_arrive(&bars[kBarVFull + s]);
+        warp_arrive(&bars[kBarVFull + s], lane);
       }
     }
   } else {
@@ -530,22 +564,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   if (warp == 12 && lane == 0 && steps > 0) {
     // --- products
     constexpr uint32_t kIdescS = idesc_f16(128, 128), kIdescO = idesc_f16(128, D);
+    // the descriptors differ in their address field, the low word's 14 bits of 16-byte
+    // units: a step of 16 adds 32 bytes, one of 64 a sub-tile, without a carry out
+    const uint32_t first = static_cast<uint32_t>(smem_desc(smem0, 0, 1024, kSwizzle128B));
+    const uint32_t high = static_cast<uint32_t>(smem_desc(smem0, 0, 1024, kSwizzle128B) >> 32);
+    auto desc = [&](uint32_t low) { return static_cast<uint64_t>(high) << 32 | low; };
     auto q_k = [&](int tile, int s) {
+      const uint32_t d = tmem + tile * 128;
+      const uint32_t qa = first + ((S::kQ + tile * S::kTile) >> 4), ka = first + ((S::kK + s * S::kTile) >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
-        const uint32_t o = (k >> 2) * 16384 + (k & 3) * 32;
-        mma_f16_ss(tmem + tile * 128, smem_desc(smem0 + S::kQ + tile * S::kTile + o, 0, 1024, kSwizzle128B),
-                   smem_desc(smem0 + S::kK + s * S::kTile + o, 0, 1024, kSwizzle128B), kIdescS, k > 0);
+        const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
+        mma_f16_ss(d, desc(qa + o), desc(ka + o), kIdescS, k > 0);
       }
       tc_commit(&bars[kBarS + tile]);
     };
-    auto p_v = [&](int tile, int s, bool first) {
+    auto p_v = [&](int tile, int s, bool begins) {
+      const uint32_t d = tmem + 256 + tile * D, a = tmem + tile * 128;
+      const uint32_t va = first + ((S::kV + s * S::kTile) >> 4);
 #pragma unroll
       for (int k = 0; k < kPreKeys / 16; ++k) {
-        const uint32_t o = (k >> 2) * (D * 128) + (k & 3) * 32;
-        mma_f16_ts(tmem + 256 + tile * D, tmem + tile * 128 + 8 * k,
-                   smem_desc(smem0 + S::kV + s * S::kTile + o, 0, 1024, kSwizzle128B), kIdescO,
-                   !(first && k == 0));
+        const uint32_t o = ((k >> 2) * (D * 128) + (k & 3) * 32) >> 4;
+        mma_f16_ts(d, a + 8 * k, desc(va + o), kIdescO, !(begins && k == 0));
       }
     };
     bool alive = mbar_wait_bounded(&bars[kBarQ], 0, wait_limit) &&
