@@ -21,8 +21,12 @@
 //                    thread takes 8 keys' codes of D / 8 channels, whose nibbles
 //                    interleave to pairs of keys), two stages of each.  One
 //                    conversion serves 256 rows.
-//   warps 12-15      one thread of warp 12 issues the products: P0 V, Q0 K' (next keys), P1 V,
-//                    Q1 K': while one tile's softmax runs the other's products do.
+//   warps 12, 13     one thread each issues one tile's products: P V, then Q K' of the
+//                    next keys into the S that P has left (products of one thread run
+//                    in order).  The two take turns, so that one tile's softmax runs
+//                    beside the other's products; while one issues, the other has its
+//                    waits and commits behind it (one thread for both tiles spends 800
+//                    of 3900 clocks a step on them; two without turns fall into step).
 //
 // Why these sizes: 128 x 128 tiles read 128 bytes of shared memory per clock at
 // the tensor cores' full rate, no less would; two tiles per CTA fill tensor
@@ -65,7 +69,7 @@ __host__ __device__ inline int64_t prefill_row_slots(int64_t B, int64_t T, int g
 }
 
 enum PrefillBar { kBarQ = 0, kBarKFull = 1, kBarKEmpty = 3, kBarVFull = 5, kBarVEmpty = 7, kBarS = 9,
-                  kBarP = 11, kBarO = 13, kBarDrain = 15, kBarCount = 16 };
+                  kBarP = 11, kBarO = 13, kBarDrain = 15, kBarTurn = 17 };
 
 // The warp's arrival, once all its lanes have come here.
 __device__ __forceinline__ void warp_arrive(uint64_t* bar, int lane) {
@@ -79,10 +83,11 @@ __device__ __forceinline__ void sts128(uint32_t a, uint32_t x, uint32_t y, uint3
 // Row numbers (and places in the page) of the eight 16-key groups of the tile
 // that begins at key0, one per lane 0-7; kNoRow without a page.
 constexpr uint32_t kPreNoRow = 0xffffffffu;
-__device__ __forceinline__ uint32_t prefill_row(const KvAttentionParams& p, int b, int kvh, int idx, int at) {
+__device__ __forceinline__ int prefill_page(const KvAttentionParams& p, int b, int idx) {
   const int32_t* entry = p.tables + static_cast<int64_t>(b) * p.max_pages + idx;
-  int page = -1;
-  if (FP4Q_IN_RANGE(p, entry, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(entry);
+  return FP4Q_IN_RANGE(p, entry, 4, p.tables, 4LL * p.B * p.max_pages) ? __ldg(entry) : -1;
+}
+__device__ __forceinline__ uint32_t prefill_row(const KvAttentionParams& p, int kvh, int page, int at) {
   return page >= 0 && page < p.c.num_pages ? (static_cast<uint32_t>(page) * p.c.heads + kvh) * p.c.page_size + at
                                            : kPreNoRow;
 }
@@ -94,7 +99,7 @@ __device__ __forceinline__ void prefill_rows(const KvAttentionParams& p, int b, 
   if (lane < 8 && key < len) {
     const int idx = key / p.c.page_size;
     at = key - idx * p.c.page_size;
-    row = prefill_row(p, b, kvh, idx, at);
+    row = prefill_row(p, kvh, prefill_page(p, b, idx), at);
   }
 }
 
@@ -111,7 +116,7 @@ struct PrefillRaw {
 
 template <int D>
 __device__ __forceinline__ void prefill_load(const KvAttentionParams& p, uint32_t row_of, uint32_t at_of,
-                                             int key0, int len, int pw, int lane, PrefillRaw<D>& r) {
+                                             int pw, int lane, PrefillRaw<D>& r) {
   constexpr int KP = PrefillRaw<D>::KP, VW = PrefillRaw<D>::VW;
   // K: piece lane / KEYS of key i * 4 KEYS + pw * KEYS + lane % KEYS; eight neighbouring
   // lanes hold eight keys, whose swizzled places lie in different banks
@@ -159,11 +164,6 @@ __device__ __forceinline__ void prefill_load(const KvAttentionParams& p, uint32_
     const uint8_t* sf = p.c.v_sf + (row - in_page) * (D / 16) +
                         static_cast<uint64_t>(dw * VW / 2) * p.c.page_size + in_page;
     if (FP4Q_IN_RANGE(p, sf, 8, p.c.v_sf, kv_sf_extent(p.c))) r.vs = __ldg(reinterpret_cast<const uint2*>(sf));
-    const int left = len - (key0 + first);             // slots behind the end may hold no numbers
-    if (left < 8) {
-      r.vs.x = left <= 0 ? 0u : left >= 4 ? r.vs.x : r.vs.x & (0xffffffffu >> (32 - 8 * left));
-      r.vs.y = left <= 4 ? 0u : r.vs.y & (0xffffffffu >> (64 - 8 * left));
-    }
   }
 }
 
@@ -189,15 +189,24 @@ __device__ __forceinline__ void prefill_store_k(const PrefillRaw<D>& r, uint32_t
 }
 
 template <int D>
-__device__ __forceinline__ void prefill_store_v(const PrefillRaw<D>& r, uint32_t dst, int pw, int lane) {
+__device__ __forceinline__ void prefill_store_v(const PrefillRaw<D>& r, uint32_t dst, int keys_left, int pw,
+                                                int lane) {
   constexpr int VW = PrefillRaw<D>::VW;
   const int kg = lane & 7, dw = (pw >> 1) * 4 + (lane >> 3);
   const uint32_t base = dst + (pw & 1) * (D * 128);
+  // slots behind the sequence's end may hold no numbers: their scales count as 0 (here
+  // and not with the load, which nothing is to wait for)
+  uint2 vs = r.vs;
+  const int left = keys_left - (pw & 1) * 64 - kg * 8;
+  if (left < 8) {
+    vs.x = left <= 0 ? 0u : left >= 4 ? vs.x : vs.x & (0xffffffffu >> (32 - 8 * left));
+    vs.y = left <= 4 ? 0u : vs.y & (0xffffffffu >> (64 - 8 * left));
+  }
   uint32_t sc[4];
-  sc[0] = e4m3x2_to_f16x2(r.vs.x);
-  sc[1] = e4m3x2_to_f16x2(r.vs.x >> 16);
-  sc[2] = e4m3x2_to_f16x2(r.vs.y);
-  sc[3] = e4m3x2_to_f16x2(r.vs.y >> 16);
+  sc[0] = e4m3x2_to_f16x2(vs.x);
+  sc[1] = e4m3x2_to_f16x2(vs.x >> 16);
+  sc[2] = e4m3x2_to_f16x2(vs.y);
+  sc[3] = e4m3x2_to_f16x2(vs.y >> 16);
 #pragma unroll
   for (int w = 0; w < VW; ++w) {
     uint32_t lo[4][4], hi[4][4];                      // [pair of keys][channel pair]
@@ -315,18 +324,19 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
 
   if (warp == 12) tmem_alloc(&tmem_slot, kPreTmemCols);
   if (tid == 0) {
-    // one arrival per warp of the writers, one commit of the products
+    // one arrival per warp of the writers, one commit of each tile's products
     mbar_init(&bars[kBarQ], 8);
     for (int i = 0; i < 2; ++i) {
       mbar_init(&bars[kBarKFull + i], 4);
-      mbar_init(&bars[kBarKEmpty + i], 1);
+      mbar_init(&bars[kBarKEmpty + i], 2);
       mbar_init(&bars[kBarVFull + i], 4);
-      mbar_init(&bars[kBarVEmpty + i], 1);
+      mbar_init(&bars[kBarVEmpty + i], 2);
       mbar_init(&bars[kBarS + i], 1);
       mbar_init(&bars[kBarP + i], 4);
       mbar_init(&bars[kBarO + i], 1);
+      mbar_init(&bars[kBarDrain + i], 1);
+      mbar_init(&bars[kBarTurn + i], 1);
     }
-    mbar_init(&bars[kBarDrain], 1);
     mbar_init_fence();
   }
   // whether a page of these keys is outside the cache: only then are the steps' pages
@@ -514,15 +524,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   } else if (warp < 12) {
     // --- key and value tiles
     const int pw = warp - 8;
-    // group `lane` (of 8) of the step after the one whose row is in row_of: page idx, place at;
+    // group `lane` (of 8) of the step after the one whose page is in page_of: page idx, place at;
     // a step of 128 keys is page_q pages and page_r places
     const int page_q = kPreKeys / p.c.page_size, page_r = kPreKeys - page_q * p.c.page_size;
     int key = t0 * kPreKeys + 16 * (lane & 7);
     int idx = key / p.c.page_size, at = key - idx * p.c.page_size;
-    uint32_t row_of, at_of;
-    auto next_rows = [&]() {
+    int page_of, at_of;                            // the page's number is looked at a step later
+    auto next_page = [&]() {
       at_of = at;
-      row_of = key < seq.len ? prefill_row(p, b, kvh, idx, at) : kPreNoRow;
+      page_of = key < seq.len ? prefill_page(p, b, idx) : -1;
       key += kPreKeys;
       idx += page_q;
       at += page_r;
@@ -532,9 +542,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       }
     };
     PrefillRaw<D> raw[2];                          // loaded one step before it is converted
-    next_rows();
-    if (steps > 0) prefill_load<D>(p, row_of, at_of, t0 * kPreKeys, seq.len, pw, lane, raw[0]);
-    next_rows();
+    next_page();
+    if (steps > 0) prefill_load<D>(p, prefill_row(p, kvh, page_of, at_of), at_of, pw, lane, raw[0]);
+    next_page();
     bool alive = true;
     for (int j0 = 0; j0 < steps && alive; j0 += 2) {
 #pragma unroll
@@ -542,8 +552,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         const int j = j0 + s;
         if (j >= steps || !alive) break;
         if (j + 1 < steps) {
-          prefill_load<D>(p, row_of, at_of, (t0 + j + 1) * kPreKeys, seq.len, pw, lane, raw[s ^ 1]);
-          next_rows();
+          prefill_load<D>(p, prefill_row(p, kvh, page_of, at_of), at_of, pw, lane, raw[s ^ 1]);
+          next_page();
         }
         const uint32_t parity = ((j >> 1) & 1) ^ 1;    // of the use before
         alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarKEmpty + s], parity, wait_limit));
@@ -553,7 +563,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         warp_arrive(&bars[kBarKFull + s], lane);
         alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit));
         if (!alive) break;
-        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, pw, lane);
+        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, seq.len - (t0 + j) * kPreKeys, pw, lane);
         fence_proxy_async_smem();
         warp_arrive(&bars[kBarVFull + s], lane);
       }
@@ -561,64 +571,66 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   } else {
     registers_down<kPreIssueRegs>();
   }
-  if (warp == 12 && lane == 0 && steps > 0) {
-    // --- products
+  if ((warp == 12 || warp == 13) && lane == 0 && steps > 0) {
+    // --- products of one tile
+    const int tile = warp - 12, mine = n[tile];
     constexpr uint32_t kIdescS = idesc_f16(128, 128), kIdescO = idesc_f16(128, D);
     // the descriptors differ in their address field, the low word's 14 bits of 16-byte
     // units: a step of 16 adds 32 bytes, one of 64 a sub-tile, without a carry out
     const uint32_t first = static_cast<uint32_t>(smem_desc(smem0, 0, 1024, kSwizzle128B));
     const uint32_t high = static_cast<uint32_t>(smem_desc(smem0, 0, 1024, kSwizzle128B) >> 32);
     auto desc = [&](uint32_t low) { return static_cast<uint64_t>(high) << 32 | low; };
-    auto q_k = [&](int tile, int s) {
-      const uint32_t d = tmem + tile * 128;
-      const uint32_t qa = first + ((S::kQ + tile * S::kTile) >> 4), ka = first + ((S::kK + s * S::kTile) >> 4);
+    const uint32_t ts = tmem + tile * 128, to = tmem + 256 + tile * D;
+    const uint32_t qa = first + ((S::kQ + tile * S::kTile) >> 4);
+    auto q_k = [&](int s, bool hand_over) {
+      const uint32_t ka = first + ((S::kK + s * S::kTile) >> 4);
 #pragma unroll
       for (int k = 0; k < D / 16; ++k) {
         const uint32_t o = ((k >> 2) * 16384 + (k & 3) * 32) >> 4;
-        mma_f16_ss(d, desc(qa + o), desc(ka + o), kIdescS, k > 0);
+        if (k == D / 16 - 2 && hand_over) mbar_arrive(&bars[kBarTurn + (tile ^ 1)]);
+        mma_f16_ss(ts, desc(qa + o), desc(ka + o), kIdescS, k > 0);
       }
       tc_commit(&bars[kBarS + tile]);
     };
-    auto p_v = [&](int tile, int s, bool begins) {
-      const uint32_t d = tmem + 256 + tile * D, a = tmem + tile * 128;
+    auto p_v = [&](int s, bool begins) {
       const uint32_t va = first + ((S::kV + s * S::kTile) >> 4);
 #pragma unroll
       for (int k = 0; k < kPreKeys / 16; ++k) {
         const uint32_t o = ((k >> 2) * (D * 128) + (k & 3) * 32) >> 4;
-        mma_f16_ts(d, a + 8 * k, desc(va + o), kIdescO, !(begins && k == 0));
+        mma_f16_ts(to, ts + 8 * k, desc(va + o), kIdescO, !(begins && k == 0));
       }
     };
+    // the release of a stage: with the tile's last product of it, or, behind the tile's
+    // last step, plainly, once the stage was filled (so no phase gets an arrival too many)
     bool alive = mbar_wait_bounded(&bars[kBarQ], 0, wait_limit) &&
                  mbar_wait_bounded(&bars[kBarKFull], 0, wait_limit);
     if (alive) {
       tc_fence_after_sync();
-      for (int tile = 0; tile < 2; ++tile)
-        if (n[tile] > 0) q_k(tile, 0);
+      if (mine > 0) q_k(0, false);
       tc_commit(&bars[kBarKEmpty]);
     }
     for (int j = 0; j < steps && alive; ++j) {
       const int s = j & 1;
-      alive = mbar_wait_bounded(&bars[kBarVFull + s], (j >> 1) & 1, wait_limit);
-      if (alive && j + 1 < steps)
-        alive = mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit);
-      for (int tile = 0; tile < 2 && alive; ++tile) {
-        if (j >= n[tile]) continue;
-        alive = mbar_wait_bounded(&bars[kBarP + tile], j & 1, wait_limit);
-        if (!alive) break;
-        tc_fence_after_sync();
-        p_v(tile, s, j == 0);
-        if (j + 1 < n[tile])
-          q_k(tile, s ^ 1);
-        else
-          tc_commit(&bars[kBarO + tile]);
+      const bool more = j + 1 < steps;
+      alive = mbar_wait_bounded(&bars[kBarVFull + s], (j >> 1) & 1, wait_limit) &&
+              (!more || mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit)) &&
+              (j >= mine || mbar_wait_bounded(&bars[kBarP + tile], j & 1, wait_limit)) &&
+              // the turns: tile 0 of step 0 has the first
+              (j + tile == 0 || mbar_wait_bounded(&bars[kBarTurn + tile], (j + tile + 1) & 1, wait_limit));
+      if (!alive) break;
+      tc_fence_after_sync();
+      if (j < mine) p_v(s, j == 0);
+      if (j + 1 < mine) {
+        q_k(s ^ 1, true);
+      } else {
+        mbar_arrive(&bars[kBarTurn + (tile ^ 1)]);
+        if (j + 1 == mine) tc_commit(&bars[kBarO + tile]);
       }
-      if (alive) {
-        tc_commit(&bars[kBarVEmpty + s]);
-        if (j + 1 < steps) tc_commit(&bars[kBarKEmpty + (s ^ 1)]);
-      }
+      tc_commit(&bars[kBarVEmpty + s]);
+      if (more) tc_commit(&bars[kBarKEmpty + (s ^ 1)]);
     }
-    tc_commit(&bars[kBarDrain]);                 // nothing may run when tensor memory is freed
-    mbar_wait_bounded(&bars[kBarDrain], 0);
+    tc_commit(&bars[kBarDrain + tile]);          // nothing may run when tensor memory is freed
+    mbar_wait_bounded(&bars[kBarDrain + tile], 0);
   }
   __syncthreads();
   tc_fence_after_sync();
