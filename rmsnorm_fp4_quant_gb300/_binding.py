@@ -3,6 +3,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import NamedTuple, Optional, Tuple
 
@@ -627,9 +628,10 @@ def kv_cache_nvfp4(num_pages: int, page_size: int, num_kv_heads: int, head_dim: 
 
 # These calls are short enough on the device that the checks count: attributes are
 # read once, devices compared by number, and the library is called directly.
-def _kv_struct(cache, k_global_scale, v_global_scale):
-    """(fp4_kv_cache_t, device number) of a cache whose buffers have been checked."""
-    u8 = _torch().uint8
+def _kv_struct(torch, cache, k_global_scale, v_global_scale):
+    """(fp4_kv_cache_t, device number, heads, head_dim) of a cache whose buffers have been
+    checked."""
+    u8 = torch.uint8
     kp, ks, vp, vs = cache
     shape = kp.shape
     dev = kp.get_device()
@@ -646,7 +648,7 @@ def _kv_struct(cache, k_global_scale, v_global_scale):
     for t in (kp, ks, vp, vs):
         if t.dtype is not u8 or not t.is_contiguous() or t.get_device() != dev:
             raise ValueError("cache buffers must be contiguous uint8 tensors on one device")
-    if dev != _torch().cuda.current_device():
+    if dev != torch.cuda.current_device():
         raise ValueError(f"the cache is on cuda:{dev}, which is not the current device")
     kg = vg = None
     if k_global_scale is not None:
@@ -655,8 +657,8 @@ def _kv_struct(cache, k_global_scale, v_global_scale):
     if v_global_scale is not None:
         _same_device(dev, "v_global_scale", v_global_scale)
         vg = _gs_ptr(v_global_scale)
-    return KVCacheStruct(kp.data_ptr(), ks.data_ptr(), vp.data_ptr(), vs.data_ptr(), kg, vg,
-                         pages, page, heads, 2 * half), dev
+    return (KVCacheStruct(kp.data_ptr(), ks.data_ptr(), vp.data_ptr(), vs.data_ptr(), kg, vg,
+                          pages, page, heads, 2 * half), dev, heads, 2 * half)
 
 
 def _same_device(dev, name, t):
@@ -685,13 +687,28 @@ def _dense_ptr(t, name, dev, dtype, shape):
     return t.data_ptr()
 
 
+_NO_STREAM = contextlib.nullcontext()
+
+
 def _on(stream):
     """What is allocated inside belongs to the stream the kernels run on."""
-    return _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext()
+    return _NO_STREAM if stream is None else _torch().cuda.stream(stream)
 
 
-def _kv_stream(stream, dev) -> int:
-    torch = _torch()
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(L, dev, B, T, hq, heads, dim) -> int:
+    return max(L.fp4_attention_workspace_bytes(B, T, hq, heads, dim), 0)
+
+
+def _kv_dtype(torch, dtype) -> int:
+    if dtype is torch.bfloat16:
+        return FP4_DT_BF16
+    if dtype is torch.float16:
+        return FP4_DT_FP16
+    raise ValueError("dtype must be bfloat16 or float16")
+
+
+def _kv_stream(torch, stream, dev) -> int:
     if stream is not None:
         return stream.cuda_stream
     raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without a Stream object
@@ -714,10 +731,9 @@ def kv_append_nvfp4(cache, k, v, slots, q=None, positions=None, cos_sin=None,
     neither its slot nor its row of out_q is written.  interleaved: pairs are
     channels 2i and 2i + 1 instead of i and i + rot_dim/2.  out_q: may be q itself."""
     torch = _torch()
-    struct, dev = _kv_struct(cache, k_global_scale, v_global_scale)
-    heads, dim = struct.num_kv_heads, struct.head_dim
+    struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
     T, dtype = k.shape[0], k.dtype
-    dt = _dtype_code(k)
+    dt = _kv_dtype(torch, dtype)
     ks = _head_rows(k, "k", dev, T, heads, dim, dtype)
     vs = _head_rows(v, "v", dev, T, heads, dim, dtype)
     hq = qs = oqs = qp = oqp = 0
@@ -746,7 +762,7 @@ def kv_append_nvfp4(cache, k, v, slots, q=None, positions=None, cos_sin=None,
     st = lib().fp4_kv_append_nvfp4(qp, qs, oqp, oqs, k.data_ptr(), ks, v.data_ptr(), vs, pos, table,
                                    rows, rot, 1 if interleaved else 0,
                                    _dense_ptr(slots, "slots", dev, torch.int64, (T,)), T, hq, dt,
-                                   struct, 1 if pdl else 0, _kv_stream(stream, dev))
+                                   struct, 1 if pdl else 0, _kv_stream(torch, stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_kv_append_nvfp4")
     return out_q
@@ -758,12 +774,12 @@ def kv_gather_nvfp4(cache, slots, dtype=None, k_global_scale=None, v_global_scal
     that of out_k / out_v); a slot outside the cache leaves its rows of out_k and
     out_v as they were."""
     torch = _torch()
-    struct, dev = _kv_struct(cache, k_global_scale, v_global_scale)
+    struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
     if dtype is None:
         dtype = out_k.dtype if out_k is not None else out_v.dtype if out_v is not None \
             else torch.bfloat16
     T = slots.shape[0]
-    shape = (T, struct.num_kv_heads, struct.head_dim)
+    shape = (T, heads, dim)
     if out_k is None or out_v is None:
         with _on(stream):
             if out_k is None:
@@ -771,9 +787,9 @@ def kv_gather_nvfp4(cache, slots, dtype=None, k_global_scale=None, v_global_scal
             if out_v is None:
                 out_v = torch.empty(shape, dtype=dtype, device=slots.device)
     st = lib().fp4_kv_gather_nvfp4(struct, _dense_ptr(slots, "slots", dev, torch.int64, (T,)), T,
-                                   _dtype_code(out_k), _dense_ptr(out_k, "out_k", dev, dtype, shape),
+                                   _kv_dtype(torch, dtype), _dense_ptr(out_k, "out_k", dev, dtype, shape),
                                    _dense_ptr(out_v, "out_v", dev, dtype, shape),
-                                   1 if pdl else 0, _kv_stream(stream, dev))
+                                   1 if pdl else 0, _kv_stream(torch, stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_kv_gather_nvfp4")
     return out_k, out_v
@@ -797,13 +813,12 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     (lse (T, heads) fp32, natural logarithm).  workspace: optional uint8 tensor of
     fp4_attention_workspace_bytes bytes, for one call at a time."""
     torch = _torch()
-    struct, dev = _kv_struct(cache, k_global_scale, v_global_scale)
+    struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
     shape, dtype = q.shape, q.dtype
     if len(shape) != 3:
         raise ValueError("q must be (T, heads, head_dim)")
-    T, hq, dim = shape
-    qs = _head_rows(q, "q", dev, T, hq, struct.head_dim, dtype)
-    heads = struct.num_kv_heads
+    T, hq = shape[0], shape[1]
+    qs = _head_rows(q, "q", dev, T, hq, dim, dtype)
     if hq % heads:
         raise ValueError("the number of query heads must be a multiple of the cache's kv_heads")
     i32 = torch.int32
@@ -819,29 +834,30 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
         raise ValueError("q must have one row per sequence without cu_seqlens_q")
     L = lib()
     if workspace is None:
-        size = max(L.fp4_attention_workspace_bytes(B, T, hq, heads, dim), 0)
+        size = _attention_workspace(L, dev, B, T, hq, heads, dim)
     else:
         _check_cuda(workspace, "workspace")
         _same_device(dev, "workspace", workspace)
         size = workspace.numel() * workspace.element_size()
     if out is None or workspace is None or (return_lse and lse is None):
+        dv = q.device
         with _on(stream):
             if out is None:
-                out = torch.empty(shape, dtype=dtype, device=q.device)
+                out = torch.empty(shape, dtype=dtype, device=dv)
             if return_lse and lse is None:
-                lse = torch.empty((T, hq), dtype=torch.float32, device=q.device)
+                lse = torch.empty((T, hq), dtype=torch.float32, device=dv)
             if workspace is None:
-                workspace = torch.empty(size, dtype=torch.uint8, device=q.device)
+                workspace = torch.empty(size, dtype=torch.uint8, device=dv)
     if status is not None:
         _same_device(dev, "status", status)
     st = L.fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
-                               _dtype_code(q),
+                               _kv_dtype(torch, dtype),
                                float(sm_scale) if sm_scale is not None else dim ** -0.5,
                                1 if causal else 0, _dense_ptr(out, "out", dev, dtype, shape),
                                _dense_ptr(lse, "lse", dev, torch.float32, (T, hq))
                                if lse is not None else 0,
                                workspace.data_ptr(), size,
-                               _status_ptr(status), 1 if pdl else 0, _kv_stream(stream, dev))
+                               _status_ptr(status), 1 if pdl else 0, _kv_stream(torch, stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_attention_nvfp4")
     return (out, lse) if return_lse else out
