@@ -33,7 +33,8 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
   if (e != cudaSuccess) return e;
   const int64_t slots = decode_row_slots(p.B, p.T, p.group, S::kRows) * p.c.heads;
   cfg.gridDim = dim3(static_cast<unsigned>(slots), S::kRows);
-  cfg.blockDim = dim3(128);
+  // few items, many parts each: more threads per row take them side by side
+  cfg.blockDim = dim3(slots * 8 <= ctas ? kJoinMost : 128);
   cfg.dynamicSmemBytes = 0;
   cfg.numAttrs = 1;                              // its launch overlaps the first kernel
   return cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<T, D, NT>, p, ctas);

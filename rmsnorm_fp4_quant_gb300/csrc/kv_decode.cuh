@@ -64,36 +64,37 @@ __host__ __device__ inline int64_t decode_row_slots(int64_t B, int64_t T, int gr
   return T * group / rows + B;
 }
 
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+template <int OFF> __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+  asm volatile("cp.async.cg.shared.global [%0+%2], [%1], 16;" :: "r"(dst), "l"(src), "n"(OFF) : "memory");
 }
 __device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> __device__ __forceinline__ void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory");
 }
-__device__ __forceinline__ uint32_t lds32(uint32_t a) {
+// Shared-memory loads at a register address and a constant offset.
+template <int OFF> __device__ __forceinline__ uint32_t lds32(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.b32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.b32 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF) : "memory");
   return v;
 }
-__device__ __forceinline__ uint32_t lds16(uint32_t a) {
-  uint16_t v;
-  asm volatile("ld.shared.b16 %0, [%1];" : "=h"(v) : "r"(a) : "memory");
-  return v;
-}
-__device__ __forceinline__ uint32_t lds8(uint32_t a) {
+template <int OFF> __device__ __forceinline__ uint32_t lds16(uint32_t a) {
   uint32_t v;
-  asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  asm volatile("ld.shared.u16 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF) : "memory");
   return v;
 }
-template <int W> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[W]) {
+template <int OFF> __device__ __forceinline__ uint32_t lds8(uint32_t a) {
+  uint32_t v;
+  asm volatile("ld.shared.u8 %0, [%1+%2];" : "=r"(v) : "r"(a), "n"(OFF) : "memory");
+  return v;
+}
+template <int W, int OFF> __device__ __forceinline__ void lds_words(uint32_t a, uint32_t (&w)[W]) {
   if constexpr (W == 4)
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a) : "memory");
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4+%5];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(a), "n"(OFF) : "memory");
   else if constexpr (W == 2)
-    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(a) : "memory");
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2+%3];" : "=r"(w[0]), "=r"(w[1]) : "r"(a), "n"(OFF) : "memory");
   else
-    w[0] = lds32(a);
+    w[0] = lds32<OFF>(a);
 }
 __device__ __forceinline__ void mma_16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
                                           uint32_t a3, uint32_t b0, uint32_t b1) {
@@ -120,6 +121,8 @@ template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
   if (D == 128) return (row ^ ((row >> 2) & 1)) * 64 + ((piece ^ (row >> 2)) & 3) * 16;
   return ((row >> 2) | ((row & 3) << 2)) * 32 + piece * 16;
 }
+
+template <int V> struct Const { static constexpr int value = V; };
 
 // What one CTA's walk over the units needs to know of the sequence it is in.
 struct DecodeWalk {
@@ -205,7 +208,7 @@ kv_decode_kernel(const KvAttentionParams p) {
   int64_t units = decode_units<ROWS>(p, start_b, w);
   w.base = start_base;
 
-  const uint32_t ring = smem_addr(smem) + warp * kDecStages * S::kTile;
+  const uint32_t ring = smem_addr(smem) + warp * kDecStages * S::kTile;   // this warp's
   const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
   const float vgs = p.c.v_gs ? __ldg(p.c.v_gs) : 1.0f;
   const int row_k = 4 * (g >> 1) + (g & 1);     // key of tile row g; row g + 8 is key row_k + 2
@@ -215,23 +218,24 @@ kv_decode_kernel(const KvAttentionParams p) {
   constexpr int kPieces = D / 32;               // per key
   const uint8_t* const k_lane = p.c.k_packed + lane * 16;
   const uint8_t* const v_lane = p.c.v_packed + lane * 16;
-  const uint32_t k_dst = k_place<D>(lane / kPieces, lane % kPieces);
-  const uint32_t v_dst = S::kV + v_place<D>(lane / kPieces, lane % kPieces);
+  const uint32_t k_dst = ring + k_place<D>(lane / kPieces, lane % kPieces);
+  const uint32_t v_dst = ring + S::kV + v_place<D>(lane / kPieces, lane % kPieces);
+  const uint32_t s_dst = ring + S::kKs + lane * 16;
   constexpr int kRows1 = 32 / kPieces;          // keys between a lane's two pieces (D = 128)
-  const uint32_t k_dst1 = D == 128 ? k_place<D>(lane / kPieces + kRows1, lane % kPieces) - k_dst : 0;
-  const uint32_t v_dst1 = D == 128 ? S::kV + v_place<D>(lane / kPieces + kRows1, lane % kPieces) - v_dst : 0;
+  const uint32_t k_dst1 = D == 128 ? ring + k_place<D>(lane / kPieces + kRows1, lane % kPieces) - k_dst : 0;
+  const uint32_t v_dst1 = D == 128 ? ring + S::kV + v_place<D>(lane / kPieces + kRows1, lane % kPieces) - v_dst : 0;
   const uint8_t* const s_lane = lane < D / 16 ? p.c.k_sf + lane * 16
                                               : p.c.v_sf + static_cast<int64_t>(lane - D / 16) * p.c.page_size;
   const int s_back = lane < D / 16 ? 0 : D / 16 - 1;
   // what it reads of a tile for the products
-  const uint32_t k_src = k_place<D>(row_k, KW * t / 4) + (KW * t % 4) * 4;
-  const uint32_t k_src2 = k_place<D>(row_k + 2, KW * t / 4) + (KW * t % 4) * 4;
-  const uint32_t ks_src = S::kKs + row_k * (D / 16) + t * (D / 64);
-  const uint32_t vs_src = S::kVs + (D == 128 ? g : g / 2) * 16 + 4 * t;
+  const uint32_t k_src = ring + k_place<D>(row_k, KW * t / 4) + (KW * t % 4) * 4;
+  const uint32_t k_src2 = ring + k_place<D>(row_k + 2, KW * t / 4) + (KW * t % 4) * 4;
+  const uint32_t ks_src = ring + S::kKs + row_k * (D / 16) + t * (D / 64);
+  const uint32_t vs_src = ring + S::kVs + (D == 128 ? g : g / 2) * 16 + 4 * t;
   uint32_t v_src[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i)
-    v_src[i] = S::kV + v_place<D>(4 * t + i, VW * g / 4) + (VW * g % 4) * 4;
+    v_src[i] = ring + S::kV + v_place<D>(4 * t + i, VW * g / 4) + (VW * g % 4) * 4;
 
   while (u < u_end) {
     while (u >= w.base + units) {               // the next sequence that has units
@@ -338,7 +342,8 @@ kv_decode_kernel(const KvAttentionParams p) {
     look_up(0, row_of, at_of);
     look_up(32, row_next, at_next);
     uint32_t valid = 0;                          // bit i: the tile issued i tiles ago holds keys
-    auto issue = [&](int x) {
+    auto issue = [&](int x, auto slot) {
+      constexpr int kSlot = decltype(slot)::value * S::kTile;
       if ((x & 31) == 0 && x) {
         row_of = row_next;
         at_of = at_next;
@@ -349,65 +354,64 @@ kv_decode_kernel(const KvAttentionParams p) {
       valid <<= 1;
       if (row != kNoRow) {
         valid |= 1;
-        const uint32_t dst = ring + (x & (kDecStages - 1)) * S::kTile;
         const uint8_t* kc = k_lane + static_cast<uint64_t>(row) * (D / 2);
         const uint8_t* vc = v_lane + static_cast<uint64_t>(row) * (D / 2);
         const uint8_t* sc = s_lane + static_cast<uint64_t>(row) * (D / 16) - static_cast<uint64_t>(at) * s_back;
 #pragma unroll
         for (int i = 0; i < D / 64; ++i) {
           if (FP4Q_IN_RANGE(p, kc + 512 * i, 16, p.c.k_packed, kv_packed_extent(p.c)))
-            cp_async16(dst + k_dst + (i ? k_dst1 : 0), kc + 512 * i);
+            cp_async16<kSlot>(k_dst + (i ? k_dst1 : 0), kc + 512 * i);
           if (FP4Q_IN_RANGE(p, vc + 512 * i, 16, p.c.v_packed, kv_packed_extent(p.c)))
-            cp_async16(dst + v_dst + (i ? v_dst1 : 0), vc + 512 * i);
+            cp_async16<kSlot>(v_dst + (i ? v_dst1 : 0), vc + 512 * i);
         }
         if (lane < D / 8 && FP4Q_IN_RANGE(p, sc, 16, lane < D / 16 ? p.c.k_sf : p.c.v_sf, kv_sf_extent(p.c)))
-          cp_async16(dst + S::kKs + lane * 16, sc);
+          cp_async16<kSlot>(s_dst, sc);
       }
     };
-    auto issue_step = [&](int step) {
-#pragma unroll
-      for (int j = 0; j < TP; ++j) issue(step * TP + j);
+    auto issue_step = [&](int step, auto phase) {
+      issue(step * TP, Const<decltype(phase)::value * TP>{});
+      if constexpr (TP == 2) issue(step * TP + 1, Const<decltype(phase)::value * TP + 1>{});
       cp_async_commit();
     };
-#pragma unroll
-    for (int i = 0; i < AHEAD; ++i) issue_step(i);
+    constexpr int PHASES = kDecStages / TP;      // steps until the ring's slots come again
+    issue_step(0, Const<0>{});
+    if constexpr (AHEAD > 1) issue_step(1, Const<1>{});
+    if constexpr (AHEAD > 2) issue_step(2, Const<2>{});
 
-    const int steps = (n_units + TP - 1) / TP;
-    for (int step = 0; step < steps; ++step) {
+    // one step, whose slots of the ring are constants
+    auto work = [&](int step, auto phase) {
+      constexpr int kPhase = decltype(phase)::value;
       cp_async_wait<AHEAD - 1>();
       __syncwarp();                              // the step's tiles are here for every lane, the last one's read
       const uint32_t here = valid >> (TP * (AHEAD - 1)) & ((1u << TP) - 1);   // bit TP - 1: the first tile
-      issue_step(step + AHEAD);
-      if (!here) continue;
-      uint32_t st[TP];
+      issue_step(step + AHEAD, Const<(kPhase + AHEAD) % PHASES>{});
+      if (!here) return;
+      constexpr int kAt[2] = {kPhase * TP * S::kTile, (kPhase * TP + TP - 1) * S::kTile};
       int key0[TP];                              // a tile without keys lies behind every limit
 #pragma unroll
-      for (int j = 0; j < TP; ++j) {
-        const int x = step * TP + j;
-        st[j] = ring + (x & (kDecStages - 1)) * S::kTile;
-        key0[j] = here >> (TP - 1 - j) & 1u ? first_key + x * kDecUnit : kNoKey;
-      }
+      for (int j = 0; j < TP; ++j)
+        key0[j] = here >> (TP - 1 - j) & 1u ? first_key + (step * TP + j) * kDecUnit : kNoKey;
 
       // S^T = K Q^T
       float s[TP][NT][4];
-#pragma unroll
-      for (int j = 0; j < TP; ++j) {
+      auto products = [&](auto tile) {
+        constexpr int j = decltype(tile)::value, at = kAt[j];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
           for (int e = 0; e < 4; ++e) s[j][n][e] = 0.0f;
         uint32_t ka[KW], kb[KW], sa[2], sb[2];
-        lds_words<KW>(st[j] + k_src, ka);
-        lds_words<KW>(st[j] + k_src2, kb);
+        lds_words<KW, at>(k_src, ka);
+        lds_words<KW, at>(k_src2, kb);
         if constexpr (D == 128) {                // two blocks per lane
-          const uint32_t fa = e4m3x2_to_f16x2(lds16(st[j] + ks_src));
-          const uint32_t fb = e4m3x2_to_f16x2(lds16(st[j] + ks_src + 16));
+          const uint32_t fa = e4m3x2_to_f16x2(lds16<at>(ks_src));
+          const uint32_t fb = e4m3x2_to_f16x2(lds16<at + 16>(ks_src));
           sa[0] = __byte_perm(fa, 0, 0x1010);
           sa[1] = __byte_perm(fa, 0, 0x3232);
           sb[0] = __byte_perm(fb, 0, 0x1010);
           sb[1] = __byte_perm(fb, 0, 0x3232);
         } else {
-          const uint32_t ba = lds8(st[j] + ks_src), bb = lds8(st[j] + ks_src + 8);
+          const uint32_t ba = lds8<at>(ks_src), bb = lds8<at + 8>(ks_src);
           sa[0] = sa[1] = e4m3x2_to_f16x2(ba | ba << 8);
           sb[0] = sb[1] = e4m3x2_to_f16x2(bb | bb << 8);
         }
@@ -427,7 +431,9 @@ kv_decode_kernel(const KvAttentionParams p) {
             mma_16816(s[j][n], ha[2], hb[2], ha[3], hb[3], qf[n][2 * i + 1][0], qf[n][2 * i + 1][1]);
           }
         }
-      }
+      };
+      products(Const<0>{});
+      if constexpr (TP == 2) products(Const<1>{});
 
       // exponents of 2 against the reference; keys that a row does not see get -inf
       float y[TP][NT][4];
@@ -496,9 +502,9 @@ kv_decode_kernel(const KvAttentionParams p) {
         }
 
       // O^T += V^T P^T: keys 4t .. 4t + 3 of each tile
-#pragma unroll
-      for (int j = 0; j < TP; ++j) {
-        uint32_t sv = lds32(st[j] + vs_src);
+      auto values = [&](auto tile) {
+        constexpr int j = decltype(tile)::value, at = kAt[j];
+        uint32_t sv = lds32<at>(vs_src);
         if (edge && key0[j] > w.s.len - 16) {    // slots behind the end may hold no numbers
           const int left = w.s.len - key0[j] - 4 * t;
           sv = left <= 0 ? 0u : left >= 4 ? sv : sv & (0xffffffffu >> (32 - 8 * left));
@@ -506,7 +512,7 @@ kv_decode_kernel(const KvAttentionParams p) {
         const uint32_t s01 = e4m3x2_to_f16x2(sv), s23 = e4m3x2_to_f16x2(sv >> 16);
         uint32_t v[4][VW];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) lds_words<VW>(st[j] + v_src[i], v[i]);
+        for (int i = 0; i < 4; ++i) lds_words<VW, at>(v_src[i], v[i]);
 #pragma unroll
         for (int i = 0; i < VW; ++i) {
           uint32_t e01[4], o01[4], e23[4], o23[4];
@@ -523,6 +529,17 @@ kv_decode_kernel(const KvAttentionParams p) {
               mma_16816(acc[n][4 * i + c], a0, a1, a2, a3, pb[j][n][0], pb[j][n][1]);
           }
         }
+      };
+      values(Const<0>{});
+      if constexpr (TP == 2) values(Const<1>{});
+    };
+    const int steps = (n_units + TP - 1) / TP;
+    for (int step = 0; step < steps; step += PHASES) {
+      work(step, Const<0>{});
+      if (step + 1 < steps) work(step + 1, Const<1>{});
+      if constexpr (PHASES > 2) {
+        if (step + 2 < steps) work(step + 2, Const<2>{});
+        if (step + 3 < steps) work(step + 3, Const<3>{});
       }
     }
     cp_async_wait<0>();
@@ -620,14 +637,16 @@ kv_decode_kernel(const KvAttentionParams p) {
 // Joins the parts of the items that several CTAs shared: block = (item, row),
 // D / 4 lanes per part, parts taken in turn by the block's groups of lanes and
 // summed in order.
+constexpr int kJoinMost = 512;                 // threads of a block at most
 template <typename T, int D, int NT>
-__global__ void __launch_bounds__(128) kv_decode_join_kernel(const KvAttentionParams p, int ctas) {
+__global__ void __launch_bounds__(kJoinMost) kv_decode_join_kernel(const KvAttentionParams p, int ctas) {
   using S = DecodeShape<D, NT>;
   constexpr int ROWS = S::kRows;
-  constexpr int LANES = D / 4, GROUPS = 128 / LANES;
-  __shared__ float red[4];
-  __shared__ float4 o_part[GROUPS][LANES];
-  __shared__ float l_part[GROUPS];
+  constexpr int LANES = D / 4;
+  const int groups = blockDim.x / LANES;
+  __shared__ float red[kJoinMost / 32];
+  __shared__ float4 o_part[kJoinMost / LANES][LANES];
+  __shared__ float l_part[kJoinMost / LANES];
   const int tid = threadIdx.x;
   const int64_t slot = blockIdx.x;
   const int kvh = static_cast<int>(slot % p.c.heads), r = blockIdx.y;
@@ -655,17 +674,17 @@ __global__ void __launch_bounds__(128) kv_decode_join_kernel(const KvAttentionPa
   // part i: the last of CTA c0 for i = 0, the first of CTA c0 + i else
   auto part = [&](int i) { return p.ws + (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * S::kPart; };
   float top = kRefStart;
-  for (int i = tid; i < n; i += 128) top = fmaxf(top, part(i)[ROWS * D + 2 * r]);
+  for (int i = tid; i < n; i += blockDim.x) top = fmaxf(top, part(i)[ROWS * D + 2 * r]);
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
   if ((tid & 31) == 0) red[tid >> 5] = top;
   __syncthreads();
-  top = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3]));
+  for (int i = 0; i < static_cast<int>(blockDim.x) / 32; ++i) top = fmaxf(top, red[i]);
   const int grp = tid / LANES, ln = tid % LANES;
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float l = 0.0f;
 #pragma unroll 4
-  for (int i = grp; i < n; i += GROUPS) {
+  for (int i = grp; i < n; i += groups) {
     const float* q = part(i);
     const float2 rl = *reinterpret_cast<const float2*>(q + ROWS * D + 2 * r);
     const float4 x = *reinterpret_cast<const float4*>(q + r * D + 4 * ln);
@@ -681,8 +700,7 @@ __global__ void __launch_bounds__(128) kv_decode_join_kernel(const KvAttentionPa
   __syncthreads();
   if (grp) return;
   l = l_part[0];
-#pragma unroll
-  for (int i = 1; i < GROUPS; ++i) {
+  for (int i = 1; i < groups; ++i) {
     const float4 x = o_part[i][ln];
     o.x += x.x;
     o.y += x.y;
