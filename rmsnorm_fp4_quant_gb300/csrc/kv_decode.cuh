@@ -41,7 +41,7 @@ constexpr int kDecMinUnits = 2;                // a CTA's share is at least this
 // What an item costs besides its keys (its queries, the ring's first tiles, the
 // join), in units: the CTAs' shares are even in these too.  Without it the one CTA
 // that has all the shortest sequences works on long after the others.
-constexpr int kDecItemCost = 4;
+constexpr int kDecItemCost = 6;
 
 template <int D, int NT>
 struct DecodeShape {
@@ -253,71 +253,19 @@ kv_decode_kernel(const KvAttentionParams p) {
     const int rows = w.s.n_q * p.group;         // of the whole sequence
     const int r0 = rt * ROWS;
 
-    // --- the item's queries, as the B operand: lane (g, t) holds channels
-    // D/4 * t ... of row g of each 8-row tile
-    uint32_t qf[NT][D / 16][2];
-    float fac[NT][2], ref[NT][2], sum[NT][2];
-    int lim[NT][2];                             // keys that columns 2t, 2t + 1 see
-    int lim_lo, lim_hi;                         // smallest and largest over the tile's rows
+    // --- the rows' limits: keys that columns 2t, 2t + 1 see, smallest and largest of the tile
     const int off = w.s.len - w.s.n_q;          // last visible key of token i: off + i
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-      const int r = r0 + 8 * n + g;
-      const bool ok = r < rows;
-      const int tok = r / p.group, hq = kvh * p.group + r - tok * p.group;
-      const T* src = static_cast<const T*>(p.q) +
-                     static_cast<int64_t>(w.s.q0 + (ok ? tok : 0)) * p.q_stride +
-                     static_cast<int64_t>(ok ? hq : 0) * D + t * (D / 4);
-      Chunk c[D / 64];
-      float top = 0.0f;
-      bool nan = false;
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i) {
-        c[i] = Chunk{};
-        if (ok && FP4Q_IN_RANGE(p, src + 16 * i, 32, p.q, 2LL * ((p.T - 1) * p.q_stride + p.Hq * D)))
-          c[i] = ld_cached_ro(src + 16 * i);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 x = Pair<T>::to_f32(c[i].u[j]);
-          top = max_abs3(top, x.x, x.y);
-          nan |= x.x != x.x || x.y != x.y;
-        }
-      }
-      if (nan) top = INFINITY;                  // no scaling: the row is NaN whatever is done
-      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
-      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
-      const int k = q_exponent(top);
-      const float up = pow2(k);
-#pragma unroll
-      for (int i = 0; i < D / 64; ++i)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const float2 x = Pair<T>::to_f32(c[i].u[j]);
-          qf[n][4 * i + j / 2][j & 1] = pack_f16x2(x.x * up, x.y * up);
-        }
-      const float f = p.sm_scale * kLog2e / kgs * pow2(-k);
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        fac[n][e] = __shfl_sync(kFullMask, f, (2 * t + e) * 4);
-        ref[n][e] = kRefStart;
-        sum[n][e] = 0.0f;
-        const int rc = r0 + 8 * n + 2 * t + e;
-        lim[n][e] = p.causal && rc < rows ? min(w.s.len, off + rc / p.group + 1) : w.s.len;
-      }
-    }
-    {
-      const int last = min(r0 + ROWS, rows) - 1;
-      lim_lo = p.causal ? off + r0 / p.group + 1 : w.s.len;
-      lim_hi = p.causal ? off + last / p.group + 1 : w.s.len;
-    }
-
-    float acc[NT][D / 16][4];
+    int lim[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i)
-#pragma unroll
-        for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
+      for (int e = 0; e < 2; ++e) {
+        const int rc = r0 + 8 * n + 2 * t + e;
+        lim[n][e] = p.causal && rc < rows ? min(w.s.len, off + rc / p.group + 1) : w.s.len;
+      }
+    const int last = min(r0 + ROWS, rows) - 1;
+    const int lim_lo = p.causal ? off + r0 / p.group + 1 : w.s.len;
+    const int lim_hi = p.causal ? off + last / p.group + 1 : w.s.len;
 
     // --- the ring: tile x of this warp is keys key0(x) ... + 15
     const int first_key = tile0 * kDecUnit + warp * 16;
@@ -341,6 +289,24 @@ kv_decode_kernel(const KvAttentionParams p) {
     };
     look_up(0, row_of, at_of);
     look_up(32, row_next, at_next);
+    // --- the item's queries, as the B operand: lane (g, t) holds channels
+    // D/4 * t ... of row g of each 8-row tile; loaded while the pages are looked up
+    Chunk qc[NT][D / 64];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      const int r = r0 + 8 * n + g;
+      const bool ok = r < rows;
+      const int tok = r / p.group, hq = kvh * p.group + r - tok * p.group;
+      const T* src = static_cast<const T*>(p.q) +
+                     static_cast<int64_t>(w.s.q0 + (ok ? tok : 0)) * p.q_stride +
+                     static_cast<int64_t>(ok ? hq : 0) * D + t * (D / 4);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        qc[n][i] = Chunk{};
+        if (ok && FP4Q_IN_RANGE(p, src + 16 * i, 32, p.q, 2LL * ((p.T - 1) * p.q_stride + p.Hq * D)))
+          qc[n][i] = ld_cached_ro(src + 16 * i);
+      }
+    }
     uint32_t valid = 0;                          // bit i: the tile issued i tiles ago holds keys
     auto issue = [&](int x, auto slot) {
       constexpr int kSlot = decltype(slot)::value * S::kTile;
@@ -377,6 +343,49 @@ kv_decode_kernel(const KvAttentionParams p) {
     issue_step(0, Const<0>{});
     if constexpr (AHEAD > 1) issue_step(1, Const<1>{});
     if constexpr (AHEAD > 2) issue_step(2, Const<2>{});
+
+    uint32_t qf[NT][D / 16][2];
+    float fac[NT][2], ref[NT][2], sum[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+      float top = 0.0f;
+      bool nan = false;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 x = Pair<T>::to_f32(qc[n][i].u[j]);
+          top = max_abs3(top, x.x, x.y);
+          nan |= x.x != x.x || x.y != x.y;
+        }
+      if (nan) top = INFINITY;                  // no scaling: the row is NaN whatever is done
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
+      top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
+      const int k = q_exponent(top);
+      const float up = pow2(k);
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const float2 x = Pair<T>::to_f32(qc[n][i].u[j]);
+          qf[n][4 * i + j / 2][j & 1] = pack_f16x2(x.x * up, x.y * up);
+        }
+      const float f = p.sm_scale * kLog2e / kgs * pow2(-k);
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        fac[n][e] = __shfl_sync(kFullMask, f, (2 * t + e) * 4);
+        ref[n][e] = kRefStart;
+        sum[n][e] = 0.0f;
+      }
+    }
+
+    float acc[NT][D / 16][4];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
 
     // one step, whose slots of the ring are constants
     auto work = [&](int step, auto phase) {
