@@ -420,8 +420,8 @@ typedef struct {
  *                      rn(rn(x2 cos) + rn(x1 sin)) in fp32; keys are quantized from these.
  *   interleaved        0: pair i is channels i and i + rot_dim/2; 1: channels 2i and 2i + 1.
  *   slots              [T] int64.  A slot outside [0, num_pages * page_size) appends nothing
- *                      (padding tokens: -1).  The slots of one call have to differ: where two
- *                      tokens name the same one it is left holding blocks of either.
+ *                      (padding tokens: -1).  The slots of one call have to differ: what a
+ *                      slot that two tokens name holds afterwards is not specified.
  *   pdl                as in fp4_add_rmsnorm_quant_ex.
  * Codes and scales are those of fp4_quantize (NVFP4) on the rotated keys and on
  * the values.  q, k, v and out_q rows start on 32-byte boundaries (strides

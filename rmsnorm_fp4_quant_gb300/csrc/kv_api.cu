@@ -156,8 +156,7 @@ fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int64_t* slo
   const fp4_status_t cs = check_cache_sizes(cache);
   if (cs != FP4_OK) return cs;
   const int64_t width = cache->num_kv_heads * cache->head_dim * 2;
-  // the grid's blocks hold 256 threads of 32 channels
-  if (T > INT32_MAX || T * cache->num_kv_heads > (int64_t{1} << 38)) return FP4_ERR_UNSUPPORTED_SHAPE;
+  if (T > INT32_MAX) return FP4_ERR_UNSUPPORTED_SHAPE;
   if (T == 0 || (!out_k && !out_v)) return FP4_OK;
   if (!slots) return FP4_ERR_INVALID_ARG;
   const fp4_status_t cb = check_cache_buffers(cache);
@@ -255,6 +254,7 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   p.out = out;
   p.lse = lse;
   p.ws = static_cast<float*>(workspace);
+  p.ws_bytes = need;
   p.status = status;
   FP4Q_SET_DEBUG(p);
   return static_cast<fp4_status_t>(record_cuda_error(launch_kv_attention(

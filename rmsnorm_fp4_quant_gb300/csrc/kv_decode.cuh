@@ -625,9 +625,13 @@ kv_decode_kernel(const KvAttentionParams p) {
           p.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (top + log2f(l));
       } else {
         float4* po = reinterpret_cast<float4*>(part + r * D + d0);
-        po[0] = make_float4(o[0], o[1], o[2], o[3]);
-        po[1] = make_float4(o[4], o[5], o[6], o[7]);
-        if (d0 == 0) *reinterpret_cast<float2*>(part + ROWS * D + 2 * r) = make_float2(top, l);
+        if (FP4Q_IN_RANGE(p, po, 32, p.ws, p.ws_bytes)) {
+          po[0] = make_float4(o[0], o[1], o[2], o[3]);
+          po[1] = make_float4(o[4], o[5], o[6], o[7]);
+        }
+        float* rl = part + ROWS * D + 2 * r;
+        if (d0 == 0 && FP4Q_IN_RANGE(p, rl, 8, p.ws, p.ws_bytes))
+          *reinterpret_cast<float2*>(rl) = make_float2(top, l);
       }
     }
     if (tid == 0 && tile0 == 0) {
@@ -636,8 +640,10 @@ kv_decode_kernel(const KvAttentionParams p) {
       const int64_t last = item_base + w.cost - 1;
       const int n = static_cast<int>(((last + 1) * G - 1) / total - cta) + 1;
       int* desc = reinterpret_cast<int*>(p.ws + 2 * static_cast<int64_t>(gridDim.x) * S::kPart) + 2 * slot;
-      desc[0] = static_cast<int>(cta);
-      desc[1] = n;
+      if (FP4Q_IN_RANGE(p, desc, 8, p.ws, p.ws_bytes)) {
+        desc[0] = static_cast<int>(cta);
+        desc[1] = n;
+      }
     }
     __syncthreads();                             // the merge buffer becomes the ring again
   }

@@ -74,6 +74,7 @@ struct KvAttentionParams {
   void* out;
   float* lse;
   float* ws;
+  int64_t ws_bytes;    // what the kernels need of it
   int* status;
   FP4Q_DEBUG_FIELD
 };

@@ -498,7 +498,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
           float* dst = p.ws + pr * D + 32 * c;
 #pragma unroll
           for (int i = 0; i < 32; i += 4)
-            *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
+            if (FP4Q_IN_RANGE(p, dst + i, 16, p.ws, p.ws_bytes))
+              *reinterpret_cast<uint4*>(dst + i) = make_uint4(x[i], x[i + 1], x[i + 2], x[i + 3]);
         } else if (ok) {
 #pragma unroll
           for (int i = 0; i < 2; ++i) {
@@ -515,9 +516,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       }
     }
     if (ok) {
-      if (parts)
-        *reinterpret_cast<float2*>(p.ws + splits * total * D + 2 * pr) = make_float2(ref, sum);
-      else if (p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * total))
+      float* rl = p.ws + splits * total * D + 2 * pr;
+      if (parts && FP4Q_IN_RANGE(p, rl, 8, p.ws, p.ws_bytes))
+        *reinterpret_cast<float2*>(rl) = make_float2(ref, sum);
+      else if (!parts && p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * total))
         p.lse[at] = sum == 0.0f ? -INFINITY : kLn2 * (ref + log2f(sum));
     }
     tc_fence_before_sync();

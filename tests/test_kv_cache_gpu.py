@@ -320,6 +320,47 @@ def test_varlen(lens, q_lens, causal, Hq, Hkv, D, page, dtype):
     check_attention(queries(T, Hq, D, dtype, 6), cache, tables, lens, cu, causal, dtype)
 
 
+# long tables and few rows: each item's keys are cut into ranges that are joined afterwards
+@pytest.mark.parametrize("lens,q_lens,causal", [
+    ([3000, 1500], [70, 130], True), ([2600], [300], False), ([64, 4200, 3], [64, 129, 200], True),
+    ([1, 2100], [90, 40], True),
+])
+@pytest.mark.parametrize("Hq,Hkv,D,page,dtype", [
+    (4, 1, 128, 16, "bf16"), (3, 1, 64, 48, "fp16"), (2, 2, 128, 128, "fp16"), (6, 2, 64, 64, "bf16")])
+def test_many_rows_over_long_sequences(lens, q_lens, causal, Hq, Hkv, D, page, dtype):
+    cu = np.cumsum([1] + q_lens).tolist()
+    bad = [(0, 3, -1)] if lens[0] > 1000 else [(1, 3, 10 ** 7), (1, 15, -2)]
+    cache, tables = fill_sequences(lens, Hkv, D, page, seed=13, bad=bad)
+    check_attention(queries(cu[-1] + 2, Hq, D, dtype, 7), cache, tables, lens, cu, causal, dtype)
+
+
+@pytest.mark.parametrize("group,q_len", [(1, 63), (1, 64), (1, 65), (3, 21), (3, 22), (64, 1), (80, 1), (9, 7), (128, 3)])
+@pytest.mark.parametrize("D", [64, 128])
+def test_rows_around_the_change_of_kernels(group, q_len, D):
+    """Rows per sequence and key/value head on both sides of each choice by their number."""
+    lens = [200, 77]
+    cache, tables = fill_sequences(lens, 1, D, 16, seed=group)
+    cu = [0, q_len, 2 * q_len]
+    check_attention(queries(2 * q_len, group, D, "bf16", 3), cache, tables, lens, cu, True, "bf16")
+
+
+def test_a_reference_that_keeps_moving():
+    """Keys whose logits grow along the sequence: the running reference moves in every
+    step of every kernel, and everything before it is scaled down."""
+    D, page, n = 64, 16, 1200
+    cache = to_np(random_cache(n // page, 1, page, D, 3))
+    k = np.zeros((n, 1, D), np.float32)
+    k[:, 0, 0] = np.linspace(0, 300, n)
+    v = torch.randn(n, 1, D, generator=gen(5)).numpy()
+    okv.append(cache, k, v, np.arange(n))
+    tables = np.arange(n // page, dtype=np.int64)[None]
+    for cu, T in ((None, 1), ([0, 100], 100)):
+        for sign in (1.0, -1.0):
+            q = torch.zeros(T, 2, D)
+            q[..., 0] = sign * torch.linspace(1, 9, T)[:, None]
+            check_attention(q.bfloat16(), cache, tables, [n], cu, True, "bf16", sm_scale=1.0)
+
+
 @pytest.mark.parametrize("q_lens", [None, [1, 40, 150]])
 @pytest.mark.parametrize("D", [64, 128])
 def test_bad_pages_are_masked(q_lens, D):
@@ -526,6 +567,108 @@ def test_status_word_is_left_alone():
         assert fq.read_device_status(status) == fq.FP4_OK
 
 
+def test_one_workspace_for_calls_in_a_row():
+    """A workspace of the caller's, any contents, used by calls one after the other, each
+    launched beside the tail of the one before it."""
+    D, Hq, Hkv = 128, 8, 2
+    lens = [2000, 300]
+    cache, tables = fill_sequences(lens, Hkv, D, 16, seed=3)
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cu = torch.tensor([0, 40, 120], dtype=torch.int32, device="cuda")
+    need = max(fq.fp4_attention_workspace_bytes(2, 2, Hq, Hkv, D), fq.fp4_attention_workspace_bytes(2, 120, Hq, Hkv, D))
+    ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
+    qs = [queries(2 if i % 2 else 120, Hq, D, "bf16", i).cuda() for i in range(6)]
+    torch.cuda.synchronize()
+    got = [fq.attention_nvfp4(q, dev, tab, sl, None if q.shape[0] == 2 else cu, workspace=ws, pdl=True) for q in qs]
+    want = [fq.attention_nvfp4(q, dev, tab, sl, None if q.shape[0] == 2 else cu) for q in qs]
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+    with pytest.raises(fq.Fp4Error):
+        fq.attention_nvfp4(qs[0], dev, tab, sl, cu, workspace=ws[:16])
+
+
+def test_tensor_calls_refuse_what_they_cannot_take():
+    T, Hq, Hkv, D = 3, 4, 2, 64
+    c = fq.kv_cache_nvfp4(4, 16, Hkv, D)
+    k = torch.zeros(T, Hkv, D, dtype=torch.bfloat16, device="cuda")
+    q = torch.zeros(T, Hq, D, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(T, device="cuda")
+    tab = torch.zeros(T, 1, dtype=torch.int32, device="cuda")
+    sl = torch.ones(T, dtype=torch.int32, device="cuda")
+    cs = torch.zeros(8, 64, device="cuda")
+    for bad in [dict(k=k.half()), dict(k=k[:2]), dict(slots=slots.int()), dict(slots=slots[:2]), dict(q=q.float()),
+                dict(k=k[:1].expand(T, Hkv, D)), dict(k=k.transpose(1, 2)), dict(cos_sin=cs), dict(positions=slots),
+                dict(cos_sin=cs.double(), positions=slots), dict(cos_sin=cs, positions=slots.int()),
+                dict(out_q=q), dict(q=q, out_q=q[:2]), dict(slots=slots.cpu()), dict(k=k.cpu()),
+                dict(cache=c[:3]), dict(cache=(c[0], c[1], c[2], c[3].transpose(2, 3))), dict(v=k.float())]:
+        a = dict(cache=c, k=k, v=k.clone(), slots=slots)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            fq.kv_append_nvfp4(a.pop("cache"), a.pop("k"), a.pop("v"), a.pop("slots"), **a)
+    with pytest.raises(fq.Fp4Error):                      # rotated channels in multiples of 32
+        fq.kv_append_nvfp4(c, k, k.clone(), slots, positions=slots, cos_sin=torch.zeros(8, 16, device="cuda"))
+    for bad in [dict(q=q[0]), dict(q=q[:, :3]), dict(q=q.float()), dict(block_tables=tab.long()), dict(block_tables=tab[:2]),
+                dict(seq_lens=sl.long()), dict(seq_lens=sl[:2]), dict(cu_seqlens_q=sl), dict(out=q.half()),
+                dict(lse=torch.zeros(T, Hq, dtype=torch.float64, device="cuda")), dict(q=q[:2]), dict(seq_lens=sl.cpu()),
+                dict(status=torch.zeros(2, dtype=torch.int32, device="cuda")), dict(block_tables=tab[0]),
+                dict(k_global_scale=torch.ones(1)), dict(v_global_scale=torch.ones(2, device="cuda"))]:
+        a = dict(q=q, cache=c, block_tables=tab, seq_lens=sl)
+        a.update(bad)
+        with pytest.raises(ValueError):
+            fq.attention_nvfp4(a.pop("q"), a.pop("cache"), a.pop("block_tables"), a.pop("seq_lens"), **a)
+    with pytest.raises(fq.Fp4Error):
+        fq.attention_nvfp4(q, c, tab, sl, sm_scale=0.0)
+    # nothing to do: no rows, no sequences, no pages
+    e = torch.empty(0, Hq, D, dtype=torch.bfloat16, device="cuda")
+    assert fq.attention_nvfp4(e, c, tab[:0], sl[:0]).shape == e.shape
+    assert fq.kv_append_nvfp4(c, k[:0], k[:0].clone(), slots[:0]) is None
+    out, lse = fq.attention_nvfp4(q, c, torch.empty(T, 0, dtype=torch.int32, device="cuda"), sl, return_lse=True)
+    assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
+
+
+def test_waits_that_run_out_are_reported():
+    """The debug build with waits cut to a microsecond: rows are NaN or right, the status
+    word says so, and the next call is as ever."""
+    fbuild.build(debug=True)
+    L = fq.debug_lib()
+    lens, cu, D, Hq = [900, 2500], [0, 200, 290], 128, 4
+    cache, tables = fill_sequences(lens, 1, D, 16, seed=4)
+    q = queries(290, Hq, D, "bf16", 2)
+    ref = okv.attention(q.double().numpy(), cache, tables, lens, cu, True, D ** -0.5)
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    cud = torch.tensor(cu, dtype=torch.int32, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    qd = q.cuda()
+
+    def call():
+        out, lse = fq.attention_nvfp4(qd, dev, tab, sl, cud, return_lse=True, status=status)
+        torch.cuda.synchronize()
+        return out.double().cpu().numpy(), lse.cpu().numpy()
+    try:
+        with fq.using_library(L):
+            for limit in (500, 3000, 20000):
+                assert L.fp4_debug_configure(limit, 0, 0, -1, -1, None) == 0
+                status.zero_()
+                out, lse = call()
+                nan = np.isnan(out).any(-1)
+                assert nan.any() == (fq.read_device_status(status) == fq.FP4_ERR_TIMEOUT)
+                assert np.array_equal(nan, np.isnan(lse))
+                assert np.all(np.abs(out - ref.out)[~nan] <= 0.02)
+                if limit == 500:
+                    assert nan.any()
+            assert L.fp4_debug_configure(2_000_000_000, 0, 0, -1, -1, None) == 0
+            status.zero_()
+            out, lse = call()
+            assert fq.read_device_status(status) == fq.FP4_OK
+            assert np.all(np.abs(out - ref.out) <= 0.02)
+    finally:
+        L.fp4_debug_configure(2_000_000_000, 0, 0, -1, -1, None)
+
+
 def test_debug_build_finds_no_access_out_of_bounds():
     fbuild.build(debug=True)
     L = fq.debug_lib()
@@ -542,6 +685,17 @@ def test_debug_build_finds_no_access_out_of_bounds():
                 test_varlen(lens, q_lens, True, 8, 2, 128, 16, "bf16")
                 test_varlen(lens, q_lens, False, 3, 3, 64, 48, "fp16")
             test_bad_pages_are_masked([1, 40, 150], 128)
+            test_many_rows_over_long_sequences([3000, 1500], [70, 130], True, 4, 1, 128, 16, "bf16")
+            test_rows_around_the_change_of_kernels(9, 7, 64)
+            # row limits that do not ascend, or lie outside, are held to the rows there are
+            c, tables = fill_sequences([100, 50, 70], 1, 64, 16, seed=1)
+            c = [torch.from_numpy(x).cuda() for x in c]
+            tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+            sl = torch.tensor([100, 50, 70], dtype=torch.int32, device="cuda")
+            for cu in ([0, 90, 20, 1000], [-5, 3, 2 ** 31 - 1, 7], [40, 30, 20, 10]):
+                for T in (12, 95):
+                    fq.attention_nvfp4(queries(T, 4, 64, "fp16", 1).cuda(), c, tab, sl,
+                                       torch.tensor(cu, dtype=torch.int32, device="cuda"))
             torch.cuda.synchronize()
             assert bad.item() == 0
             # with every extent one byte shorter the checks see the last accesses
