@@ -65,6 +65,11 @@ cudaError_t launch_prefill(const KvAttentionParams& p, int pdl, cudaStream_t str
     if (dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
     std::lock_guard<std::mutex> lock(mu);
     if (!done[dev]) {
+      // the warpgroups' register budgets must be covered by the launch's registers
+      cudaFuncAttributes fa;
+      e = cudaFuncGetAttributes(&fa, kv_prefill_kernel<T, D>);
+      if (e != cudaSuccess) return e;
+      if (fa.numRegs * kPreThreads < kPreRegs) return cudaErrorInvalidConfiguration;
       e = cudaFuncSetAttribute(kv_prefill_kernel<T, D>, cudaFuncAttributeMaxDynamicSharedMemorySize, S::kSmem);
       if (e != cudaSuccess) return e;
       done[dev] = true;

@@ -47,8 +47,10 @@ constexpr int kPreRows = 256;            // query rows of an item, two tiles of 
 constexpr int kPreKeys = 128;            // keys of a step
 constexpr int kPreThreads = 16 * 32;
 // Registers per thread of the three kinds of warpgroups: 2 x 128 x 160 + 128 x 128 +
-// 128 x 64 = 65536, what 512 threads of 128 are launched with.
-constexpr int kPreSoftmaxRegs = 160, kPreIssueRegs = 64;
+// 128 x 64 = 65536.  Together they may not pass what the CTA is launched with (512
+// threads of 128), or the increase would wait forever: the launch checks that.
+constexpr int kPreSoftmaxRegs = 160, kPreTileRegs = 128, kPreIssueRegs = 64;
+constexpr int kPreRegs = 256 * kPreSoftmaxRegs + 128 * kPreTileRegs + 128 * kPreIssueRegs;
 // A row's weights of one step are taken against the reference of the steps before;
 // only if their sum passes this is the maximum looked for and the reference moved to
 // kRefBelow below it (which leaves the sum at 128 * 2^6 at most).  Weights then stay
@@ -615,13 +617,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       const int s = j & 1;
       const bool more = j + 1 < steps;
       alive = mbar_wait_bounded(&bars[kBarVFull + s], (j >> 1) & 1, wait_limit) &&
-              (!more || mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit)) &&
               (j >= mine || mbar_wait_bounded(&bars[kBarP + tile], j & 1, wait_limit)) &&
               // the turns: tile 0 of step 0 has the first
               (j + tile == 0 || mbar_wait_bounded(&bars[kBarTurn + tile], (j + tile + 1) & 1, wait_limit));
       if (!alive) break;
       tc_fence_after_sync();
       if (j < mine) p_v(s, j == 0);
+      if (more) alive = mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit);
+      if (!alive) break;
+      tc_fence_after_sync();
       if (j + 1 < mine) {
         q_k(s ^ 1, true);
       } else {
