@@ -487,9 +487,10 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
                                           fp4q_stream_t stream);
 
 /* Bytes of workspace fp4_attention_nvfp4 needs for these sizes on the current
- * device (152 SMs taken when none is visible); 0 or more, -1 on bad arguments. */
+ * device (152 SMs taken when none is visible); max_keys = max_pages * page_size of its
+ * call.  0 or more (0: none, workspace may be NULL), -1 on bad arguments. */
 FP4Q_API int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
-                                               int64_t head_dim);
+                                               int64_t head_dim, int64_t max_keys);
 
 /*
  * fp4_read_device_status - synchronises `stream`, then copies the device

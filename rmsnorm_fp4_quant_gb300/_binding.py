@@ -143,7 +143,7 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_attention_nvfp4.argtypes = [vp, i64, cp, vp, i64, vp, vp, i64, i64, i64, ci,
                                       ctypes.c_float, ci, vp, vp, vp, i64, vp, ci, vp]
     L.fp4_attention_nvfp4.restype = ci
-    L.fp4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64]
+    L.fp4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
     L.fp4_attention_workspace_bytes.restype = i64
     L.fp4_debug_build.argtypes = []
     L.fp4_debug_build.restype = ci
@@ -273,9 +273,9 @@ def fp4_attention_nvfp4(q_ptr: int, q_stride: int, cache: KVCacheStruct, block_t
                                      status_ptr or None, pdl, stream or None)
 
 
-def fp4_attention_workspace_bytes(B: int, T: int, Hq: int, num_kv_heads: int,
-                                  head_dim: int) -> int:
-    return lib().fp4_attention_workspace_bytes(B, T, Hq, num_kv_heads, head_dim)
+def fp4_attention_workspace_bytes(B: int, T: int, Hq: int, num_kv_heads: int, head_dim: int,
+                                  max_keys: int) -> int:
+    return lib().fp4_attention_workspace_bytes(B, T, Hq, num_kv_heads, head_dim, max_keys)
 
 
 def fp4_read_device_status(status_ptr: int, stream: int) -> int:
@@ -696,8 +696,8 @@ def _on(stream):
 
 
 @functools.lru_cache(maxsize=256)
-def _attention_workspace(L, dev, B, T, hq, heads, dim) -> int:
-    return max(L.fp4_attention_workspace_bytes(B, T, hq, heads, dim), 0)
+def _attention_workspace(L, dev, B, T, hq, heads, dim, keys) -> int:
+    return max(L.fp4_attention_workspace_bytes(B, T, hq, heads, dim, keys), 0)
 
 
 def _kv_dtype(torch, dtype) -> int:
@@ -833,21 +833,24 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     elif T != B:
         raise ValueError("q must have one row per sequence without cu_seqlens_q")
     L = lib()
+    ws = 0
     if workspace is None:
-        size = _attention_workspace(L, dev, B, T, hq, heads, dim)
+        size = _attention_workspace(L, dev, B, T, hq, heads, dim, max_pages * struct.page_size)
     else:
         _check_cuda(workspace, "workspace")
         _same_device(dev, "workspace", workspace)
         size = workspace.numel() * workspace.element_size()
-    if out is None or workspace is None or (return_lse and lse is None):
+        ws = workspace.data_ptr()
+    if out is None or (size and not ws) or (return_lse and lse is None):
         dv = q.device
         with _on(stream):
             if out is None:
                 out = torch.empty(shape, dtype=dtype, device=dv)
             if return_lse and lse is None:
                 lse = torch.empty((T, hq), dtype=torch.float32, device=dv)
-            if workspace is None:
+            if size and not ws:
                 workspace = torch.empty(size, dtype=torch.uint8, device=dv)
+                ws = workspace.data_ptr()
     if status is not None:
         _same_device(dev, "status", status)
     st = L.fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
@@ -856,7 +859,7 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
                                1 if causal else 0, _dense_ptr(out, "out", dev, dtype, shape),
                                _dense_ptr(lse, "lse", dev, torch.float32, (T, hq))
                                if lse is not None else 0,
-                               workspace.data_ptr(), size,
+                               ws, size,
                                _status_ptr(status), 1 if pdl else 0, _kv_stream(torch, stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_attention_nvfp4")

@@ -183,12 +183,12 @@ fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int64_t* slo
 }
 
 int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
-                                      int64_t head_dim) {
-  if (B < 0 || T < 0 || Hq <= 0 || num_kv_heads <= 0 || Hq % num_kv_heads || Hq > kMaxHeads ||
+                                      int64_t head_dim, int64_t max_keys) {
+  if (B < 0 || T < 0 || max_keys < 0 || Hq <= 0 || num_kv_heads <= 0 || Hq % num_kv_heads || Hq > kMaxHeads ||
       (head_dim != 64 && head_dim != 128))
     return -1;
   return kv_attention_workspace(sm_count_current_device(), B, T, static_cast<int>(Hq),
-                                static_cast<int>(num_kv_heads), static_cast<int>(head_dim));
+                                static_cast<int>(num_kv_heads), static_cast<int>(head_dim), max_keys);
 }
 
 fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_cache_t* cache,
@@ -221,7 +221,7 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
       !abi_aligned(block_tables, 4) || !abi_aligned(seq_lens, 4) || !abi_aligned(cu_seqlens_q, 4) ||
       !abi_aligned(workspace, 16) || !abi_aligned(status, 4))
     return FP4_ERR_MISALIGNED;
-  const int64_t need = fp4_attention_workspace_bytes(B, T, Hq, Hkv, D);
+  const int64_t need = fp4_attention_workspace_bytes(B, T, Hq, Hkv, D, max_pages * cache->page_size);
   if (workspace_bytes < need || (need && !workspace)) return FP4_ERR_INVALID_ARG;
   const CacheBuffers cbuf = buffers(*cache);
   const Rows writes[] = {flat(out, T * Hq * D * 2), flat(lse, T * Hq * 4),

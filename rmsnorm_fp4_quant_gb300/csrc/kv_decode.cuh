@@ -37,6 +37,7 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecUnit = 16 * kDecWarps;       // keys of a unit
 constexpr int kDecStages = 4;
+constexpr int kDecCluster = 8;                 // CTAs of a cluster that share an item
 constexpr int kDecMinUnits = 2;                // a CTA's share is at least this long
 // What an item costs besides its keys (its queries, the ring's first tiles, the
 // join), in units: the CTAs' shares are even in these too.  Without it the one CTA
@@ -51,7 +52,9 @@ struct DecodeShape {
   static constexpr int kMergeStride = D + 8;   // floats per row in the merge buffer
   static constexpr int kRing = kDecWarps * kDecStages * kTile;
   static constexpr int kMerge = kDecWarps * kRows * kMergeStride * 4;
+  static constexpr int kResult = (kRows * D + 4 * kRows) * 4;   // what a cluster's CTAs read of each other
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
+  static constexpr int kSmemCluster = kRing > kMerge + kResult ? kRing : kMerge + kResult;
   static constexpr int kCtas = NT == 1 ? 4 : 3;   // resident per SM
   // Tiles a warp takes per step.  Two share the loop's, the addresses' and the
   // maximum's instructions and fill each other's waits; 16 rows have no registers for it.
@@ -124,6 +127,39 @@ template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
 
 template <int V> struct Const { static constexpr int value = V; };
 
+// One row's result in 8 channels: o relative to 2^ref, l the sum of weights.
+template <typename T, int D>
+__device__ __forceinline__ void decode_write(const KvAttentionParams& p, const KvSeq& s, int kvh, int row, int d0,
+                                             const float (&o)[8], float ref, float l, float vgs) {
+  const int tok = row / p.group;
+  const int64_t at = static_cast<int64_t>(s.q0 + tok) * p.Hq + kvh * p.group + row - tok * p.group;
+  const float inv = l > 0.0f ? 1.0f / (l * vgs) : l == 0.0f ? 0.0f : l;   // NaN stays
+  T* dst = static_cast<T*>(p.out) + at * D + d0;
+  if (FP4Q_IN_RANGE(p, dst, 16, p.out, 2LL * p.T * p.Hq * D))
+    *reinterpret_cast<uint4*>(dst) = make_uint4(
+        Pair<T>::from_f32(o[0] * inv, o[1] * inv), Pair<T>::from_f32(o[2] * inv, o[3] * inv),
+        Pair<T>::from_f32(o[4] * inv, o[5] * inv), Pair<T>::from_f32(o[6] * inv, o[7] * inv));
+  if (d0 == 0 && p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * p.T * p.Hq))
+    p.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (ref + log2f(l));
+}
+
+// The sequence of row slot rs, and which of its row tiles that is: the last sequence
+// whose slots begin at or before rs (the tile may lie behind the sequence's last).
+template <int ROWS>
+__device__ __forceinline__ int decode_sequence(const KvAttentionParams& p, int64_t rs, int64_t& tile) {
+  auto slots_from = [&](int b) {
+    const int64_t q0 = p.cu ? min(max(p.cu[b], 0), static_cast<int>(p.T)) : b;
+    return q0 * p.group / ROWS + b;
+  };
+  int b = 0, hi = p.B - 1;
+  while (b < hi) {
+    const int mid = (b + hi + 1) / 2;
+    if (slots_from(mid) <= rs) b = mid; else hi = mid - 1;
+  }
+  tile = rs - slots_from(b);
+  return b;
+}
+
 // What one CTA's walk over the units needs to know of the sequence it is in.
 struct DecodeWalk {
   int b;             // sequence
@@ -144,7 +180,10 @@ __device__ __forceinline__ int64_t decode_units(const KvAttentionParams& p, int 
   return static_cast<int64_t>(w.cost) * w.row_tiles * p.c.heads;
 }
 
-template <typename T, int D, int NT>
+// CLUSTER: instead, an item's keys go to the 8 CTAs of a cluster, which read each
+// other's results from shared memory: no workspace and no second kernel, for few
+// items of moderate length (kv_attention.cu chooses).
+template <typename T, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, NT>::kCtas)
 kv_decode_kernel(const KvAttentionParams p) {
   using S = DecodeShape<D, NT>;
@@ -165,48 +204,61 @@ kv_decode_kernel(const KvAttentionParams p) {
   griddep_wait();
   griddep_launch_dependents();
 
-  // total units, and the sequence that holds this CTA's first one: each thread
-  // sums a run of consecutive sequences
-  const int run = (p.B + kDecThreads - 1) / kDecThreads;
-  const int b_lo = min(tid * run, p.B), b_hi = min(b_lo + run, p.B);
-  int64_t mine = 0;
-  DecodeWalk w;
-  for (int b = b_lo; b < b_hi; ++b) mine += decode_units<ROWS>(p, b, w);
-  int64_t incl = mine;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const int64_t up = __shfl_up_sync(kFullMask, incl, o);
-    if (lane >= o) incl += up;
-  }
-  if (lane == 31) scan_tot[warp] = incl;
-  __syncthreads();
-  int64_t before = incl - mine, total = 0;
-#pragma unroll
-  for (int i = 0; i < kDecThreads / 32; ++i) {
-    if (i < warp) before += scan_tot[i];
-    total += scan_tot[i];
-  }
-  int64_t G = (total + kDecMinUnits - 1) / kDecMinUnits;
-  if (G > static_cast<int64_t>(gridDim.x)) G = gridDim.x;
   const int64_t cta = blockIdx.x;
-  if (cta >= G) return;
-  int64_t u = cta * total / G;
-  const int64_t u_end = (cta + 1) * total / G;
-  if (u >= before && u < before + mine) {       // exactly one thread
-    int64_t base = before;
-    int b = b_lo;
-    for (;;) {
-      const int64_t n = decode_units<ROWS>(p, b, w);
-      if (u < base + n) break;
-      base += n;
-      ++b;
+  DecodeWalk w;
+  int64_t total = 0, G = 0, units = 0, u = 0, u_end = 1;
+  int kvh = 0, rt = 0;                           // key/value head, tile of rows
+  const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+  if constexpr (CLUSTER) {
+    const int64_t slot = cta / kDecCluster;
+    kvh = static_cast<int>(slot % p.c.heads);
+    int64_t tile;
+    const int b = decode_sequence<ROWS>(p, slot / p.c.heads, tile);
+    decode_units<ROWS>(p, b, w);
+    if (tile < 0 || tile >= w.row_tiles) return;   // the whole cluster
+    rt = static_cast<int>(tile);
+  } else {
+    // total units, and the sequence that holds this CTA's first one: each thread
+    // sums a run of consecutive sequences
+    const int run = (p.B + kDecThreads - 1) / kDecThreads;
+    const int b_lo = min(tid * run, p.B), b_hi = min(b_lo + run, p.B);
+    int64_t mine = 0;
+    for (int b = b_lo; b < b_hi; ++b) mine += decode_units<ROWS>(p, b, w);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int64_t up = __shfl_up_sync(kFullMask, incl, o);
+      if (lane >= o) incl += up;
     }
-    start_b = b;
-    start_base = base;
+    if (lane == 31) scan_tot[warp] = incl;
+    __syncthreads();
+    int64_t before = incl - mine;
+#pragma unroll
+    for (int i = 0; i < kDecThreads / 32; ++i) {
+      if (i < warp) before += scan_tot[i];
+      total += scan_tot[i];
+    }
+    G = (total + kDecMinUnits - 1) / kDecMinUnits;
+    if (G > static_cast<int64_t>(gridDim.x)) G = gridDim.x;
+    if (cta >= G) return;
+    u = cta * total / G;
+    u_end = (cta + 1) * total / G;
+    if (u >= before && u < before + mine) {       // exactly one thread
+      int64_t base = before;
+      int b = b_lo;
+      for (;;) {
+        const int64_t n = decode_units<ROWS>(p, b, w);
+        if (u < base + n) break;
+        base += n;
+        ++b;
+      }
+      start_b = b;
+      start_base = base;
+    }
+    __syncthreads();
+    units = decode_units<ROWS>(p, start_b, w);
+    w.base = start_base;
   }
-  __syncthreads();
-  int64_t units = decode_units<ROWS>(p, start_b, w);
-  w.base = start_base;
 
   const uint32_t ring = smem_addr(smem) + warp * kDecStages * S::kTile;   // this warp's
   const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
@@ -238,18 +290,26 @@ kv_decode_kernel(const KvAttentionParams p) {
     v_src[i] = ring + S::kV + v_place<D>(4 * t + i, VW * g / 4) + (VW * g % 4) * 4;
 
   while (u < u_end) {
-    while (u >= w.base + units) {               // the next sequence that has units
-      w.base += units;
-      units = decode_units<ROWS>(p, w.b + 1, w);
+    int64_t item_base = 0;
+    int tile0, n_units;
+    if constexpr (CLUSTER) {
+      tile0 = w.tiles * rank / kDecCluster;
+      n_units = w.tiles * (rank + 1) / kDecCluster - tile0;
+      u = u_end;                                // one item
+    } else {
+      while (u >= w.base + units) {             // the next sequence that has units
+        w.base += units;
+        units = decode_units<ROWS>(p, w.b + 1, w);
+      }
+      const int item = static_cast<int>((u - w.base) / w.cost);
+      item_base = w.base + static_cast<int64_t>(item) * w.cost;
+      kvh = item / w.row_tiles;
+      rt = item - kvh * w.row_tiles;
+      tile0 = max(0, static_cast<int>(u - item_base) - kDecItemCost);
+      n_units = static_cast<int>(min(static_cast<int64_t>(w.cost), u_end - item_base)) - kDecItemCost - tile0;
+      u = item_base + w.cost;                   // the next item, or beyond this share
+      if (n_units <= 0) continue;               // the share ends in the item's own cost
     }
-    const int item = static_cast<int>((u - w.base) / w.cost);
-    const int64_t item_base = w.base + static_cast<int64_t>(item) * w.cost;
-    const int kvh = item / w.row_tiles, rt = item - kvh * w.row_tiles;
-    const int tile0 = max(0, static_cast<int>(u - item_base) - kDecItemCost);
-    const int tile1 = static_cast<int>(min(static_cast<int64_t>(w.cost), u_end - item_base)) - kDecItemCost;
-    u = item_base + w.cost;                     // the next item, or beyond this share
-    const int n_units = tile1 - tile0;
-    if (n_units <= 0) continue;                 // the share ends in the item's own cost
     const int rows = w.s.n_q * p.group;         // of the whole sequence
     const int r0 = rt * ROWS;
 
@@ -587,6 +647,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     // a part that begins the item is this CTA's last, one that does not its first
     float* part = p.ws + (2 * cta + (tile0 == 0 ? 1 : 0)) * S::kPart;
     const float* m0 = reinterpret_cast<const float*>(smem);
+    float* c_out = reinterpret_cast<float*>(smem + S::kMerge);   // CLUSTER: this CTA's results
     for (int x = tid; x < ROWS * (D / 8); x += kDecThreads) {
       const int r = x / (D / 8), d0 = (x % (D / 8)) * 8;
       float top = merge_r[0][r];
@@ -612,17 +673,13 @@ kv_decode_kernel(const KvAttentionParams p) {
       }
       const int row = r0 + r;
       if (row >= rows) continue;
-      if (whole_item) {
-        const int tok = row / p.group;
-        const int64_t at = static_cast<int64_t>(w.s.q0 + tok) * p.Hq + kvh * p.group + row - tok * p.group;
-        const float inv = l > 0.0f ? 1.0f / (l * vgs) : l == 0.0f ? 0.0f : l;   // NaN stays
-        T* dst = static_cast<T*>(p.out) + at * D + d0;
-        if (FP4Q_IN_RANGE(p, dst, 16, p.out, 2LL * p.T * p.Hq * D))
-          *reinterpret_cast<uint4*>(dst) = make_uint4(
-              Pair<T>::from_f32(o[0] * inv, o[1] * inv), Pair<T>::from_f32(o[2] * inv, o[3] * inv),
-              Pair<T>::from_f32(o[4] * inv, o[5] * inv), Pair<T>::from_f32(o[6] * inv, o[7] * inv));
-        if (d0 == 0 && p.lse && FP4Q_IN_RANGE(p, p.lse + at, 4, p.lse, 4LL * p.T * p.Hq))
-          p.lse[at] = l == 0.0f ? -INFINITY : kLn2 * (top + log2f(l));
+      if (CLUSTER) {
+        float* co = c_out + r * D + d0;
+        *reinterpret_cast<float4*>(co) = make_float4(o[0], o[1], o[2], o[3]);
+        *reinterpret_cast<float4*>(co + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        if (d0 == 0) *reinterpret_cast<float4*>(c_out + ROWS * D + 4 * r) = make_float4(top, l, 0.0f, 0.0f);
+      } else if (whole_item) {
+        decode_write<T, D>(p, w.s, kvh, row, d0, o, top, l, vgs);
       } else {
         float4* po = reinterpret_cast<float4*>(part + r * D + d0);
         if (FP4Q_IN_RANGE(p, po, 32, p.ws, p.ws_bytes)) {
@@ -633,6 +690,42 @@ kv_decode_kernel(const KvAttentionParams p) {
         if (d0 == 0 && FP4Q_IN_RANGE(p, rl, 8, p.ws, p.ws_bytes))
           *reinterpret_cast<float2*>(rl) = make_float2(top, l);
       }
+    }
+    if constexpr (CLUSTER) {
+      cluster_arrive_release();
+      cluster_wait_acquire();                    // every CTA's results are there
+      const uint32_t mine = smem_addr(c_out);
+      for (int x = tid * kDecCluster + rank; x < ROWS * (D / 8); x += kDecThreads * kDecCluster) {
+        const int r = x / (D / 8), d0 = (x % (D / 8)) * 8;
+        if (r0 + r >= rows) continue;
+        float4 rl[kDecCluster];
+        float top = kRefStart, l = 0.0f;
+        float o[8] = {};
+#pragma unroll
+        for (int i = 0; i < kDecCluster; ++i) {
+          rl[i] = ld_peer_f32x4(peer_smem_addr(mine + (ROWS * D + 4 * r) * 4, i));
+          top = fmaxf(top, rl[i].x);
+        }
+#pragma unroll
+        for (int i = 0; i < kDecCluster; ++i) {
+          const uint32_t peer = peer_smem_addr(mine + (r * D + d0) * 4, i);
+          const float4 y = ld_peer_f32x4(peer), z = ld_peer_f32x4(peer + 16);
+          const float f = ex2(rl[i].x - top);
+          l += rl[i].y * f;
+          o[0] += y.x * f;
+          o[1] += y.y * f;
+          o[2] += y.z * f;
+          o[3] += y.w * f;
+          o[4] += z.x * f;
+          o[5] += z.y * f;
+          o[6] += z.z * f;
+          o[7] += z.w * f;
+        }
+        decode_write<T, D>(p, w.s, kvh, r0 + r, d0, o, top, l, vgs);
+      }
+      cluster_arrive_release();
+      cluster_wait_acquire();                    // no CTA leaves while another reads from it
+      return;
     }
     if (tid == 0 && tile0 == 0) {
       // where the joining kernel finds the item's parts
@@ -668,17 +761,8 @@ __global__ void __launch_bounds__(kJoinMost) kv_decode_join_kernel(const KvAtten
   const int64_t rs = slot / p.c.heads;
   griddep_wait();
   griddep_launch_dependents();
-  // the last sequence whose slots begin at or before rs
-  auto slots_from = [&](int b) {
-    const int64_t q0 = p.cu ? min(max(p.cu[b], 0), static_cast<int>(p.T)) : b;
-    return q0 * p.group / ROWS + b;
-  };
-  int b = 0, hi = p.B - 1;
-  while (b < hi) {
-    const int mid = (b + hi + 1) / 2;
-    if (slots_from(mid) <= rs) b = mid; else hi = mid - 1;
-  }
-  const int64_t rt = rs - slots_from(b);
+  int64_t rt;
+  const int b = decode_sequence<ROWS>(p, rs, rt);
   const KvSeq s = kv_sequence(p, b);
   const int rows = s.n_q * p.group;
   if (rt < 0 || rt * ROWS + r >= rows) return;

@@ -83,6 +83,7 @@ struct KvAttentionParams {
 cudaError_t launch_kv_append(int dtype, const KvAppendParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_gather(int dtype, const KvGatherParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream);
-int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads, int D);
+// Bytes for sequences of at most `keys` keys.
+int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys);
 
 }  // namespace fp4q

@@ -127,14 +127,19 @@ def test_attention_refusals(kw, status):
 
 def test_workspace_sizes():
     f = fq.fp4_attention_workspace_bytes
-    assert f(4, 4, 8, 2, 128) >= 0
-    for bad in [(-1, 4, 8, 2, 128), (4, -1, 8, 2, 128), (4, 4, 0, 2, 128), (4, 4, 8, 3, 128),
-                (4, 4, 8, 2, 96), (4, 4, 8, 0, 128)]:
+    for bad in [(-1, 4, 8, 2, 128, 512), (4, -1, 8, 2, 128, 512), (4, 4, 0, 2, 128, 512), (4, 4, 8, 3, 128, 512),
+                (4, 4, 8, 2, 96, 512), (4, 4, 8, 0, 128, 512), (4, 4, 8, 2, 128, -1)]:
         assert f(*bad) == -1
-    need = f(5, 5, 4, 2, 128)
-    if need:
-        assert attention(wsb=need - 1) == 1 and attention(ws=0) == 1 and attention(ws=at(11) + 8) == 3
-        assert attention(ws=at(5)) == 1 and attention(ws=at(0)) == 1
+    assert f(0, 0, 8, 2, 128, 512) == 0
+    assert f(1, 1, 8, 2, 128, 1024) == 0                 # a cluster per item
+    # tables of 2^20 keys: parts of CTAs; 100 x 100 rows over them: ranges of keys
+    for a, kw in (((5, 5, 4, 2, 128), {}), ((5, 500, 4, 2, 128), dict(T=500, cu=at(12)))):
+        kw["pages"] = 65536
+        need = f(*a, 1 << 20)
+        assert need > 0
+        assert attention(wsb=need - 1, **kw) == 1 and attention(ws=0, **kw) == 1
+        assert attention(ws=at(11) + 8, **kw) == 3
+        assert attention(ws=at(5), **kw) == 1 and attention(ws=at(0), **kw) == 1
 
 
 def test_the_struct_matches_the_header():

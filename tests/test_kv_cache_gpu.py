@@ -577,7 +577,9 @@ def test_one_workspace_for_calls_in_a_row():
     tab = torch.from_numpy(tables.astype(np.int32)).cuda()
     sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
     cu = torch.tensor([0, 40, 120], dtype=torch.int32, device="cuda")
-    need = max(fq.fp4_attention_workspace_bytes(2, 2, Hq, Hkv, D), fq.fp4_attention_workspace_bytes(2, 120, Hq, Hkv, D))
+    keys = tab.shape[1] * 16
+    need = max(fq.fp4_attention_workspace_bytes(2, T, Hq, Hkv, D, keys) for T in (2, 120))
+    assert need > 0
     ws = torch.full((need,), 255, dtype=torch.uint8, device="cuda")
     qs = [queries(2 if i % 2 else 120, Hq, D, "bf16", i).cuda() for i in range(6)]
     torch.cuda.synchronize()
