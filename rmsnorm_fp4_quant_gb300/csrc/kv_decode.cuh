@@ -55,10 +55,14 @@ struct DecodeShape {
   static constexpr int kResult = (kRows * D + 4 * kRows) * 4;   // what a cluster's CTAs read of each other
   static constexpr int kSmem = kRing > kMerge ? kRing : kMerge;
   static constexpr int kSmemCluster = kRing > kMerge + kResult ? kRing : kMerge + kResult;
-  static constexpr int kCtas = NT == 1 ? 4 : 3;   // resident per SM
-  // Tiles a warp takes per step.  Two share the loop's, the addresses' and the
-  // maximum's instructions and fill each other's waits; 16 rows have no registers for it.
-  static constexpr int kStep = NT == 1 ? 2 : 1;
+  // CTAs per SM, and with them registers per thread (128, 168 or 255), and tiles a warp
+  // takes per step.  Two tiles share the loop's, the addresses' and the maximum's
+  // instructions and fill each other's waits.  Registers count for more than warps
+  // with 128 channels: 128 sequences of 12-16 K tokens, 8 rows, 382 us with four CTAs,
+  // 358 with three, 405 with two; 16 rows 63 us with three, 58 with two.  With 64
+  // channels it is the other way: 8 rows 68 us with four, 74 with three, 76 with five.
+  static constexpr int kCtas = D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);
+  static constexpr int kStep = NT == 1 || D == 128 ? 2 : 1;
   static constexpr int kPart = kRows * (D + 2);   // floats of one part in the workspace
 };
 
