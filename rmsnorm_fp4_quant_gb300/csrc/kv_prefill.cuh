@@ -617,15 +617,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       const int s = j & 1;
       const bool more = j + 1 < steps;
       alive = mbar_wait_bounded(&bars[kBarVFull + s], (j >> 1) & 1, wait_limit) &&
+              (!more || mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit)) &&
               (j >= mine || mbar_wait_bounded(&bars[kBarP + tile], j & 1, wait_limit)) &&
               // the turns: tile 0 of step 0 has the first
               (j + tile == 0 || mbar_wait_bounded(&bars[kBarTurn + tile], (j + tile + 1) & 1, wait_limit));
       if (!alive) break;
       tc_fence_after_sync();
       if (j < mine) p_v(s, j == 0);
-      if (more) alive = mbar_wait_bounded(&bars[kBarKFull + (s ^ 1)], ((j + 1) >> 1) & 1, wait_limit);
-      if (!alive) break;
-      tc_fence_after_sync();
       if (j + 1 < mine) {
         q_k(s ^ 1, true);
       } else {

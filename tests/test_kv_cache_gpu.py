@@ -334,6 +334,16 @@ def test_many_rows_over_long_sequences(lens, q_lens, causal, Hq, Hkv, D, page, d
     check_attention(queries(cu[-1] + 2, Hq, D, dtype, 7), cache, tables, lens, cu, causal, dtype)
 
 
+@pytest.mark.parametrize("causal", [True, False])
+@pytest.mark.parametrize("D", [64, 128])
+def test_many_rows_of_empty_and_short_sequences(causal, D):
+    """Hundreds of rows per sequence, over no keys, fewer keys than rows, one key more than a step."""
+    lens, q_lens = [0, 5, 129, 1], [140, 260, 130, 257]
+    cu = np.cumsum([0] + q_lens).tolist()
+    cache, tables = fill_sequences(lens, 2, D, 16, seed=9)
+    check_attention(queries(cu[-1], 4, D, "bf16", 7), cache, tables, lens, cu, causal, "bf16")
+
+
 @pytest.mark.parametrize("group,q_len", [(1, 63), (1, 64), (1, 65), (3, 21), (3, 22), (64, 1), (80, 1), (9, 7), (128, 3)])
 @pytest.mark.parametrize("D", [64, 128])
 def test_rows_around_the_change_of_kernels(group, q_len, D):
