@@ -427,30 +427,39 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       }
       tc_fence_after_sync();
       const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu;
+      // the weights against the reference there is; where a row's sum passes the limit
+      // (rare after the first step, which begins with its maximum), once more
       uint32_t h[64];
-      float step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, fac, ref, h)
-                            : prefill_weights<false>(ts, key0, lim, have, fac, ref, h);
-      const bool moved = !(step_sum <= kPreMostSum);
-      if (__any_sync(kFullMask, moved)) {          // rare after the first steps
-        const float m = prefill_maximum(ts, key0, lim, have, edge);
-        float f = 1.0f;
-        if (moved && m > -INFINITY) {
-          const float to_ref = fmaxf(ref, m * fac - kRefBelow);
-          f = ex2(ref - to_ref);
-          ref = to_ref;
-          sum *= f;
-        }
-        if (j > 0) {
+      float step_sum;
+      bool moved = j == 0, last = j == 0;
 #pragma unroll 1
-          for (int c = 0; c < D / 32; ++c) {
-            uint32_t x[32];
-            tmem_load_32cols(to + 32 * c, x);
+      for (;;) {
+        if (last) {
+          const float m = prefill_maximum(ts, key0, lim, have, edge);
+          float f = 1.0f;
+          if (moved && m > -INFINITY) {
+            const float to_ref = fmaxf(ref, m * fac - kRefBelow);
+            f = ex2(ref - to_ref);
+            ref = to_ref;
+            sum *= f;
+          }
+          if (j > 0) {
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t x[32];
+              tmem_load_32cols(to + 32 * c, x);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-            tmem_store_32cols(to + 32 * c, x);
+              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
+              tmem_store_32cols(to + 32 * c, x);
+            }
           }
         }
-        step_sum = prefill_weights<true>(ts, key0, edge ? lim : INT32_MAX, have, fac, ref, h);
+        step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, fac, ref, h)
+                        : prefill_weights<false>(ts, key0, lim, have, fac, ref, h);
+        if (last) break;
+        moved = !(step_sum <= kPreMostSum);
+        if (!__any_sync(kFullMask, moved)) break;
+        last = true;
       }
       sum += step_sum;
 #pragma unroll
