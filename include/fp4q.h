@@ -474,6 +474,7 @@ FP4Q_API fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int
  *                   contents; two calls that may run at the same time need one each.
  *   status, pdl     as in fp4_add_rmsnorm_quant_ex.
  * Lengths and tables are read on the device, so a captured call follows them.
+ * Rows that a kernel gave up on (a bounded wait ran out: status) are NaN, lse too.
  * Accumulators, maxima and sums are fp32.  Nothing that is written may overlap
  * anything else the call reads or writes.
  */

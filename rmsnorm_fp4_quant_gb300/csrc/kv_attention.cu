@@ -15,15 +15,23 @@ namespace {
 // 8 rows 46 us, 16 rows 63 us; two tiles of 8 for 16 rows would read every key twice).
 int decode_tiles(int64_t B, int64_t T, int group) { return T * group <= 8 * B ? 1 : 2; }
 
-// Few items of moderate length (by the table's width: the lengths are on the device)
-// go to one cluster each: every CTA of every cluster runs at once, and has at most 16
-// units of keys.  One sequence of 1000 tokens, 2 key/value heads: 5.8 us on the device
-// and one launch, against 8.6 us and two.
-constexpr int kClusterKeys = kDecCluster * kDecUnit * 16;
+// CTAs of the cluster that takes one item each, 0 where the keys are to be split evenly
+// over all CTAs instead (by the table's width: the lengths are on the device).  A CTA
+// has at most 16 units of keys then; an item gets more CTAs than that asks for as long
+// as all run at once and have a unit each, and where even the fewest do not run at
+// once it has to be one each (short sequences, which the hardware then deals out).
+// One sequence of 1000 tokens, 2 key/value heads: 5.8 us on the device and one launch,
+// against 8.6 us and two.
+constexpr int kClusterKeys = kDecUnit * 16;
 template <int D, int NT>
-bool use_cluster(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys) {
-  constexpr int kCtas = DecodeShape<D, NT>::kCtas;
-  return keys <= kClusterKeys && decode_row_slots(B, T, group, 8 * NT) * heads * kDecCluster <= sms * kCtas;
+int cluster_of(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys) {
+  const int64_t items = decode_row_slots(B, T, group, 8 * NT) * heads;
+  const int64_t at_once = static_cast<int64_t>(sms) * DecodeShape<D, NT>::kCtas;
+  int64_t c = 1;
+  while (c < kDecCluster && keys > c * kClusterKeys) c *= 2;
+  if (keys > c * kClusterKeys || (c > 1 && items * c > at_once) || items * c > INT32_MAX) return 0;
+  while (c < kDecCluster && items * c * 2 <= at_once && keys >= c * 2 * kDecUnit) c *= 2;
+  return static_cast<int>(c);
 }
 
 template <typename T, int D, int NT>
@@ -34,7 +42,8 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
   const int64_t slots = decode_row_slots(p.B, p.T, p.group, S::kRows) * p.c.heads;
   cudaLaunchAttribute attr[2];
   attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = kDecCluster;
+  const int cluster = cluster_of<D, NT>(sms, p.B, p.T, p.group, p.c.heads, p.max_pages * p.c.page_size);
+  attr[0].val.clusterDim.x = static_cast<unsigned>(cluster);
   attr[0].val.clusterDim.y = 1;
   attr[0].val.clusterDim.z = 1;
   attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -42,8 +51,8 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
   cudaLaunchConfig_t cfg = {};
   cfg.blockDim = dim3(kDecThreads);
   cfg.stream = stream;
-  if (use_cluster<D, NT>(sms, p.B, p.T, p.group, p.c.heads, p.max_pages * p.c.page_size)) {
-    cfg.gridDim = dim3(static_cast<unsigned>(slots * kDecCluster));
+  if (cluster) {
+    cfg.gridDim = dim3(static_cast<unsigned>(slots * cluster));
     cfg.dynamicSmemBytes = S::kSmemCluster;
     cfg.attrs = attr;
     cfg.numAttrs = pdl ? 2 : 1;
@@ -139,7 +148,7 @@ cudaError_t launch_type(const KvAttentionParams& p, int pdl, cudaStream_t stream
 template <int D, int NT>
 int64_t decode_workspace(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys) {
   using S = DecodeShape<D, NT>;
-  if (use_cluster<D, NT>(sms, B, T, group, heads, keys)) return 0;
+  if (cluster_of<D, NT>(sms, B, T, group, heads, keys)) return 0;
   return 4LL * (2LL * sms * S::kCtas * S::kPart) + 8LL * decode_row_slots(B, T, group, S::kRows) * heads;
 }
 

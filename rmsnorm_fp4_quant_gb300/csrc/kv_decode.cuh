@@ -37,7 +37,7 @@ constexpr int kDecWarps = 4;
 constexpr int kDecThreads = 32 * kDecWarps;
 constexpr int kDecUnit = 16 * kDecWarps;       // keys of a unit
 constexpr int kDecStages = 4;
-constexpr int kDecCluster = 8;                 // CTAs of a cluster that share an item
+constexpr int kDecCluster = 8;                 // CTAs of a cluster that share an item, at most
 constexpr int kDecMinUnits = 2;                // a CTA's share is at least this long
 // What an item costs besides its keys (its queries, the ring's first tiles, the
 // join), in units: the CTAs' shares are even in these too.  Without it the one CTA
@@ -184,9 +184,9 @@ __device__ __forceinline__ int64_t decode_units(const KvAttentionParams& p, int 
   return static_cast<int64_t>(w.cost) * w.row_tiles * p.c.heads;
 }
 
-// CLUSTER: instead, an item's keys go to the 8 CTAs of a cluster, which read each
-// other's results from shared memory: no workspace and no second kernel, for few
-// items of moderate length (kv_attention.cu chooses).
+// CLUSTER: instead, an item's keys go to one CTA or to the 2 to 8 of a cluster, which
+// read each other's results from shared memory: no workspace and no second kernel, for
+// short sequences and for few of moderate length (kv_attention.cu chooses).
 template <typename T, int D, int NT, bool CLUSTER>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, NT>::kCtas)
 kv_decode_kernel(const KvAttentionParams p) {
@@ -213,8 +213,9 @@ kv_decode_kernel(const KvAttentionParams p) {
   int64_t total = 0, G = 0, units = 0, u = 0, u_end = 1;
   int kvh = 0, rt = 0;                           // key/value head, tile of rows
   const int rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
+  const int peers = CLUSTER ? static_cast<int>(cluster_nctarank()) : 1;
   if constexpr (CLUSTER) {
-    const int64_t slot = cta / kDecCluster;
+    const int64_t slot = cta / peers;
     kvh = static_cast<int>(slot % p.c.heads);
     int64_t tile;
     const int b = decode_sequence<ROWS>(p, slot / p.c.heads, tile);
@@ -297,8 +298,8 @@ kv_decode_kernel(const KvAttentionParams p) {
     int64_t item_base = 0;
     int tile0, n_units;
     if constexpr (CLUSTER) {
-      tile0 = w.tiles * rank / kDecCluster;
-      n_units = w.tiles * (rank + 1) / kDecCluster - tile0;
+      tile0 = w.tiles * rank / peers;
+      n_units = w.tiles * (rank + 1) / peers - tile0;
       u = u_end;                                // one item
     } else {
       while (u >= w.base + units) {             // the next sequence that has units
@@ -677,12 +678,12 @@ kv_decode_kernel(const KvAttentionParams p) {
       }
       const int row = r0 + r;
       if (row >= rows) continue;
-      if (CLUSTER) {
+      if (CLUSTER && peers > 1) {
         float* co = c_out + r * D + d0;
         *reinterpret_cast<float4*>(co) = make_float4(o[0], o[1], o[2], o[3]);
         *reinterpret_cast<float4*>(co + 4) = make_float4(o[4], o[5], o[6], o[7]);
         if (d0 == 0) *reinterpret_cast<float4*>(c_out + ROWS * D + 4 * r) = make_float4(top, l, 0.0f, 0.0f);
-      } else if (whole_item) {
+      } else if (CLUSTER || whole_item) {
         decode_write<T, D>(p, w.s, kvh, row, d0, o, top, l, vgs);
       } else {
         float4* po = reinterpret_cast<float4*>(part + r * D + d0);
@@ -696,10 +697,11 @@ kv_decode_kernel(const KvAttentionParams p) {
       }
     }
     if constexpr (CLUSTER) {
+      if (peers == 1) return;
       cluster_arrive_release();
       cluster_wait_acquire();                    // every CTA's results are there
       const uint32_t mine = smem_addr(c_out);
-      for (int x = tid * kDecCluster + rank; x < ROWS * (D / 8); x += kDecThreads * kDecCluster) {
+      for (int x = tid * peers + rank; x < ROWS * (D / 8); x += kDecThreads * peers) {
         const int r = x / (D / 8), d0 = (x % (D / 8)) * 8;
         if (r0 + r >= rows) continue;
         float4 rl[kDecCluster];
@@ -707,13 +709,15 @@ kv_decode_kernel(const KvAttentionParams p) {
         float o[8] = {};
 #pragma unroll
         for (int i = 0; i < kDecCluster; ++i) {
-          rl[i] = ld_peer_f32x4(peer_smem_addr(mine + (ROWS * D + 4 * r) * 4, i));
+          // (a smaller cluster's last CTA again: the loads stay side by side)
+          rl[i] = ld_peer_f32x4(peer_smem_addr(mine + (ROWS * D + 4 * r) * 4, min(i, peers - 1)));
           top = fmaxf(top, rl[i].x);
         }
 #pragma unroll
         for (int i = 0; i < kDecCluster; ++i) {
-          const uint32_t peer = peer_smem_addr(mine + (r * D + d0) * 4, i);
+          const uint32_t peer = peer_smem_addr(mine + (r * D + d0) * 4, min(i, peers - 1));
           const float4 y = ld_peer_f32x4(peer), z = ld_peer_f32x4(peer + 16);
+          if (i >= peers) continue;
           const float f = ex2(rl[i].x - top);
           l += rl[i].y * f;
           o[0] += y.x * f;

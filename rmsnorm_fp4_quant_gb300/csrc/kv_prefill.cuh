@@ -11,7 +11,8 @@
 // takes the place of its S) and O of both (2 D columns).
 //
 //   warps 0-3, 4-7   softmax of tile 0, 1: one row per thread, so a row's sum never
-//                    leaves the thread.  S is read once, P written back over it.
+//                    leaves the thread.  S is read once (in an item's first step
+//                    twice), P written back over it.
 //                    O is rescaled in place, by the same threads, in the rare step
 //                    in which a row's reference moves; when S of a step is there the
 //                    product before it has ended, so nothing else touches O then.

@@ -298,6 +298,18 @@ def test_decode_many_sequences():
     check_attention(queries(700, 2, 64, "bf16", 4), cache, tables, lens, None, True, "bf16")
 
 
+@pytest.mark.parametrize("B,Hkv", [(1, 1), (3, 4), (14, 5), (40, 6), (150, 8)])
+@pytest.mark.parametrize("longest", [20, 100, 200, 500, 1000, 2000, 6000])
+def test_decode_items_by_length(B, Hkv, longest):
+    """One CTA, each size of cluster, and the even split: by the number of items and the table."""
+    if B * longest > 20000:
+        pytest.skip("the oracle takes its time")
+    lens = [1 + (i * 7919) % longest for i in range(B)]
+    lens[B // 2] = longest
+    cache, tables = fill_sequences(lens, Hkv, 64, 16, seed=B)
+    check_attention(queries(B, Hkv * (2 if B > 3 else 12), 64, "bf16", 4), cache, tables, lens, None, True, "bf16")
+
+
 VARLEN = [
     # lens, q lengths (rows before, between and behind them belong to nobody)
     ([40, 17, 0, 129, 64, 5], [1, 17, 3, 2, 0, 9]),
