@@ -494,6 +494,19 @@ FP4Q_API int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq,
                                                int64_t head_dim, int64_t max_keys);
 
 /*
+ * fp4_attention_launch_shape - the kernel fp4_attention_nvfp4 would run for these
+ * sizes on the current device (diagnostics; launches nothing; arguments as above).
+ * Fills out[2] = {kernel (0 = the one for few rows or short sequences, 1 = the one in
+ * 256-row items), parts}: of kernel 0 the CTAs that share an item (1 to 8; 0 = the keys
+ * of all items are split evenly over the device and joined by a second kernel), of
+ * kernel 1 the ranges that an item's keys are cut into (joined likewise if more than one).
+ * FP4_OK, or FP4_ERR_INVALID_ARG.
+ */
+FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t Hq,
+                                                 int64_t num_kv_heads, int64_t head_dim,
+                                                 int64_t max_keys, int64_t out[2]);
+
+/*
  * fp4_read_device_status - synchronises `stream`, then copies the device
  * status word back and returns it as a status: FP4_OK (0) or FP4_ERR_TIMEOUT;
  * FP4_ERR_INVALID_ARG for a NULL or misaligned pointer or a value that is no

@@ -54,6 +54,7 @@ from ._binding import (  # noqa: F401
     fp4_add_rmsnorm_quant,
     fp4_add_rmsnorm_quant_ex,
     fp4_add_rmsnorm_quant_gs,
+    fp4_attention_launch_shape,
     fp4_attention_nvfp4,
     fp4_attention_workspace_bytes,
     fp4_dequant,

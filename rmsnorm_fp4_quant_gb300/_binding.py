@@ -145,6 +145,8 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_attention_nvfp4.restype = ci
     L.fp4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
     L.fp4_attention_workspace_bytes.restype = i64
+    L.fp4_attention_launch_shape.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
+    L.fp4_attention_launch_shape.restype = ci
     L.fp4_debug_build.argtypes = []
     L.fp4_debug_build.restype = ci
     L.fp4_debug_configure.argtypes = [i64, i64, ci, ci, ci, vp]
@@ -317,6 +319,17 @@ def fp4_launch_shape(M: int, H: int, dtype: int, fmt: int, sf_layout: int) -> di
     d = dict(zip(_SHAPE_KEYS, list(out)))
     d["kernel"] = "fused_tma_kernel" if d["kernel"] == 0 else "fused_direct_kernel"
     return d
+
+
+def fp4_attention_launch_shape(B: int, T: int, Hq: int, num_kv_heads: int, head_dim: int,
+                               max_keys: int) -> dict:
+    """The kernel fp4_attention_nvfp4 would run for these sizes on the current device:
+    {"kernel", "parts"} (include/fp4q.h)."""
+    out = (ctypes.c_int64 * 2)()
+    st = lib().fp4_attention_launch_shape(B, T, Hq, num_kv_heads, head_dim, max_keys, out)
+    if st != 0:
+        raise Fp4Error(st, "fp4_attention_launch_shape")
+    return {"kernel": "kv_prefill_kernel" if out[0] else "kv_decode_kernel", "parts": out[1]}
 
 
 # GEMM schedules by `variant` number: (kernel, output tile width)

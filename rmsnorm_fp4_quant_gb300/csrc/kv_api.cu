@@ -72,6 +72,18 @@ KvCache device_cache(const fp4_kv_cache_t& c) {
                  static_cast<int>(c.head_dim)};
 }
 
+// Keys of a sequence and rows of a key/value head are 32-bit numbers in the kernels, and
+// so are the grids over rows and sequences times heads.
+bool numbered_in_32_bits(int64_t B, int64_t T, int64_t Hq, int64_t Hkv, int64_t max_keys) {
+  return Hq <= kMaxHeads && B <= INT32_MAX / 2 && T <= INT32_MAX / 2 && B * Hkv <= INT32_MAX / 2 &&
+         T * Hq <= INT32_MAX && max_keys <= INT32_MAX / 2;
+}
+bool valid_attention_sizes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads, int64_t head_dim,
+                           int64_t max_keys) {
+  return B >= 0 && T >= 0 && max_keys >= 0 && Hq > 0 && num_kv_heads > 0 && Hq % num_kv_heads == 0 &&
+         (head_dim == 64 || head_dim == 128) && numbered_in_32_bits(B, T, Hq, num_kv_heads, max_keys);
+}
+
 bool valid_dtype(fp4_dtype_t d) { return d == FP4_DT_BF16 || d == FP4_DT_FP16; }
 
 }  // namespace
@@ -184,11 +196,18 @@ fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int64_t* slo
 
 int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
                                       int64_t head_dim, int64_t max_keys) {
-  if (B < 0 || T < 0 || max_keys < 0 || Hq <= 0 || num_kv_heads <= 0 || Hq % num_kv_heads || Hq > kMaxHeads ||
-      (head_dim != 64 && head_dim != 128))
-    return -1;
+  if (!valid_attention_sizes(B, T, Hq, num_kv_heads, head_dim, max_keys)) return -1;
   return kv_attention_workspace(sm_count_current_device(), B, T, static_cast<int>(Hq),
                                 static_cast<int>(num_kv_heads), static_cast<int>(head_dim), max_keys);
+}
+
+fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
+                                        int64_t head_dim, int64_t max_keys, int64_t out[2]) {
+  if (!valid_attention_sizes(B, T, Hq, num_kv_heads, head_dim, max_keys) || !B || !T || !out)
+    return FP4_ERR_INVALID_ARG;
+  kv_attention_shape(sm_count_current_device(), B, T, static_cast<int>(Hq),
+                     static_cast<int>(num_kv_heads), static_cast<int>(head_dim), max_keys, out);
+  return FP4_OK;
 }
 
 fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_cache_t* cache,
@@ -208,10 +227,8 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   if (q_stride == 0) q_stride = Hq * D;
   if (q_stride < Hq * D) return FP4_ERR_INVALID_ARG;
   if (!cu_seqlens_q && B != T) return FP4_ERR_INVALID_ARG;
-  // keys of a sequence and rows of a key/value head are 32-bit numbers in the
-  // kernels, and so are the grids over rows and sequences times heads
-  if (Hq > kMaxHeads || B > INT32_MAX / 2 || T > INT32_MAX / 2 || B * Hkv > INT32_MAX / 2 ||
-      T * Hq > INT32_MAX || max_pages > INT32_MAX / 2 / cache->page_size)
+  if (max_pages > INT32_MAX / 2 / cache->page_size ||
+      !numbered_in_32_bits(B, T, Hq, Hkv, max_pages * cache->page_size))
     return FP4_ERR_UNSUPPORTED_SHAPE;
   if (B == 0 || T == 0) return FP4_OK;
   if (!q || !out || !seq_lens || (max_pages && !block_tables)) return FP4_ERR_INVALID_ARG;

@@ -72,22 +72,59 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<T, D, NT>, p, ctas);
 }
 
-// Rows of a key/value head per sequence (on average: the lengths are on the device)
-// from which on the 256-row items are used.  32 sequences of 4096 tokens, 8 heads of
-// 128, 256-row items against 16-row items: 32 rows 164 / 104 us, 48 rows 141 / 143 us,
-// 64 rows 141 / 183 us, 128 rows 145 / 340 us; heads of 64: 111 / 101 us at 48 rows,
-// 112 / 126 us at 64.
-constexpr int kPrefillRows = 64;
-bool use_prefill(int64_t B, int64_t T, int group) { return T * group >= kPrefillRows * B; }
+// The choices between the kernels, and of the prefill kernel's ranges of keys, compare
+// times in microseconds, estimated from the sizes (the lengths are on the device: every
+// sequence counts with the average number of rows and the table's width).  The constants
+// are fits to calls timed with both kernels and with 1 to 8 ranges (heads of 64 and 128,
+// 1 to 100 sequences of 1 to 4000 rows and 48 to 60000 keys).  Over 831 of them the choice
+// is 0.9 % slower than the faster kernel on average and 35 % at most; a fixed limit of 64
+// rows was 11 % and a factor of 2.6, and ranges for two CTAs per SM 10 % and a factor of 2.1.  8 heads of 128, 4 query heads each, 16-row items against 256-row
+// items: one sequence of 80 rows and keys 6.7 / 13.4 us, of 320 over 1320 keys 57 / 43;
+// one range against two: 2048 rows and keys 46 / 97 us, 500 over 4000 keys 65 / 47.
+constexpr double kPreItem = 10.0, kPreJoin = 6.0, kPreJoinBytes = 3e6;   // per CTA; per join, bytes per us
+constexpr double kDecStart = 5.0, kDecItem = 5.0;
+constexpr int kPreMostSplits = 32;
 
-// Ranges of keys that an item is cut into: so many that every SM gets two CTAs, each
-// range being four steps at least (by the table's width).
-int prefill_splits(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys) {
-  const int64_t items = prefill_row_slots(B, T, group) * heads;
-  int64_t s = (2 * sms + items - 1) / items;
-  s = s < 8 ? s : 8;
-  while (s > 1 && keys < 4 * kPreKeys * s) --s;
-  return static_cast<int>(s);
+int64_t row_tiles(int64_t B, int64_t T, int group, int rows) {
+  const int64_t each = (T * group + B - 1) / B;
+  return B * ((each + rows - 1) / rows);
+}
+
+// A wave is one CTA per SM: its setup and its steps.
+double prefill_cost(int sms, int64_t items, int64_t rows, int D, int64_t keys, int splits) {
+  const int64_t steps = ((keys + splits - 1) / splits + kPreKeys - 1) / kPreKeys;
+  const int64_t waves = (items * splits + sms - 1) / sms;
+  return waves * (kPreItem + steps * (D == 128 ? 2.1 : 1.7)) +
+         (splits > 1 ? kPreJoin + rows * D * 8.0 * splits / kPreJoinBytes : 0.0);
+}
+
+// Ranges of keys that an item is cut into: the fewest of the best.
+int prefill_splits(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys, double* cost) {
+  const int64_t items = row_tiles(B, T, Hq / heads, kPreRows) * heads;
+  int best = 1;
+  double least = prefill_cost(sms, items, T * Hq, D, keys, 1);
+  // more waves than four only add CTAs to set up
+  for (int s = 2; s <= kPreMostSplits && (s - 1) * kPreKeys < keys && items * s <= 4LL * sms; ++s) {
+    const double c = prefill_cost(sms, items, T * Hq, D, keys, s);
+    if (c < least) least = c, best = s;
+  }
+  if (cost) *cost = least;
+  return best;
+}
+
+// Two 16-row items run on an SM at a time with 128 channels, three with 64.
+double decode_cost(int sms, int64_t B, int64_t T, int group, int heads, int D, int64_t keys) {
+  const double items = static_cast<double>(row_tiles(B, T, group, 16)) * heads;
+  return kDecStart + items * (kDecItem + keys / 16.0 * (D == 128 ? 0.3 : 0.25)) / (sms * (D == 128 ? 2 : 3));
+}
+
+// Up to 16 rows of a key/value head per sequence are one item of the decode kernel.
+bool use_prefill(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys) {
+  const int group = Hq / heads;
+  if (T * group <= 16 * B) return false;
+  double prefill = 0.0;
+  prefill_splits(sms, B, T, Hq, heads, D, keys, &prefill);
+  return prefill < decode_cost(sms, B, T, group, heads, D, keys);
 }
 
 template <typename T, int D>
@@ -113,8 +150,8 @@ cudaError_t launch_prefill(const KvAttentionParams& p, int pdl, cudaStream_t str
       done[dev] = true;
     }
   }
-  const int splits = prefill_splits(sm_count_current_device(), p.B, p.T, p.group, p.c.heads,
-                                    p.max_pages * p.c.page_size);
+  const int splits = prefill_splits(sm_count_current_device(), p.B, p.T, p.Hq, p.c.heads, D,
+                                    p.max_pages * p.c.page_size, nullptr);
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
@@ -137,7 +174,7 @@ cudaError_t launch_prefill(const KvAttentionParams& p, int pdl, cudaStream_t str
 
 template <typename T>
 cudaError_t launch_type(const KvAttentionParams& p, int pdl, cudaStream_t stream) {
-  if (use_prefill(p.B, p.T, p.group))
+  if (use_prefill(sm_count_current_device(), p.B, p.T, p.Hq, p.c.heads, p.c.D, p.max_pages * p.c.page_size))
     return p.c.D == 128 ? launch_prefill<T, 128>(p, pdl, stream) : launch_prefill<T, 64>(p, pdl, stream);
   const int nt = decode_tiles(p.B, p.T, p.group);
   if (p.c.D == 128)
@@ -146,27 +183,35 @@ cudaError_t launch_type(const KvAttentionParams& p, int pdl, cudaStream_t stream
 }
 
 template <int D, int NT>
-int64_t decode_workspace(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys) {
+int64_t decode_workspace(int sms, int64_t B, int64_t T, int group, int heads) {
   using S = DecodeShape<D, NT>;
-  if (cluster_of<D, NT>(sms, B, T, group, heads, keys)) return 0;
   return 4LL * (2LL * sms * S::kCtas * S::kPart) + 8LL * decode_row_slots(B, T, group, S::kRows) * heads;
 }
 
 }  // namespace
 
+void kv_attention_shape(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys, int64_t out[2]) {
+  const int group = Hq / heads, nt = decode_tiles(B, T, group);
+  out[0] = use_prefill(sms, B, T, Hq, heads, D, keys) ? 1 : 0;
+  out[1] = out[0]     ? prefill_splits(sms, B, T, Hq, heads, D, keys, nullptr)
+           : D == 128 ? (nt == 1 ? cluster_of<128, 1>(sms, B, T, group, heads, keys)
+                                 : cluster_of<128, 2>(sms, B, T, group, heads, keys))
+                      : (nt == 1 ? cluster_of<64, 1>(sms, B, T, group, heads, keys)
+                                 : cluster_of<64, 2>(sms, B, T, group, heads, keys));
+}
+
 int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys) {
-  const int group = Hq / heads;
   if (B == 0 || T == 0) return 0;
-  if (use_prefill(B, T, group)) {
-    const int64_t splits = prefill_splits(sms, B, T, group, heads, keys);
-    return splits > 1 ? splits * T * Hq * (D + 2) * 4 : 0;
-  }
-  const int nt = decode_tiles(B, T, group);
+  int64_t shape[2];
+  kv_attention_shape(sms, B, T, Hq, heads, D, keys, shape);
+  if (shape[0]) return shape[1] > 1 ? shape[1] * T * Hq * (D + 2) * 4 : 0;
+  if (shape[1]) return 0;
+  const int group = Hq / heads;
   if (D == 128)
-    return nt == 1 ? decode_workspace<128, 1>(sms, B, T, group, heads, keys)
-                   : decode_workspace<128, 2>(sms, B, T, group, heads, keys);
-  return nt == 1 ? decode_workspace<64, 1>(sms, B, T, group, heads, keys)
-                 : decode_workspace<64, 2>(sms, B, T, group, heads, keys);
+    return decode_tiles(B, T, group) == 1 ? decode_workspace<128, 1>(sms, B, T, group, heads)
+                                          : decode_workspace<128, 2>(sms, B, T, group, heads);
+  return decode_tiles(B, T, group) == 1 ? decode_workspace<64, 1>(sms, B, T, group, heads)
+                                        : decode_workspace<64, 2>(sms, B, T, group, heads);
 }
 
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl,

@@ -132,6 +132,9 @@ def test_workspace_sizes():
         assert f(*bad) == -1
     assert f(0, 0, 8, 2, 128, 512) == 0
     assert f(1, 1, 8, 2, 128, 1024) == 0                 # a cluster per item
+    for bad in [(1 << 30, 4, 8, 2, 128, 512), (4, 1 << 29, 8, 2, 128, 512), (4, 4, 8, 2, 128, 1 << 30),
+                (4, 4, 8192, 2, 128, 512)]:
+        assert f(*bad) == -1                             # sizes the call refuses
     # tables of 2^20 keys: parts of CTAs; 100 x 100 rows over them: ranges of keys
     for a, kw in (((5, 5, 4, 2, 128), {}), ((5, 500, 4, 2, 128), dict(T=500, cu=at(12)))):
         kw["pages"] = 65536
@@ -162,3 +165,26 @@ def test_tensor_calls_refuse_cpu_tensors_and_bad_shapes():
         fq.kv_cache_nvfp4(4, 24, 2, 128, device="cpu")
     with pytest.raises(ValueError):
         fq.kv_cache_nvfp4(4, 16, 2, 96, device="cpu")
+
+
+def test_attention_launch_shape():
+    """The choice of kernel: host only (152 SMs without a device)."""
+    f = fq.fp4_attention_launch_shape
+    decode, prefill = "kv_decode_kernel", "kv_prefill_kernel"
+    assert f(1, 1, 12, 2, 128, 1000) == {"kernel": decode, "parts": 8}
+    assert f(128, 128, 56, 8, 128, 16384) == {"kernel": decode, "parts": 0}
+    assert f(200, 200, 32, 8, 128, 200) == {"kernel": decode, "parts": 1}
+    assert f(1, 80, 32, 8, 128, 80)["kernel"] == decode          # few items of few keys
+    assert f(1, 4096, 32, 8, 128, 4096) == {"kernel": prefill, "parts": 1}
+    assert f(1, 64, 32, 8, 128, 60000)["kernel"] == prefill and f(1, 64, 32, 8, 128, 60000)["parts"] > 8
+    for B, T, keys in [(1, 1, 0), (1, 10 ** 6, 1), (7, 3, 10 ** 6), (10 ** 6, 1, 16), (3, 100, 2 ** 30 - 16)]:
+        for Hq, Hkv, D in [(1, 1, 64), (128, 1, 128), (24, 24, 64)]:
+            s = f(B, T, Hq, Hkv, D, keys)
+            assert 1 <= s["parts"] <= 32 if s["kernel"] == prefill else s["parts"] in (0, 1, 2, 4, 8)
+            # only what is joined from memory has a workspace
+            need = fq.fp4_attention_workspace_bytes(B, T, Hq, Hkv, D, keys)
+            assert (need > 0) == (s["parts"] > 1 if s["kernel"] == prefill else s["parts"] == 0)
+    for bad in [(0, 1, 8, 2, 128, 512), (1, 0, 8, 2, 128, 512), (4, 4, 8, 3, 128, 512), (4, 4, 8, 2, 96, 512),
+                (1 << 30, 4, 8, 2, 128, 512)]:
+        with pytest.raises(fq.Fp4Error):
+            f(*bad)

@@ -229,22 +229,85 @@ def fill_sequences(lens, Hkv, D, page, seed, extra_pages=3, bad=()):
     return cache, tables
 
 
+def shape_of(B, T, Hq, Hkv, D, keys):
+    return fq.fp4_attention_launch_shape(B, T, Hq, Hkv, D, keys)
+
+
+def widened(tables, T, Hq, Hkv, D, page, wanted):
+    """The tables, widened by pages of no sequence until the call's launch shape is as
+    wanted; None if no width does it."""
+    B, width = tables.shape
+    while width * page < 1 << 22:
+        if wanted(shape_of(B, T, Hq, Hkv, D, width * page)):
+            wide = np.full((B, width), -7, tables.dtype)
+            wide[:, :tables.shape[1]] = tables
+            return wide
+        width *= 2
+    return None
+
+
+def for_ranges(*args):
+    """256-row items whose keys are cut into ranges."""
+    return widened(*args, lambda s: s["kernel"] == "kv_prefill_kernel" and s["parts"] > 1)
+
+
+def for_even_split(*args):
+    """The keys of all items split evenly over the CTAs."""
+    return widened(*args, lambda s: s == {"kernel": "kv_decode_kernel", "parts": 0})
+
+
+def times_for_items(B, T, Hq, Hkv, D, keys):
+    """How often the batch has to be repeated for a call that takes 256-row items with
+    all their keys; None if no number does."""
+    n = 1
+    while n <= 128:
+        if shape_of(n * B, n * T, Hq, Hkv, D, keys) == {"kernel": "kv_prefill_kernel", "parts": 1}:
+            return n
+        n *= 2
+    return None
+
+
 def check_attention(q, cache, tables, lens, cu, causal, dtype, sm_scale=None, kg=1.0, vg=1.0, **kw):
-    """Runs the call and compares every row with the oracle; returns (out, lse)."""
+    """Runs the call and compares every row with the oracle; returns (out, lse).  The same
+    rows are run in the other launch shapes, too: over wider tables (an even split of the
+    keys, 256-row items with ranges of them) and with the batch repeated (256-row items)."""
     T, Hq, D = q.shape
+    B, page, Hkv = len(lens), cache[0].shape[2], cache[0].shape[1]
     scale = D ** -0.5 if sm_scale is None else sm_scale
     ref = okv.attention(q.double().numpy(), cache, tables, lens, cu, causal, scale, kg, vg)
     dev = [torch.from_numpy(c).cuda() for c in cache]
-    out = torch.full((T, Hq, D), 5.0, dtype=DT[dtype], device="cuda")
-    lse = torch.full((T, Hq), 6.0, device="cuda")
     gs = dict(k_global_scale=torch.tensor([kg], device="cuda") if kg != 1 else None,
               v_global_scale=torch.tensor([vg], device="cuda") if vg != 1 else None)
-    fq.attention_nvfp4(q.cuda(), dev, torch.from_numpy(tables.astype(np.int32)).cuda(),
-                       torch.tensor(lens, dtype=torch.int32, device="cuda"),
-                       None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"),
-                       causal=causal, sm_scale=sm_scale, out=out, return_lse=True, lse=lse, **gs, **kw)
-    torch.cuda.synchronize()
+
+    def run(q, tables, lens, cu):
+        T = q.shape[0]
+        out = torch.full((T, Hq, D), 5.0, dtype=DT[dtype], device="cuda")
+        lse = torch.full((T, Hq), 6.0, device="cuda")
+        fq.attention_nvfp4(q.cuda(), dev, torch.from_numpy(tables.astype(np.int32)).cuda(),
+                           torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                           None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                           causal=causal, sm_scale=sm_scale, out=out, return_lse=True, lse=lse, **gs, **kw)
+        torch.cuda.synchronize()
+        return out, lse
+    out, lse = run(q, tables, lens, cu)
     compare_attention(out, lse, ref, D, dtype)
+    if max(lens) <= tables.shape[1] * page:
+        for wide in (for_even_split(tables, T, Hq, Hkv, D, page), for_ranges(tables, T, Hq, Hkv, D, page)):
+            if wide is not None and wide.shape != tables.shape:
+                compare_attention(*run(q, wide, lens, cu), ref, D, dtype)
+    n = times_for_items(B, T, Hq, Hkv, D, tables.shape[1] * page)
+    if n is not None and cu is not None:
+        first, last = cu[0], cu[-1]
+        rows = last - first
+        starts = [first + i * rows + c - first for i in range(n) for c in cu[:-1]] + [first + n * rows]
+        o, s = run(torch.cat([q[:first], q[first:last].repeat(n, 1, 1), q[last:]]), np.tile(tables, (n, 1)), list(lens) * n,
+                   starts)
+        for i in (0, n - 1):
+            pick = torch.cat([torch.arange(first), first + i * rows + torch.arange(rows),
+                              first + n * rows + torch.arange(T - last)]).cuda()
+            compare_attention(o[pick], s[pick], ref, D, dtype)
+        body = o[first:first + n * rows].view(n, rows, Hq, D)
+        assert torch.equal(body, body[:1].expand_as(body))
     return out, lse
 
 
@@ -431,6 +494,8 @@ def test_a_bad_query_row_stays_alone(varlen, bad):
     cache, tables = fill_sequences(lens, 2, 64, 16, seed=31)
     cu = [0, 30, 170] if varlen else None
     T = 170 if varlen else 2
+    if varlen:
+        tables = for_ranges(tables, T, 4, 2, 64, 16)
     dev = [torch.from_numpy(c).cuda() for c in cache]
     tab = torch.from_numpy(tables.astype(np.int32)).cuda()
     sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -455,6 +520,8 @@ def test_strided_queries_graphs_streams_and_repeats(varlen):
     cache, tables = fill_sequences(lens, 2, D, 16, seed=31)
     cu = [0, 30, 170, 180] if varlen else None
     T = 180 if varlen else 3
+    if varlen:
+        tables = for_ranges(tables, T, Hq, 2, D, 16)
     wide = torch.randn(T, (Hq + 3) * D, generator=gen(0)).bfloat16().cuda()
     q = wide[:, D:(Hq + 1) * D].unflatten(-1, (Hq, D))
     dev = [torch.from_numpy(c).cuda() for c in cache]
@@ -595,6 +662,7 @@ def test_one_workspace_for_calls_in_a_row():
     D, Hq, Hkv = 128, 8, 2
     lens = [2000, 300]
     cache, tables = fill_sequences(lens, Hkv, D, 16, seed=3)
+    tables = for_ranges(tables, 120, Hq, Hkv, D, 16)
     dev = [torch.from_numpy(c).cuda() for c in cache]
     tab = torch.from_numpy(tables.astype(np.int32)).cuda()
     sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -661,6 +729,7 @@ def test_waits_that_run_out_are_reported():
     cache, tables = fill_sequences(lens, 1, D, 16, seed=4)
     q = queries(290, Hq, D, "bf16", 2)
     ref = okv.attention(q.double().numpy(), cache, tables, lens, cu, True, D ** -0.5)
+    tables = for_ranges(tables, 290, Hq, 1, D, 16)       # the kernel that waits
     dev = [torch.from_numpy(c).cuda() for c in cache]
     tab = torch.from_numpy(tables.astype(np.int32)).cuda()
     sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
@@ -714,11 +783,12 @@ def test_debug_build_finds_no_access_out_of_bounds():
             # row limits that do not ascend, or lie outside, are held to the rows there are
             c, tables = fill_sequences([100, 50, 70], 1, 64, 16, seed=1)
             c = [torch.from_numpy(x).cuda() for x in c]
-            tab = torch.from_numpy(tables.astype(np.int32)).cuda()
             sl = torch.tensor([100, 50, 70], dtype=torch.int32, device="cuda")
+            more = for_ranges(tables, 95, 4, 1, 64, 16)
             for cu in ([0, 90, 20, 1000], [-5, 3, 2 ** 31 - 1, 7], [40, 30, 20, 10]):
-                for T in (12, 95):
-                    fq.attention_nvfp4(queries(T, 4, 64, "fp16", 1).cuda(), c, tab, sl,
+                for T, tab in ((12, tables), (95, tables), (95, more)):
+                    fq.attention_nvfp4(queries(T, 4, 64, "fp16", 1).cuda(), c,
+                                       torch.from_numpy(tab.astype(np.int32)).cuda(), sl,
                                        torch.tensor(cu, dtype=torch.int32, device="cuda"))
             torch.cuda.synchronize()
             assert bad.item() == 0
