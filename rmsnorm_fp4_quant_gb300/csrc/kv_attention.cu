@@ -1,6 +1,7 @@
 // kv_attention.cu - attention over the paged NVFP4 key/value cache: choice of
 // kernel and launch.
 
+#include <cmath>
 #include <mutex>
 
 #include "fp4q_launch.h"
@@ -15,23 +16,61 @@ namespace {
 // 8 rows 46 us, 16 rows 63 us; two tiles of 8 for 16 rows would read every key twice).
 int decode_tiles(int64_t B, int64_t T, int group) { return T * group <= 8 * B ? 1 : 2; }
 
-// CTAs of the cluster that takes one item each, 0 where the keys are to be split evenly
-// over all CTAs instead (by the table's width: the lengths are on the device).  A CTA
-// has at most 16 units of keys then; an item gets more CTAs than that asks for as long
-// as all run at once and have a unit each, and where even the fewest do not run at
-// once it has to be one each (short sequences, which the hardware then deals out).
-// One sequence of 1000 tokens, 2 key/value heads: 5.8 us on the device and one launch,
-// against 8.6 us and two.
-constexpr int kClusterKeys = kDecUnit * 16;
+// The choices below compare times in microseconds, estimated from the sizes (the lengths
+// are on the device: every sequence counts with the average number of rows and the
+// table's width).  Their constants are fits to timed calls.
+int64_t row_tiles(int64_t B, int64_t T, int group, int rows) {
+  const int64_t each = (T * group + B - 1) / B;
+  return B * ((each + rows - 1) / rows);
+}
+
+// A 16-key tile in a CTA that has an SM to itself, and per CTA where several share one;
+// an item's setup, and its join in a cluster; the even split's two kernels, an item's
+// share of them, and the second one's time per part of an item; how many of an SM's places
+// clusters find.
+struct DecodeTimes {
+  double alone, shared, item, peers, split, split_item, part, places;
+};
 template <int D, int NT>
-int cluster_of(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys) {
-  const int64_t items = decode_row_slots(B, T, group, 8 * NT) * heads;
-  const int64_t at_once = static_cast<int64_t>(sms) * DecodeShape<D, NT>::kCtas;
-  int64_t c = 1;
-  while (c < kDecCluster && keys > c * kClusterKeys) c *= 2;
-  if (keys > c * kClusterKeys || (c > 1 && items * c > at_once) || items * c > INT32_MAX) return 0;
-  while (c < kDecCluster && items * c * 2 <= at_once && keys >= c * 2 * kDecUnit) c *= 2;
-  return static_cast<int>(c);
+constexpr DecodeTimes kDecTimes =
+    D == 64 ? (NT == 1 ? DecodeTimes{0.076, 0.033, 4.0, 1.8, 6.5, 2.0, 0.09, 0.95}
+                       : DecodeTimes{0.101, 0.044, 4.0, 4.3, 8.8, 3.1, 0.12, 0.95})
+            : (NT == 1 ? DecodeTimes{0.084, 0.063, 4.7, 1.9, 8.4, 3.0, 0.03, 0.95}
+                       : DecodeTimes{0.099, 0.065, 5.7, 4.3, 10.9, 4.4, 0.04, 0.88});
+
+constexpr double kEvenSplit = 0.95;
+
+// CTAs that share an item (more than one as a cluster, joined in shared memory; the
+// hardware deals the items out), or 0 where the keys are split evenly over all CTAs and
+// joined by a second kernel.  1055 calls of 1 to 128 sequences with 100 to 16000 keys, each
+// timed with every choice: the one made is 1.7 % slower than the best on average and 30 %
+// at most (a twentieth off the even split costs those nothing, and 100 sequences of 400 to
+// 10000 keys, 8 heads of 128, take 124 us instead of 155).  One CTA an item against the even split: 128 sequences of 2000 keys, 24 heads
+// of 64, 111 / 144 us, 16 of 8000 with 4 rows each 72 / 59; 8 CTAs: one sequence of 1000
+// keys, 2 heads of 128, 6.1 / 9.0 us, 4 of 16000 with 8 heads 23.8 / 19.3.
+template <int D, int NT>
+int cluster_of(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys, double* cost = nullptr) {
+  constexpr DecodeTimes t = kDecTimes<D, NT>;
+  constexpr int kCtas = DecodeShape<D, NT>::kCtas;
+  const double items = static_cast<double>(row_tiles(B, T, group, 8 * NT)) * heads;
+  const int64_t units = (keys + kDecUnit - 1) / kDecUnit;
+  int best = 0;
+  // the even split follows the lengths, where a cluster takes as long as its own: the more
+  // they differ the better for it
+  double least = kEvenSplit * (t.split + items * (t.split_item + keys / 16.0 * t.shared) / sms +
+                               t.part * std::fmin(sms * kCtas / items, static_cast<double>(units)));
+  for (const int c : {1, 2, 3, 4, 6, 8}) {
+    if (decode_row_slots(B, T, group, 8 * NT) * heads > INT32_MAX / c) break;
+    const double per_sm = items * c / sms;
+    const double side = std::fmin(std::ceil(per_sm), kCtas);
+    const double waves = std::fmax(1.0, per_sm / (kCtas * (c > 1 ? t.places : 1.0)));
+    const double tiles = static_cast<double>((units + c - 1) / c * (kDecUnit / 16));
+    const double x = 0.5 * (waves + std::ceil(waves)) *
+                     (t.item + (c > 1 ? t.peers : 0.0) + tiles * std::fmax(t.alone, side * t.shared));
+    if (x < least) least = x, best = c;
+  }
+  if (cost) *cost = least;
+  return best;
 }
 
 template <typename T, int D, int NT>
@@ -72,29 +111,22 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
   return cudaLaunchKernelEx(&cfg, kv_decode_join_kernel<T, D, NT>, p, ctas);
 }
 
-// The choices between the kernels, and of the prefill kernel's ranges of keys, compare
-// times in microseconds, estimated from the sizes (the lengths are on the device: every
-// sequence counts with the average number of rows and the table's width).  The constants
-// are fits to calls timed with both kernels and with 1 to 8 ranges (heads of 64 and 128,
-// 1 to 100 sequences of 1 to 4000 rows and 48 to 60000 keys).  Over 831 of them the choice
-// is 0.9 % slower than the faster kernel on average and 35 % at most; a fixed limit of 64
-// rows was 11 % and a factor of 2.6, and ranges for two CTAs per SM 10 % and a factor of 2.1.  8 heads of 128, 4 query heads each, 16-row items against 256-row
-// items: one sequence of 80 rows and keys 6.7 / 13.4 us, of 320 over 1320 keys 57 / 43;
-// one range against two: 2048 rows and keys 46 / 97 us, 500 over 4000 keys 65 / 47.
-constexpr double kPreItem = 10.0, kPreJoin = 6.0, kPreJoinBytes = 3e6;   // per CTA; per join, bytes per us
-constexpr double kDecStart = 5.0, kDecItem = 5.0;
+// Constants as above, from calls timed with both kernels and with 1 to 8 ranges of keys
+// (heads of 64 and 128, 1 to 100 sequences of 1 to 4000 rows and 48 to 60000 keys).  Over
+// 831 of them the choice of kernel is 0.4 % slower than the faster one on average and 24 %
+// at most; a fixed limit of 64 rows was 11 % and a factor of 2.6, and ranges for two CTAs
+// per SM 10 % and a factor of 2.1.  8 heads of 128, 4 query heads each, 16-row items
+// against 256-row items: one sequence of 80 rows and keys 6.7 / 13.4 us, of 320 over 1320
+// keys 57 / 43; one range against two: 2048 rows and keys 46 / 97 us, 500 over 4000 keys
+// 65 / 47.
+constexpr double kPreItem = 9.0, kPreJoin = 4.0, kPreJoinBytes = 5e6;   // per CTA; per join, bytes per us
 constexpr int kPreMostSplits = 32;
-
-int64_t row_tiles(int64_t B, int64_t T, int group, int rows) {
-  const int64_t each = (T * group + B - 1) / B;
-  return B * ((each + rows - 1) / rows);
-}
 
 // A wave is one CTA per SM: its setup and its steps.
 double prefill_cost(int sms, int64_t items, int64_t rows, int D, int64_t keys, int splits) {
   const int64_t steps = ((keys + splits - 1) / splits + kPreKeys - 1) / kPreKeys;
   const int64_t waves = (items * splits + sms - 1) / sms;
-  return waves * (kPreItem + steps * (D == 128 ? 2.1 : 1.7)) +
+  return waves * (kPreItem + steps * (D == 128 ? 1.7 : 1.3)) +
          (splits > 1 ? kPreJoin + rows * D * 8.0 * splits / kPreJoinBytes : 0.0);
 }
 
@@ -112,19 +144,15 @@ int prefill_splits(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int6
   return best;
 }
 
-// Two 16-row items run on an SM at a time with 128 channels, three with 64.
-double decode_cost(int sms, int64_t B, int64_t T, int group, int heads, int D, int64_t keys) {
-  const double items = static_cast<double>(row_tiles(B, T, group, 16)) * heads;
-  return kDecStart + items * (kDecItem + keys / 16.0 * (D == 128 ? 0.3 : 0.25)) / (sms * (D == 128 ? 2 : 3));
-}
-
 // Up to 16 rows of a key/value head per sequence are one item of the decode kernel.
 bool use_prefill(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys) {
   const int group = Hq / heads;
   if (T * group <= 16 * B) return false;
-  double prefill = 0.0;
+  double prefill = 0.0, decode = 0.0;
   prefill_splits(sms, B, T, Hq, heads, D, keys, &prefill);
-  return prefill < decode_cost(sms, B, T, group, heads, D, keys);
+  if (D == 128) cluster_of<128, 2>(sms, B, T, group, heads, keys, &decode);
+  else cluster_of<64, 2>(sms, B, T, group, heads, keys, &decode);
+  return prefill < decode;
 }
 
 template <typename T, int D>
