@@ -427,7 +427,8 @@ kv_decode_kernel(const KvAttentionParams p) {
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 1));
       top = fmaxf(top, __shfl_xor_sync(kFullMask, top, 2));
       const int k = q_exponent(top);
-      const float up = pow2(k);
+      // a row with an infinity or NaN is NaN, and its products with every key are
+      const float up = top < INFINITY ? pow2(k) : __uint_as_float(0x7fc00000u);
 #pragma unroll
       for (int i = 0; i < D / 64; ++i)
 #pragma unroll

@@ -390,7 +390,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       }
       if (nan) top = INFINITY;
       const int k = q_exponent(top);
-      const float up = pow2(k);
+      // a row with an infinity or NaN is NaN, and its products with every key are
+      const float up = top < INFINITY ? pow2(k) : __uint_as_float(0x7fc00000u);
       const uint32_t dst = smem0 + S::kQ + tile * S::kTile + r_in * 128;
 #pragma unroll
       for (int i = 0; i < D / 8; ++i) {          // 16 bytes: 8 channels

@@ -511,6 +511,30 @@ def test_a_bad_query_row_stays_alone(varlen, bad):
     assert torch.isnan(b[T // 2, 1]).all()
 
 
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 150])
+def test_a_row_whose_logits_are_all_minus_infinity(T, D):
+    """-inf - -inf: NaN, as from the formula; a row that sees no key is 0 all the same."""
+    n = 40
+    cache = to_np(random_cache(3, 1, 16, D, 3))
+    okv.append(cache, np.ones((n, 1, D), np.float32), torch.randn(n, 1, D, generator=gen(5)).numpy(), np.arange(n))
+    tables = np.arange(3, dtype=np.int64)[None]
+    cu = None if T == 1 else [0, T]
+    for tab in [tables] + ([] if T == 1 else [for_ranges(tables, T, 4, 1, D, 16)]):
+        q = queries(T, 4, D, "bf16", 2).cuda()
+        q[:, 1] = -float("inf")
+        out, lse = fq.attention_nvfp4(q, [torch.from_numpy(c).cuda() for c in cache],
+                                      torch.from_numpy(tab.astype(np.int32)).cuda(),
+                                      torch.tensor([n], dtype=torch.int32, device="cuda"),
+                                      None if cu is None else torch.tensor(cu, dtype=torch.int32, device="cuda"),
+                                      return_lse=True)
+        seen = torch.arange(T) >= T - n
+        assert torch.isnan(out.cpu()[seen, 1]).all() and torch.isnan(lse.cpu()[seen, 1]).all()
+        assert torch.all(out.cpu()[~seen] == 0) and torch.all(torch.isneginf(lse.cpu()[~seen]))
+        keep = [0, 2, 3]
+        assert torch.isfinite(out.cpu()[seen][:, keep]).all()
+
+
 @pytest.mark.parametrize("varlen", [False, True])
 def test_strided_queries_graphs_streams_and_repeats(varlen):
     """A column slice of a wider matrix as q; the same bits on repeats, on another
