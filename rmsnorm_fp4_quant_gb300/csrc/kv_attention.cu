@@ -113,13 +113,13 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
 
 // Constants as above, from calls timed with both kernels and with 1 to 8 ranges of keys
 // (heads of 64 and 128, 1 to 100 sequences of 1 to 4000 rows and 48 to 60000 keys).  Over
-// 831 of them the choice of kernel is 0.4 % slower than the faster one on average and 24 %
+// 831 of them the choice of kernel is 0.4 % slower than the faster one on average and 25 %
 // at most; a fixed limit of 64 rows was 11 % and a factor of 2.6, and ranges for two CTAs
 // per SM 10 % and a factor of 2.1.  8 heads of 128, 4 query heads each, 16-row items
 // against 256-row items: one sequence of 80 rows and keys 6.7 / 13.4 us, of 320 over 1320
 // keys 57 / 43; one range against two: 2048 rows and keys 46 / 97 us, 500 over 4000 keys
 // 65 / 47.
-constexpr double kPreItem = 9.0, kPreJoin = 4.0, kPreJoinBytes = 5e6;   // per CTA; per join, bytes per us
+constexpr double kPreItem = 8.0, kPreJoin = 4.0, kPreJoinBytes = 5e6;   // per CTA; per join, bytes per us
 constexpr int kPreMostSplits = 32;
 
 // A wave is one CTA per SM: its setup and its steps.

@@ -87,6 +87,12 @@ __device__ __forceinline__ uint32_t low_nibbles_of(uint32_t lo, uint32_t hi) {
   return d;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // k with 2^k * m in [2^14, 2^15) for m > 0 (held to where 2^k and 2^-k are
 // normal numbers); 0 for zero, infinity and NaN.
 __device__ __forceinline__ int q_exponent(float m) {

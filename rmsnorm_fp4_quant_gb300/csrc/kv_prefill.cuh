@@ -271,16 +271,27 @@ __device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim,
   return sum2.x + sum2.y;
 }
 // The largest product of a row with a key that it sees.
-__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, uint32_t have, bool edge) {
+template <bool EDGE>
+__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, uint32_t have) {
   float m = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
     uint32_t x[32];
     tmem_load_32cols(ts + 32 * c, x);
+    float y[2] = {-INFINITY, -INFINITY};           // two chains
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-      if (!edge || (key0 + 32 * c + i < lim && (have >> (2 * c + i / 16) & 1u)))
-        m = fmaxf(m, __uint_as_float(x[i]));
+    for (int i = 0; i < 32; i += 4)
+#pragma unroll
+      for (int k = 0; k < 2; ++k) {
+        float u = __uint_as_float(x[i + 2 * k]), v = __uint_as_float(x[i + 2 * k + 1]);
+        if (EDGE) {
+          const bool page = have >> (2 * c + i / 16) & 1u;
+          if (!page || key0 + 32 * c + i + 2 * k >= lim) u = -INFINITY;
+          if (!page || key0 + 32 * c + i + 2 * k + 1 >= lim) v = -INFINITY;
+        }
+        y[k] = max3(y[k], u, v);
+      }
+    m = max3(m, y[0], y[1]);
   }
   return m;
 }
@@ -437,7 +448,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
 #pragma unroll 1
       for (;;) {
         if (last) {
-          const float m = prefill_maximum(ts, key0, lim, have, edge);
+          const float m = edge ? prefill_maximum<true>(ts, key0, lim, have)
+                               : prefill_maximum<false>(ts, key0, lim, have);
           float f = 1.0f;
           if (moved && m > -INFINITY) {
             const float to_ref = fmaxf(ref, m * fac - kRefBelow);
