@@ -361,16 +361,29 @@ def test_decode_many_sequences():
     check_attention(queries(700, 2, 64, "bf16", 4), cache, tables, lens, None, True, "bf16")
 
 
-@pytest.mark.parametrize("B,Hkv", [(1, 1), (3, 4), (14, 5), (40, 6), (150, 8)])
-@pytest.mark.parametrize("longest", [20, 100, 200, 500, 1000, 2000, 6000])
+# (more than 20000 keys in all take the oracle long)
+@pytest.mark.parametrize("B,Hkv,longest", [
+    (B, Hkv, n) for n in (20, 100, 200, 500, 1000, 2000, 6000)
+    for B, Hkv in ((1, 1), (3, 4), (14, 5), (40, 6), (150, 8)) if B * n <= 20000])
 def test_decode_items_by_length(B, Hkv, longest):
-    """One CTA, each size of cluster, and the even split: by the number of items and the table."""
-    if B * longest > 20000:
-        pytest.skip("the oracle takes its time")
     lens = [1 + (i * 7919) % longest for i in range(B)]
     lens[B // 2] = longest
     cache, tables = fill_sequences(lens, Hkv, 64, 16, seed=B)
     check_attention(queries(B, Hkv * (2 if B > 3 else 12), 64, "bf16", 4), cache, tables, lens, None, True, "bf16")
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [2, 12])
+@pytest.mark.parametrize("parts", [0, 1, 2, 3, 4, 6, 8])
+def test_every_way_to_share_an_item(D, group, parts):
+    """One CTA, each size of cluster, the even split: the first sizes that lead to it."""
+    B, Hkv, longest = next((B, Hkv, n) for n in (100, 400, 700, 1000, 1500, 2200, 3000, 6000, 12000)
+                           for B in (1, 2, 4, 6, 9, 12, 16, 20, 26) for Hkv in (1, 2, 4, 8)
+                           if shape_of(B, B, Hkv * group, Hkv, D, n + 32)["parts"] == parts)
+    lens = [longest] + [(i * 131) % min(longest, 500) for i in range(1, B)]
+    cache, tables = fill_sequences(lens, Hkv, D, 32, seed=parts)
+    assert shape_of(B, B, Hkv * group, Hkv, D, 32 * tables.shape[1]) == {"kernel": "kv_decode_kernel", "parts": parts}
+    check_attention(queries(B, Hkv * group, D, "fp16", 4), cache, tables, lens, None, True, "fp16")
 
 
 VARLEN = [
