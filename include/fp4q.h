@@ -466,7 +466,7 @@ FP4Q_API fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int
  *                   left as they were.
  *   causal          nonzero: row i of a sequence's n_q rows sees its first len - n_q + i + 1
  *                   keys; zero: all of them (cross attention to an encoder's states).
- *   sm_scale        > 0, finite.
+ *   sm_scale        > 0, finite; a logit times log2(e) has to stay within fp32's numbers.
  *   out             [T, Hq, head_dim] dtype, dense, 32-byte aligned.  A row that sees no key is
  *                   0, with lse -inf.
  *   lse             [T, Hq] fp32 (natural logarithm), or NULL.

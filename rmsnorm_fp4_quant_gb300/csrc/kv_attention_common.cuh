@@ -22,10 +22,25 @@ constexpr float kLn2 = 0.6931471805599453f;
 // Exponents of 2 are taken against a reference r kept 6 below the largest logit
 // seen when it was set, and it is set again once a logit passes r + 14: weights
 // stay below 2^14 in fp16, and one that is 2^30 times smaller than the largest
-// still has a bit.  A finite start keeps "nothing seen yet" free of inf - inf.
-constexpr float kRefStart = -1e30f;
+// still has a bit.  A finite start keeps "nothing seen yet" free of inf - inf, and
+// no logit lies below it.
+constexpr float kRefStart = -3.402823466e38f;
 constexpr float kRefBelow = 6.0f;
 constexpr float kRefSlack = 14.0f;
+// The usual exponent is one fused s * fac - r, whose product is not rounded.  r is, and
+// where its steps pass kRefBelow (from 2^27) no r lies within reach of the largest
+// product: the exponent of the very key that set r would be anything up to half a step
+// of r.  From kRefCoarse on the product is rounded first, as the one r was made from,
+// so that the largest exponent is between 0 and 8.
+constexpr float kRefCoarse = 4194304.0f;
+__device__ __forceinline__ bool is_coarse(float ref) { return fabsf(ref) >= kRefCoarse && ref > kRefStart; }
+// The reference that a largest logit calls for.
+__device__ __forceinline__ float ref_for(float ref, float product, float fac) {
+  return fmaxf(ref, __fsub_rn(__fmul_rn(product, fac), kRefBelow));
+}
+__device__ __forceinline__ float coarse_exponent(float product, float fac, float ref) {
+  return __fsub_rn(__fmul_rn(product, fac), ref);
+}
 
 // The sequence's place: rows [q0, q0 + n_q) of q, `len` keys.
 struct KvSeq {

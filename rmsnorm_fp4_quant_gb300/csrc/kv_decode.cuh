@@ -453,6 +453,9 @@ kv_decode_kernel(const KvAttentionParams p) {
 #pragma unroll
         for (int e = 0; e < 4; ++e) acc[n][i][e] = 0.0f;
 
+    // a reference of the warp's rows is_coarse: its steps take the masked steps' code, where
+    // the product is rounded before the reference is taken from it
+    bool coarse = false;
     // one step, whose slots of the ring are constants
     auto work = [&](int step, auto phase) {
       constexpr int kPhase = decltype(phase)::value;
@@ -512,7 +515,7 @@ kv_decode_kernel(const KvAttentionParams p) {
 
       // exponents of 2 against the reference; keys that a row does not see get -inf
       float y[TP][NT][4];
-      bool over = false, edge = false;
+      bool over = false, edge = coarse;
 #pragma unroll
       for (int j = 0; j < TP; ++j) {
         edge |= key0[j] > lim_lo - 16;
@@ -527,8 +530,10 @@ kv_decode_kernel(const KvAttentionParams p) {
 #pragma unroll
           for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
+            for (int e = 0; e < 4; ++e) {
+              y[j][n][e] = coarse_exponent(s[j][n][e], fac[n][e & 1], ref[n][e & 1]);
               if (key0[j] + row_k + (e & 2) >= lim[n][e & 1]) y[j][n][e] = s[j][n][e] = -INFINITY;
+            }
       }
 #pragma unroll
       for (int j = 0; j < TP; ++j)
@@ -537,6 +542,7 @@ kv_decode_kernel(const KvAttentionParams p) {
 #pragma unroll
           for (int e = 0; e < 4; ++e) over |= y[j][n][e] > kRefSlack;
       if (__any_sync(kFullMask, over)) {         // rare after the first tiles
+        bool far = false;
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -545,22 +551,27 @@ kv_decode_kernel(const KvAttentionParams p) {
             if (TP == 2) m = fmaxf(m, fmaxf(s[TP - 1][n][e], s[TP - 1][n][e + 2]));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
-            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16)) * fac[n][e];
-            const float r = fmaxf(ref[n][e], m - kRefBelow);
+            m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
+            const float r = ref_for(ref[n][e], m, fac[n][e]);
             const float f = ex2(ref[n][e] - r);
             ref[n][e] = r;
+            far |= is_coarse(r);
             sum[n][e] *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
               acc[n][i][e] *= f;
               acc[n][i][e + 2] *= f;
             }
-#pragma unroll
-            for (int j = 0; j < TP; ++j)
-#pragma unroll
-              for (int k = e; k < 4; k += 2)
-                y[j][n][k] = s[j][n][k] == -INFINITY ? -INFINITY : fmaf(s[j][n][k], fac[n][e], -r);
           }
+        coarse = __any_sync(kFullMask, far);
+#pragma unroll
+        for (int j = 0; j < TP; ++j)
+#pragma unroll
+          for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              y[j][n][e] = s[j][n][e] == -INFINITY ? -INFINITY
+                                                   : coarse_exponent(s[j][n][e], fac[n][e & 1], ref[n][e & 1]);
       }
       uint32_t pb[TP][NT][2];
 #pragma unroll

@@ -296,6 +296,18 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim,
   return m;
 }
 
+// Multiplies 32 n columns of tensor memory, this thread's lane of them, by f.
+__device__ __forceinline__ void prefill_scale(uint32_t taddr, int n, float f) {
+#pragma unroll 1
+  for (int c = 0; c < n; ++c) {
+    uint32_t x[32];
+    tmem_load_32cols(taddr + 32 * c, x);
+#pragma unroll
+    for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__fmul_rn(__uint_as_float(x[i]), f));
+    tmem_store_32cols(taddr + 32 * c, x);
+  }
+}
+
 template <typename T, int D>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAttentionParams p, int splits) {
   using S = PrefillShape<D>;
@@ -424,6 +436,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     const int lim = ok ? limit_of(r) : 0;
     int lim_lo = ok ? lim : INT32_MAX;           // smallest of the warp's rows
     lim_lo = __reduce_min_sync(kFullMask, lim_lo);
+    constexpr int kCoarseRows = INT32_MIN;       // in lim_lo's place: a row's reference is_coarse, or was
     float ref = kRefStart, sum = 0.0f;
     bool alive = true;
     for (int j = 0; j < n[tile]; ++j) {
@@ -441,10 +454,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       tc_fence_after_sync();
       const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu;
       // the weights against the reference there is; where a row's sum passes the limit
-      // (rare after the first step, which begins with its maximum), once more
+      // (rare after the first step, which begins with its maximum), once more.  A warp that
+      // had a coarse reference begins every step so, and rounds S times the factor in place
+      // after it: the exponents' code is the usual one, with a factor of 1 (other code for
+      // such rows, or two roundings in the masked steps', made every call 1 to 2 % slower)
       uint32_t h[64];
       float step_sum;
-      bool moved = j == 0, last = j == 0;
+      bool moved = j == 0 || lim_lo == kCoarseRows, last = moved;
 #pragma unroll 1
       for (;;) {
         if (last) {
@@ -452,24 +468,21 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
                                : prefill_maximum<false>(ts, key0, lim, have);
           float f = 1.0f;
           if (moved && m > -INFINITY) {
-            const float to_ref = fmaxf(ref, m * fac - kRefBelow);
+            const float to_ref = ref_for(ref, m, fac);
             f = ex2(ref - to_ref);
             ref = to_ref;
             sum *= f;
           }
-          if (j > 0) {
-#pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t x[32];
-              tmem_load_32cols(to + 32 * c, x);
-#pragma unroll
-              for (int i = 0; i < 32; ++i) x[i] = __float_as_uint(__uint_as_float(x[i]) * f);
-              tmem_store_32cols(to + 32 * c, x);
-            }
+          if (j > 0) prefill_scale(to, D / 32, f);
+          if (lim_lo == kCoarseRows || __any_sync(kFullMask, is_coarse(ref))) {
+            lim_lo = kCoarseRows;
+            prefill_scale(ts, kPreKeys / 32, fac);
+            tmem_store_wait();
           }
         }
-        step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, fac, ref, h)
-                        : prefill_weights<false>(ts, key0, lim, have, fac, ref, h);
+        const float f = lim_lo == kCoarseRows ? 1.0f : fac;
+        step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, f, ref, h)
+                        : prefill_weights<false>(ts, key0, lim, have, f, ref, h);
         if (last) break;
         moved = !(step_sum <= kPreMostSum);
         if (!__any_sync(kFullMask, moved)) break;

@@ -548,6 +548,71 @@ def test_a_row_whose_logits_are_all_minus_infinity(T, D):
         assert torch.isfinite(out.cpu()[seen][:, keep]).all()
 
 
+# what one element of channel 0 makes of a logit: queries up to the ends of their types
+LOGIT_SIZES = [("bf16", x) for x in (3e4, 1e7, 1e9, 3e13, 1e20, 2e30, 1e33)] + [("fp16", 3e4)]
+
+
+@pytest.mark.parametrize("dtype,size", LOGIT_SIZES)
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("T", [1, 150])
+@pytest.mark.parametrize("zeros", [False, True])
+def test_logits_of_any_size(dtype, size, D, T, zeros):
+    """Keys and queries with one channel: a logit is one exact product, so equal keys share
+    a row's weight equally and the next smaller logit is more than 1000 below.  Rows of
+    either sign; the largest logit is in a first, a middle and the last key; the last row
+    of all sees one key of the largest negative logit; with zeros, 100 keys further on have
+    logits of 0, which are a negative row's largest.  In every launch shape."""
+    n, page = 500, 16
+    scale = 1.0 if dtype == "bf16" else 2.0 ** 13
+    cache = to_np(random_cache(-(-n // page), 1, page, D, 3))
+    k = np.zeros((n, 1, D), np.float32)
+    k[:, 0, 0] = np.where(np.arange(n) % 2, 2, 4)        # times +-size: the rows want 4 or 2
+    for j in (0, 201, 203, n - 1):
+        k[j, 0, 0] = 6 if j != 203 else 1
+    if zeros:
+        k[300:400] = 0
+    v = torch.randn(n, 1, D, generator=gen(5)).numpy()
+    okv.append(cache, k, v, np.arange(n))
+    values = okv.gather(cache, np.arange(n))[1][:, 0]
+    keys = okv.gather(cache, np.arange(n))[0][:, 0, 0]
+    q = torch.zeros(T, 4, D, dtype=torch.float64)
+    q[:, :, 0] = torch.tensor([1.0, -1.0, 0.25, -0.25]) * size
+    q = q.to(DT[dtype])
+    slim = np.arange(-(-n // page), dtype=np.int64)[None]
+    calls = [(1, t) for t in (slim, for_even_split(slim, T, 4, 1, D, page), for_ranges(slim, T, 4, 1, D, page))]
+    calls.append((times_for_items(1, T, 4, 1, D, slim.size * page) or 1, slim))
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    for seen_last in (n, 1):
+        for copies, tables in calls:
+            if tables is None:
+                continue
+            i32 = dict(dtype=torch.int32, device="cuda")
+            out, lse = fq.attention_nvfp4(q.repeat(copies, 1, 1).cuda(), dev,
+                                          torch.from_numpy(np.tile(tables, (copies, 1))).to(**i32),
+                                          torch.tensor([seen_last] * copies, **i32),
+                                          None if T == 1 else torch.arange(0, copies * T + 1, T, **i32),
+                                          sm_scale=scale, return_lse=True)
+            out, lse = out.double().cpu().numpy()[-T:], lse.double().cpu().numpy()[-T:]
+            for t in range(T):
+                seen = seen_last - T + t + 1
+                for h in range(4):
+                    if seen <= 0:
+                        assert np.all(out[t, h] == 0) and np.isneginf(lse[t, h])
+                        continue
+                    x = scale * float(q[t, h, 0]) * keys[:seen]
+                    best = x == x.max()
+                    assert np.max(x[~best], initial=-np.inf) < x.max() - 1000
+                    want = values[:seen][best].mean(0)
+                    # equal weights 1 / m in 11 bits and their fp32 sum, then the output's rounding
+                    tol = HALF_STEP[dtype] * np.abs(want) + \
+                        (2.0 ** -11 + best.sum() * 2.0 ** -22) * np.abs(values[:seen][best]).mean(0) + 2.0 ** -24
+                    assert np.all(np.abs(out[t, h] - want) <= tol), (t, h, seen_last)
+                    want = x.max() + np.log(best.sum())
+                    # 8 roundings of 2^-24: the factor's three, the product, the reference, the sum
+                    # with the logarithm, and the factor back
+                    assert abs(lse[t, h] - want) <= 2.0 ** -21 * (abs(want) + 1), (t, h, seen_last)
+
+
 @pytest.mark.parametrize("varlen", [False, True])
 def test_strided_queries_graphs_streams_and_repeats(varlen):
     """A column slice of a wider matrix as q; the same bits on repeats, on another
