@@ -470,8 +470,9 @@ FP4Q_API fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int
  *   out             [T, Hq, head_dim] dtype, dense, 32-byte aligned.  A row that sees no key is
  *                   0, with lse -inf.
  *   lse             [T, Hq] fp32 (natural logarithm), or NULL.
- *   workspace       at least fp4_attention_workspace_bytes(...) bytes, 16-byte aligned, any
- *                   contents; two calls that may run at the same time need one each.
+ *   workspace       at least fp4_attention_workspace_bytes(...) bytes (or _bound's, of the
+ *                   largest sizes), 16-byte aligned, any contents; two calls that may run at
+ *                   the same time need one each.
  *   status, pdl     as in fp4_add_rmsnorm_quant_ex.
  * Lengths and tables are read on the device, so a captured call follows them.
  * Rows that a kernel gave up on (a bounded wait ran out: status) are NaN, lse too.
@@ -487,10 +488,20 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
                                           int64_t workspace_bytes, int32_t* status, int pdl,
                                           fp4q_stream_t stream);
 
-/* Bytes of workspace fp4_attention_nvfp4 needs for these sizes on the current
+/* Bytes of workspace fp4_attention_nvfp4 needs for exactly these sizes on the current
  * device (152 SMs taken when none is visible); max_keys = max_pages * page_size of its
- * call.  0 or more (0: none, workspace may be NULL), -1 on bad arguments. */
+ * call.  0 or more (0: none, workspace may be NULL), -1 on bad arguments.  A call with
+ * fewer rows, sequences or keys may need more: one that fills the device by itself needs
+ * none, one that has to cut its keys into ranges does. */
 FP4Q_API int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
+                                               int64_t head_dim, int64_t max_keys);
+
+/* Bytes that are enough for every call of at most B sequences, T query rows and
+ * max_keys keys with these heads on the current device: what a program allocates once.
+ * Grows with each size up to 4096 * SMs * (head_dim + 2) bytes (81 MB with 152 SMs and 128
+ * channels), or to 8 bytes per sequence and per 8 rows of every key/value head where that
+ * is more.  -1 on bad arguments. */
+FP4Q_API int64_t fp4_attention_workspace_bound(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
                                                int64_t head_dim, int64_t max_keys);
 
 /*

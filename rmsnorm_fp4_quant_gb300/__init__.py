@@ -56,6 +56,7 @@ from ._binding import (  # noqa: F401
     fp4_add_rmsnorm_quant_gs,
     fp4_attention_launch_shape,
     fp4_attention_nvfp4,
+    fp4_attention_workspace_bound,
     fp4_attention_workspace_bytes,
     fp4_dequant,
     fp4_gemm_mxfp4_bf16,

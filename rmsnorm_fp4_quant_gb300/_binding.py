@@ -145,6 +145,8 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_attention_nvfp4.restype = ci
     L.fp4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
     L.fp4_attention_workspace_bytes.restype = i64
+    L.fp4_attention_workspace_bound.argtypes = [i64, i64, i64, i64, i64, i64]
+    L.fp4_attention_workspace_bound.restype = i64
     L.fp4_attention_launch_shape.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
     L.fp4_attention_launch_shape.restype = ci
     L.fp4_debug_build.argtypes = []
@@ -278,6 +280,14 @@ def fp4_attention_nvfp4(q_ptr: int, q_stride: int, cache: KVCacheStruct, block_t
 def fp4_attention_workspace_bytes(B: int, T: int, Hq: int, num_kv_heads: int, head_dim: int,
                                   max_keys: int) -> int:
     return lib().fp4_attention_workspace_bytes(B, T, Hq, num_kv_heads, head_dim, max_keys)
+
+
+def fp4_attention_workspace_bound(B: int, T: int, Hq: int, num_kv_heads: int, head_dim: int,
+                                  max_keys: int) -> int:
+    """Bytes that are enough for every call of at most these sizes, what a program
+    allocates once (fp4_attention_workspace_bytes is for one call: a smaller call may
+    need more than a larger one)."""
+    return lib().fp4_attention_workspace_bound(B, T, Hq, num_kv_heads, head_dim, max_keys)
 
 
 def fp4_read_device_status(status_ptr: int, stream: int) -> int:
@@ -824,7 +834,8 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     head_dim ** -0.5.  A row that sees no key gives 0 and lse -inf; rows of no
     sequence are left as they were.  Returns out, or (out, lse) with return_lse
     (lse (T, heads) fp32, natural logarithm).  workspace: optional uint8 tensor of
-    fp4_attention_workspace_bytes bytes, for one call at a time."""
+    fp4_attention_workspace_bytes bytes (one for calls of several sizes:
+    fp4_attention_workspace_bound), for one call at a time."""
     torch = _torch()
     struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
     shape, dtype = q.shape, q.dtype

@@ -201,6 +201,13 @@ int64_t fp4_attention_workspace_bytes(int64_t B, int64_t T, int64_t Hq, int64_t 
                                 static_cast<int>(num_kv_heads), static_cast<int>(head_dim), max_keys);
 }
 
+int64_t fp4_attention_workspace_bound(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
+                                      int64_t head_dim, int64_t max_keys) {
+  if (!valid_attention_sizes(B, T, Hq, num_kv_heads, head_dim, max_keys)) return -1;
+  return kv_attention_workspace_bound(sm_count_current_device(), B, T, static_cast<int>(Hq),
+                                      static_cast<int>(num_kv_heads), static_cast<int>(head_dim), max_keys);
+}
+
 fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_heads,
                                         int64_t head_dim, int64_t max_keys, int64_t out[2]) {
   if (!valid_attention_sizes(B, T, Hq, num_kv_heads, head_dim, max_keys) || !B || !T || !out)

@@ -1,6 +1,7 @@
 // kv_attention.cu - attention over the paged NVFP4 key/value cache: choice of
 // kernel and launch.
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -240,6 +241,21 @@ int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads,
                                           : decode_workspace<128, 2>(sms, B, T, group, heads);
   return decode_tiles(B, T, group) == 1 ? decode_workspace<64, 1>(sms, B, T, group, heads)
                                         : decode_workspace<64, 2>(sms, B, T, group, heads);
+}
+
+// The decode kernel's size grows with B and T.  The other's is splits * T * Hq * (D + 2)
+// floats, where the splits are those that prefill_splits may choose: items * splits <= 4
+// SMs, and the items are T * Hq / 256 or more.
+int64_t kv_attention_workspace_bound(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys) {
+  if (B == 0 || T == 0) return 0;
+  const int group = Hq / heads;
+  const int64_t decode = D == 128 ? std::max(decode_workspace<128, 1>(sms, B, T, group, heads),
+                                             decode_workspace<128, 2>(sms, B, T, group, heads))
+                                  : std::max(decode_workspace<64, 1>(sms, B, T, group, heads),
+                                             decode_workspace<64, 2>(sms, B, T, group, heads));
+  const int64_t splits = std::min<int64_t>(kPreMostSplits, (keys + kPreKeys - 1) / kPreKeys);
+  const int64_t rows = splits > 1 ? std::min<int64_t>(splits * T * Hq, 4LL * sms * kPreRows) : 0;
+  return std::max(decode, rows * (D + 2) * 4);
 }
 
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl,

@@ -85,6 +85,8 @@ cudaError_t launch_kv_gather(int dtype, const KvGatherParams& p, int pdl, cudaSt
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream);
 // Bytes for sequences of at most `keys` keys.
 int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys);
+// Bytes for every call of at most B sequences, T rows and `keys` keys.
+int64_t kv_attention_workspace_bound(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys);
 // fp4_attention_launch_shape (B and T not zero).
 void kv_attention_shape(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys, int64_t out[2]);
 

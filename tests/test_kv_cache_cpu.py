@@ -145,6 +145,25 @@ def test_workspace_sizes():
         assert attention(ws=at(5), **kw) == 1 and attention(ws=at(0), **kw) == 1
 
 
+@pytest.mark.parametrize("Hq,Hkv,D", [(32, 8, 128), (12, 2, 64), (24, 24, 64), (17, 1, 128), (1, 1, 128), (256, 2, 64)])
+def test_one_workspace_for_every_smaller_call(Hq, Hkv, D):
+    """The exact size is not monotone; the bound is, and covers every call below it."""
+    exact, bound = fq.fp4_attention_workspace_bytes, fq.fp4_attention_workspace_bound
+    sizes = [1, 2, 3, 7, 16, 17, 60, 100, 256, 300, 512, 1024, 2048, 5000]
+    keys = [0, 16, 128, 144, 512, 4096, 20000, 131072, 1 << 20]
+    most = {}                                    # the largest call below each size
+    for i, B in enumerate(sizes):
+        for j, T in enumerate(sizes):
+            for k, n in enumerate(keys):
+                here = [exact(B, T, Hq, Hkv, D, n)] + [most.get(x, 0) for x in ((i - 1, j, k), (i, j - 1, k), (i, j, k - 1))]
+                most[i, j, k] = max(here)
+                assert most[i, j, k] <= bound(B, T, Hq, Hkv, D, n), (B, T, n)
+                assert bound(B, T, Hq, Hkv, D, n) <= bound(B + 1, T + 3, Hq, Hkv, D, n + 16)
+    assert any(exact(1, sizes[j], Hq, Hkv, D, 131072) > exact(1, 5000, Hq, Hkv, D, 131072) for j in range(len(sizes)))
+    assert bound(0, 0, Hq, Hkv, D, 512) == 0 and bound(-1, 4, Hq, Hkv, D, 512) == -1
+    assert bound(4, 4, Hq, Hkv, 96, 512) == -1 and bound(4, 4, 8192, Hkv, D, 512) == -1
+
+
 def test_the_struct_matches_the_header():
     assert ctypes.sizeof(fq.KVCacheStruct) == 6 * ctypes.sizeof(ctypes.c_void_p) + 4 * 8
 

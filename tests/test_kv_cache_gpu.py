@@ -783,6 +783,27 @@ def test_one_workspace_for_calls_in_a_row():
         fq.attention_nvfp4(qs[0], dev, tab, sl, cu, workspace=ws[:16])
 
 
+def test_one_workspace_of_the_largest_size():
+    """A workspace for the largest call takes the smaller ones that need more than it."""
+    D, Hq, Hkv, page = 64, 8, 1, 16
+    lens = [2000]
+    cache, tables = fill_sequences(lens, Hkv, D, page, seed=3)
+    wide = np.full((1, 2048), -7, tables.dtype)
+    wide[:, :tables.shape[1]] = tables
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(wide.astype(np.int32)).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    size = [fq.fp4_attention_workspace_bytes(1, T, Hq, Hkv, D, 2048 * page) for T in (20000, 300, 1)]
+    assert size[0] < size[1]
+    ws = torch.full((fq.fp4_attention_workspace_bound(1, 20000, Hq, Hkv, D, 2048 * page),), 255, dtype=torch.uint8,
+                    device="cuda")
+    for T in (20000, 300, 1):
+        q = queries(T, Hq, D, "bf16", T).cuda()
+        cu = torch.tensor([0, T], dtype=torch.int32, device="cuda")
+        got = fq.attention_nvfp4(q, dev, tab, sl, cu, workspace=ws, causal=False)
+        assert torch.equal(got, fq.attention_nvfp4(q, dev, tab, sl, cu, causal=False))
+
+
 def test_tensor_calls_refuse_what_they_cannot_take():
     T, Hq, Hkv, D = 3, 4, 2, 64
     c = fq.kv_cache_nvfp4(4, 16, Hkv, D)
