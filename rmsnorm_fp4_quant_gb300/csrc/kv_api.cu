@@ -36,6 +36,10 @@ bool rows_overlap(const Rows& a, const Rows& b) {
   return off < a.width || off + b.width > a.stride;
 }
 
+// Whether n rows, `stride` 16-bit elements apart, span bytes that 64 bits number: the
+// overlaps above could not be seen otherwise.
+bool spans_64_bits(int64_t n, int64_t stride) { return n <= 1 || stride <= INT64_MAX / 4 / n; }
+
 struct CacheBuffers {
   Rows rows[4];
 };
@@ -112,6 +116,10 @@ fp4_status_t fp4_kv_append_nvfp4(const void* q, int64_t q_stride, void* out_q,
   if ((q && (q_stride < Hq * D || out_q_stride < Hq * D)) || k_stride < Hkv * D ||
       v_stride < Hkv * D)
     return FP4_ERR_INVALID_ARG;
+  if (!spans_64_bits(T, k_stride) || !spans_64_bits(T, v_stride) ||
+      (q && (!spans_64_bits(T, q_stride) || !spans_64_bits(T, out_q_stride))) ||
+      (rot_dim && max_position > INT64_MAX / 8 / rot_dim))
+    return FP4_ERR_UNSUPPORTED_SHAPE;
   if (T == 0) return FP4_OK;
   if (!k || !v || !slots || (rot_dim && (!positions || !cos_sin))) return FP4_ERR_INVALID_ARG;
   const fp4_status_t cb = check_cache_buffers(cache);
@@ -234,7 +242,7 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   if (q_stride == 0) q_stride = Hq * D;
   if (q_stride < Hq * D) return FP4_ERR_INVALID_ARG;
   if (!cu_seqlens_q && B != T) return FP4_ERR_INVALID_ARG;
-  if (max_pages > INT32_MAX / 2 / cache->page_size ||
+  if (max_pages > INT32_MAX / 2 / cache->page_size || !spans_64_bits(T, q_stride) ||
       !numbered_in_32_bits(B, T, Hq, Hkv, max_pages * cache->page_size))
     return FP4_ERR_UNSUPPORTED_SHAPE;
   if (B == 0 || T == 0) return FP4_OK;

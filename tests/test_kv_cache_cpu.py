@@ -73,6 +73,15 @@ def test_append_refusals(kw, status):
     assert append(**kw) == status
 
 
+@pytest.mark.parametrize("kw", [
+    dict(maxp=1 << 60), dict(maxp=(1 << 63) - 1), dict(ks=1 << 61), dict(vs=1 << 61), dict(qs=1 << 61),
+    dict(oqs=1 << 61), dict(ks=(1 << 63) - 16)])
+def test_append_refuses_extents_beyond_64_bits(kw):
+    """Whose overlaps could not be told."""
+    assert append(**kw) == 2
+    assert append(oq=at(8) + 64, maxp=1 << 60) == 2
+
+
 def test_append_refuses_shared_cache_buffers():
     assert append(cache(v_packed=at(0) + 64)) == 1
     assert append(cache(k_sf=at(2))) == 1
@@ -123,6 +132,11 @@ def test_attention_refuses_bad_caches(kw, status):
 ])
 def test_attention_refusals(kw, status):
     assert attention(**kw) == status
+
+
+def test_attention_refuses_extents_beyond_64_bits():
+    for qs in (1 << 61, (1 << 63) - 16):
+        assert attention(qs=qs) == 2
 
 
 def test_workspace_sizes():
