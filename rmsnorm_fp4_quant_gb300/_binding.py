@@ -734,7 +734,7 @@ def _kv_dtype(torch, dtype) -> int:
 def _kv_stream(torch, stream, dev) -> int:
     if stream is not None:
         return stream.cuda_stream
-    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # without a Stream object
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)     # skips the Stream object
     return raw(dev) if raw is not None else torch.cuda.current_stream(dev).cuda_stream
 
 
@@ -879,11 +879,17 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     lse_ptr = _dense_ptr(lse, "lse", dev, torch.float32, (T, hq)) if lse is not None else 0
     dt, scale = _kv_dtype(torch, dtype), float(sm_scale) if sm_scale is not None else dim ** -0.5
     handle = _kv_stream(torch, stream, dev)
-    own_ws = 0
+    own_ws = held = 0
     if size and not ws:
-        # from the caching allocator's own calls, which skip the tensor (0.8 us against
-        # 3.6 after a launch); given back below in the order of the kernels' stream
-        ws = own_ws = torch._C._cuda_cudaCachingAllocator_raw_alloc(size, handle)
+        raw = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+        if raw is not None:
+            # the caching allocator's own calls, which skip the tensor (0.8 us against 3.6
+            # after a launch); given back below in the order of the kernels' stream
+            ws = own_ws = raw(size, handle)
+        else:
+            with _on(stream):
+                held = torch.empty(size, dtype=torch.uint8, device=q.device)
+            ws = held.data_ptr()
     try:
         st = L.fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
                                    dt, scale, 1 if causal else 0, out_ptr, lse_ptr, ws, size,

@@ -783,6 +783,25 @@ def test_one_workspace_for_calls_in_a_row():
         fq.attention_nvfp4(qs[0], dev, tab, sl, cu, workspace=ws[:16])
 
 
+def test_without_the_private_calls_of_torch(monkeypatch):
+    """The short cuts to the allocator and the current stream have a public way beside them."""
+    cache, tables = fill_sequences([300], 1, 64, 16, seed=3)
+    tables = for_even_split(tables, 1, 4, 1, 64, 16)
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    assert fq.fp4_attention_workspace_bytes(1, 1, 4, 1, 64, tab.shape[1] * 16) > 0
+    sl = torch.tensor([300], dtype=torch.int32, device="cuda")
+    q = queries(1, 4, 64, "bf16", 1).cuda()
+    want = fq.attention_nvfp4(q, dev, tab, sl)
+    for name in ("_cuda_cudaCachingAllocator_raw_alloc", "_cuda_getCurrentRawStream"):
+        monkeypatch.delattr(torch._C, name, raising=False)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.default_stream())
+    got = [fq.attention_nvfp4(q, dev, tab, sl), fq.attention_nvfp4(q, dev, tab, sl, stream=side)]
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want) and torch.equal(got[1], want)
+
+
 def test_one_workspace_of_the_largest_size():
     """A workspace for the largest call takes the smaller ones that need more than it."""
     D, Hq, Hkv, page = 64, 8, 1, 16
