@@ -42,6 +42,14 @@ __device__ __forceinline__ float coarse_exponent(float product, float fac, float
   return __fsub_rn(__fmul_rn(product, fac), ref);
 }
 
+// Entries of the call's small arrays (0 for one outside: the debug build's checks).
+__device__ __forceinline__ int kv_len(const KvAttentionParams& p, int b) {
+  return FP4Q_IN_RANGE(p, p.seq_lens + b, 4, p.seq_lens, 4LL * p.B) ? p.seq_lens[b] : 0;
+}
+__device__ __forceinline__ int kv_cu(const KvAttentionParams& p, int b) {
+  return FP4Q_IN_RANGE(p, p.cu + b, 4, p.cu, 4LL * (p.B + 1)) ? p.cu[b] : 0;
+}
+
 // The sequence's place: rows [q0, q0 + n_q) of q, `len` keys.
 struct KvSeq {
   int q0;
@@ -51,12 +59,11 @@ struct KvSeq {
 __device__ __forceinline__ KvSeq kv_sequence(const KvAttentionParams& p, int b) {
   KvSeq s;
   const int limit = static_cast<int>(p.max_pages) * p.c.page_size;
-  const int len = p.seq_lens[b];
-  s.len = min(max(len, 0), limit);
+  s.len = min(max(kv_len(p, b), 0), limit);
   if (p.cu) {
     const int T = static_cast<int>(p.T);
-    s.q0 = min(max(p.cu[b], 0), T);
-    s.n_q = max(min(p.cu[b + 1], T) - s.q0, 0);
+    s.q0 = min(max(kv_cu(p, b), 0), T);
+    s.n_q = max(min(kv_cu(p, b + 1), T) - s.q0, 0);
   } else {
     s.q0 = b;
     s.n_q = 1;

@@ -110,10 +110,10 @@ __global__ void __launch_bounds__(128, ROT ? 5 : 7) kv_append_kernel(const KvApp
     if (FP4Q_IN_RANGE(p, src + c1 * 16, 32, base, extent)) x1 = ld_stream_rw(src + c1 * 16);
   };
   load(h);
-  const int64_t slot = p.slots[t];
+  const int64_t slot = FP4Q_IN_RANGE(p, p.slots + t, 8, p.slots, 8LL * p.T) ? p.slots[t] : -1;
   float cs[16], sn[16];
   if (ROT) {
-    const int64_t pos = p.positions[t];
+    const int64_t pos = FP4Q_IN_RANGE(p, p.positions + t, 8, p.positions, 8LL * p.T) ? p.positions[t] : -1;
     if (pos < 0 || pos >= p.max_position) return;   // the whole token is left out
     if (rotated) {
       const float* row = p.cos_sin + pos * p.rot + u * 16;
@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(128) kv_gather_kernel(const KvGatherParams p, 
   if (t >= p.T) return;
   griddep_wait();
   griddep_launch_dependents();
-  const int64_t slot = p.slots[t];
+  const int64_t slot = FP4Q_IN_RANGE(p, p.slots + t, 8, p.slots, 8LL * p.T) ? p.slots[t] : -1;
   if (slot < 0 || slot >= p.c.num_pages * p.c.page_size) return;
   const uint32_t page = static_cast<uint32_t>(slot) / p.c.page_size;
   const uint32_t in_page = static_cast<uint32_t>(slot) - page * p.c.page_size;

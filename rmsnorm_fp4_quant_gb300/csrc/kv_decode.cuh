@@ -152,7 +152,7 @@ __device__ __forceinline__ void decode_write(const KvAttentionParams& p, const K
 template <int ROWS>
 __device__ __forceinline__ int decode_sequence(const KvAttentionParams& p, int64_t rs, int64_t& tile) {
   auto slots_from = [&](int b) {
-    const int64_t q0 = p.cu ? min(max(p.cu[b], 0), static_cast<int>(p.T)) : b;
+    const int64_t q0 = p.cu ? min(max(kv_cu(p, b), 0), static_cast<int>(p.T)) : b;
     return q0 * p.group / ROWS + b;
   };
   int b = 0, hi = p.B - 1;
@@ -788,12 +788,16 @@ __global__ void __launch_bounds__(kJoinMost) kv_decode_join_kernel(const KvAtten
   if (rt < 0 || rt * ROWS + r >= rows) return;
   const int row = static_cast<int>(rt) * ROWS + r;
   const int* desc = reinterpret_cast<const int*>(p.ws + 2 * static_cast<int64_t>(ctas) * S::kPart) + 2 * slot;
+  if (!FP4Q_IN_RANGE(p, desc, 8, p.ws, p.ws_bytes)) return;
   const int c0 = desc[0], n = desc[1];
   if (n <= 1 || c0 < 0 || n > ctas - c0) return;
   // part i: the last of CTA c0 for i = 0, the first of CTA c0 + i else
   auto part = [&](int i) { return p.ws + (2 * static_cast<int64_t>(c0 + i) + (i == 0 ? 1 : 0)) * S::kPart; };
   float top = kRefStart;
-  for (int i = tid; i < n; i += blockDim.x) top = fmaxf(top, part(i)[ROWS * D + 2 * r]);
+  for (int i = tid; i < n; i += blockDim.x) {
+    const float* ref = part(i) + ROWS * D + 2 * r;
+    if (FP4Q_IN_RANGE(p, ref, 4, p.ws, p.ws_bytes)) top = fmaxf(top, *ref);
+  }
 #pragma unroll
   for (int o = 16; o; o >>= 1) top = fmaxf(top, __shfl_xor_sync(kFullMask, top, o));
   if ((tid & 31) == 0) red[tid >> 5] = top;
@@ -805,6 +809,9 @@ __global__ void __launch_bounds__(kJoinMost) kv_decode_join_kernel(const KvAtten
 #pragma unroll 4
   for (int i = grp; i < n; i += groups) {
     const float* q = part(i);
+    if (!FP4Q_IN_RANGE(p, q + ROWS * D + 2 * r, 8, p.ws, p.ws_bytes) ||
+        !FP4Q_IN_RANGE(p, q + r * D + 4 * ln, 16, p.ws, p.ws_bytes))
+      continue;
     const float2 rl = *reinterpret_cast<const float2*>(q + ROWS * D + 2 * r);
     const float4 x = *reinterpret_cast<const float4*>(q + r * D + 4 * ln);
     const float f = ex2(rl.x - top);

@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   const int kvh = static_cast<int>(blockIdx.x % p.c.heads);
   const int64_t rs = prefill_row_slots(p.B, p.T, p.group) - 1 - blockIdx.x / p.c.heads;
   auto slots_from = [&](int b) {
-    const int64_t q0 = p.cu ? min(max(p.cu[b], 0), static_cast<int>(p.T)) : b;
+    const int64_t q0 = p.cu ? min(max(kv_cu(p, b), 0), static_cast<int>(p.T)) : b;
     return q0 * p.group / kPreRows + b;
   };
   int b = 0, b_hi = p.B - 1;
@@ -694,7 +694,7 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttentionP
     int b = 0, hi = p.B - 1;
     while (b < hi) {
       const int mid = (b + hi + 1) / 2;
-      if (p.cu[mid] <= t) b = mid; else hi = mid - 1;
+      if (kv_cu(p, mid) <= t) b = mid; else hi = mid - 1;
     }
     // of several sequences that begin at one row all but the last are empty
     const KvSeq s = kv_sequence(p, b);
@@ -702,11 +702,18 @@ __global__ void __launch_bounds__(256) kv_prefill_join_kernel(const KvAttentionP
   }
   if (!mine) return;
   float top = kRefStart;
-  for (int i = 0; i < splits; ++i) top = fmaxf(top, p.ws[splits * total * D + 2 * (i * total + at)]);
+  const float* stats = p.ws + splits * total * D;
+  for (int i = 0; i < splits; ++i) {
+    const float* ref = stats + 2 * (i * total + at);
+    if (FP4Q_IN_RANGE(p, ref, 4, p.ws, p.ws_bytes)) top = fmaxf(top, *ref);
+  }
   float4 o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   float l = 0.0f;
   for (int i = 0; i < splits; ++i) {
-    const float2 rl = *reinterpret_cast<const float2*>(p.ws + splits * total * D + 2 * (i * total + at));
+    if (!FP4Q_IN_RANGE(p, stats + 2 * (i * total + at), 8, p.ws, p.ws_bytes) ||
+        !FP4Q_IN_RANGE(p, p.ws + (i * total + at) * D + 4 * ln, 16, p.ws, p.ws_bytes))
+      continue;
+    const float2 rl = *reinterpret_cast<const float2*>(stats + 2 * (i * total + at));
     if (rl.y == 0.0f) continue;                  // saw no key: its O was not written
     const float4 x = *reinterpret_cast<const float4*>(p.ws + (i * total + at) * D + 4 * ln);
     const float f = ex2(rl.x - top);

@@ -948,3 +948,33 @@ def test_debug_build_finds_no_access_out_of_bounds():
             assert bad.item() > n1
     finally:
         L.fp4_debug_configure(2_000_000_000, 0, 0, -1, -1, None)
+
+
+def test_debug_build_checks_every_attention_kernel():
+    """One CTA or cluster an item, the even split, 256-row items, ranges of keys: no access
+    out of bounds, and with every extent one byte shorter the last accesses are seen (the
+    lengths, the tables, queries, cache, outputs and workspace end where the call says)."""
+    fbuild.build(debug=True)
+    L = fq.debug_lib()
+    bad = torch.zeros(1, dtype=torch.int32, device="cuda")
+    D, page, lens = 64, 16, [300, 40, 170]
+    few, many = 4, 256                                   # rows of a key/value head
+    cache, tables = fill_sequences(lens, 1, D, page, seed=1)
+    n = times_for_items(3, 3, many, 1, D, tables.shape[1] * page)
+    calls = [(few, tables, 1), (few, for_even_split(tables, 3, few, 1, D, page), 1),
+             (many, tables, n), (many, for_ranges(tables, 3, many, 1, D, page), 1)]
+    assert shape_of(3, 3, few, 1, D, tables.shape[1] * page)["parts"] > 0
+    dev = [torch.from_numpy(x).cuda() for x in cache]
+    try:
+        with fq.using_library(L):
+            for shrink in (0, 1):
+                for Hq, tab, copies in calls:
+                    assert L.fp4_debug_configure(2_000_000_000, shrink, 0, -1, -1, bad.data_ptr()) == 0
+                    before = bad.item()
+                    fq.attention_nvfp4(queries(3 * copies, Hq, D, "bf16", 2).cuda(), dev,
+                                       torch.from_numpy(np.tile(tab, (copies, 1)).astype(np.int32)).cuda(),
+                                       torch.tensor(lens * copies, dtype=torch.int32, device="cuda"), return_lse=True)
+                    torch.cuda.synchronize()
+                    assert (bad.item() > before) == bool(shrink), (Hq, copies, tab.shape)
+    finally:
+        L.fp4_debug_configure(2_000_000_000, 0, 0, -1, -1, None)
