@@ -691,6 +691,101 @@ def test_offsets_beyond_32_bits():
 
 
 # ---------------------------------------------------------------------------
+# every key counts: equal weights
+# ---------------------------------------------------------------------------
+def equal_cache(lens, Hkv, D, page, seed):
+    """Values of +-6 at random (one code, scale 1), keys of any finite bytes, garbage behind
+    the ends; (cache, tables, running sums of the signs per sequence: [n + 1, Hkv, D])."""
+    rng = np.random.default_rng(seed)
+    used = [-(-n // page) for n in lens]
+    pages = sum(used) + 2
+    bits = lambda *s: rng.integers(0, 256, (pages, Hkv, *s), dtype=np.uint8)  # noqa: E731
+    cache = [bits(page, D // 2), bits(page, D // 16) & 0x77, bits(page, D // 2), np.full((pages, Hkv, D // 16, page), 0xFF, np.uint8)]
+    order = rng.permutation(pages)
+    tables = np.full((len(lens), max(used + [1])), -1, np.int64)
+    sums, at = [], 0
+    for b, n in enumerate(lens):
+        tables[b, :used[b]] = order[at:at + used[b]]
+        at += used[b]
+        minus = rng.integers(0, 2, (n, Hkv, D), dtype=np.uint8)
+        code = 7 + 8 * minus
+        pg, i = tables[b][np.arange(n) // page], np.arange(n) % page
+        cache[2][pg, :, i] = code[..., 0::2] | code[..., 1::2] << 4
+        cache[3][pg, :, :, i] = 0x38
+        if n % page:                                        # keys behind the end: scales that are no numbers
+            cache[1][tables[b, used[b] - 1], :, n % page:] = 0x7F
+        sums.append(np.concatenate([np.zeros((1, Hkv, D), np.int32), (1 - 2 * minus.astype(np.int32)).cumsum(0, dtype=np.int32)]))
+    return cache, tables, sums
+
+
+def check_equal(lens, q_lens, causal, Hq, Hkv, D, page, shape, seed):
+    """Queries of 0: every logit is 0 and every weight 2^6, exact in 16 bits as in the sums,
+    which stay below 2^24.  So lse is log(n) but for log2, a sum and a product in 32 bits, and
+    out the mean of the values but for a reciprocal, a product and its rounding: one key lost
+    or taken twice moves all channels of a row by more."""
+    cache, tables, sums = equal_cache(lens, Hkv, D, page, seed)
+    cu = None if q_lens is None else np.cumsum([0] + q_lens)
+    T = len(lens) if cu is None else int(cu[-1])
+    tables = widened(tables, T, Hq, Hkv, D, page, shape)
+    out, lse = fq.attention_nvfp4(torch.zeros(T, Hq, D, dtype=torch.float16, device="cuda"),
+                                  [torch.from_numpy(c).cuda() for c in cache],
+                                  torch.from_numpy(tables.astype(np.int32)).cuda(),
+                                  torch.tensor(lens, dtype=torch.int32, device="cuda"),
+                                  None if cu is None else torch.from_numpy(cu.astype(np.int32)).cuda(),
+                                  causal=causal, return_lse=True)
+    out, lse = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, n in enumerate(lens):
+        rows = np.arange(b, b + 1) if cu is None else np.arange(cu[b], cu[b + 1])
+        seen = np.clip(n - len(rows) + 1 + np.arange(len(rows)), 0, n) if causal else np.full(len(rows), n)
+        some = seen > 0
+        assert np.all(out[rows[~some]] == 0) and np.all(np.isneginf(lse[rows[~some]]))
+        rows, seen = rows[some], seen[some].astype(np.float64)
+        want = np.repeat(6 * sums[b][seen.astype(int)] / seen[:, None, None], Hq // Hkv, 1)
+        # the rounding to 16 bits (below its normals: absolute) and two of 2^-24, doubled
+        tol = (2.0 ** -11 + 2.0 ** -22) * np.abs(want) + 2.0 ** -25
+        assert np.all(np.abs(out[rows] - want) <= tol), b
+        assert np.all(tol < 0.5 * (6 - np.abs(want)) / seen[:, None, None], where=np.abs(want) < 5.9)
+        # log2 of 64 n: a unit (2^-19 up to 32), the sum with the reference half of one, the product
+        ltol = 1.5 * 2.0 ** -19 + 2.0 ** -23 * np.log(seen)
+        assert np.all(np.abs(lse[rows] - np.log(seen)[:, None]) <= ltol[:, None]), b
+        assert np.all(ltol < 0.5 * np.log1p(1 / seen))
+
+
+@pytest.mark.parametrize("D", [64, 128])
+@pytest.mark.parametrize("group", [2, 12])
+@pytest.mark.parametrize("parts", [0, 1, 2, 3, 4, 6, 8])
+def test_every_key_counts_once_in_each_share(D, group, parts):
+    """Lengths around the edges of tiles, units and shares, for every way to share an item."""
+    B, Hkv, longest = next((B, Hkv, n) for n in (400, 700, 1000, 1500, 2200, 3000, 6000, 12000)
+                           for B in (1, 2, 4, 6, 9, 12, 16, 20, 26) for Hkv in (1, 2, 4, 8)
+                           if shape_of(B, B, Hkv * group, Hkv, D, n)["parts"] == parts)
+    for shift in (0, 1, 63):
+        less = [0, 1, 15, 16, 17, 31, 33, 47, 63, 64, 65, 79, 127, 128, 129, 191, 193, 255, 256, 257, 300, 320, 350, 399]
+        lens = [max(0, longest - shift - x) for x in less][:B] + [longest // 2] * (B - len(less))
+        check_equal(lens, None, True, Hkv * group, Hkv, D, 16, lambda s: s["parts"] == parts, seed=shift)
+
+
+@pytest.mark.parametrize("lens,Hq,Hkv,D,page", [
+    ([40001], 4, 1, 128, 16), ([12345], 12, 1, 64, 48), ([5000, 9001, 3, 0, 20050], 12, 2, 64, 64),
+    ([30000 - 13 * i for i in range(7)], 3, 3, 128, 128), ([17 * i for i in range(400)], 2, 1, 64, 16),
+])
+def test_every_key_counts_once_in_the_even_split(lens, Hq, Hkv, D, page):
+    check_equal(lens, None, True, Hq, Hkv, D, page, lambda s: s == {"kernel": "kv_decode_kernel", "parts": 0}, seed=1)
+
+
+@pytest.mark.parametrize("lens,q_lens,Hq,Hkv,D,page,ranges", [
+    ([5000, 2049, 127], [300, 129, 300], 4, 1, 128, 16, True), ([12801], [257], 3, 1, 64, 48, True),
+    ([4096, 4095, 4097, 128], [128, 129, 127, 200], 6, 2, 128, 128, True),
+    ([1024, 1023, 1025, 1000], [600, 513, 1025, 64], 48, 24, 64, 16, False),
+    ([2000, 1921], [700, 650], 48, 12, 128, 64, False),
+])
+@pytest.mark.parametrize("causal", [True, False])
+def test_every_key_counts_once_for_many_rows(lens, q_lens, Hq, Hkv, D, page, ranges, causal):
+    check_equal(lens, q_lens, causal, Hq, Hkv, D, page,
+                lambda s: s["kernel"] == "kv_prefill_kernel" and (s["parts"] > 1) == ranges, seed=2)
+
+
+# ---------------------------------------------------------------------------
 # together, as a serving step uses them
 # ---------------------------------------------------------------------------
 @pytest.mark.parametrize("pdl", [False, True])
