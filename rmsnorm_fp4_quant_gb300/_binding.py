@@ -755,6 +755,8 @@ def kv_append_nvfp4(cache, k, v, slots, q=None, positions=None, cos_sin=None,
     channels 2i and 2i + 1 instead of i and i + rot_dim/2.  out_q: may be q itself."""
     torch = _torch()
     struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
+    if k.dim() != 3 or (q is not None and q.dim() != 3):
+        raise ValueError("q, k and v must be (T, heads, head_dim)")
     T, dtype = k.shape[0], k.dtype
     dt = _kv_dtype(torch, dtype)
     ks = _head_rows(k, "k", dev, T, heads, dim, dtype)
@@ -801,6 +803,8 @@ def kv_gather_nvfp4(cache, slots, dtype=None, k_global_scale=None, v_global_scal
     if dtype is None:
         dtype = out_k.dtype if out_k is not None else out_v.dtype if out_v is not None \
             else torch.bfloat16
+    if slots.dim() != 1:
+        raise ValueError("slots must be (T,)")
     T = slots.shape[0]
     shape = (T, heads, dim)
     if out_k is None or out_v is None:

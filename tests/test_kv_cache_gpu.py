@@ -957,6 +957,27 @@ def test_tensor_calls_refuse_what_they_cannot_take():
     assert torch.all(out == 0) and torch.all(torch.isneginf(lse))
 
 
+def test_tensor_calls_refuse_too_few_dimensions():
+    c = fq.kv_cache_nvfp4(4, 16, 2, 64)
+    k = torch.zeros(3, 2, 64, dtype=torch.bfloat16, device="cuda")
+    slots = torch.arange(3, device="cuda")
+    one = torch.zeros((), dtype=torch.bfloat16, device="cuda")
+    for a in (one, k[0], k[None]):
+        with pytest.raises(ValueError):
+            fq.kv_append_nvfp4(c, a, a.clone(), slots)
+        with pytest.raises(ValueError):
+            fq.kv_append_nvfp4(c, k, k.clone(), slots, q=a)
+        with pytest.raises(ValueError):
+            fq.attention_nvfp4(a, c, torch.zeros(3, 1, dtype=torch.int32, device="cuda"), slots.int())
+    with pytest.raises(ValueError):
+        fq.kv_append_nvfp4(c, k, k[0], slots)
+    for s in (slots[0], slots[None]):
+        with pytest.raises(ValueError):
+            fq.kv_gather_nvfp4(c, s)
+        with pytest.raises(ValueError):
+            fq.kv_append_nvfp4(c, k, k.clone(), s)
+
+
 def test_waits_that_run_out_are_reported():
     """The debug build with waits cut to a microsecond: rows are NaN or right, the status
     word says so, and the next call is as ever."""
