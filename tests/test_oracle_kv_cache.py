@@ -100,3 +100,25 @@ def test_attention_picks_the_matching_key():
     r = okv.attention(q, c, np.array([[0]]), [8])
     assert np.isclose(r.out[0, 1, 0], 6 / 6 * 2 * (6 / 6), rtol=0.2)
     assert np.isclose(r.lse[0, 1], 600, atol=1)
+
+
+def test_attention_weights_by_hand():
+    """Two keys whose logits differ by log 3: weights 1/4 and 3/4, in each head of a group."""
+    c = empty()
+    k = np.zeros((2, 2, 64), np.float32)
+    k[1, :, 0] = 6
+    v = np.zeros((2, 2, 64), np.float32)
+    v[0, :, 0], v[1, :, 0], v[1, 1, 17] = 6, -6, 3            # 3 alone in its block: code 6, scale 1/2
+    okv.append(c, k, v, np.arange(2))
+    q = np.zeros((1, 4, 64))
+    q[0, :, 0] = [np.log(3) / 6, -np.log(3) / 6, np.log(3) / 6, 0]
+    r = okv.attention(q, c, np.array([[0]]), [2])
+    p1 = np.array([0.75, 0.25, 0.75, 0.5])
+    assert np.allclose(r.out[0, :, 0], 6 * (1 - p1) - 6 * p1, rtol=1e-12)
+    assert np.allclose(r.out[0, :, 17], [0, 0, 3 * 0.75, 3 * 0.5], rtol=1e-12)
+    assert np.allclose(r.lse[0], np.log([4, 4 / 3, 4, 2]), rtol=1e-12)
+    assert np.allclose(r.weight[0, :, 0], 6) and np.allclose(r.logit[0], np.log(3) * np.array([1, 1, 1, 0]))
+    half = okv.attention(2 * q, c, np.array([[0]]), [2], sm_scale=0.5)
+    assert np.allclose(half.out, r.out, rtol=1e-12) and np.allclose(half.lse, r.lse, rtol=1e-12)
+    scaled = okv.attention(2 * q, c, np.array([[0]]), [2], k_gs=2.0, v_gs=4.0)
+    assert np.allclose(4 * scaled.out, r.out, rtol=1e-12) and np.allclose(scaled.lse, r.lse, rtol=1e-12)
