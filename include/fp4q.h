@@ -476,8 +476,15 @@ FP4Q_API fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int
  *   status, pdl     as in fp4_add_rmsnorm_quant_ex.
  * Lengths and tables are read on the device, so a captured call follows them.
  * Rows that a kernel gave up on (a bounded wait ran out: status) are NaN, lse too.
- * Accumulators, maxima and sums are fp32.  Nothing that is written may overlap
- * anything else the call reads or writes.
+ * Logits, references, sums and accumulators are fp32.  Two things are rounded to 16
+ * bits on the way: each weight exp(..) to fp16's 11 bits (relative 2^-11) before it is
+ * multiplied with v, while the sum takes it unrounded; and each query element, scaled
+ * by a power of two, by at most 2^-39 of its row's largest (most elements by nothing).
+ * Keys and values are exact.  One kernel serves a call, chosen by the average number of
+ * rows per sequence and the table's width: prompts and single rows are faster in two
+ * calls (each over its rows of q and out), and so are short sequences in a table cut
+ * to their pages.  Nothing that is written may overlap anything else the call reads or
+ * writes.
  */
 FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
                                           const fp4_kv_cache_t* cache, const int32_t* block_tables,

@@ -836,7 +836,9 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     causal: the last row of a sequence sees all its keys, the row before it one
     less, and so on; else every row sees all of them.  sm_scale: default
     head_dim ** -0.5.  A row that sees no key gives 0 and lse -inf; rows of no
-    sequence are left as they were.  Returns out, or (out, lse) with return_lse
+    sequence are left as they were.  Sums are fp32, the weights rounded to 11 bits
+    before they meet v.  Prompts and single rows are faster in two calls than in one,
+    short sequences with a table cut to their pages.  Returns out, or (out, lse) with return_lse
     (lse (T, heads) fp32, natural logarithm).  workspace: optional uint8 tensor of
     fp4_attention_workspace_bytes bytes (one for calls of several sizes:
     fp4_attention_workspace_bound), for one call at a time."""

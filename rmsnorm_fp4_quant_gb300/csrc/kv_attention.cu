@@ -19,7 +19,12 @@ int decode_tiles(int64_t B, int64_t T, int group) { return T * group <= 8 * B ? 
 
 // The choices below compare times in microseconds, estimated from the sizes (the lengths
 // are on the device: every sequence counts with the average number of rows and the
-// table's width).  Their constants are fits to timed calls.
+// table's width).  Their constants are fits to timed calls whose tables were as wide as
+// their longest sequence and whose sequences had the same number of rows; what is said of
+// them holds for such calls.  Elsewhere the choice can be far off.  Wider tables than the
+// lengths: 64 sequences of 200 keys, 8 heads of 128, 13.1 us with a table of 200 keys, 21.1
+// of 8192; one of 80 rows and keys 7.0 and 18.4.  Rows that differ: one sequence of 1000
+// rows and 60 of one, 4000 keys each, 278 us in one call, 62 + 64 in two.
 int64_t row_tiles(int64_t B, int64_t T, int group, int rows) {
   const int64_t each = (T * group + B - 1) / B;
   return B * ((each + rows - 1) / rows);
@@ -43,12 +48,14 @@ constexpr double kEvenSplit = 0.95;
 
 // CTAs that share an item (more than one as a cluster, joined in shared memory; the
 // hardware deals the items out), or 0 where the keys are split evenly over all CTAs and
-// joined by a second kernel.  1055 calls of 1 to 128 sequences with 100 to 16000 keys, each
-// timed with every choice: the one made is 1.7 % slower than the best on average and 30 %
-// at most (a twentieth off the even split costs those nothing, and 100 sequences of 400 to
-// 10000 keys, 8 heads of 128, take 124 us instead of 155).  One CTA an item against the even split: 128 sequences of 2000 keys, 24 heads
-// of 64, 111 / 144 us, 16 of 8000 with 4 rows each 72 / 59; 8 CTAs: one sequence of 1000
-// keys, 2 heads of 128, 6.1 / 9.0 us, 4 of 16000 with 8 heads 23.8 / 19.3.
+// joined by a second kernel.  1055 calls of 1 to 128 sequences with 100 to 16000 keys (all
+// of them, or from 0.3 of the longest up), each timed with every choice: the one made is
+// 1.7 % slower than the best on average and 30 % at most.  The even split's estimate is
+// taken at kEvenSplit of itself, as it gains where lengths differ: that costs those calls
+// nothing, and 100 sequences of 400 to 10000 keys, 8 heads of 128, take 124 us instead of
+// 155.  One CTA an item against the even split: 128 sequences of 2000 keys, 24 heads of 64,
+// 111 / 144 us, 16 of 8000 with 4 rows each 72 / 59; 8 CTAs: one sequence of 1000 keys, 2
+// heads of 128, 6.1 / 9.0 us, 4 of 16000 with 8 heads 23.8 / 19.3.
 template <int D, int NT>
 int cluster_of(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys, double* cost = nullptr) {
   constexpr DecodeTimes t = kDecTimes<D, NT>;

@@ -408,6 +408,26 @@ def test_varlen(lens, q_lens, causal, Hq, Hkv, D, page, dtype):
     check_attention(queries(T, Hq, D, dtype, 6), cache, tables, lens, cu, causal, dtype)
 
 
+def test_a_mixed_batch_in_one_call_and_in_two():
+    """A prompt's piece and single rows together, and apart over their rows of q, out and lse
+    and their rows of the tables."""
+    lens, q_lens, Hq, Hkv, D, page = [310] + [40 + 7 * i for i in range(9)], [150] + [1] * 9, 8, 2, 64, 16
+    cache, tables = fill_sequences(lens, Hkv, D, page, seed=17)
+    cu = np.cumsum([0] + q_lens).tolist()
+    q = queries(cu[-1], Hq, D, "bf16", 5)
+    check_attention(q, cache, tables, lens, cu, True, "bf16")
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    tab = torch.from_numpy(tables.astype(np.int32)).cuda()
+    sl = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    qd = q.cuda()
+    out = torch.full_like(qd, 5.0)
+    lse = torch.full(qd.shape[:2], 6.0, device="cuda")
+    fq.attention_nvfp4(qd[:150], dev, tab[:1], sl[:1], torch.tensor([0, 150], dtype=torch.int32, device="cuda"),
+                       out=out[:150], return_lse=True, lse=lse[:150])
+    fq.attention_nvfp4(qd[150:], dev, tab[1:], sl[1:], out=out[150:], return_lse=True, lse=lse[150:])
+    compare_attention(out, lse, okv.attention(q.double().numpy(), cache, tables, lens, cu, True, D ** -0.5), D, "bf16")
+
+
 # long tables and few rows: each item's keys are cut into ranges that are joined afterwards
 @pytest.mark.parametrize("lens,q_lens,causal", [
     ([3000, 1500], [70, 130], True), ([2600], [300], False), ([64, 4200, 3], [64, 129, 200], True),
