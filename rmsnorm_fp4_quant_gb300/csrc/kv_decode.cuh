@@ -131,6 +131,12 @@ template <int D> __device__ __forceinline__ int v_place(int row, int piece) {
 
 template <int V> struct Const { static constexpr int value = V; };
 
+__device__ __forceinline__ uint32_t cluster_nctarank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(r));
+  return r;
+}
+
 // One row's result in 8 channels: o relative to 2^ref, l the sum of weights.
 template <typename T, int D>
 __device__ __forceinline__ void decode_write(const KvAttentionParams& p, const KvSeq& s, int kvh, int row, int d0,

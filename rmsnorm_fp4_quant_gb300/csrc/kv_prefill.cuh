@@ -40,7 +40,7 @@
 #pragma once
 
 #include "kv_attention_common.cuh"
-#include "tcgen05.cuh"
+#include "kv_tcgen05.cuh"
 
 namespace fp4q {
 

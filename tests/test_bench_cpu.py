@@ -77,3 +77,16 @@ def test_kernel_source_hash_covers_only_each_kernels_files():
     for op, files in bench.KERNEL_SOURCES.items():
         for f in files:
             assert os.path.exists(os.path.join(ROOT, "rmsnorm_fp4_quant_gb300", "csrc", f)), f
+
+
+def test_committed_profiles_are_of_the_current_sources():
+    """The bench line reports a capture's DRAM bytes only while the kernel's files are the
+    captured ones: a change to them takes a new capture (what only other kernels need goes
+    into files of their own)."""
+    import glob
+    import re
+    current = {bench.kernel_source_sha(op) for op in bench.KERNEL_SOURCES}
+    for p in glob.glob(os.path.join(ROOT, "profiles", "*kernel__*.md")):
+        assert re.search(r"^source_sha256:\s*([0-9a-f]{64})", open(p).read(), re.M).group(1) in current, p
+    traffic, path = bench.recorded_traffic("C3_M8192_H7168_bf16_mxfp4_swizzled_outliers")
+    assert traffic == 332909056 and path.startswith("profiles")
