@@ -114,6 +114,10 @@ KERNEL_SOURCES = {
     "quantize": ("api.cu", "fp4q_device.cuh", "fp4q_launch.h", "quantize.cu"),
     "gemm": ("async_copy.cuh", "fp4q_device.cuh", "gemm_api.cu", "gemm_launch.h", "gemm_nvfp4.cu",
              "tcgen05.cuh"),
+    # the key/value cache: captures only, no workload of this benchmark
+    "kv": ("async_copy.cuh", "debug_checks.h", "fp4q_device.cuh", "fp4q_launch.h",
+           "fused_common.cuh", "kv_attention.cu", "kv_attention_common.cuh", "kv_cache.cu",
+           "kv_decode.cuh", "kv_launch.h", "kv_prefill.cuh", "kv_tcgen05.cuh", "tcgen05.cuh"),
 }
 
 

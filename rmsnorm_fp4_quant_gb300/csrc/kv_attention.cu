@@ -50,12 +50,12 @@ constexpr double kEvenSplit = 0.95;
 // hardware deals the items out), or 0 where the keys are split evenly over all CTAs and
 // joined by a second kernel.  1055 calls of 1 to 128 sequences with 100 to 16000 keys (all
 // of them, or from 0.3 of the longest up), each timed with every choice: the one made is
-// 1.7 % slower than the best on average and 30 % at most.  The even split's estimate is
+// 2.2 % slower than the best on average and 30 % at most.  The even split's estimate is
 // taken at kEvenSplit of itself, as it gains where lengths differ: that costs those calls
 // nothing, and 100 sequences of 400 to 10000 keys, 8 heads of 128, take 124 us instead of
 // 155.  One CTA an item against the even split: 128 sequences of 2000 keys, 24 heads of 64,
-// 111 / 144 us, 16 of 8000 with 4 rows each 72 / 59; 8 CTAs: one sequence of 1000 keys, 2
-// heads of 128, 6.1 / 9.0 us, 4 of 16000 with 8 heads 23.8 / 19.3.
+// 112 / 144 us, 16 of 8000 with 4 rows each 74 / 59; 8 CTAs: one sequence of 1000 keys, 2
+// heads of 128, 6.1 / 8.9 us, 4 of 16000 with 8 heads 26.2 / 22.5.
 template <int D, int NT>
 int cluster_of(int sms, int64_t B, int64_t T, int group, int heads, int64_t keys, double* cost = nullptr) {
   constexpr DecodeTimes t = kDecTimes<D, NT>;
@@ -121,12 +121,12 @@ cudaError_t launch_decode(const KvAttentionParams& p, int pdl, cudaStream_t stre
 
 // Constants as above, from calls timed with both kernels and with 1 to 8 ranges of keys
 // (heads of 64 and 128, 1 to 100 sequences of 1 to 4000 rows and 48 to 60000 keys).  Over
-// 831 of them the choice of kernel is 0.4 % slower than the faster one on average and 25 %
-// at most; a fixed limit of 64 rows was 11 % and a factor of 2.6, and ranges for two CTAs
-// per SM 10 % and a factor of 2.1.  8 heads of 128, 4 query heads each, 16-row items
-// against 256-row items: one sequence of 80 rows and keys 6.7 / 13.4 us, of 320 over 1320
-// keys 57 / 43; one range against two: 2048 rows and keys 46 / 97 us, 500 over 4000 keys
-// 65 / 47.
+// 831 of them the choice of kernel is 0.7 % slower than the faster one on average and 30 %
+// at most (a fixed limit of 64 rows: 6.5 % and a factor of 2.1); over 214 the ranges are
+// 11 % slower than the best of 1 to 8 at most.  8 heads of 128, 4 query heads each, 16-row
+// items against 256-row items: one sequence of 80 rows and keys 6.7 / 11.8 us, of 320 over
+// 1320 keys 43 / 26; one range against two: 2048 rows and keys 43 / 100 us, 500 over 4000
+// keys 62 / 46.
 constexpr double kPreItem = 8.0, kPreJoin = 4.0, kPreJoinBytes = 5e6;   // per CTA; per join, bytes per us
 constexpr int kPreMostSplits = 32;
 
