@@ -55,7 +55,8 @@ extern "C" {
 /* Same handle type as cudaStream_t / CUstream. */
 typedef struct CUstream_st* fp4q_stream_t;
 
-typedef enum { FP4_DT_BF16 = 0, FP4_DT_FP16 = 1 } fp4_dtype_t;
+/* FP4_DT_FP32 is a type of logits alone (fp4_beam_select). */
+typedef enum { FP4_DT_BF16 = 0, FP4_DT_FP16 = 1, FP4_DT_FP32 = 2 } fp4_dtype_t;
 
 /* NVFP4: 16-element blocks, E4M3 scale bytes.  MXFP4: 32-element blocks,
  * UE8M0 scale bytes.  E4M3_B32: 32-element blocks with E4M3 scale bytes
@@ -523,6 +524,48 @@ FP4Q_API int64_t fp4_attention_workspace_bound(int64_t B, int64_t T, int64_t Hq,
 FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t Hq,
                                                  int64_t num_kv_heads, int64_t head_dim,
                                                  int64_t max_keys, int64_t out[2]);
+
+/*
+ * fp4_beam_select - the best continuations of every beam search of a batch:
+ * of batch entry b the n candidates (beam k, token v) with the largest
+ *
+ *   scores[b, k] + logits[b, k, v] - log(sum_v exp(logits[b, k, v]))
+ *
+ * in descending order.  Candidates of one beam are ordered by their logits,
+ * equal ones by token, lowest first; of different beams by their scores in 64 bits,
+ * equal ones by beam.
+ *
+ *   logits, row_stride  [B * K, V] dtype (bf16, fp16 or fp32), row_stride elements between rows
+ *                  (0: V); row b * K + k is beam k of entry b.  Any alignment that the type has.
+ *   scores         [B, K] fp32.  A beam whose score is not finite has no candidates (dead beams, and
+ *                  all but one at the start: -infinity), nor has one with a logit that is NaN or
+ *                  +infinity or with none above -infinity.  A logit of -infinity is no candidate.
+ *   finished       [B, K] bytes or NULL: a beam with a nonzero byte has ended; its one candidate
+ *                  is end_token with its score as it is, and its logits are not read.
+ *   end_token      in [0, V).
+ *   K, V, n        beams (at most 256), vocabulary (at most 2^24), candidates to take (at most 64).
+ *   out_scores     [B, n] fp32: the scores, rounded once; -infinity behind the last candidate.
+ *   out_parents    [B, n] int32: row b * K + k of logits; -1 behind the last candidate.
+ *   out_tokens     [B, n] int32: v; -1 behind the last candidate.
+ *   out_finished   [B, n] bytes, NULL exactly when finished is: 1 where the parent has ended or the
+ *                  token is end_token.
+ *   workspace      at least fp4_beam_select_workspace_bytes(...) bytes, 16-byte aligned, any
+ *                  contents; two calls that may run at the same time need one each.
+ *   pdl            as in fp4_add_rmsnorm_quant_ex.
+ * The sums of exponentials are fp32 over at most 8192 logits each, joined in 64 bits.  Results
+ * do not change from call to call.  Nothing that is written may overlap anything else the call
+ * reads or writes.  out_parents is what fp4_kv_fork_nvfp4 takes as parents.
+ */
+FP4Q_API fp4_status_t fp4_beam_select(const void* logits, int64_t row_stride, fp4_dtype_t dtype,
+                                      const float* scores, const uint8_t* finished,
+                                      int64_t end_token, int64_t B, int64_t K, int64_t V, int64_t n,
+                                      float* out_scores, int32_t* out_parents, int32_t* out_tokens,
+                                      uint8_t* out_finished, void* workspace,
+                                      int64_t workspace_bytes, int pdl, fp4q_stream_t stream);
+
+/* Bytes of workspace of fp4_beam_select; grows with each size.  -1 on bad arguments. */
+FP4Q_API int64_t fp4_beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t n,
+                                                 fp4_dtype_t dtype);
 
 /*
  * fp4_read_device_status - synchronises `stream`, then copies the device

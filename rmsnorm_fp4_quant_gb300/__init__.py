@@ -28,6 +28,7 @@ device ``status`` word learns of a wait that ran out (``read_device_status``).
 from ._binding import (  # noqa: F401
     FP4_DT_BF16,
     FP4_DT_FP16,
+    FP4_DT_FP32,
     FP4_E4M3_B32,
     FP4_MXFP4,
     FP4_NVFP4,
@@ -48,6 +49,7 @@ from ._binding import (  # noqa: F401
     NVFP4KVCache,
     add_rmsnorm_fp4quant,
     attention_nvfp4,
+    beam_select,
     dequant,
     gemm_nvfp4_bf16,
     gemm_nvfp4_gelu,
@@ -58,6 +60,8 @@ from ._binding import (  # noqa: F401
     fp4_attention_nvfp4,
     fp4_attention_workspace_bound,
     fp4_attention_workspace_bytes,
+    fp4_beam_select,
+    fp4_beam_select_workspace_bytes,
     fp4_dequant,
     fp4_gemm_mxfp4_bf16,
     fp4_gemm_nvfp4_gelu_bf16,

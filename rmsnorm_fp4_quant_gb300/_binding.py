@@ -9,7 +9,7 @@ from typing import NamedTuple, Optional, Tuple
 
 from .build import DEBUG_LIBPATH, LIBPATH
 
-FP4_DT_BF16, FP4_DT_FP16 = 0, 1
+FP4_DT_BF16, FP4_DT_FP16, FP4_DT_FP32 = 0, 1, 2
 FP4_NVFP4, FP4_MXFP4, FP4_E4M3_B32 = 0, 1, 2
 FP4_SF_ROWMAJOR, FP4_SF_SWIZZLED, FP4_SF_BOTH = 0, 1, 2
 FP4_OK, FP4_ERR_INVALID_ARG, FP4_ERR_UNSUPPORTED_SHAPE, FP4_ERR_MISALIGNED = 0, 1, 2, 3
@@ -149,6 +149,11 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_attention_workspace_bound.restype = i64
     L.fp4_attention_launch_shape.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
     L.fp4_attention_launch_shape.restype = ci
+    L.fp4_beam_select.argtypes = [vp, i64, ci, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
+                                  i64, ci, vp]
+    L.fp4_beam_select.restype = ci
+    L.fp4_beam_select_workspace_bytes.argtypes = [i64, i64, i64, i64, ci]
+    L.fp4_beam_select_workspace_bytes.restype = i64
     L.fp4_debug_build.argtypes = []
     L.fp4_debug_build.restype = ci
     L.fp4_debug_configure.argtypes = [i64, i64, ci, ci, ci, vp]
@@ -288,6 +293,21 @@ def fp4_attention_workspace_bound(B: int, T: int, Hq: int, num_kv_heads: int, he
     allocates once (fp4_attention_workspace_bytes is for one call: a smaller call may
     need more than a larger one)."""
     return lib().fp4_attention_workspace_bound(B, T, Hq, num_kv_heads, head_dim, max_keys)
+
+
+def fp4_beam_select(logits_ptr: int, row_stride: int, dtype: int, scores_ptr: int, finished_ptr: int,
+                    end_token: int, B: int, K: int, V: int, n: int, out_scores_ptr: int,
+                    out_parents_ptr: int, out_tokens_ptr: int, out_finished_ptr: int,
+                    workspace_ptr: int, workspace_bytes: int, pdl: int, stream: int) -> int:
+    return lib().fp4_beam_select(logits_ptr or None, row_stride, dtype, scores_ptr or None,
+                                 finished_ptr or None, end_token, B, K, V, n, out_scores_ptr or None,
+                                 out_parents_ptr or None, out_tokens_ptr or None,
+                                 out_finished_ptr or None, workspace_ptr or None, workspace_bytes,
+                                 pdl, stream or None)
+
+
+def fp4_beam_select_workspace_bytes(B: int, K: int, V: int, n: int, dtype: int) -> int:
+    return lib().fp4_beam_select_workspace_bytes(B, K, V, n, dtype)
 
 
 def fp4_read_device_status(status_ptr: int, stream: int) -> int:
@@ -906,3 +926,113 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     if st != 0:
         raise Fp4Error(st, "fp4_attention_nvfp4")
     return (out, lse) if return_lse else out
+
+
+# ---------------------------------------------------------------------------
+# between the tokens of a batch: beam search, and the cache's pages
+# ---------------------------------------------------------------------------
+class _Workspace:
+    """A workspace for the kernels that are launched inside: the caller's, or one that goes
+    back to the caching allocator in the order of the kernels' stream."""
+    __slots__ = ("size", "ptr", "own", "held")
+
+    def __init__(self, torch, workspace, size, dev, handle, stream):
+        self.size, self.ptr, self.own, self.held = size, 0, 0, None
+        if workspace is not None:
+            _check_cuda(workspace, "workspace")
+            _same_device(dev, "workspace", workspace)
+            self.size = workspace.numel() * workspace.element_size()
+            self.ptr = workspace.data_ptr()
+        elif size > 0:
+            raw = getattr(torch._C, "_cuda_cudaCachingAllocator_raw_alloc", None)
+            if raw is not None:                  # skips the tensor (as in attention_nvfp4)
+                self.ptr = self.own = raw(size, handle)
+            else:
+                with _on(stream):
+                    self.held = torch.empty(size, dtype=torch.uint8, device=f"cuda:{dev}")
+                self.ptr = self.held.data_ptr()
+
+    def __enter__(self):
+        return self
+
+    def __exit__(self, *_):
+        if self.own:
+            _torch()._C._cuda_cudaCachingAllocator_raw_delete(self.own)
+
+
+def _current(torch, t, name):
+    """Device number of a CUDA tensor, which has to be the current one's."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{name} must be a CUDA tensor (the library has no CPU path)")
+    if dev != torch.cuda.current_device():
+        raise ValueError(f"{name} is on cuda:{dev}, which is not the current device")
+    return dev
+
+
+@functools.lru_cache(maxsize=256)
+def _beam_workspace(L, B, K, V, n, dt) -> int:
+    return max(L.fp4_beam_select_workspace_bytes(B, K, V, n, dt), 0)
+
+
+def beam_select(logits, scores, take: Optional[int] = None, finished=None, end_token: int = 0, out=None,
+                workspace=None, pdl: bool = False, stream=None):
+    """The `take` best continuations of every beam search of a batch: candidates
+    (beam k, token v) by scores[b, k] + log_softmax(logits[b, k])[v], in descending
+    order; equal ones lowest beam, then lowest token first.
+
+    logits: (B, K, V) bf16, fp16 or fp32, rows of unit stride that lie evenly (a slice
+    of a wider product's columns).  scores: (B, K) fp32; a beam whose score is not finite
+    has no candidates, nor has one with a logit that is NaN or +infinity.  take: default K,
+    at most 64.  finished: (B, K) bool: an ended beam's one candidate is end_token with
+    the score it has.  Returns (scores (B, take) fp32, parents, tokens (B, take) int32),
+    and with finished also (B, take) bool: ended before or with this token.  parents are
+    rows b * K + k, as kv_fork_nvfp4 takes them.  Places behind the last candidate are
+    -infinity, -1, -1 and False.  out: the outputs to write, in this order.  workspace:
+    optional uint8 tensor of fp4_beam_select_workspace_bytes bytes, for one call at a
+    time."""
+    torch = _torch()
+    if logits.dim() != 3:
+        raise ValueError("logits must be (B, K, V)")
+    dev = _current(torch, logits, "logits")
+    B, K, V = logits.shape
+    dtype = logits.dtype
+    if dtype is torch.float32:
+        dt = FP4_DT_FP32
+    elif dtype is torch.bfloat16:
+        dt = FP4_DT_BF16
+    elif dtype is torch.float16:
+        dt = FP4_DT_FP16
+    else:
+        raise ValueError("logits must be bfloat16, float16 or float32")
+    sb, sk, one = logits.stride()
+    if B * K <= 1:
+        sk = V
+    elif K == 1:
+        sk = sb
+    if (V > 1 and one != 1) or (B > 1 and K > 1 and sb != K * sk) or sk < V:
+        raise ValueError("logits must have rows of unit stride that lie evenly and do not overlap")
+    n = K if take is None else take
+    score_ptr = _dense_ptr(scores, "scores", dev, torch.float32, (B, K))
+    done = 0
+    if finished is not None:
+        done = _dense_ptr(finished, "finished", dev, torch.bool, (B, K))
+    if out is None:
+        with _on(stream):
+            out = [torch.empty(B, n, dtype=t, device=logits.device)
+                   for t in (torch.float32, torch.int32, torch.int32) + ((torch.bool,) if done else ())]
+    elif len(out) != (4 if finished is not None else 3):
+        raise ValueError("out must be (scores, parents, tokens), and finished with finished")
+    shape = (B, n)
+    o_s = _dense_ptr(out[0], "out[0]", dev, torch.float32, shape)
+    o_p = _dense_ptr(out[1], "out[1]", dev, torch.int32, shape)
+    o_t = _dense_ptr(out[2], "out[2]", dev, torch.int32, shape)
+    o_f = _dense_ptr(out[3], "out[3]", dev, torch.bool, shape) if finished is not None else 0
+    L = lib()
+    handle = _kv_stream(torch, stream, dev)
+    with _Workspace(torch, workspace, _beam_workspace(L, B, K, V, n, dt), dev, handle, stream) as ws:
+        st = L.fp4_beam_select(logits.data_ptr(), sk, dt, score_ptr, done or None, end_token, B, K, V, n,
+                               o_s, o_p, o_t, o_f or None, ws.ptr, ws.size, 1 if pdl else 0, handle)
+    if st != 0:
+        raise Fp4Error(st, "fp4_beam_select")
+    return tuple(out)
