@@ -532,14 +532,15 @@ FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t H
  *   scores[b, k] + logits[b, k, v] - log(sum_v exp(logits[b, k, v]))
  *
  * in descending order.  Candidates of one beam are ordered by their logits,
- * equal ones by token, lowest first; of different beams by their scores in 64 bits,
+ * equal ones by token, lowest first; of different beams by their scores (48 bits),
  * equal ones by beam.
  *
  *   logits, row_stride  [B * K, V] dtype (bf16, fp16 or fp32), row_stride elements between rows
  *                  (0: V); row b * K + k is beam k of entry b.  Any alignment that the type has.
  *   scores         [B, K] fp32.  A beam whose score is not finite has no candidates (dead beams, and
  *                  all but one at the start: -infinity), nor has one with a logit that is NaN or
- *                  +infinity or with none above -infinity.  A logit of -infinity is no candidate.
+ *                  above 2^125.  A logit of at most -2^125 (a mask of -infinity or of the type's lowest
+ *                  value) is no candidate and adds nothing to the sum.
  *   finished       [B, K] bytes or NULL: a beam with a nonzero byte has ended; its one candidate
  *                  is end_token with its score as it is, and its logits are not read.
  *   end_token      in [0, V).
@@ -552,8 +553,8 @@ FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t H
  *   workspace      at least fp4_beam_select_workspace_bytes(...) bytes, 16-byte aligned, any
  *                  contents; two calls that may run at the same time need one each.
  *   pdl            as in fp4_add_rmsnorm_quant_ex.
- * The sums of exponentials are fp32 over at most 8192 logits each, joined in 64 bits.  Results
- * do not change from call to call.  Nothing that is written may overlap anything else the call
+ * The exponentials are summed in fp32, the sums of a row's parts and the scores in pairs of fp32
+ * (48 bits).  Results do not change from call to call.  Nothing that is written may overlap anything else the call
  * reads or writes.  out_parents is what fp4_kv_fork_nvfp4 takes as parents.
  */
 FP4Q_API fp4_status_t fp4_beam_select(const void* logits, int64_t row_stride, fp4_dtype_t dtype,

@@ -19,7 +19,7 @@ int beam_dtype(fp4_dtype_t d) {
 fp4_status_t check_sizes(int64_t B, int64_t K, int64_t V, int64_t n) {
   if (B < 0 || K <= 0 || V <= 0 || n <= 0) return FP4_ERR_INVALID_ARG;
   if (K > kBeamMostBeams || n > kBeamMostTake || V > kBeamMostVocab || B > INT32_MAX / (2 * K) ||
-      B * K > INT32_MAX / (V / 8192 + 2))
+      B * K > INT32_MAX / (V / 512 + 2))
     return FP4_ERR_UNSUPPORTED_SHAPE;   // the kernels number rows and their parts in 32 bits
   return FP4_OK;
 }
@@ -36,7 +36,7 @@ extern "C" {
 int64_t fp4_beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V, int64_t n, fp4_dtype_t dtype) {
   const int dt = beam_dtype(dtype);
   if (dt < 0 || check_sizes(B, K, V, n) != FP4_OK) return -1;
-  return beam_workspace(dt, B, K, V, n);
+  return beam_workspace(sm_count_current_device(), B, K, V);
 }
 
 fp4_status_t fp4_beam_select(const void* logits, int64_t row_stride, fp4_dtype_t dtype, const float* scores,
@@ -54,7 +54,7 @@ fp4_status_t fp4_beam_select(const void* logits, int64_t row_stride, fp4_dtype_t
   if ((finished == nullptr) != (out_finished == nullptr)) return FP4_ERR_INVALID_ARG;
   if (row_stride > INT64_MAX / 8 / (B * K + 1)) return FP4_ERR_UNSUPPORTED_SHAPE;   // extents that 64 bits number
   if (B == 0) return FP4_OK;
-  const int64_t need = beam_workspace(dt, B, K, V, n);
+  const int64_t need = beam_workspace(sm_count_current_device(), B, K, V);
   if (!logits || !scores || !out_scores || !out_parents || !out_tokens || !workspace || workspace_bytes < need)
     return FP4_ERR_INVALID_ARG;
   if (!abi_aligned(logits, static_cast<uintptr_t>(size)) || !abi_aligned(scores, 4) || !abi_aligned(out_scores, 4) ||
@@ -85,9 +85,9 @@ fp4_status_t fp4_beam_select(const void* logits, int64_t row_stride, fp4_dtype_t
   p.out_parents = out_parents;
   p.out_tokens = out_tokens;
   p.out_finished = out_finished;
-  beam_shape(dt, &p);
-  p.keys = static_cast<uint64_t*>(workspace);
-  p.stats = reinterpret_cast<float2*>(p.keys + B * K * p.parts * n);
+  beam_shape(sm_count_current_device(), &p);
+  p.stats = static_cast<float2*>(workspace);
+  p.tops = reinterpret_cast<float*>(static_cast<char*>(workspace) + beam_stats_bytes(p));
   FP4Q_SET_DEBUG(p);
   return static_cast<fp4_status_t>(
       record_cuda_error(launch_beam_select(dt, p, pdl, reinterpret_cast<cudaStream_t>(stream))));

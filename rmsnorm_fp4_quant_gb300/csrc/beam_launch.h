@@ -24,10 +24,10 @@ struct BeamParams {
   int32_t* out_parents;
   int32_t* out_tokens;
   uint8_t* out_finished;     // or null
-  uint64_t* keys;            // workspace: n keys of every part of every row,
-  float2* stats;             // and its {largest logit, sum of exp(logit - largest)}
+  float2* stats;             // workspace: of every part of every row {M, sum of 2^(logit log2(e) - M)},
+  float* tops;               // and the largest logit of every group of every row
   int parts;                 // pieces that a row is cut into
-  int part_len;              // elements of one, a multiple of the vector
+  int groups;                // of a row
   FP4Q_DEBUG_FIELD
 };
 
@@ -35,9 +35,12 @@ __host__ __device__ inline long long beam_logits_extent(const BeamParams& p, int
   return ((static_cast<long long>(p.B) * p.K - 1) * p.stride + p.V) * size;
 }
 
-// parts and part_len of the call's other sizes.  dtype 0 = bf16, 1 = fp16, 2 = fp32.
-void beam_shape(int dtype, BeamParams* p);
-int64_t beam_workspace(int dtype, int64_t B, int64_t K, int64_t V, int64_t n);
+// The parts and groups that the call's other sizes lead to.
+void beam_shape(int sms, BeamParams* p);
+int64_t beam_stats_bytes(const BeamParams& p);
+// An upper bound that grows with each size.
+int64_t beam_workspace(int sms, int64_t B, int64_t K, int64_t V);
+// dtype 0 = bf16, 1 = fp16, 2 = fp32; sizes and alignment checked by the caller.
 cudaError_t launch_beam_select(int dtype, const BeamParams& p, int pdl, cudaStream_t stream);
 
 }  // namespace fp4q
