@@ -35,11 +35,14 @@ namespace {
 
 constexpr int kScanThreads = 128;
 constexpr int kScanWarps = kScanThreads / 32;
-constexpr int kScanCtas = 5;              // per SM
+constexpr int kScanCtas = 8;              // per SM
 constexpr int kGroup = 512;               // logits of a warp's step, 16 a lane
 constexpr int kJoinThreads = 512;
 constexpr int kJoinWarps = kJoinThreads / 32;
 constexpr int kJoinList = 1024;
+constexpr int kJoinPerWarp = kBeamMostTake / kJoinWarps + 1;
+constexpr int kJoinGroups = 160;          // groups that are looked through without choosing among them
+constexpr int kJoinEarly = 2560;          // groups whose largest is read at once
 constexpr float kLog2eHi = 1.44269502f, kLog2eLo = 1.925963e-08f;
 constexpr float kLn2Hi = 0.693147182f, kLn2Lo = -1.9046542e-09f;
 constexpr float kSlack = 64.0f;
@@ -108,6 +111,13 @@ __device__ __forceinline__ float pow2_whole(float d) {
   return d < -126.0f ? 0.0f : __uint_as_float(static_cast<uint32_t>(static_cast<int>(d) + 127) << 23);
 }
 
+// The largest of the lanes' values, none of which is NaN.
+__device__ __forceinline__ float warp_max(float x) {
+  float m;
+  asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(x));
+  return m;
+}
+
 // Group `group` of row `row`: the lane's 16 logits, -infinity outside the row.  Elements are
 // numbered from the 32-byte boundary at or before the row: number e is token e - lead, and
 // whole vectors are aligned loads whatever the row's address is.
@@ -115,13 +125,13 @@ template <typename T>
 __device__ __forceinline__ void load_group(const BeamParams& p, const T* base, int lead, int group, int lane,
                                            Chunk (&c)[Logits<T>::kVectors]) {
   using L = Logits<T>;
-  constexpr int VEC = L::kVec, SIZE = sizeof(T);
+  constexpr int VEC = L::kVec;
   const int end = lead + p.V;
 #pragma unroll
   for (int j = 0; j < L::kVectors; ++j) {
     const int e = group * kGroup + (j * 32 + lane) * VEC;
     const T* src = base + (e - lead);
-    if (e >= lead && e + VEC <= end && FP4Q_IN_RANGE(p, src, 32, p.logits, beam_logits_extent(p, SIZE))) {
+    if (e >= lead && e + VEC <= end && FP4Q_IN_RANGE(p, src, 32, p.logits, beam_logits_extent(p, sizeof(T)))) {
       c[j] = ld_stream_ro(src);
     } else {
 #pragma unroll
@@ -129,7 +139,7 @@ __device__ __forceinline__ void load_group(const BeamParams& p, const T* base, i
       if (e < end && e + VEC > lead) {
 #pragma unroll
         for (int i = 0; i < VEC; ++i)
-          if (e + i >= lead && e + i < end && FP4Q_IN_RANGE(p, src + i, SIZE, p.logits, beam_logits_extent(p, SIZE)))
+          if (e + i >= lead && e + i < end && FP4Q_IN_RANGE(p, src + i, sizeof(T), p.logits, beam_logits_extent(p, sizeof(T))))
             L::set(c[j], i, src + i);
       }
     }
@@ -145,7 +155,7 @@ template <typename T>
 __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(const BeamParams p) {
   using L = Logits<T>;
   constexpr int NV = L::kVectors;
-  constexpr int kAhead = 4 - NV;             // groups on their way
+  constexpr int kAhead = 3 - NV;             // groups on their way
 
   const int lane = threadIdx.x & 31;
   const int64_t slot = static_cast<int64_t>(blockIdx.x) * kScanWarps + (threadIdx.x >> 5);
@@ -153,23 +163,41 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
   griddep_launch_dependents();
   if (slot >= static_cast<int64_t>(p.B) * p.K * p.parts) return;
   const int row = static_cast<int>(slot / p.parts), part = static_cast<int>(slot - static_cast<int64_t>(row) * p.parts);
-  if (!beam_live(p, row)) return;
   int lead;
   const T* base = beam_row<T>(p, row, lead);
   const int g0 = static_cast<int>(static_cast<int64_t>(p.groups) * part / p.parts);
   const int g1 = static_cast<int>(static_cast<int64_t>(p.groups) * (part + 1) / p.parts);
 
-  float ref = kNoRef, sum = 0.0f;
-  auto work = [&](int group, const Chunk (&c)[NV]) {
+  // groups that lie in the row as a whole
+  const int whole0 = lead ? 1 : 0, whole1 = (lead + p.V) / kGroup;
+  const T* mine = base - lead + lane * L::kVec;
+  auto load = [&](int g, Chunk (&c)[NV]) {
+    if (g >= whole0 && g < whole1) {
+      const T* src = mine + static_cast<int64_t>(g) * kGroup;
+#pragma unroll
+      for (int j = 0; j < NV; ++j)
+        if (FP4Q_IN_RANGE(p, src + 32 * j * L::kVec, 32, p.logits, beam_logits_extent(p, sizeof(T))))
+          c[j] = ld_stream_ro(src + 32 * j * L::kVec);
+    } else if (g < g1) {
+      load_group<T>(p, base, lead, g, lane, c);
+    }
+  };
+  float ref = kNoRef, sum = 0.0f, keep = 0.0f;
+  auto flush = [&](int first, int n) {                     // lane i: the largest of group first + i
+    float* out = p.tops + static_cast<int64_t>(row) * p.groups + first + lane;
+    if (lane < n && FP4Q_IN_RANGE(p, out, 4, p.tops, 4LL * p.B * p.K * p.groups)) *out = keep;
+  };
+  auto work = [&](int g, const Chunk (&c)[NV]) {
     float top = -INFINITY;
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
       const float2 x = L::pair(c, i);
       top = max3_beam(top, x.x, x.y);                      // skips NaN
     }
-    const uint32_t most = __reduce_max_sync(kFullMask, ordered(top));
-    float* out = p.tops + static_cast<int64_t>(row) * p.groups + group;
-    if (lane == 0 && FP4Q_IN_RANGE(p, out, 4, p.tops, 4LL * p.B * p.K * p.groups)) *out = from_ordered(most);
+    const float most = warp_max(top);
+    const int at = (g - g0) & 31;
+    if (lane == at) keep = most;
+    if (at == 31) flush(g - 31, 32);
     // the reference moves where a term would pass 2^kSlack
     if (fmaf(top, kLog2eHi, -ref) > kSlack) {
       const float to = rintf(top * kLog2eHi);
@@ -191,16 +219,18 @@ __global__ void __launch_bounds__(kScanThreads, kScanCtas) beam_scan_kernel(cons
   };
   Chunk c[kAhead + 1][NV];
 #pragma unroll
-  for (int i = 0; i < kAhead; ++i)
-    if (g0 + i < g1) load_group<T>(p, base, lead, g0 + i, lane, c[i]);
+  for (int i = 0; i < kAhead; ++i) load(g0 + i, c[i]);
+  if (!beam_live(p, row)) return;                          // (looked up beside the first logits)
   for (int g = g0; g < g1; g += kAhead + 1) {
 #pragma unroll
     for (int i = 0; i <= kAhead; ++i) {
       if (g + i >= g1) break;
-      if (g + i + kAhead < g1) load_group<T>(p, base, lead, g + i + kAhead, lane, c[(i + kAhead) % (kAhead + 1)]);
+      load(g + i + kAhead, c[(i + kAhead) % (kAhead + 1)]);
       work(g + i, c[i]);
     }
   }
+  const int left = (g1 - g0) & 31;
+  flush(g1 - left, left);
   float m = ref;
 #pragma unroll
   for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
@@ -220,29 +250,38 @@ __device__ __forceinline__ float2 add_pairs(float2 a, float2 b) {
   const float2 s = two_sum(a.x, b.x);
   return two_sum(s.x, __fadd_rn(s.y, __fadd_rn(a.y, b.y)));
 }
-// m ln(2) + log(s) for a whole number m and s > 0: s = f 2^e with f in [0.707, 1.414], and
-// log(f) = 2 artanh(z), z = (f - 1) / (f + 1), by its series, of which only the first term needs
-// both floats.  Off by less than 2^-28 for |m| < 1000.
+// m ln(2) + log(s) for a whole number m and a normal s > 0: s = f 2^e with f in [0.707, 1.414],
+// and log(f) = 2 artanh(z), z = (f - 1) / (f + 1), by its series, of which only the first term
+// needs both floats (z itself may be off: z_lo is what is left of the division).  Off by less than
+// 2^-28 for |m| < 1000.
 __device__ __forceinline__ float2 log_pair(float m, float2 s) {
-  int e;
-  float f = frexpf(s.x, &e) * 2.0f;
-  --e;
+  const uint32_t bits = __float_as_uint(s.x);
+  int e = static_cast<int>(bits >> 23) - 127;
+  float f = __uint_as_float((bits & 0x007fffffu) | 0x3f800000u);
   if (f > 1.4140625f) {
     f *= 0.5f;
     ++e;
   }
-  const float lo = ldexpf(s.y, -e);
+  const float lo = s.y * __uint_as_float(static_cast<uint32_t>(127 - e) << 23);
   const float num = __fsub_rn(f, 1.0f), den = __fadd_rn(f, 1.0f);
   const float den_lo = __fsub_rn(num, __fsub_rn(den, 2.0f));
-  const float z = __fdiv_rn(num, den);
-  const float z_lo = fmaf(-z, den_lo, fmaf(-z, den, num)) / den;
+  const float z = __fdividef(num, den);
+  const float z_lo = __fdividef(fmaf(-z, den_lo, fmaf(-z, den, num)), den);
   const float zz = z * z;
   const float series = fmaf(zz, fmaf(zz, fmaf(zz, fmaf(zz, 2.0f / 11, 2.0f / 9), 2.0f / 7), 2.0f / 5), 2.0f / 3);
-  const float rest = z * zz * series + 2.0f * z_lo + lo / f;
+  const float rest = z * zz * series + 2.0f * z_lo + __fdividef(lo, f);
   const float E = m + static_cast<float>(e);
   const float a = __fmul_rn(E, kLn2Hi);
   const float2 t = two_sum(a, 2.0f * z);
   return two_sum(t.x, t.y + (rest + (fmaf(E, kLn2Hi, -a) + E * kLn2Lo)));
+}
+
+// s + (x - l) in order.
+__device__ __forceinline__ uint64_t pair_score(float x, float2 l, float s) {
+  float2 v = two_sum(x, -l.x);
+  v.y -= l.y;
+  v = add_pairs(v, make_float2(s, 0.0f));
+  return static_cast<uint64_t>(ordered(v.x)) << 32 | ordered(v.y);
 }
 
 // A candidate of the join, or a group by its largest: a score of two floats in order, then
@@ -272,39 +311,43 @@ struct CandidateList {
       k[at] = static_cast<uint8_t>(x.k);
     }
   }
-  // After a barrier: calls out(rank, some, candidate) once for every rank below n, by one
-  // thread each.  All threads call it; `each` calls its argument for every candidate of the thread,
-  // for where the list was too short for them: n rounds of a maximum then.
-  template <typename Each, typename Out>
-  __device__ void best(int n, int tid, Each each, Out out) {
+  __device__ Candidate at(int i) const { return Candidate{score[i], key[i], k[i]}; }
+  // Calls out(rank, some, candidate) once for every rank below n, by one thread each; after
+  // a barrier, with at most kJoinList candidates.
+  template <typename Out> __device__ void best(int n, int tid, Out out) {
     const int found = count;
-    if (found <= kJoinList) {
-      for (int i = tid; i < max(found, n); i += kJoinThreads) {
-        Candidate x{};
-        int rank = i;
-        if (i < found) {
-          x = Candidate{score[i], key[i], k[i]};
-          rank = 0;
+    for (int i = tid; i < max(found, n); i += kJoinThreads) {
+      Candidate x{};
+      int rank = i;
+      if (i < found) {
+        x = at(i);
+        rank = 0;
+        int same = 0;
 #pragma unroll 4
-          for (int j = 0; j < found; ++j) {
-            const uint64_t other = score[j];
-            if (other == x.score && j != i)                // rare: the rest of the order counts
-              rank += before(Candidate{other, key[j], k[j]}, x);
-            else
-              rank += other > x.score;
-          }
+        for (int j = 0; j < found; ++j) {
+          const uint64_t other = score[j];
+          rank += other > x.score;
+          same += other == x.score;
         }
-        if (rank < n) out(rank, i < found, x);
+        if (same > 1) {                                    // rare: the rest of the order counts
+          rank = 0;
+#pragma unroll 1
+          for (int j = 0; j < found; ++j) rank += before(at(j), x);
+        }
       }
-      return;
+      if (rank < n) out(rank, i < found, x);
     }
+  }
+  // The same of any number of candidates, which `each` calls its argument for, thread by
+  // thread: n rounds of a maximum.  All threads call it.
+  template <typename Each, typename Out> __device__ void best_in_rounds(int n, int tid, Each each, Out out) {
     Candidate last{~0ull, 0, -1};
     for (int r = 0; r < n; ++r) {
       Candidate top{0, 0, kBeamMostBeams};
       each([&](const Candidate& x) {
         if (before(last, x) && before(x, top)) top = x;
       });
-#pragma unroll
+#pragma unroll 1
       for (int o = 16; o; o >>= 1) {
         const Candidate y{__shfl_xor_sync(kFullMask, top.score, o), __shfl_xor_sync(kFullMask, top.key, o),
                           __shfl_xor_sync(kFullMask, top.k, o)};
@@ -327,145 +370,177 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
   __shared__ float2 lse[kBeamMostBeams];                   // NaN: the row has no candidates of its own
   __shared__ float score[kBeamMostBeams];
   __shared__ bool ended[kBeamMostBeams];
-  __shared__ CandidateList groups, list;
-  __shared__ uint32_t warp_top[kJoinWarps];
-  __shared__ Candidate chosen[kBeamMostTake];
+  __shared__ CandidateList list;
+  __shared__ float early[kJoinEarly];                      // groups' largest,
+  __shared__ uint32_t early_score[kJoinEarly];             // and the first floats of their scores in order
+  __shared__ uint32_t tops_of_warps[kJoinWarps * kJoinPerWarp];
+  __shared__ Candidate chosen[kJoinGroups];
   __shared__ int n_chosen;
 
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int b = blockIdx.x;
   griddep_wait();
   griddep_launch_dependents();
-  if (tid == 0) groups.count = list.count = n_chosen = 0;
+  // everything that the log-sums do not change is on its way before they are computed
+  auto row_score = [&](int k) {
+    const float* s = p.scores + static_cast<int64_t>(b) * p.K + k;
+    return k < p.K && FP4Q_IN_RANGE(p, s, 4, p.scores, 4LL * p.B * p.K) ? __ldg(s) : __uint_as_float(0x7fc00000u);
+  };
+  auto row_ended = [&](int k) {
+    const uint8_t* f = p.finished + static_cast<int64_t>(b) * p.K + k;
+    return p.finished && k < p.K && FP4Q_IN_RANGE(p, f, 1, p.finished, 1LL * p.B * p.K) && __ldg(f) != 0;
+  };
+  auto stat = [&](int k, int i) {
+    const float2* st = p.stats + (static_cast<int64_t>(b) * p.K + k) * p.parts + i;
+    const bool here = k < p.K && i < p.parts && FP4Q_IN_RANGE(p, st, 8, p.stats, 8LL * p.B * p.K * p.parts);
+    return here ? *st : make_float2(kNoRef, 0.0f);
+  };
+  const float s_first = row_score(warp);
+  const bool over_first = row_ended(warp);
+  const float2 stat_first = stat(warp, lane);
+  const int total = p.K * p.groups;
+  const float* tops = p.tops + static_cast<int64_t>(b) * total;
+  auto group_top = [&](int e) {                            // (of rows without candidates: any bytes)
+    return FP4Q_IN_RANGE(p, tops + e, 4, p.tops, 4LL * p.B * p.K * p.groups) ? tops[e] : -INFINITY;
+  };
+  {
+    constexpr int kEach = kJoinEarly / kJoinThreads;
+    float t[kEach];
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) t[i] = tid + i * kJoinThreads < total ? group_top(tid + i * kJoinThreads) : 0.0f;
+#pragma unroll
+    for (int i = 0; i < kEach; ++i) early[tid + i * kJoinThreads] = t[i];
+  }
+  if (tid == 0) list.count = n_chosen = 0;
   // --- log-sums of the rows, a warp each
   for (int k = warp; k < p.K; k += kJoinWarps) {
-    const int row = b * p.K + k;
-    float s = __uint_as_float(0x7fc00000u);
-    if (FP4Q_IN_RANGE(p, p.scores + row, 4, p.scores, 4LL * p.B * p.K)) s = __ldg(p.scores + row);
-    bool over = false;
-    if (p.finished && FP4Q_IN_RANGE(p, p.finished + row, 1, p.finished, 1LL * p.B * p.K))
-      over = __ldg(p.finished + row) != 0;
-    float2 total = make_float2(__uint_as_float(0x7fc00000u), 0.0f);
-    if (isfinite(s) && !over) {
-      const float2* st = p.stats + static_cast<int64_t>(row) * p.parts;
-      const long long stat_bytes = 8LL * p.B * p.K * p.parts;
-      float m = kNoRef;
-      for (int i = lane; i < p.parts; i += 32)
-        if (FP4Q_IN_RANGE(p, st + i, 8, p.stats, stat_bytes)) m = fmaxf(m, st[i].x);
-#pragma unroll
-      for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFullMask, m, o));
-      float2 sum = make_float2(0.0f, 0.0f);
-      for (int i = lane; i < p.parts; i += 32)
-        if (FP4Q_IN_RANGE(p, st + i, 8, p.stats, stat_bytes))
-          sum = add_pairs(sum, make_float2(st[i].y * pow2_whole(fmaxf(st[i].x - m, -200.0f)), 0.0f));
-#pragma unroll
-      for (int o = 16; o; o >>= 1)
-        sum = add_pairs(sum, make_float2(__shfl_xor_sync(kFullMask, sum.x, o), __shfl_xor_sync(kFullMask, sum.y, o)));
-      if (sum.x > 0.0f && isfinite(sum.x) && isfinite(m)) total = log_pair(m, sum);
-    }
+    const float s = k == warp ? s_first : row_score(k);
+    const bool over = k == warp ? over_first : row_ended(k);
+    const float2 x0 = k == warp ? stat_first : stat(k, lane);
+    float m = x0.x;
+    for (int i = lane + 32; i < p.parts; i += 32) m = fmaxf(m, stat(k, i).x);
+    m = warp_max(m);
+    auto scaled = [&](float2 x) { return make_float2(x.y * pow2_whole(fmaxf(x.x - m, -200.0f)), 0.0f); };
+    float2 sum = scaled(x0);
+#pragma unroll 1
+    for (int i = lane + 32; i < p.parts; i += 32) sum = add_pairs(sum, scaled(stat(k, i)));
+#pragma unroll 1
+    for (int o = 16; o; o >>= 1)
+      sum = add_pairs(sum, make_float2(__shfl_xor_sync(kFullMask, sum.x, o), __shfl_xor_sync(kFullMask, sum.y, o)));
     if (lane == 0) {
-      lse[k] = total;
+      const bool has = isfinite(s) && !over && sum.x > 0.0f && isfinite(sum.x) && isfinite(m);
+      lse[k] = has ? log_pair(m, sum) : make_float2(__uint_as_float(0x7fc00000u), 0.0f);
       score[k] = s;
       ended[k] = over && isfinite(s);
     }
   }
   __syncthreads();
-  auto scored = [&](int k, float x) {
-    const float2 l = lse[k];
-    float2 v = two_sum(x, -l.x);
-    v.y -= l.y;
-    v = add_pairs(v, make_float2(score[k], 0.0f));
-    return static_cast<uint64_t>(ordered(v.x)) << 32 | ordered(v.y);
-  };
 
-  // --- the n best groups; an ended beam counts as its first group, with its score as it is
-  const int total = p.K * p.groups;
-  const float* tops = p.tops + static_cast<int64_t>(b) * total;
-  auto group = [&](int e, Candidate& x) {
-    x.k = e / p.groups;
-    const int g = e - x.k * p.groups;
-    if (ended[x.k]) {
-      x.key = beam_key(0.0f, 0);
-      x.score = static_cast<uint64_t>(ordered(score[x.k])) << 32 | ordered(0.0f);
-      return g == 0;
-    }
-    if (isnan(lse[x.k].x) || !FP4Q_IN_RANGE(p, tops + e, 4, p.tops, 4LL * p.B * p.K * p.groups)) return false;
-    const float t = tops[e];
-    if (!(t > kLowest)) return false;
-    x.key = beam_key(t, g);
-    x.score = scored(x.k, t);
-    return true;
+  // --- the best groups; an ended beam counts as its first group, with its score as it is
+  auto group_score = [&](int k, int g, float t) -> uint64_t {   // 0: no candidate
+    if (ended[k]) return g ? 0 : static_cast<uint64_t>(ordered(score[k])) << 32 | ordered(0.0f);
+    return isnan(lse[k].x) || !(t > kLowest) ? 0 : pair_score(t, lse[k], score[k]);
   };
+  // calls f(e, k, g) for the thread's groups, numbered through the rows
   auto each_group = [&](auto f) {
+    int k = tid / p.groups, g = tid - k * p.groups;
+#pragma unroll 1
     for (int e = tid; e < total; e += kJoinThreads) {
-      Candidate x;
-      if (group(e, x)) f(x);
+      f(e, k, g);
+      for (g += kJoinThreads; g >= p.groups; g -= p.groups) ++k;
     }
   };
+  auto top_of = [&](int e) { return e < kJoinEarly ? early[e] : group_top(e); };
   uint32_t mine = 0;
-  each_group([&](const Candidate& x) { mine = max(mine, static_cast<uint32_t>(x.score >> 32)); });
-  // A bound that n groups are not below and not many more than n: of the threads' largest, by
-  // halving what lies between 0 and the largest of all until n to 2 n of them are left.
-  uint32_t low = 0;
-  if (__syncthreads_count(mine != 0) > p.n) {
+  each_group([&](int e, int k, int g) {
+    const uint32_t o = static_cast<uint32_t>(group_score(k, g, top_of(e)) >> 32);
+    if (e < kJoinEarly) early_score[e] = o;
+    mine = max(mine, o);
+  });
+  // A bound that n groups are not below and not many more than n: the n-th largest of what the
+  // warps' lanes have, ceil(n / warps) + 1 of each warp's.
+  const int per_warp = (p.n + kJoinWarps - 1) / kJoinWarps + 1;
+  for (int i = 0; i < per_warp; ++i) {
     const uint32_t top = __reduce_max_sync(kFullMask, mine);
-    if (lane == 0) warp_top[warp] = top;
-    __syncthreads();
-    uint32_t high = 0;                                     // fewer than n are above it
-#pragma unroll
-    for (int w = 0; w < kJoinWarps; ++w) high = max(high, warp_top[w]);
-    while (high - low > 1) {
-      const uint32_t mid = low + (high - low) / 2;
-      const int above = __syncthreads_count(mine >= mid);
-      if (above >= p.n) low = mid; else high = mid;
-      if (above >= p.n && above <= 2 * p.n) break;
-    }
+    const uint32_t who = __ballot_sync(kFullMask, mine == top);
+    if (lane == 0) tops_of_warps[warp * per_warp + i] = top;
+    if (lane == __ffs(who) - 1) mine = 0;
   }
-  if (mine != 0 && mine >= low)
-    each_group([&](const Candidate& x) {
-      if (static_cast<uint32_t>(x.score >> 32) >= low) groups.add(x);
-    });
   __syncthreads();
-  groups.best(p.n, tid, each_group, [&](int rank, bool some, const Candidate& x) {
-    if (!some) return;
-    chosen[rank] = x;
-    atomicAdd(&n_chosen, 1);
+  uint32_t low = 0;
+  const int n_tops = kJoinWarps * per_warp;
+  for (int i = lane; i - lane < n_tops; i += 32) {         // the one with n - 1 before it
+    const uint32_t x = i < n_tops ? tops_of_warps[i] : 0;
+    int rank = 0;
+#pragma unroll 4
+    for (int j = 0; j < n_tops; ++j) {
+      const uint32_t other = tops_of_warps[j];
+      rank += other > x || (other == x && j < i);
+    }
+    const uint32_t who = __ballot_sync(kFullMask, i < n_tops && rank == p.n - 1);
+    if (who) low = __shfl_sync(kFullMask, x, __ffs(who) - 1);
+  }
+  const uint64_t bound = static_cast<uint64_t>(low) << 32 | 1u;   // (1: what scores 0 is no candidate)
+  auto group = [&](int e, int k, int g) {
+    const float t = top_of(e);
+    return Candidate{group_score(k, g, t), beam_key(ended[k] ? 0.0f : t, g), k};
+  };
+  each_group([&](int e, int k, int g) {
+    if (e < kJoinEarly && early_score[e] < max(low, 1u)) return;
+    const Candidate x = group(e, k, g);
+    if (x.score < bound) return;
+    const int at = atomicAdd(&n_chosen, 1);
+    if (at < kJoinGroups) chosen[at] = x;
   });
   __syncthreads();
+  // few enough to look through all of them; else the n best alone
+  uint64_t least = bound;
+  int n_groups = n_chosen;
+  if (n_groups > kJoinGroups) {
+    list.best_in_rounds(p.n, tid, [&](auto f) {
+      each_group([&](int e, int k, int g) {
+        const Candidate x = group(e, k, g);
+        if (x.score) f(x);
+      });
+    }, [&](int rank, bool, const Candidate& x) { chosen[rank] = x; });
+    n_groups = p.n;                                        // (there are more than that)
+    least = chosen[p.n - 1].score;
+  }
 
-  // --- their logits: those that are not behind the n-th group's largest
-  const int n_groups = n_chosen;
-  const uint64_t least = n_groups == p.n ? chosen[p.n - 1].score : 0;
+  // --- their logits, as far as they may be among the n
   auto each_logit = [&](auto f) {
+#pragma unroll 1
     for (int i = warp; i < n_groups; i += kJoinWarps) {
-      const int k = chosen[i].k;
-      if (ended[k]) {
-        if (lane == 0) f(Candidate{chosen[i].score, beam_key(0.0f, p.end_token), k});
+      const Candidate from = chosen[i];
+      if (ended[from.k]) {
+        if (lane == 0) f(Candidate{from.score, beam_key(0.0f, p.end_token), from.k});
         continue;
       }
-      const int g = key_token(chosen[i].key);
+      const int g = key_token(from.key);
       int lead;
-      const T* base = beam_row<T>(p, b * p.K + k, lead);
-      // most logits are far below: their scores need not be computed
-      const float far_from = key_high(least), s0 = score[k], l0 = lse[k].x;
-      const float far = least ? far_from - s0 + l0 - 1e-6f * (fabsf(far_from) + fabsf(s0) + fabsf(l0)) : kLowest;
+      const T* base = beam_row<T>(p, b * p.K + from.k, lead);
       Chunk c[L::kVectors];
       load_group<T>(p, base, lead, g, lane, c);
+      // most logits are far below: their scores need not be computed
+      const float far_from = key_high(least), s0 = score[from.k];
+      const float2 l = lse[from.k];
+      const float far = far_from > -INFINITY
+                            ? far_from - s0 + l.x - 1e-6f * (fabsf(far_from) + fabsf(s0) + fabsf(l.x))
+                            : kLowest;                     // (a bound below every number)
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
         const float2 pr = L::pair(c, j / 2);
         const float x = j & 1 ? pr.y : pr.x;
-        if (!(x > kLowest) || x < far) continue;
-        const uint64_t s = scored(k, x);
-        if (s < least) continue;
-        f(Candidate{s, beam_key(x, g * kGroup + ((j / L::kVec) * 32 + lane) * L::kVec + j % L::kVec - lead), k});
+        if (x > kLowest && x >= far)
+          f(Candidate{pair_score(x, l, s0),
+                      beam_key(x, g * kGroup + ((j / L::kVec) * 32 + lane) * L::kVec + j % L::kVec - lead), from.k});
       }
     }
   };
   each_logit([&](const Candidate& x) { list.add(x); });
   __syncthreads();
   const long long outs = static_cast<long long>(p.B) * p.n;
-  list.best(p.n, tid, each_logit, [&](int rank, bool some, const Candidate& x) {
+  auto out = [&](int rank, bool some, const Candidate& x) {
     const int64_t at = static_cast<int64_t>(b) * p.n + rank;
     const int token = some ? key_token(x.key) : -1;
     if (FP4Q_IN_RANGE(p, p.out_scores + at, 4, p.out_scores, 4 * outs))
@@ -475,13 +550,18 @@ __global__ void __launch_bounds__(kJoinThreads) beam_join_kernel(const BeamParam
     if (FP4Q_IN_RANGE(p, p.out_tokens + at, 4, p.out_tokens, 4 * outs)) p.out_tokens[at] = token;
     if (p.out_finished && FP4Q_IN_RANGE(p, p.out_finished + at, 1, p.out_finished, outs))
       p.out_finished[at] = some && (ended[x.k] || token == p.end_token);
-  });
+  };
+  if (list.count <= kJoinList)
+    list.best(p.n, tid, out);
+  else
+    list.best_in_rounds(p.n, tid, each_logit, out);
 }
 
 }  // namespace
 
-// Parts of a row: four times as many warps as the device holds at a time, of whole groups.
-constexpr int kScanWarpsPerSm = 4 * kScanCtas * kScanWarps;
+// Parts of a row: twice as many warps as the device holds at a time, of whole groups (64 x 8
+// beams of 131072 logits: 35.7 us; as many 36.6, four times 37.9).
+constexpr int kScanWarpsPerSm = 2 * kScanCtas * kScanWarps;
 
 static int64_t groups_of(int64_t V) { return (V + 15 + kGroup - 1) / kGroup; }   // of a row of any alignment
 static int64_t part_slots(int sms, int64_t rows) { return std::max<int64_t>(rows, static_cast<int64_t>(sms) * kScanWarpsPerSm); }
