@@ -76,7 +76,8 @@ typedef enum {
   FP4_ERR_UNSUPPORTED_SHAPE = 2, /* H % b != 0, H < 64, or H above the maximum     */
   FP4_ERR_MISALIGNED = 3,        /* a pointer breaks the alignment rule below       */
   FP4_ERR_CUDA = 4,              /* the CUDA runtime reported an error on launch    */
-  FP4_ERR_TIMEOUT = 5            /* a kernel gave up on a bounded wait (device status word) */
+  FP4_ERR_TIMEOUT = 5,           /* a kernel gave up on a bounded wait (device status word) */
+  FP4_ERR_NO_PAGES = 6           /* a sequence found no free page, or no room in its table (device status word) */
 } fp4_status_t;
 
 /*
@@ -87,7 +88,8 @@ typedef enum {
  * trap: it stops, marks what it could not compute and returns, and the
  * context stays usable.  The calls that take an optional `status` (a DEVICE
  * pointer to one int32_t owned by the caller) then store FP4_ERR_TIMEOUT
- * there.  The library never writes anything else to it and never clears it:
+ * there.  The library never clears it (and writes nothing else to it, but
+ * FP4_ERR_NO_PAGES in fp4_kv_fork_nvfp4):
  * zero it before the call, synchronise, and read it (fp4_read_device_status
  * does the last two).  What a timed-out call leaves behind:
  *   fused op: every scale byte of the rows the CTA did not finish is 0xFF
@@ -526,6 +528,94 @@ FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t H
                                                  int64_t max_keys, int64_t out[2]);
 
 /*
+ * Pages of the cache between two tokens.  A sequence's pages are the first
+ * ceil(len / page_size) entries of its row of block_tables; refs counts for every page
+ * how many entries hold it, those of tables that are not in the call and those of any other
+ * keeper (a store of prompts) included.  A page with refs <= 0 is free.  Entries outside
+ * [0, num_pages) hold no page (pages given up behind a window: -1).
+ * The three calls below read tables, lengths and counts and write new ones: the old ones
+ * stay as they are, so a call can be repeated, and a loop goes back and forth between two
+ * sets of buffers.  What they choose goes by the lowest number and does not change from call
+ * to call.  All arrays are on the device and read there, so that a captured call follows
+ * them; nothing that is written may overlap anything else the call reads or writes.
+ *
+ * fp4_kv_fork_nvfp4 - sequences are continued by their children (the next step of a beam
+ * search, samples of one prompt, one more token of every sequence), and end.
+ *
+ *   refs           [num_pages] int32.
+ *   tables, max_pages, seq_lens  [B, max_pages] and [B] int32: the old sequences.  All of them end
+ *                  with the call; one goes on as itself by being a child's parent.
+ *   parents        [N] int32: the old sequence that child i continues; outside [0, B) (beams that have
+ *                  no candidate: -1): the child is empty.  NULL: child i continues sequence i (N == B).
+ *   new_lens, new_tokens  [N] int32, or NULL: tokens that child i is about to append, at most (NULL:
+ *                  exactly) new_tokens; 0 for an empty child.
+ *   out_tables, out_seq_lens  [N, max_pages] and [N] int32: the children, with room for their new
+ *                  tokens, which out_seq_lens counts (as fp4_attention_nvfp4 does); -1 behind a row's end.
+ *   out_refs       [num_pages] int32, never negative.
+ *   out_slots      [N, new_tokens] int64: where the new tokens go, as fp4_kv_append_nvfp4 takes them; -1
+ *                  behind a child's last and where there is no page.  NULL with new_tokens 0.
+ *   workspace      at least fp4_kv_pages_workspace_bytes(num_pages, N) bytes, 16-byte aligned, any
+ *                  contents; two calls that may run at the same time need one each.
+ *   status         as in fp4_add_rmsnorm_quant_ex; receives FP4_ERR_NO_PAGES where free pages or a
+ *                  table's entries run out: the children behind (in order) then lack pages (entries
+ *                  and slots -1), and a length stops at max_pages * page_size.
+ * Children share their parents' full pages.  A last page that is not full and is about to be
+ * written stays with its first child if nobody else holds it; every other child gets a
+ * copy, of its tokens up to the next multiple of 16.  Pages are taken in the children's order, each the
+ * lowest free one, those that the old sequences have left among them.
+ */
+FP4Q_API fp4_status_t fp4_kv_fork_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs,
+                                        const int32_t* tables, int64_t max_pages,
+                                        const int32_t* seq_lens, int64_t B, const int32_t* parents,
+                                        const int32_t* new_lens, int64_t N, int64_t new_tokens,
+                                        int32_t* out_tables, int32_t* out_seq_lens,
+                                        int32_t* out_refs, int64_t* out_slots, void* workspace,
+                                        int64_t workspace_bytes, int32_t* status, int pdl,
+                                        fp4q_stream_t stream);
+
+/*
+ * fp4_kv_trim_nvfp4 - sequences give up tokens: those that end, drafted tokens that were not
+ * taken, what lies behind a window.
+ *
+ *   first, end     [B] int32, or NULL (0; the length): tokens first .. end - 1 stay.  Pages that hold
+ *                  none of them are given up: out_tables has -1 there and everywhere behind the
+ *                  sequence's pages (and for an entry that holds no page).
+ *   out_seq_lens   [B] int32: min(end, length), not changed by first.
+ *   out_refs       [num_pages] int32.
+ * Other arguments as above.  Only the sizes of `cache` count; no page is read or written.
+ */
+FP4Q_API fp4_status_t fp4_kv_trim_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs,
+                                        const int32_t* tables, int64_t max_pages,
+                                        const int32_t* seq_lens, int64_t B, const int32_t* first,
+                                        const int32_t* end, int32_t* out_tables,
+                                        int32_t* out_seq_lens, int32_t* out_refs, int pdl,
+                                        fp4q_stream_t stream);
+
+/*
+ * fp4_kv_compact_nvfp4 - the n pages with refs > 0 become pages 0 .. n - 1: those from n on
+ * move to the free ones before n, both in ascending order, the others stay.
+ *
+ *   out_tables     [B, max_pages] int32: tables with the new numbers, -1 behind a sequence's pages and
+ *                  for an entry that holds no page.
+ *   out_refs       [num_pages] int32: the counts by the new numbers, 0 from n on.
+ *   out_map        [num_pages] int32: every page's new number, -1 for a free one (for tables that
+ *                  are not in the call).
+ *   out_live       one int32: n.
+ *   workspace      at least fp4_kv_pages_workspace_bytes(num_pages, 0) bytes, as above.
+ * Pages from n on keep their bytes.
+ */
+FP4Q_API fp4_status_t fp4_kv_compact_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs,
+                                           const int32_t* tables, int64_t max_pages,
+                                           const int32_t* seq_lens, int64_t B, int32_t* out_tables,
+                                           int32_t* out_refs, int32_t* out_map, int32_t* out_live,
+                                           void* workspace, int64_t workspace_bytes, int pdl,
+                                           fp4q_stream_t stream);
+
+/* Bytes of workspace of a fork into N children (of a compaction: N = 0); grows with both.
+ * -1 on bad arguments. */
+FP4Q_API int64_t fp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t N);
+
+/*
  * fp4_beam_select - the best continuations of every beam search of a batch:
  * of batch entry b the n candidates (beam k, token v) with the largest
  *
@@ -542,7 +632,7 @@ FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t H
  *                  above 2^125.  A logit of at most -2^125 (a mask of -infinity or of the type's lowest
  *                  value) is no candidate and adds nothing to the sum.
  *   finished       [B, K] bytes or NULL: a beam with a nonzero byte has ended; its one candidate
- *                  is end_token with its score as it is, and its logits are not read.
+ *                  is end_token with its score as it is, whatever its logits are.
  *   end_token      in [0, V).
  *   K, V, n        beams (at most 256), vocabulary (at most 2^24), candidates to take (at most 64).
  *   out_scores     [B, n] fp32: the scores, rounded once; -infinity behind the last candidate.
@@ -570,7 +660,7 @@ FP4Q_API int64_t fp4_beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V
 
 /*
  * fp4_read_device_status - synchronises `stream`, then copies the device
- * status word back and returns it as a status: FP4_OK (0) or FP4_ERR_TIMEOUT;
+ * status word back and returns it as a status: FP4_OK (0), FP4_ERR_TIMEOUT or FP4_ERR_NO_PAGES;
  * FP4_ERR_INVALID_ARG for a NULL or misaligned pointer or a value that is no
  * status; FP4_ERR_CUDA if the synchronisation or the copy failed.  Blocks the
  * calling thread; not for use inside stream capture.

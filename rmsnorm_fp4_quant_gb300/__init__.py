@@ -41,6 +41,7 @@ from ._binding import (  # noqa: F401
     FP4_ERR_MISALIGNED,
     FP4_ERR_CUDA,
     FP4_ERR_TIMEOUT,
+    FP4_ERR_NO_PAGES,
     FP4_EPI_BF16,
     FP4_EPI_GELU_BF16,
     FP4_EPI_GELU_NVFP4,
@@ -69,10 +70,17 @@ from ._binding import (  # noqa: F401
     fp4_gemm_nvfp4_bf16,
     fp4_gemm_ex,
     fp4_kv_append_nvfp4,
+    fp4_kv_compact_nvfp4,
+    fp4_kv_fork_nvfp4,
     fp4_kv_gather_nvfp4,
+    fp4_kv_pages_workspace_bytes,
+    fp4_kv_trim_nvfp4,
     kv_append_nvfp4,
     kv_cache_nvfp4,
+    kv_compact_nvfp4,
+    kv_fork_nvfp4,
     kv_gather_nvfp4,
+    kv_trim_nvfp4,
     fp4_read_device_status,
     read_device_status,
     fp4_quantize,

@@ -13,7 +13,7 @@ FP4_DT_BF16, FP4_DT_FP16, FP4_DT_FP32 = 0, 1, 2
 FP4_NVFP4, FP4_MXFP4, FP4_E4M3_B32 = 0, 1, 2
 FP4_SF_ROWMAJOR, FP4_SF_SWIZZLED, FP4_SF_BOTH = 0, 1, 2
 FP4_OK, FP4_ERR_INVALID_ARG, FP4_ERR_UNSUPPORTED_SHAPE, FP4_ERR_MISALIGNED = 0, 1, 2, 3
-FP4_ERR_CUDA, FP4_ERR_TIMEOUT = 4, 5
+FP4_ERR_CUDA, FP4_ERR_TIMEOUT, FP4_ERR_NO_PAGES = 4, 5, 6
 FP4_EPI_BF16, FP4_EPI_GELU_BF16, FP4_EPI_GELU_NVFP4 = 0, 1, 2
 
 _FORMATS = {"nvfp4": FP4_NVFP4, "mxfp4": FP4_MXFP4, "e4m3b32": FP4_E4M3_B32}
@@ -149,6 +149,15 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_attention_workspace_bound.restype = i64
     L.fp4_attention_launch_shape.argtypes = [i64, i64, i64, i64, i64, i64, ctypes.POINTER(i64)]
     L.fp4_attention_launch_shape.restype = ci
+    L.fp4_kv_fork_nvfp4.argtypes = [cp, vp, vp, i64, vp, i64, vp, vp, i64, i64, vp, vp, vp, vp, vp,
+                                    i64, vp, ci, vp]
+    L.fp4_kv_fork_nvfp4.restype = ci
+    L.fp4_kv_trim_nvfp4.argtypes = [cp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, ci, vp]
+    L.fp4_kv_trim_nvfp4.restype = ci
+    L.fp4_kv_compact_nvfp4.argtypes = [cp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, ci, vp]
+    L.fp4_kv_compact_nvfp4.restype = ci
+    L.fp4_kv_pages_workspace_bytes.argtypes = [i64, i64]
+    L.fp4_kv_pages_workspace_bytes.restype = i64
     L.fp4_beam_select.argtypes = [vp, i64, ci, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
                                   i64, ci, vp]
     L.fp4_beam_select.restype = ci
@@ -293,6 +302,41 @@ def fp4_attention_workspace_bound(B: int, T: int, Hq: int, num_kv_heads: int, he
     allocates once (fp4_attention_workspace_bytes is for one call: a smaller call may
     need more than a larger one)."""
     return lib().fp4_attention_workspace_bound(B, T, Hq, num_kv_heads, head_dim, max_keys)
+
+
+def fp4_kv_fork_nvfp4(cache: KVCacheStruct, refs_ptr: int, tables_ptr: int, max_pages: int,
+                      seq_lens_ptr: int, B: int, parents_ptr: int, new_lens_ptr: int, N: int,
+                      new_tokens: int, out_tables_ptr: int, out_seq_lens_ptr: int, out_refs_ptr: int,
+                      out_slots_ptr: int, workspace_ptr: int, workspace_bytes: int, status_ptr: int,
+                      pdl: int, stream: int) -> int:
+    return lib().fp4_kv_fork_nvfp4(cache, refs_ptr or None, tables_ptr or None, max_pages,
+                                   seq_lens_ptr or None, B, parents_ptr or None, new_lens_ptr or None,
+                                   N, new_tokens, out_tables_ptr or None, out_seq_lens_ptr or None,
+                                   out_refs_ptr or None, out_slots_ptr or None, workspace_ptr or None,
+                                   workspace_bytes, status_ptr or None, pdl, stream or None)
+
+
+def fp4_kv_trim_nvfp4(cache: KVCacheStruct, refs_ptr: int, tables_ptr: int, max_pages: int,
+                      seq_lens_ptr: int, B: int, first_ptr: int, end_ptr: int, out_tables_ptr: int,
+                      out_seq_lens_ptr: int, out_refs_ptr: int, pdl: int, stream: int) -> int:
+    return lib().fp4_kv_trim_nvfp4(cache, refs_ptr or None, tables_ptr or None, max_pages,
+                                   seq_lens_ptr or None, B, first_ptr or None, end_ptr or None,
+                                   out_tables_ptr or None, out_seq_lens_ptr or None,
+                                   out_refs_ptr or None, pdl, stream or None)
+
+
+def fp4_kv_compact_nvfp4(cache: KVCacheStruct, refs_ptr: int, tables_ptr: int, max_pages: int,
+                         seq_lens_ptr: int, B: int, out_tables_ptr: int, out_refs_ptr: int,
+                         out_map_ptr: int, out_live_ptr: int, workspace_ptr: int,
+                         workspace_bytes: int, pdl: int, stream: int) -> int:
+    return lib().fp4_kv_compact_nvfp4(cache, refs_ptr or None, tables_ptr or None, max_pages,
+                                      seq_lens_ptr or None, B, out_tables_ptr or None,
+                                      out_refs_ptr or None, out_map_ptr or None, out_live_ptr or None,
+                                      workspace_ptr or None, workspace_bytes, pdl, stream or None)
+
+
+def fp4_kv_pages_workspace_bytes(num_pages: int, N: int) -> int:
+    return lib().fp4_kv_pages_workspace_bytes(num_pages, N)
 
 
 def fp4_beam_select(logits_ptr: int, row_stride: int, dtype: int, scores_ptr: int, finished_ptr: int,
@@ -461,9 +505,9 @@ def _status_ptr(status) -> int:
 
 def read_device_status(status, stream=None) -> int:
     """Synchronises the stream and returns the device status word as a status
-    code (FP4_OK or FP4_ERR_TIMEOUT)."""
+    code (FP4_OK, FP4_ERR_TIMEOUT or FP4_ERR_NO_PAGES)."""
     st = fp4_read_device_status(_status_ptr(status), _stream_handle(stream))
-    if st not in (FP4_OK, FP4_ERR_TIMEOUT):
+    if st not in (FP4_OK, FP4_ERR_TIMEOUT, FP4_ERR_NO_PAGES):
         raise Fp4Error(st, "fp4_read_device_status")
     return st
 
@@ -1036,3 +1080,131 @@ def beam_select(logits, scores, take: Optional[int] = None, finished=None, end_t
     if st != 0:
         raise Fp4Error(st, "fp4_beam_select")
     return tuple(out)
+
+
+def _page_state(torch, cache, refs, tables, seq_lens):
+    """(fp4_kv_cache_t, device, B, max_pages, addresses of refs, tables and seq_lens)."""
+    struct, dev, _, _ = _kv_struct(torch, cache, None, None)
+    i32 = torch.int32
+    if tables.dim() != 2:
+        raise ValueError("tables must be (B, max_pages)")
+    B, most = tables.shape
+    return (struct, dev, B, most, _dense_ptr(refs, "refs", dev, i32, (struct.num_pages,)),
+            _dense_ptr(tables, "tables", dev, i32, (B, most)), _dense_ptr(seq_lens, "seq_lens", dev, i32, (B,)))
+
+
+def kv_fork_nvfp4(cache, refs, tables, seq_lens, parents=None, new_tokens: int = 1, new_lens=None,
+                  out_tables=None, out_seq_lens=None, out_refs=None, out_slots=None, workspace=None,
+                  status=None, pdl: bool = False, stream=None):
+    """Continues the cache's sequences by their children, with room for new tokens; returns
+    (tables, seq_lens, refs, slots) of the children.
+
+    refs: (num_pages,) int32, how many table entries (and other keepers) hold each page, 0 = free.
+    tables: (B, max_pages) int32 and seq_lens: (B,) int32: the old sequences, which all end with
+    the call.  parents: (N,) int32, the old sequence that each child continues, -1 for an
+    empty child; None: every sequence continues itself.  new_tokens: tokens that each child
+    is about to append; new_lens: optional (N,) int32, how many of them.  Children share
+    full pages; a last page that is about to be written stays with its first child if nobody
+    else holds it and is copied for the others.  seq_lens come back with the new tokens
+    counted, slots (N, new_tokens) int64 say where they go (kv_append_nvfp4; -1: nowhere).
+    Nothing that the call is given changes, except free pages of the cache.  out_*: what to
+    write instead of new tensors.  status: as in attention_nvfp4; receives FP4_ERR_NO_PAGES
+    where pages, or a table's entries, run out.  workspace: optional uint8 tensor of
+    fp4_kv_pages_workspace_bytes(num_pages, N) bytes, for one call at a time."""
+    torch = _torch()
+    struct, dev, B, most, r, t, l = _page_state(torch, cache, refs, tables, seq_lens)
+    i32 = torch.int32
+    par = 0
+    N = B
+    if parents is not None:
+        if parents.dim() != 1:
+            raise ValueError("parents must be (N,)")
+        N = parents.shape[0]
+        par = _dense_ptr(parents, "parents", dev, i32, (N,))
+    if new_tokens < 0:
+        raise ValueError("new_tokens must not be negative")
+    more = _dense_ptr(new_lens, "new_lens", dev, i32, (N,)) if new_lens is not None else 0
+    if out_tables is None or out_seq_lens is None or out_refs is None or out_slots is None:
+        with _on(stream):
+            if out_tables is None:
+                out_tables = torch.empty(N, most, dtype=i32, device=tables.device)
+            if out_seq_lens is None:
+                out_seq_lens = torch.empty(N, dtype=i32, device=tables.device)
+            if out_refs is None:
+                out_refs = torch.empty_like(refs)
+            if out_slots is None:
+                out_slots = torch.empty(N, new_tokens, dtype=torch.int64, device=tables.device)
+    o_t = _dense_ptr(out_tables, "out_tables", dev, i32, (N, most))
+    o_l = _dense_ptr(out_seq_lens, "out_seq_lens", dev, i32, (N,))
+    o_r = _dense_ptr(out_refs, "out_refs", dev, i32, (struct.num_pages,))
+    o_s = _dense_ptr(out_slots, "out_slots", dev, torch.int64, (N, new_tokens))
+    if status is not None:
+        _same_device(dev, "status", status)
+    status_ptr = _status_ptr(status)
+    L = lib()
+    handle = _kv_stream(torch, stream, dev)
+    size = max(L.fp4_kv_pages_workspace_bytes(struct.num_pages, N), 0)
+    with _Workspace(torch, workspace, size, dev, handle, stream) as ws:
+        st = L.fp4_kv_fork_nvfp4(struct, r, t, most, l, B, par or None, more or None, N, new_tokens, o_t, o_l,
+                                 o_r, o_s, ws.ptr, ws.size, status_ptr or None, 1 if pdl else 0, handle)
+    if st != 0:
+        raise Fp4Error(st, "fp4_kv_fork_nvfp4")
+    return out_tables, out_seq_lens, out_refs, out_slots
+
+
+def kv_trim_nvfp4(cache, refs, tables, seq_lens, first=None, end=None, out_tables=None, out_seq_lens=None,
+                  out_refs=None, pdl: bool = False, stream=None):
+    """Sequences keep tokens first .. end - 1 and give up the pages that hold none of them;
+    returns (tables, seq_lens, refs).
+
+    first, end: (B,) int32 or None (0; the length): end 0 for a sequence that has ended, less
+    than its length where drafted tokens were not taken, first behind 0 where a window has
+    moved on.  Given-up pages are -1 in tables; seq_lens are min(end, length), as keys keep
+    their places.  Other arguments as in kv_fork_nvfp4; of the cache only the sizes count."""
+    torch = _torch()
+    struct, dev, B, most, r, t, l = _page_state(torch, cache, refs, tables, seq_lens)
+    i32 = torch.int32
+    f = _dense_ptr(first, "first", dev, i32, (B,)) if first is not None else 0
+    e = _dense_ptr(end, "end", dev, i32, (B,)) if end is not None else 0
+    if out_tables is None or out_seq_lens is None or out_refs is None:
+        with _on(stream):
+            out_tables = torch.empty_like(tables) if out_tables is None else out_tables
+            out_seq_lens = torch.empty_like(seq_lens) if out_seq_lens is None else out_seq_lens
+            out_refs = torch.empty_like(refs) if out_refs is None else out_refs
+    st = lib().fp4_kv_trim_nvfp4(struct, r, t, most, l, B, f or None, e or None,
+                                 _dense_ptr(out_tables, "out_tables", dev, i32, (B, most)),
+                                 _dense_ptr(out_seq_lens, "out_seq_lens", dev, i32, (B,)),
+                                 _dense_ptr(out_refs, "out_refs", dev, i32, (struct.num_pages,)),
+                                 1 if pdl else 0, _kv_stream(torch, stream, dev))
+    if st != 0:
+        raise Fp4Error(st, "fp4_kv_trim_nvfp4")
+    return out_tables, out_seq_lens, out_refs
+
+
+def kv_compact_nvfp4(cache, refs, tables, seq_lens, out_tables=None, out_refs=None, out_map=None, out_live=None,
+                     workspace=None, pdl: bool = False, stream=None):
+    """Moves the pages that are held (refs > 0) to the lowest numbers; returns (tables, refs,
+    map, live): tables and counts by the new numbers, (num_pages,) int32 with every page's new
+    number (-1: free; for tables that are not in the call), and (1,) int32, how many are held.
+    Other arguments as in kv_fork_nvfp4, the workspace for N = 0."""
+    torch = _torch()
+    struct, dev, B, most, r, t, l = _page_state(torch, cache, refs, tables, seq_lens)
+    i32, pages = torch.int32, struct.num_pages
+    if out_tables is None or out_refs is None or out_map is None or out_live is None:
+        with _on(stream):
+            out_tables = torch.empty_like(tables) if out_tables is None else out_tables
+            out_refs = torch.empty_like(refs) if out_refs is None else out_refs
+            out_map = torch.empty_like(refs) if out_map is None else out_map
+            out_live = torch.empty(1, dtype=i32, device=refs.device) if out_live is None else out_live
+    o_t = _dense_ptr(out_tables, "out_tables", dev, i32, (B, most))
+    o_r = _dense_ptr(out_refs, "out_refs", dev, i32, (pages,))
+    o_m = _dense_ptr(out_map, "out_map", dev, i32, (pages,))
+    o_n = _dense_ptr(out_live, "out_live", dev, i32, (1,))
+    L = lib()
+    handle = _kv_stream(torch, stream, dev)
+    with _Workspace(torch, workspace, max(L.fp4_kv_pages_workspace_bytes(pages, 0), 0), dev, handle, stream) as ws:
+        st = L.fp4_kv_compact_nvfp4(struct, r, t, most, l, B, o_t, o_r, o_m, o_n, ws.ptr, ws.size,
+                                    1 if pdl else 0, handle)
+    if st != 0:
+        raise Fp4Error(st, "fp4_kv_compact_nvfp4")
+    return out_tables, out_refs, out_map, out_live

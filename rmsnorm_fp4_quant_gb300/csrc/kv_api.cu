@@ -1,6 +1,6 @@
 // kv_api.cu - the C entry points of the NVFP4 key/value cache (declared in
-// include/fp4q.h): argument checks; the kernels are in kv_cache.cu and
-// kv_attention.cu.
+// include/fp4q.h): argument checks; the kernels are in kv_cache.cu,
+// kv_attention.cu and kv_pages.cu.
 #include <cuda_runtime.h>
 
 #include <cmath>
@@ -86,6 +86,24 @@ bool valid_attention_sizes(int64_t B, int64_t T, int64_t Hq, int64_t num_kv_head
                            int64_t max_keys) {
   return B >= 0 && T >= 0 && max_keys >= 0 && Hq > 0 && num_kv_heads > 0 && Hq % num_kv_heads == 0 &&
          (head_dim == 64 || head_dim == 128) && numbered_in_32_bits(B, T, Hq, num_kv_heads, max_keys);
+}
+
+// Page tables, lengths and counts of fork, trim and compact: sizes that the kernels number
+// in 32 bits (tokens of a sequence, slots of children, entries of the plan's grid).
+bool pages_in_32_bits(const fp4_kv_cache_t& c, int64_t rows, int64_t max_pages) {
+  return max_pages <= INT32_MAX / 2 / c.page_size && rows <= INT32_MAX / 4 &&
+         (max_pages == 0 || rows <= INT32_MAX / 2 / max_pages);
+}
+// What is written overlaps nothing else that is written or read.
+template <int W, int R>
+bool apart(const Rows (&writes)[W], const Rows (&reads)[R]) {
+  for (int i = 0; i < W; ++i) {
+    for (int j = i + 1; j < W; ++j)
+      if (rows_overlap(writes[i], writes[j])) return false;
+    for (const Rows& r : reads)
+      if (rows_overlap(writes[i], r)) return false;
+  }
+  return true;
 }
 
 bool valid_dtype(fp4_dtype_t d) { return d == FP4_DT_BF16 || d == FP4_DT_FP16; }
@@ -291,6 +309,141 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   FP4Q_SET_DEBUG(p);
   return static_cast<fp4_status_t>(record_cuda_error(launch_kv_attention(
       dtype == FP4_DT_BF16 ? 0 : 1, p, pdl, reinterpret_cast<cudaStream_t>(stream))));
+}
+
+int64_t fp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t N) {
+  if (num_pages < 0 || num_pages > INT32_MAX || N < 0 || N > INT32_MAX / 4) return -1;
+  return 4 * kv_pages_workspace(num_pages, N);
+}
+
+fp4_status_t fp4_kv_fork_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs, const int32_t* tables,
+                               int64_t max_pages, const int32_t* seq_lens, int64_t B, const int32_t* parents,
+                               const int32_t* new_lens, int64_t N, int64_t new_tokens, int32_t* out_tables,
+                               int32_t* out_seq_lens, int32_t* out_refs, int64_t* out_slots, void* workspace,
+                               int64_t workspace_bytes, int32_t* status, int pdl, fp4q_stream_t stream) {
+  if (B < 0 || N < 0 || max_pages < 0 || new_tokens < 0 || workspace_bytes < 0) return FP4_ERR_INVALID_ARG;
+  const fp4_status_t cs = check_cache_sizes(cache);
+  if (cs != FP4_OK) return cs;
+  if (!parents && N != B) return FP4_ERR_INVALID_ARG;
+  if (!pages_in_32_bits(*cache, B, max_pages) || !pages_in_32_bits(*cache, N, max_pages) ||
+      new_tokens > INT32_MAX / 4 || (new_tokens && N > INT32_MAX / new_tokens))
+    return FP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t pages = cache->num_pages, need = fp4_kv_pages_workspace_bytes(pages, N);
+  if (pages == 0 && B == 0 && N == 0) return FP4_OK;
+  if ((pages && (!refs || !out_refs)) || (B && !seq_lens) || (B && max_pages && !tables) ||
+      (N && (!out_seq_lens || (max_pages && !out_tables) || (new_tokens && !out_slots))) || !workspace ||
+      workspace_bytes < need)
+    return FP4_ERR_INVALID_ARG;
+  const fp4_status_t cb = check_cache_buffers(cache);
+  if (cb != FP4_OK) return cb;
+  if (!abi_aligned(refs, 4) || !abi_aligned(tables, 4) || !abi_aligned(seq_lens, 4) || !abi_aligned(parents, 4) ||
+      !abi_aligned(new_lens, 4) || !abi_aligned(out_tables, 4) || !abi_aligned(out_seq_lens, 4) ||
+      !abi_aligned(out_refs, 4) || !abi_aligned(out_slots, 8) || !abi_aligned(workspace, 16) || !abi_aligned(status, 4))
+    return FP4_ERR_MISALIGNED;
+  const CacheBuffers cbuf = buffers(*cache);
+  const Rows writes[] = {flat(out_tables, N * max_pages * 4), flat(out_seq_lens, N * 4), flat(out_refs, pages * 4),
+                         flat(out_slots, N * new_tokens * 8), flat(workspace, need), flat(status, 4),
+                         cbuf.rows[0], cbuf.rows[1], cbuf.rows[2], cbuf.rows[3]};
+  const Rows reads[] = {flat(refs, pages * 4), flat(tables, B * max_pages * 4), flat(seq_lens, B * 4),
+                        flat(parents, N * 4), flat(new_lens, N * 4)};
+  if (!apart(writes, reads)) return FP4_ERR_INVALID_ARG;
+  KvPagesParams p{};
+  p.c = device_cache(*cache);
+  p.refs = refs;
+  p.tables = tables;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.B = static_cast<int>(B);
+  p.out_tables = out_tables;
+  p.out_lens = out_seq_lens;
+  p.out_refs = out_refs;
+  p.parents = parents;
+  p.new_lens = new_lens;
+  p.N = static_cast<int>(N);
+  p.new_tokens = static_cast<int>(new_tokens);
+  p.out_slots = out_slots;
+  p.status = status;
+  p.ws = static_cast<int*>(workspace);
+  p.ws_ints = need / 4;
+  FP4Q_SET_DEBUG(p);
+  return static_cast<fp4_status_t>(
+      record_cuda_error(launch_kv_fork(p, pdl, reinterpret_cast<cudaStream_t>(stream))));
+}
+
+fp4_status_t fp4_kv_trim_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs, const int32_t* tables,
+                               int64_t max_pages, const int32_t* seq_lens, int64_t B, const int32_t* first,
+                               const int32_t* end, int32_t* out_tables, int32_t* out_seq_lens, int32_t* out_refs,
+                               int pdl, fp4q_stream_t stream) {
+  if (B < 0 || max_pages < 0) return FP4_ERR_INVALID_ARG;
+  const fp4_status_t cs = check_cache_sizes(cache);
+  if (cs != FP4_OK) return cs;
+  if (!pages_in_32_bits(*cache, B, max_pages)) return FP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t pages = cache->num_pages;
+  if (pages == 0 && B == 0) return FP4_OK;
+  if ((pages && (!refs || !out_refs)) || (B && (!seq_lens || !out_seq_lens || (max_pages && (!tables || !out_tables)))))
+    return FP4_ERR_INVALID_ARG;
+  if (!abi_aligned(refs, 4) || !abi_aligned(tables, 4) || !abi_aligned(seq_lens, 4) || !abi_aligned(first, 4) ||
+      !abi_aligned(end, 4) || !abi_aligned(out_tables, 4) || !abi_aligned(out_seq_lens, 4) || !abi_aligned(out_refs, 4))
+    return FP4_ERR_MISALIGNED;
+  const Rows writes[] = {flat(out_tables, B * max_pages * 4), flat(out_seq_lens, B * 4), flat(out_refs, pages * 4)};
+  const Rows reads[] = {flat(refs, pages * 4), flat(tables, B * max_pages * 4), flat(seq_lens, B * 4),
+                        flat(first, B * 4), flat(end, B * 4)};
+  if (!apart(writes, reads)) return FP4_ERR_INVALID_ARG;
+  KvPagesParams p{};
+  p.c = device_cache(*cache);
+  p.refs = refs;
+  p.tables = tables;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.B = static_cast<int>(B);
+  p.out_tables = out_tables;
+  p.out_lens = out_seq_lens;
+  p.out_refs = out_refs;
+  p.first = first;
+  p.end = end;
+  FP4Q_SET_DEBUG(p);
+  return static_cast<fp4_status_t>(
+      record_cuda_error(launch_kv_trim(p, pdl, reinterpret_cast<cudaStream_t>(stream))));
+}
+
+fp4_status_t fp4_kv_compact_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs, const int32_t* tables,
+                                  int64_t max_pages, const int32_t* seq_lens, int64_t B, int32_t* out_tables,
+                                  int32_t* out_refs, int32_t* out_map, int32_t* out_live, void* workspace,
+                                  int64_t workspace_bytes, int pdl, fp4q_stream_t stream) {
+  if (B < 0 || max_pages < 0 || workspace_bytes < 0) return FP4_ERR_INVALID_ARG;
+  const fp4_status_t cs = check_cache_sizes(cache);
+  if (cs != FP4_OK) return cs;
+  if (!pages_in_32_bits(*cache, B, max_pages)) return FP4_ERR_UNSUPPORTED_SHAPE;
+  const int64_t pages = cache->num_pages, need = fp4_kv_pages_workspace_bytes(pages, 0);
+  if ((pages && (!refs || !out_refs || !out_map)) || !out_live ||
+      (B && (!seq_lens || (max_pages && (!tables || !out_tables)))) || !workspace || workspace_bytes < need)
+    return FP4_ERR_INVALID_ARG;
+  const fp4_status_t cb = check_cache_buffers(cache);
+  if (cb != FP4_OK) return cb;
+  if (!abi_aligned(refs, 4) || !abi_aligned(tables, 4) || !abi_aligned(seq_lens, 4) || !abi_aligned(out_tables, 4) ||
+      !abi_aligned(out_refs, 4) || !abi_aligned(out_map, 4) || !abi_aligned(out_live, 4) || !abi_aligned(workspace, 16))
+    return FP4_ERR_MISALIGNED;
+  const CacheBuffers cbuf = buffers(*cache);
+  const Rows writes[] = {flat(out_tables, B * max_pages * 4), flat(out_refs, pages * 4), flat(out_map, pages * 4),
+                         flat(out_live, 4), flat(workspace, need), cbuf.rows[0], cbuf.rows[1], cbuf.rows[2], cbuf.rows[3]};
+  const Rows reads[] = {flat(refs, pages * 4), flat(tables, B * max_pages * 4), flat(seq_lens, B * 4)};
+  if (!apart(writes, reads)) return FP4_ERR_INVALID_ARG;
+  KvPagesParams p{};
+  p.c = device_cache(*cache);
+  p.refs = refs;
+  p.tables = tables;
+  p.max_pages = max_pages;
+  p.seq_lens = seq_lens;
+  p.B = static_cast<int>(B);
+  p.out_tables = out_tables;
+  p.out_refs = out_refs;
+  p.out_map = out_map;
+  p.out_live = out_live;
+  p.ws = static_cast<int*>(workspace);
+  p.ws_ints = need / 4;
+  FP4Q_SET_DEBUG(p);
+  return static_cast<fp4_status_t>(
+      record_cuda_error(launch_kv_compact(p, pdl, reinterpret_cast<cudaStream_t>(stream))));
 }
 
 }  // extern "C"

@@ -79,10 +79,44 @@ struct KvAttentionParams {
   FP4Q_DEBUG_FIELD
 };
 
+// Page tables, lengths and reference counts, before and after (kv_pages.cu).
+struct KvPagesParams {
+  KvCache c;
+  const int32_t* refs;
+  const int32_t* tables;
+  int64_t max_pages;
+  const int32_t* seq_lens;
+  int B;
+  int32_t* out_tables;
+  int32_t* out_lens;
+  int32_t* out_refs;
+  // fork
+  const int32_t* parents;    // or null: child i continues sequence i
+  const int32_t* new_lens;   // or null: new_tokens each
+  int N;
+  int new_tokens;
+  int64_t* out_slots;
+  int* status;
+  // trim
+  const int32_t* first;      // or null: 0
+  const int32_t* end;        // or null: the sequence's length
+  // compact
+  int32_t* out_map;
+  int32_t* out_live;
+  int* ws;
+  int64_t ws_ints;           // what the kernels need of it
+  FP4Q_DEBUG_FIELD
+};
+
 // dtype 0 = bf16, 1 = fp16; sizes and alignment checked by the caller.
 cudaError_t launch_kv_append(int dtype, const KvAppendParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_gather(int dtype, const KvGatherParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_fork(const KvPagesParams& p, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_trim(const KvPagesParams& p, int pdl, cudaStream_t stream);
+cudaError_t launch_kv_compact(const KvPagesParams& p, int pdl, cudaStream_t stream);
+// Ints of workspace of a fork of N children (0: of trim and compact).
+int64_t kv_pages_workspace(int64_t num_pages, int64_t N);
 // Bytes for sequences of at most `keys` keys.
 int64_t kv_attention_workspace(int sms, int64_t B, int64_t T, int Hq, int heads, int D, int64_t keys);
 // Bytes for every call of at most B sequences, T rows and `keys` keys.
