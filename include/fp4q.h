@@ -498,6 +498,41 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
                                           int64_t workspace_bytes, int32_t* status, int pdl,
                                           fp4q_stream_t stream);
 
+/*
+ * fp4_attention_nvfp4_ex - the same with capped logits, a bias that grows with distance,
+ * a window and a prefix.  With a sequence's rows at places pos = len - n_q + i of its keys
+ * (i = 0 .. n_q - 1), the logit of row pos, query head h and key j is
+ *
+ *   x = sm_scale * q k^T                             (softcap = 0)
+ *   x = softcap * tanh(sm_scale * q k^T / softcap)    (softcap > 0)
+ *   x - alibi_slopes[h] * |pos - j|                   (alibi_slopes not NULL)
+ *
+ * and the row sees the keys j with
+ *
+ *   j <= pos, or j < prefix_lens[b]        (causal; prefix_lens NULL: the first alone)
+ *   j > pos - window                       (window > 0)
+ *
+ *   softcap        >= 0, finite.
+ *   alibi_slopes   [Hq] fp32 or NULL.
+ *   window         >= 0; 0: none.  With causal only.  Pages that hold nothing but keys before the
+ *                  first row's window are not read (fp4_kv_trim_nvfp4 gives them up).
+ *   prefix_lens    [B] int32 or NULL (taken as clamped to [0, len]).  With causal only.
+ *   workspace      fp4_attention_workspace_bytes for max_keys, with a window for
+ *                  min(max_keys, window + ceil(T / B) + 63) (or _bound's).
+ * Logits are fp32, rounded once after each of the steps above; the cap's is off by a few 2^-24
+ * of softcap.  Other arguments, and what is rounded, as above.
+ */
+FP4Q_API fp4_status_t fp4_attention_nvfp4_ex(const void* q, int64_t q_stride,
+                                             const fp4_kv_cache_t* cache,
+                                             const int32_t* block_tables, int64_t max_pages,
+                                             const int32_t* seq_lens, const int32_t* cu_seqlens_q,
+                                             int64_t B, int64_t T, int64_t Hq, fp4_dtype_t dtype,
+                                             float sm_scale, int causal, float softcap,
+                                             const float* alibi_slopes, int64_t window,
+                                             const int32_t* prefix_lens, void* out, float* lse,
+                                             void* workspace, int64_t workspace_bytes,
+                                             int32_t* status, int pdl, fp4q_stream_t stream);
+
 /* Bytes of workspace fp4_attention_nvfp4 needs for exactly these sizes on the current
  * device (152 SMs taken when none is visible); max_keys = max_pages * page_size of its
  * call.  0 or more (0: none, workspace may be NULL), -1 on bad arguments.  A call with

@@ -143,6 +143,10 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_attention_nvfp4.argtypes = [vp, i64, cp, vp, i64, vp, vp, i64, i64, i64, ci,
                                       ctypes.c_float, ci, vp, vp, vp, i64, vp, ci, vp]
     L.fp4_attention_nvfp4.restype = ci
+    L.fp4_attention_nvfp4_ex.argtypes = [vp, i64, cp, vp, i64, vp, vp, i64, i64, i64, ci,
+                                         ctypes.c_float, ci, ctypes.c_float, vp, i64, vp, vp, vp,
+                                         vp, i64, vp, ci, vp]
+    L.fp4_attention_nvfp4_ex.restype = ci
     L.fp4_attention_workspace_bytes.argtypes = [i64, i64, i64, i64, i64, i64]
     L.fp4_attention_workspace_bytes.restype = i64
     L.fp4_attention_workspace_bound.argtypes = [i64, i64, i64, i64, i64, i64]
@@ -289,6 +293,20 @@ def fp4_attention_nvfp4(q_ptr: int, q_stride: int, cache: KVCacheStruct, block_t
                                      T, Hq, dtype, sm_scale, causal, out_ptr or None,
                                      lse_ptr or None, workspace_ptr or None, workspace_bytes,
                                      status_ptr or None, pdl, stream or None)
+
+
+def fp4_attention_nvfp4_ex(q_ptr: int, q_stride: int, cache: KVCacheStruct, block_tables_ptr: int,
+                           max_pages: int, seq_lens_ptr: int, cu_seqlens_q_ptr: int, B: int, T: int,
+                           Hq: int, dtype: int, sm_scale: float, causal: int, softcap: float,
+                           alibi_slopes_ptr: int, window: int, prefix_lens_ptr: int, out_ptr: int,
+                           lse_ptr: int, workspace_ptr: int, workspace_bytes: int, status_ptr: int,
+                           pdl: int, stream: int) -> int:
+    return lib().fp4_attention_nvfp4_ex(q_ptr or None, q_stride, cache, block_tables_ptr or None,
+                                        max_pages, seq_lens_ptr or None, cu_seqlens_q_ptr or None, B,
+                                        T, Hq, dtype, sm_scale, causal, softcap,
+                                        alibi_slopes_ptr or None, window, prefix_lens_ptr or None,
+                                        out_ptr or None, lse_ptr or None, workspace_ptr or None,
+                                        workspace_bytes, status_ptr or None, pdl, stream or None)
 
 
 def fp4_attention_workspace_bytes(B: int, T: int, Hq: int, num_kv_heads: int, head_dim: int,
@@ -889,7 +907,8 @@ def kv_gather_nvfp4(cache, slots, dtype=None, k_global_scale=None, v_global_scal
 def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal: bool = True,
                     sm_scale: Optional[float] = None, k_global_scale=None, v_global_scale=None,
                     out=None, return_lse: bool = False, lse=None, workspace=None, status=None,
-                    pdl: bool = False, stream=None):
+                    pdl: bool = False, stream=None, softcap: Optional[float] = None, alibi_slopes=None,
+                    window: Optional[int] = None, prefix_lens=None):
     """softmax(sm_scale * q k^T) v over the cached tokens of every sequence.
 
     q: (T, heads, head_dim) bf16 or fp16, heads a multiple of the cache's kv_heads.
@@ -905,7 +924,14 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     short sequences with a table cut to their pages.  Returns out, or (out, lse) with return_lse
     (lse (T, heads) fp32, natural logarithm).  workspace: optional uint8 tensor of
     fp4_attention_workspace_bytes bytes (one for calls of several sizes:
-    fp4_attention_workspace_bound), for one call at a time."""
+    fp4_attention_workspace_bound), for one call at a time.
+
+    softcap: logits become softcap * tanh(logit / softcap).  alibi_slopes: (heads,) fp32; then
+    slope * distance between the row's place and the key's is taken off.  With causal:
+    window: a row sees the latest `window` of its keys only (pages before that may have
+    been given up: kv_trim_nvfp4); prefix_lens: (B,) int32, every row of the sequence
+    also sees its first prefix_lens[b] keys.  (A workspace of the exact size is then
+    that for min(max_keys, window + ceil(T / B) + 63) keys.)"""
     torch = _torch()
     struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
     shape, dtype = q.shape, q.dtype
@@ -927,9 +953,23 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     elif T != B:
         raise ValueError("q must have one row per sequence without cu_seqlens_q")
     L = lib()
+    keys = max_pages * struct.page_size
+    extra = softcap is not None or alibi_slopes is not None or window is not None or prefix_lens is not None
+    if extra:
+        slopes = _dense_ptr(alibi_slopes, "alibi_slopes", dev, torch.float32, (hq,)) if alibi_slopes is not None else None
+        prefix = _dense_ptr(prefix_lens, "prefix_lens", dev, i32, (B,)) if prefix_lens is not None else None
+        if softcap is not None and not softcap > 0:
+            raise ValueError("softcap must be positive")
+        if window is not None:
+            if window <= 0:
+                raise ValueError("window must be positive")
+            if B:
+                keys = min(keys, window + (T + B - 1) // B + 63)
+        if not causal and (window is not None or prefix is not None):
+            raise ValueError("window and prefix_lens go with causal")
     ws = 0
     if workspace is None:
-        size = _attention_workspace(L, dev, B, T, hq, heads, dim, max_pages * struct.page_size)
+        size = _attention_workspace(L, dev, B, T, hq, heads, dim, keys)
     else:
         _check_cuda(workspace, "workspace")
         _same_device(dev, "workspace", workspace)
@@ -961,9 +1001,15 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
                 held = torch.empty(size, dtype=torch.uint8, device=q.device)
             ws = held.data_ptr()
     try:
-        st = L.fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
-                                   dt, scale, 1 if causal else 0, out_ptr, lse_ptr, ws, size,
-                                   status_ptr, 1 if pdl else 0, handle)
+        if extra:
+            st = L.fp4_attention_nvfp4_ex(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T,
+                                          hq, dt, scale, 1 if causal else 0, softcap or 0.0, slopes,
+                                          min(window or 0, 1 << 62), prefix, out_ptr, lse_ptr, ws, size,
+                                          status_ptr, 1 if pdl else 0, handle)
+        else:
+            st = L.fp4_attention_nvfp4(q.data_ptr(), qs, struct, tables, max_pages, lens, cu, B, T, hq,
+                                       dt, scale, 1 if causal else 0, out_ptr, lse_ptr, ws, size,
+                                       status_ptr, 1 if pdl else 0, handle)
     finally:
         if own_ws:
             torch._C._cuda_cudaCachingAllocator_raw_delete(own_ws)

@@ -243,16 +243,19 @@ fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t Hq, int64_
   return FP4_OK;
 }
 
-fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_cache_t* cache,
-                                 const int32_t* block_tables, int64_t max_pages,
-                                 const int32_t* seq_lens, const int32_t* cu_seqlens_q, int64_t B,
-                                 int64_t T, int64_t Hq, fp4_dtype_t dtype, float sm_scale,
-                                 int causal, void* out, float* lse, void* workspace,
-                                 int64_t workspace_bytes, int32_t* status, int pdl,
-                                 fp4q_stream_t stream) {
+fp4_status_t fp4_attention_nvfp4_ex(const void* q, int64_t q_stride, const fp4_kv_cache_t* cache,
+                                    const int32_t* block_tables, int64_t max_pages,
+                                    const int32_t* seq_lens, const int32_t* cu_seqlens_q, int64_t B,
+                                    int64_t T, int64_t Hq, fp4_dtype_t dtype, float sm_scale,
+                                    int causal, float softcap, const float* alibi_slopes, int64_t window,
+                                    const int32_t* prefix_lens, void* out, float* lse, void* workspace,
+                                    int64_t workspace_bytes, int32_t* status, int pdl,
+                                    fp4q_stream_t stream) {
   if (!valid_dtype(dtype) || B < 0 || T < 0 || Hq <= 0 || max_pages < 0 || workspace_bytes < 0)
     return FP4_ERR_INVALID_ARG;
   if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return FP4_ERR_INVALID_ARG;
+  if (!(softcap >= 0.0f) || !std::isfinite(softcap) || window < 0 || (!causal && (window || prefix_lens)))
+    return FP4_ERR_INVALID_ARG;
   const fp4_status_t cs = check_cache_sizes(cache);
   if (cs != FP4_OK) return cs;
   const int64_t D = cache->head_dim, Hkv = cache->num_kv_heads;
@@ -269,9 +272,12 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   if (cb != FP4_OK) return cb;
   if (!abi_aligned(q, 32) || q_stride % 16 || !abi_aligned(out, 32) || !abi_aligned(lse, 4) ||
       !abi_aligned(block_tables, 4) || !abi_aligned(seq_lens, 4) || !abi_aligned(cu_seqlens_q, 4) ||
-      !abi_aligned(workspace, 16) || !abi_aligned(status, 4))
+      !abi_aligned(workspace, 16) || !abi_aligned(status, 4) || !abi_aligned(alibi_slopes, 4) ||
+      !abi_aligned(prefix_lens, 4))
     return FP4_ERR_MISALIGNED;
-  const int64_t need = fp4_attention_workspace_bytes(B, T, Hq, Hkv, D, max_pages * cache->page_size);
+  if (window > INT32_MAX / 2) window = 0;             // longer than any sequence
+  const int64_t keys = kv_attention_keys(B, T, max_pages * cache->page_size, window);
+  const int64_t need = fp4_attention_workspace_bytes(B, T, Hq, Hkv, D, keys);
   if (workspace_bytes < need || (need && !workspace)) return FP4_ERR_INVALID_ARG;
   const CacheBuffers cbuf = buffers(*cache);
   const Rows writes[] = {flat(out, T * Hq * D * 2), flat(lse, T * Hq * 4),
@@ -279,7 +285,7 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   const Rows reads[] = {Rows{q, T, q_stride * 2, Hq * D * 2},
                         cbuf.rows[0], cbuf.rows[1], cbuf.rows[2], cbuf.rows[3],
                         flat(block_tables, B * max_pages * 4), flat(seq_lens, B * 4),
-                        flat(cu_seqlens_q, (B + 1) * 4),
+                        flat(cu_seqlens_q, (B + 1) * 4), flat(alibi_slopes, Hq * 4), flat(prefix_lens, B * 4),
                         flat(cache->k_global_scale, 4), flat(cache->v_global_scale, 4)};
   for (int i = 0; i < 4; ++i) {
     for (int j = i + 1; j < 4; ++j)
@@ -301,15 +307,33 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
   p.group = static_cast<int>(Hq / Hkv);
   p.sm_scale = sm_scale;
   p.causal = causal ? 1 : 0;
+  p.softcap = softcap;
+  p.slopes = alibi_slopes;
+  p.window = static_cast<int>(window);
+  p.prefix = prefix_lens;
   p.out = out;
   p.lse = lse;
   p.ws = static_cast<float*>(workspace);
   p.ws_bytes = need;
   p.status = status;
   FP4Q_SET_DEBUG(p);
-  return static_cast<fp4_status_t>(record_cuda_error(launch_kv_attention(
+  const bool plain = softcap == 0.0f && !alibi_slopes && !window && !prefix_lens;
+  return static_cast<fp4_status_t>(record_cuda_error((plain ? launch_kv_attention : launch_kv_attention_masked)(
       dtype == FP4_DT_BF16 ? 0 : 1, p, pdl, reinterpret_cast<cudaStream_t>(stream))));
 }
+
+fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_cache_t* cache,
+                                 const int32_t* block_tables, int64_t max_pages,
+                                 const int32_t* seq_lens, const int32_t* cu_seqlens_q, int64_t B,
+                                 int64_t T, int64_t Hq, fp4_dtype_t dtype, float sm_scale,
+                                 int causal, void* out, float* lse, void* workspace,
+                                 int64_t workspace_bytes, int32_t* status, int pdl,
+                                 fp4q_stream_t stream) {
+  return fp4_attention_nvfp4_ex(q, q_stride, cache, block_tables, max_pages, seq_lens, cu_seqlens_q, B, T, Hq,
+                                dtype, sm_scale, causal, 0.0f, nullptr, 0, nullptr, out, lse, workspace,
+                                workspace_bytes, status, pdl, stream);
+}
+
 
 int64_t fp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t N) {
   if (num_pages < 0 || num_pages > INT32_MAX || N < 0 || N > INT32_MAX / 4) return -1;

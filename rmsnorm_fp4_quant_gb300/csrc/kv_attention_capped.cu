@@ -1,0 +1,11 @@
+// kv_attention_capped.cu - attention over the paged NVFP4 key/value cache with capped
+// logits (and a window, a prefix or a bias besides).
+#include "kv_attention_launch.cuh"
+
+namespace fp4q {
+
+cudaError_t launch_kv_attention_capped(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream) {
+  return dtype == 0 ? launch_type<__nv_bfloat16, kCapped>(p, pdl, stream) : launch_type<__half, kCapped>(p, pdl, stream);
+}
+
+}  // namespace fp4q

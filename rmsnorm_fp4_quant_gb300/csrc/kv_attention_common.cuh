@@ -48,6 +48,10 @@ __device__ __forceinline__ float coarse_exponent(float product, float fac, float
   return __fsub_rn(__fmul_rn(product, fac), ref);
 }
 
+// What a kernel does to the products: nothing but the causal mask; keys from a window's first
+// to a prefix's end too, and a bias; and a cap besides.
+enum KvLogits { kPlain = 0, kMasked = 1, kCapped = 2 };
+
 // Entries of the call's small arrays (0 for one outside: the debug build's checks).
 __device__ __forceinline__ int kv_len(const KvAttentionParams& p, int b) {
   return FP4Q_IN_RANGE(p, p.seq_lens + b, 4, p.seq_lens, 4LL * p.B) ? p.seq_lens[b] : 0;
@@ -75,6 +79,34 @@ __device__ __forceinline__ KvSeq kv_sequence(const KvAttentionParams& p, int b) 
     s.n_q = 1;
   }
   return s;
+}
+
+// Keys [first, limit) that token `tok` of a sequence sees; both grow with tok.  MODE kPlain
+// knows no window and no prefix.
+template <int MODE>
+struct KvSeen {
+  int len, off, prefix, window;
+  bool causal;
+  __device__ __forceinline__ KvSeen(const KvAttentionParams& p, const KvSeq& s, int b)
+      : len(s.len), off(s.len - s.n_q), prefix(0), window(0), causal(p.causal != 0) {
+    if constexpr (MODE != kPlain) {
+      window = p.window;
+      if (p.prefix && FP4Q_IN_RANGE(p, p.prefix + b, 4, p.prefix, 4LL * p.B)) prefix = min(max(__ldg(p.prefix + b), 0), len);
+    }
+  }
+  __device__ __forceinline__ int limit(int tok) const {
+    const int own = causal ? min(len, off + tok + 1) : len;
+    return MODE == kPlain ? own : max(own, prefix);
+  }
+  __device__ __forceinline__ int first(int tok) const {
+    return MODE == kPlain || !window ? 0 : max(0, off + tok + 1 - window);
+  }
+};
+
+__device__ __forceinline__ float rcp(float x) {
+  float y;
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
 }
 
 __device__ __forceinline__ float ex2(float x) {
@@ -119,6 +151,30 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// A row's logit in units of log(2) from its product s and the distance to the key:
+//   kMasked   s fac - slope |away|
+//   kCapped   cap tanh(s fac / cap) - slope |away|, cap and slope in the same units; tanh(x) as
+//             1 - 2 / (1 + exp(2 x)): off by a few 2^-24 of the cap, where the hardware's own
+//             tanh would be off by 2^-11 of it.
+// fac is the product's factor, of kCapped times 2 log2(e) / cap for the exponential's argument.
+template <int MODE>
+__device__ __forceinline__ float kv_logit(float s, float fac, float cap, float slope, float away) {
+  float z;
+  if constexpr (MODE == kCapped)
+    z = fmaf(-2.0f * cap, rcp(1.0f + ex2(s * fac)), cap);
+  else
+    z = __fmul_rn(s, fac);
+  return fmaf(-slope, fabsf(away), z);
+}
+// The factor from the one that turns a product into a logit in units of log(2).
+template <int MODE>
+__device__ __forceinline__ float kv_factor(const KvAttentionParams& p, float fac) {
+  return MODE == kCapped ? fac * __fdiv_rn(2.0f, p.softcap) : fac;
+}
+__device__ __forceinline__ float kv_slope(const KvAttentionParams& p, int hq) {
+  return p.slopes && FP4Q_IN_RANGE(p, p.slopes + hq, 4, p.slopes, 4LL * p.Hq) ? kLog2e * __ldg(p.slopes + hq) : 0.0f;
 }
 
 // k with 2^k * m in [2^14, 2^15) for m > 0 (held to where 2^k and 2^-k are

@@ -174,17 +174,19 @@ __device__ __forceinline__ int decode_sequence(const KvAttentionParams& p, int64
 struct DecodeWalk {
   int b;             // sequence
   int64_t base;      // its first unit
+  int skip;          // units of keys before the first that a row sees
   int tiles;         // units of keys per item
   int cost;          // kDecItemCost + tiles: places per item in the numbering
   int row_tiles;     // row tiles
   KvSeq s;
 };
-template <int ROWS>
+template <int ROWS, int MODE>
 __device__ __forceinline__ int64_t decode_units(const KvAttentionParams& p, int b, DecodeWalk& w) {
   w.s = kv_sequence(p, b);
   w.b = b;
+  w.skip = MODE != kPlain && p.window ? max(0, w.s.len - w.s.n_q + 1 - p.window) / kDecUnit : 0;
   // a sequence without keys still has a unit: its rows are written as 0
-  w.tiles = max(1, (w.s.len + kDecUnit - 1) / kDecUnit);
+  w.tiles = max(1, (w.s.len + kDecUnit - 1) / kDecUnit - w.skip);
   w.cost = w.tiles + kDecItemCost;
   w.row_tiles = (w.s.n_q * p.group + ROWS - 1) / ROWS;
   return static_cast<int64_t>(w.cost) * w.row_tiles * p.c.heads;
@@ -193,7 +195,7 @@ __device__ __forceinline__ int64_t decode_units(const KvAttentionParams& p, int 
 // CLUSTER: instead, an item's keys go to one CTA or to the 2 to 8 of a cluster, which
 // read each other's results from shared memory: no workspace and no second kernel, for
 // short sequences and for few of moderate length (kv_attention.cu chooses).
-template <typename T, int D, int NT, bool CLUSTER>
+template <typename T, int D, int NT, bool CLUSTER, int MODE = kPlain>
 __global__ void __launch_bounds__(kDecThreads, DecodeShape<D, NT>::kCtas)
 kv_decode_kernel(const KvAttentionParams p) {
   using S = DecodeShape<D, NT>;
@@ -225,7 +227,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     kvh = static_cast<int>(slot % p.c.heads);
     int64_t tile;
     const int b = decode_sequence<ROWS>(p, slot / p.c.heads, tile);
-    decode_units<ROWS>(p, b, w);
+    decode_units<ROWS, MODE>(p, b, w);
     if (tile < 0 || tile >= w.row_tiles) return;   // the whole cluster
     rt = static_cast<int>(tile);
   } else {
@@ -234,7 +236,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     const int run = (p.B + kDecThreads - 1) / kDecThreads;
     const int b_lo = min(tid * run, p.B), b_hi = min(b_lo + run, p.B);
     int64_t mine = 0;
-    for (int b = b_lo; b < b_hi; ++b) mine += decode_units<ROWS>(p, b, w);
+    for (int b = b_lo; b < b_hi; ++b) mine += decode_units<ROWS, MODE>(p, b, w);
     int64_t incl = mine;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -258,7 +260,7 @@ kv_decode_kernel(const KvAttentionParams p) {
       int64_t base = before;
       int b = b_lo;
       for (;;) {
-        const int64_t n = decode_units<ROWS>(p, b, w);
+        const int64_t n = decode_units<ROWS, MODE>(p, b, w);
         if (u < base + n) break;
         base += n;
         ++b;
@@ -267,7 +269,7 @@ kv_decode_kernel(const KvAttentionParams p) {
       start_base = base;
     }
     __syncthreads();
-    units = decode_units<ROWS>(p, start_b, w);
+    units = decode_units<ROWS, MODE>(p, start_b, w);
     w.base = start_base;
   }
 
@@ -310,7 +312,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     } else {
       while (u >= w.base + units) {             // the next sequence that has units
         w.base += units;
-        units = decode_units<ROWS>(p, w.b + 1, w);
+        units = decode_units<ROWS, MODE>(p, w.b + 1, w);
       }
       const int item = static_cast<int>((u - w.base) / w.cost);
       item_base = w.base + static_cast<int64_t>(item) * w.cost;
@@ -326,20 +328,30 @@ kv_decode_kernel(const KvAttentionParams p) {
 
     // --- the rows' limits: keys that columns 2t, 2t + 1 see, smallest and largest of the tile
     const int off = w.s.len - w.s.n_q;          // last visible key of token i: off + i
+    const KvSeen<MODE> seen(p, w.s, w.b);
     int lim[NT][2];
+    [[maybe_unused]] int from[NT][2];            // first visible keys
+    [[maybe_unused]] float slope[NT][2], own[NT][2];   // of the distance to the token's own place
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int rc = r0 + 8 * n + 2 * t + e;
-        lim[n][e] = p.causal && rc < rows ? min(w.s.len, off + rc / p.group + 1) : w.s.len;
+        const int tok = rc / p.group;
+        lim[n][e] = rc < rows ? seen.limit(tok) : w.s.len;
+        if constexpr (MODE != kPlain) {
+          from[n][e] = rc < rows ? seen.first(tok) : 0;
+          own[n][e] = static_cast<float>(off + tok);
+          slope[n][e] = rc < rows ? kv_slope(p, kvh * p.group + rc - tok * p.group) : 0.0f;
+        }
       }
     const int last = min(r0 + ROWS, rows) - 1;
-    const int lim_lo = p.causal ? off + r0 / p.group + 1 : w.s.len;
-    const int lim_hi = p.causal ? off + last / p.group + 1 : w.s.len;
+    const int lim_lo = MODE != kPlain ? seen.limit(r0 / p.group) : p.causal ? off + r0 / p.group + 1 : w.s.len;
+    const int lim_hi = MODE != kPlain ? seen.limit(last / p.group) : p.causal ? off + last / p.group + 1 : w.s.len;
+    const int from_hi = MODE != kPlain ? seen.first(last / p.group) : 0;
 
     // --- the ring: tile x of this warp is keys key0(x) ... + 15
-    const int first_key = tile0 * kDecUnit + warp * 16;
+    const int first_key = (w.skip + tile0) * kDecUnit + warp * 16;
     const int32_t* table = p.tables + static_cast<int64_t>(w.b) * p.max_pages;
     // a row number counts slots of all pages and heads and fits 32 bits
     constexpr uint32_t kNoRow = 0xffffffffu;
@@ -442,7 +454,7 @@ kv_decode_kernel(const KvAttentionParams p) {
           const float2 x = Pair<T>::to_f32(qc[n][i].u[j]);
           qf[n][4 * i + j / 2][j & 1] = pack_f16x2(x.x * up, x.y * up);
         }
-      const float f = p.sm_scale * kLog2e / kgs * pow2(-k);
+      const float f = kv_factor<MODE>(p, p.sm_scale * kLog2e / kgs * pow2(-k));
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         fac[n][e] = __shfl_sync(kFullMask, f, (2 * t + e) * 4);
@@ -462,6 +474,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     // a reference of the warp's rows is_coarse: its steps take the masked steps' code, where
     // the product is rounded before the reference is taken from it
     bool coarse = false;
+    [[maybe_unused]] const float cap = MODE == kCapped ? kLog2e * p.softcap : 0.0f;
     // one step, whose slots of the ring are constants
     auto work = [&](int step, auto phase) {
       constexpr int kPhase = decltype(phase)::value;
@@ -528,9 +541,31 @@ kv_decode_kernel(const KvAttentionParams p) {
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) y[j][n][e] = fmaf(s[j][n][e], fac[n][e & 1], -ref[n][e & 1]);
+          for (int e = 0; e < 4; ++e) {
+            if constexpr (MODE == kPlain) {
+              y[j][n][e] = fmaf(s[j][n][e], fac[n][e & 1], -ref[n][e & 1]);
+            } else {                             // the logit itself in the product's place, rounded once
+              const float away = static_cast<float>(key0[j] + row_k + (e & 2)) - own[n][e & 1];
+              s[j][n][e] = kv_logit<MODE>(s[j][n][e], fac[n][e & 1], cap, slope[n][e & 1], away);
+              y[j][n][e] = __fsub_rn(s[j][n][e], ref[n][e & 1]);
+            }
+          }
       }
-      if (edge) {
+      if constexpr (MODE != kPlain) {
+#pragma unroll
+        for (int j = 0; j < TP; ++j) edge |= key0[j] < from_hi;
+        if (edge) {
+#pragma unroll
+          for (int j = 0; j < TP; ++j)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const int key = key0[j] + row_k + (e & 2);
+                if (key >= lim[n][e & 1] || key < from[n][e & 1]) y[j][n][e] = s[j][n][e] = -INFINITY;
+              }
+        }
+      } else if (edge) {
 #pragma unroll
         for (int j = 0; j < TP; ++j)
 #pragma unroll
@@ -558,10 +593,10 @@ kv_decode_kernel(const KvAttentionParams p) {
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
-            const float r = ref_for(ref[n][e], m, fac[n][e]);
+            const float r = ref_for(ref[n][e], m, MODE == kPlain ? fac[n][e] : 1.0f);
             const float f = ex2(ref[n][e] - r);
             ref[n][e] = r;
-            far |= is_coarse(r);
+            far |= MODE == kPlain && is_coarse(r);   // (a logit that is rounded needs no other code)
             sum[n][e] *= f;
 #pragma unroll
             for (int i = 0; i < D / 16; ++i) {
@@ -577,7 +612,8 @@ kv_decode_kernel(const KvAttentionParams p) {
 #pragma unroll
             for (int e = 0; e < 4; ++e)
               y[j][n][e] = s[j][n][e] == -INFINITY ? -INFINITY
-                                                   : coarse_exponent(s[j][n][e], fac[n][e & 1], ref[n][e & 1]);
+                                                   : coarse_exponent(s[j][n][e], MODE == kPlain ? fac[n][e & 1] : 1.0f,
+                                                                     ref[n][e & 1]);
       }
       uint32_t pb[TP][NT][2];
 #pragma unroll

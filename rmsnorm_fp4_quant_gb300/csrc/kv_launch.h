@@ -71,6 +71,10 @@ struct KvAttentionParams {
   int group;           // Hq / heads
   float sm_scale;
   int causal;
+  float softcap;         // 0: none (this and the three below: kernels with MASKED or more)
+  const float* slopes;   // [Hq] or null
+  int window;            // 0: none
+  const int32_t* prefix; // [B] or null
   void* out;
   float* lse;
   float* ws;
@@ -112,6 +116,14 @@ struct KvPagesParams {
 cudaError_t launch_kv_append(int dtype, const KvAppendParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_gather(int dtype, const KvGatherParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream);
+// The same with capped logits, biases, windows and prefixes (kv_attention_masked.cu).
+cudaError_t launch_kv_attention_masked(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream);
+// Keys that the choice of kernel counts a sequence with: at most a window and what its rows add.
+inline int64_t kv_attention_keys(int64_t B, int64_t T, int64_t max_keys, int64_t window) {
+  if (!window || !B) return max_keys;
+  const int64_t most = window + (T + B - 1) / B + 63;
+  return most < max_keys ? most : max_keys;
+}
 cudaError_t launch_kv_fork(const KvPagesParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_trim(const KvPagesParams& p, int pdl, cudaStream_t stream);
 cudaError_t launch_kv_compact(const KvPagesParams& p, int pdl, cudaStream_t stream);

@@ -296,6 +296,56 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim,
   return m;
 }
 
+// What a row needs to turn products into logits (MODE kMasked, kCapped): kv_logit's arguments,
+// its own place, and the keys [from, lim) that it sees.
+struct PrefillLogits {
+  float fac, cap, slope, own;
+  int from, lim;
+};
+template <int MODE, bool EDGE>
+__device__ __forceinline__ float prefill_logit(uint32_t s, int key, bool page, const PrefillLogits& l) {
+  const float z = kv_logit<MODE>(__uint_as_float(s), l.fac, l.cap, l.slope, static_cast<float>(key) - l.own);
+  return EDGE && (!page || key >= l.lim || key < l.from) ? -INFINITY : z;
+}
+// As prefill_weights and prefill_maximum above.
+template <int MODE, bool EDGE>
+__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
+                                                 float ref, uint32_t (&h)[64]) {
+  float2 sum2 = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    uint32_t x[16];
+    tmem_load_16cols_async(ts + 16 * c, x);
+    tmem_load_wait(x);
+#pragma unroll
+    for (int i = 0; i < 16; i += 2) {
+      const bool page = have >> c & 1u;
+      float2 y;
+      y.x = ex2(__fsub_rn(prefill_logit<MODE, EDGE>(x[i], key0 + 16 * c + i, page, l), ref));
+      y.y = ex2(__fsub_rn(prefill_logit<MODE, EDGE>(x[i + 1], key0 + 16 * c + i + 1, page, l), ref));
+      sum2 = __fadd2_rn(sum2, y);
+      h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
+    }
+  }
+  return sum2.x + sum2.y;
+}
+template <int MODE, bool EDGE>
+__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l) {
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    uint32_t x[16];
+    tmem_load_16cols_async(ts + 16 * c, x);
+    tmem_load_wait(x);
+    const bool page = have >> c & 1u;
+#pragma unroll
+    for (int i = 0; i < 16; i += 2)
+      m = max3(m, prefill_logit<MODE, EDGE>(x[i], key0 + 16 * c + i, page, l),
+               prefill_logit<MODE, EDGE>(x[i + 1], key0 + 16 * c + i + 1, page, l));
+  }
+  return m;
+}
+
 // Multiplies 32 n columns of tensor memory, this thread's lane of them, by f.
 __device__ __forceinline__ void prefill_scale(uint32_t taddr, int n, float f) {
 #pragma unroll 1
@@ -308,7 +358,7 @@ __device__ __forceinline__ void prefill_scale(uint32_t taddr, int n, float f) {
   }
 }
 
-template <typename T, int D>
+template <typename T, int D, int MODE = kPlain>
 __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAttentionParams p, int splits) {
   using S = PrefillShape<D>;
   extern __shared__ uint8_t smem_raw[];
@@ -336,14 +386,15 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   const int rows = seq.n_q * p.group;
   if (rt < 0 || rt * kPreRows >= rows) return;
   const int r0 = static_cast<int>(rt) * kPreRows;
-  const int off = seq.len - seq.n_q;
+  const KvSeen<MODE> seen(p, seq, b);
   // steps of 128 keys: this split's share of what the last row sees, and how many of
   // them each tile's last row sees
-  auto limit_of = [&](int r) { return p.causal ? min(seq.len, off + r / p.group + 1) : seq.len; };
+  auto limit_of = [&](int r) { return seen.limit(r / p.group); };
+  const int from_key = seen.first(r0 / p.group), skip = from_key / kPreKeys;   // (0 of kPlain)
   const int last0 = min(r0 + 128, rows) - 1, last1 = min(r0 + 256, rows) - 1;
   const int all = (max(0, limit_of(last1)) + kPreKeys - 1) / kPreKeys;
-  const int per = (all + splits - 1) / splits;
-  const int t0 = min(all, static_cast<int>(blockIdx.y) * per), t1 = min(all, t0 + per);
+  const int per = (max(0, all - skip) + splits - 1) / splits;
+  const int t0 = min(all, skip + static_cast<int>(blockIdx.y) * per), t1 = min(all, t0 + per);
   const int all0 = (max(0, limit_of(last0)) + kPreKeys - 1) / kPreKeys;
   const int n[2] = {max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
   const int steps = max(n[0], n[1]);
@@ -371,7 +422,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   {
     const int32_t* table = p.tables + static_cast<int64_t>(b) * p.max_pages;
     const int end = min(t1 * kPreKeys, seq.len);
-    for (int i = t0 * kPreKeys / p.c.page_size + tid; static_cast<int64_t>(i) * p.c.page_size < end; i += kPreThreads) {
+    for (int i = max(from_key, t0 * kPreKeys) / p.c.page_size + tid; static_cast<int64_t>(i) * p.c.page_size < end; i += kPreThreads) {
       if (!FP4Q_IN_RANGE(p, table + i, 4, p.tables, 4LL * p.B * p.max_pages)) continue;
       const int page = __ldg(table + i);
       bad |= page < 0 || page >= p.c.num_pages;
@@ -429,13 +480,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       fence_proxy_async_smem();
       warp_arrive(&bars[kBarQ], lane);
       const float kgs = p.c.k_gs ? __ldg(p.c.k_gs) : 1.0f;
-      fac = p.sm_scale * kLog2e / kgs * pow2(-k);
+      fac = kv_factor<MODE>(p, p.sm_scale * kLog2e / kgs * pow2(-k));
     }
     const uint32_t ts = tmem + tile * 128 + ((warp & 3) * 32 << 16);
     const uint32_t to = tmem + 256 + tile * D + ((warp & 3) * 32 << 16);
     const int lim = ok ? limit_of(r) : 0;
     int lim_lo = ok ? lim : INT32_MAX;           // smallest of the warp's rows
     lim_lo = __reduce_min_sync(kFullMask, lim_lo);
+    [[maybe_unused]] int from_hi = 0;            // largest first key of the warp's rows
+    [[maybe_unused]] PrefillLogits logits;
+    if constexpr (MODE != kPlain) {
+      logits = PrefillLogits{fac, MODE == kCapped ? kLog2e * p.softcap : 0.0f, ok ? kv_slope(p, hq) : 0.0f,
+                             static_cast<float>(seen.off + tok), ok ? seen.first(tok) : 0, lim};
+      from_hi = __reduce_max_sync(kFullMask, logits.from);
+    }
     constexpr int kCoarseRows = INT32_MIN;       // in lim_lo's place: a row's reference is_coarse, or was
     float ref = kRefStart, sum = 0.0f;
     bool alive = true;
@@ -452,7 +510,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         break;
       }
       tc_fence_after_sync();
-      const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu;
+      const bool edge = key0 + kPreKeys > lim_lo || have != 0xffu || (MODE != kPlain && key0 < from_hi);
       // the weights against the reference there is; where a row's sum passes the limit
       // (rare after the first step, which begins with its maximum), once more.  A warp that
       // had a coarse reference begins every step so, and rounds S times the factor in place
@@ -464,25 +522,35 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
 #pragma unroll 1
       for (;;) {
         if (last) {
-          const float m = edge ? prefill_maximum<true>(ts, key0, lim, have)
-                               : prefill_maximum<false>(ts, key0, lim, have);
+          float m;
+          if constexpr (MODE == kPlain)
+            m = edge ? prefill_maximum<true>(ts, key0, lim, have) : prefill_maximum<false>(ts, key0, lim, have);
+          else
+            m = edge ? prefill_maximum<MODE, true>(ts, key0, have, logits)
+                     : prefill_maximum<MODE, false>(ts, key0, have, logits);
           float f = 1.0f;
           if (moved && m > -INFINITY) {
-            const float to_ref = ref_for(ref, m, fac);
+            const float to_ref = ref_for(ref, m, MODE == kPlain ? fac : 1.0f);
             f = ex2(ref - to_ref);
             ref = to_ref;
             sum *= f;
           }
           if (j > 0) prefill_scale(to, D / 32, f);
-          if (lim_lo == kCoarseRows || __any_sync(kFullMask, is_coarse(ref))) {
+          // (a logit that is rounded before the reference is taken from it needs none of this)
+          if (MODE == kPlain && (lim_lo == kCoarseRows || __any_sync(kFullMask, is_coarse(ref)))) {
             lim_lo = kCoarseRows;
             prefill_scale(ts, kPreKeys / 32, fac);
             tmem_store_wait();
           }
         }
-        const float f = lim_lo == kCoarseRows ? 1.0f : fac;
-        step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, f, ref, h)
-                        : prefill_weights<false>(ts, key0, lim, have, f, ref, h);
+        if constexpr (MODE == kPlain) {
+          const float f = lim_lo == kCoarseRows ? 1.0f : fac;
+          step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, f, ref, h)
+                          : prefill_weights<false>(ts, key0, lim, have, f, ref, h);
+        } else {
+          step_sum = edge ? prefill_weights<MODE, true>(ts, key0, have, logits, ref, h)
+                          : prefill_weights<MODE, false>(ts, key0, have, logits, ref, h);
+        }
         if (last) break;
         moved = !(step_sum <= kPreMostSum);
         if (!__any_sync(kFullMask, moved)) break;
