@@ -353,12 +353,15 @@ kv_decode_kernel(const KvAttentionParams p) {
     // --- the ring: tile x of this warp is keys key0(x) ... + 15
     const int first_key = (w.skip + tile0) * kDecUnit + warp * 16;
     const int32_t* table = p.tables + static_cast<int64_t>(w.b) * p.max_pages;
+    // (MODE kMasked, kCapped: from the last tile to the first, as a bias makes logits grow towards
+    // a row's own place and every step would move its reference)
+    auto key_of = [&](int x) { return first_key + (MODE == kPlain ? x : n_units - 1 - x) * kDecUnit; };
     // a row number counts slots of all pages and heads and fits 32 bits
     constexpr uint32_t kNoRow = 0xffffffffu;
     uint32_t row_of = kNoRow, row_next = kNoRow;
     int at_of = 0, at_next = 0;
     auto look_up = [&](int x, uint32_t& row, int& at) {      // tile x + lane
-      const int key = first_key + (x + lane) * kDecUnit;
+      const int key = key_of(x + lane);
       row = kNoRow;
       if (x + lane < n_units && key < lim_hi) {
         const int idx = key / p.c.page_size;
@@ -487,7 +490,7 @@ kv_decode_kernel(const KvAttentionParams p) {
       int key0[TP];                              // a tile without keys lies behind every limit
 #pragma unroll
       for (int j = 0; j < TP; ++j)
-        key0[j] = here >> (TP - 1 - j) & 1u ? first_key + (step * TP + j) * kDecUnit : kNoKey;
+        key0[j] = here >> (TP - 1 - j) & 1u ? key_of(step * TP + j) : kNoKey;
 
       // S^T = K Q^T
       float s[TP][NT][4];

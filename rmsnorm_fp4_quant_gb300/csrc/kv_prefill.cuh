@@ -301,35 +301,37 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim,
 struct PrefillLogits {
   float fac, cap, slope, own;
   int from, lim;
+  __device__ __forceinline__ bool sees(int key, bool page) const { return page && key < lim && key >= from; }
 };
-template <int MODE, bool EDGE>
+template <int MODE>
 __device__ __forceinline__ float prefill_logit(uint32_t s, int key, bool page, const PrefillLogits& l) {
   const float z = kv_logit<MODE>(__uint_as_float(s), l.fac, l.cap, l.slope, static_cast<float>(key) - l.own);
-  return EDGE && (!page || key >= l.lim || key < l.from) ? -INFINITY : z;
+  return l.sees(key, page) ? z : -INFINITY;
 }
-// As prefill_weights and prefill_maximum above.
-template <int MODE, bool EDGE>
-__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
-                                                 float ref, uint32_t (&h)[64]) {
+// As prefill_weights above, logit by logit, each rounded before the reference is taken from it:
+// for steps on both sides of a row's own place, and for coarse references.
+template <int MODE>
+__device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
+                                                          float ref, uint32_t (&h)[64]) {
   float2 sum2 = make_float2(0.0f, 0.0f);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t x[16];
     tmem_load_16cols_async(ts + 16 * c, x);
     tmem_load_wait(x);
+    const bool page = have >> c & 1u;
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
-      const bool page = have >> c & 1u;
       float2 y;
-      y.x = ex2(__fsub_rn(prefill_logit<MODE, EDGE>(x[i], key0 + 16 * c + i, page, l), ref));
-      y.y = ex2(__fsub_rn(prefill_logit<MODE, EDGE>(x[i + 1], key0 + 16 * c + i + 1, page, l), ref));
+      y.x = ex2(__fsub_rn(prefill_logit<MODE>(x[i], key0 + 16 * c + i, page, l), ref));
+      y.y = ex2(__fsub_rn(prefill_logit<MODE>(x[i + 1], key0 + 16 * c + i + 1, page, l), ref));
       sum2 = __fadd2_rn(sum2, y);
       h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
     }
   }
   return sum2.x + sum2.y;
 }
-template <int MODE, bool EDGE>
+template <int MODE>
 __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l) {
   float m = -INFINITY;
 #pragma unroll 1
@@ -340,10 +342,85 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t
     const bool page = have >> c & 1u;
 #pragma unroll
     for (int i = 0; i < 16; i += 2)
-      m = max3(m, prefill_logit<MODE, EDGE>(x[i], key0 + 16 * c + i, page, l),
-               prefill_logit<MODE, EDGE>(x[i + 1], key0 + 16 * c + i + 1, page, l));
+      m = max3(m, prefill_logit<MODE>(x[i], key0 + 16 * c + i, page, l),
+               prefill_logit<MODE>(x[i + 1], key0 + 16 * c + i + 1, page, l));
   }
   return m;
+}
+// The same where the step lies on one side of the row's own place, so that the bias is a
+// straight line: `base` is its value at the step's first key (with the reference, and the cap,
+// taken in), `grow` what it grows by from key to key.  Pairs of floats.  The cap's reciprocals
+// come four at a time from one, of their product: its arguments are held to 2^30, where tanh is 1
+// to the last bit, and special functions bound the step (three a logit, 2.25 so).
+template <int MODE, bool EDGE, bool BIAS>
+__device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c, int key0, uint32_t have,
+                                                  const PrefillLogits& l, float base, float grow, float2 sum2,
+                                                  uint32_t (&h)[64]) {
+  const float2 fac2 = make_float2(l.fac, l.fac), grow2 = make_float2(2.0f * grow, 2.0f * grow);
+  const float2 cap2 = make_float2(-2.0f * l.cap, -2.0f * l.cap), one2 = make_float2(1.0f, 1.0f);
+  float2 t = BIAS ? make_float2(fmaf(16.0f * c, grow, base), fmaf(16.0f * c + 1.0f, grow, base)) : make_float2(base, base);
+#pragma unroll
+  for (int i = 0; i < 16; i += 4) {
+    float2 a = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+    float2 b = make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+    bool seen[4] = {true, true, true, true};
+    if (EDGE) {
+      const bool page = have >> c & 1u;
+#pragma unroll
+      for (int k = 0; k < 4; ++k) seen[k] = l.sees(key0 + 16 * c + i + k, page);
+      if (MODE == kCapped) {                       // what is in the other keys' place must not meet theirs
+        a = make_float2(seen[0] ? a.x : 0.0f, seen[1] ? a.y : 0.0f);
+        b = make_float2(seen[2] ? b.x : 0.0f, seen[3] ? b.y : 0.0f);
+      }
+    }
+    const float2 tb = BIAS ? __fadd2_rn(t, grow2) : t;
+    float2 y, z;
+    if constexpr (MODE == kCapped) {
+      const float2 u = __fmul2_rn(a, fac2), v = __fmul2_rn(b, fac2);
+      const float2 d = __fadd2_rn(make_float2(ex2(min_nan(u.x, 30.0f)), ex2(min_nan(u.y, 30.0f))), one2);
+      const float2 e = __fadd2_rn(make_float2(ex2(min_nan(v.x, 30.0f)), ex2(min_nan(v.y, 30.0f))), one2);
+      const float2 q = __fmul2_rn(make_float2(d.x, e.x), make_float2(d.y, e.y));   // d.x d.y, e.x e.y
+      const float r = rcp(q.x * q.y);
+      const float2 w = __fmul2_rn(make_float2(r, r), make_float2(q.y, q.x));       // 1 / (d.x d.y), 1 / (e.x e.y)
+      y = __ffma2_rn(__fmul2_rn(make_float2(w.x, w.x), make_float2(d.y, d.x)), cap2, t);
+      z = __ffma2_rn(__fmul2_rn(make_float2(w.y, w.y), make_float2(e.y, e.x)), cap2, tb);
+    } else {
+      y = __ffma2_rn(a, fac2, t);
+      z = __ffma2_rn(b, fac2, tb);
+    }
+    if (EDGE) {
+      y = make_float2(seen[0] ? y.x : -INFINITY, seen[1] ? y.y : -INFINITY);
+      z = make_float2(seen[2] ? z.x : -INFINITY, seen[3] ? z.y : -INFINITY);
+    }
+    y.x = ex2(y.x);
+    y.y = ex2(y.y);
+    z.x = ex2(z.x);
+    z.y = ex2(z.y);
+    sum2 = __fadd2_rn(sum2, y);
+    sum2 = __fadd2_rn(sum2, z);
+    h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
+    h[8 * c + i / 2 + 1] = pack_f16x2(z.x, z.y);
+    if (BIAS) t = __fadd2_rn(tb, grow2);
+  }
+  return sum2;
+}
+template <int MODE, bool EDGE, bool BIAS>
+__device__ __forceinline__ float prefill_weights_line(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
+                                                      float base, float grow, uint32_t (&h)[64]) {
+  float2 sum2 = make_float2(0.0f, 0.0f);
+  uint32_t a[16], b[16];
+  tmem_load_16cols_async(ts, a);
+  tmem_load_wait(a);
+#pragma unroll
+  for (int c = 0; c < 8; c += 2) {
+    tmem_load_16cols_async(ts + 16 * c + 16, b);
+    sum2 = prefill_line_16<MODE, EDGE, BIAS>(a, c, key0, have, l, base, grow, sum2, h);
+    tmem_load_wait(b);
+    if (c < 6) tmem_load_16cols_async(ts + 16 * c + 32, a);
+    sum2 = prefill_line_16<MODE, EDGE, BIAS>(b, c + 1, key0, have, l, base, grow, sum2, h);
+    if (c < 6) tmem_load_wait(a);
+  }
+  return sum2.x + sum2.y;
 }
 
 // Multiplies 32 n columns of tensor memory, this thread's lane of them, by f.
@@ -396,7 +473,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   const int per = (max(0, all - skip) + splits - 1) / splits;
   const int t0 = min(all, skip + static_cast<int>(blockIdx.y) * per), t1 = min(all, t0 + per);
   const int all0 = (max(0, limit_of(last0)) + kPreKeys - 1) / kPreKeys;
-  const int n[2] = {max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
+  // MODE kMasked, kCapped: from the last keys to the first, as a bias makes logits grow towards
+  // a row's own place and every step would move its reference; tile 0 then begins with keys
+  // that it may not see
+  constexpr bool kBackwards = MODE != kPlain;
+  const int n[2] = {kBackwards ? t1 - t0 : max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
   const int steps = max(n[0], n[1]);
 
   if (warp == 12) tmem_alloc(&tmem_slot, kPreTmemCols);
@@ -488,17 +569,20 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     int lim_lo = ok ? lim : INT32_MAX;           // smallest of the warp's rows
     lim_lo = __reduce_min_sync(kFullMask, lim_lo);
     [[maybe_unused]] int from_hi = 0;            // largest first key of the warp's rows
+    [[maybe_unused]] float own_lo = 0.0f, own_hi = 0.0f;   // the rows' own places
     [[maybe_unused]] PrefillLogits logits;
     if constexpr (MODE != kPlain) {
       logits = PrefillLogits{fac, MODE == kCapped ? kLog2e * p.softcap : 0.0f, ok ? kv_slope(p, hq) : 0.0f,
                              static_cast<float>(seen.off + tok), ok ? seen.first(tok) : 0, lim};
       from_hi = __reduce_max_sync(kFullMask, logits.from);
+      own_lo = static_cast<float>(__reduce_min_sync(kFullMask, ok ? seen.off + tok : INT32_MAX / 2));
+      own_hi = static_cast<float>(__reduce_max_sync(kFullMask, ok ? seen.off + tok : INT32_MIN / 2));
     }
     constexpr int kCoarseRows = INT32_MIN;       // in lim_lo's place: a row's reference is_coarse, or was
     float ref = kRefStart, sum = 0.0f;
     bool alive = true;
     for (int j = 0; j < n[tile]; ++j) {
-      const int key0 = (t0 + j) * kPreKeys;
+      const int key0 = (kBackwards ? t1 - 1 - j : t0 + j) * kPreKeys;
       uint32_t have = 0xffu;                       // 16-key groups that have a page
       if (bad_pages) {
         uint32_t row_of, at_of;
@@ -518,7 +602,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       // such rows, or two roundings in the masked steps', made every call 1 to 2 % slower)
       uint32_t h[64];
       float step_sum;
-      bool moved = j == 0 || lim_lo == kCoarseRows, last = moved;
+      bool moved = j == 0 || lim_lo == kCoarseRows;
+      if constexpr (MODE != kPlain)                // a row's first keys may come later
+        moved = __any_sync(kFullMask, j == 0 || (ref == kRefStart && key0 < lim && key0 + kPreKeys > logits.from));
+      bool last = moved;
 #pragma unroll 1
       for (;;) {
         if (last) {
@@ -526,8 +613,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
           if constexpr (MODE == kPlain)
             m = edge ? prefill_maximum<true>(ts, key0, lim, have) : prefill_maximum<false>(ts, key0, lim, have);
           else
-            m = edge ? prefill_maximum<MODE, true>(ts, key0, have, logits)
-                     : prefill_maximum<MODE, false>(ts, key0, have, logits);
+            m = prefill_maximum<MODE>(ts, key0, have, logits);
           float f = 1.0f;
           if (moved && m > -INFINITY) {
             const float to_ref = ref_for(ref, m, MODE == kPlain ? fac : 1.0f);
@@ -548,8 +634,22 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
           step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, f, ref, h)
                           : prefill_weights<false>(ts, key0, lim, have, f, ref, h);
         } else {
-          step_sum = edge ? prefill_weights<MODE, true>(ts, key0, have, logits, ref, h)
-                          : prefill_weights<MODE, false>(ts, key0, have, logits, ref, h);
+          // the side of the rows' own places that the step lies on (keys behind them that no
+          // row sees do not count)
+          const bool left = !p.slopes || key0 + kPreKeys - 1 <= own_lo || (seen.causal && key0 >= seen.prefix);
+          const bool line = left || key0 >= own_hi;
+          if (!line || __any_sync(kFullMask, is_coarse(ref))) {
+            step_sum = prefill_weights_by_logit<MODE>(ts, key0, have, logits, ref, h);
+          } else {
+            const float grow = left ? logits.slope : -logits.slope;
+            const float base = fmaf(grow, static_cast<float>(key0) - logits.own, logits.cap - ref);
+            if (p.slopes)
+              step_sum = edge ? prefill_weights_line<MODE, true, true>(ts, key0, have, logits, base, grow, h)
+                              : prefill_weights_line<MODE, false, true>(ts, key0, have, logits, base, grow, h);
+            else
+              step_sum = edge ? prefill_weights_line<MODE, true, false>(ts, key0, have, logits, base, grow, h)
+                              : prefill_weights_line<MODE, false, false>(ts, key0, have, logits, base, grow, h);
+          }
         }
         if (last) break;
         moved = !(step_sum <= kPreMostSum);
@@ -635,18 +735,28 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     // group `lane` (of 8) of the step after the one whose page is in page_of: page idx, place at;
     // a step of 128 keys is page_q pages and page_r places
     const int page_q = kPreKeys / p.c.page_size, page_r = kPreKeys - page_q * p.c.page_size;
-    int key = t0 * kPreKeys + 16 * (lane & 7);
+    int key = (kBackwards ? t1 - 1 : t0) * kPreKeys + 16 * (lane & 7);
     int idx = key / p.c.page_size, at = key - idx * p.c.page_size;
     int page_of, at_of;                            // the page's number is looked at a step later
     auto next_page = [&]() {
       at_of = at;
-      page_of = key < seq.len ? prefill_page(p, b, idx) : -1;
-      key += kPreKeys;
-      idx += page_q;
-      at += page_r;
-      if (at >= p.c.page_size) {
-        at -= p.c.page_size;
-        ++idx;
+      page_of = key < seq.len && (!kBackwards || key >= 0) ? prefill_page(p, b, idx) : -1;
+      if constexpr (kBackwards) {
+        key -= kPreKeys;
+        idx -= page_q;
+        at -= page_r;
+        if (at < 0) {
+          at += p.c.page_size;
+          --idx;
+        }
+      } else {
+        key += kPreKeys;
+        idx += page_q;
+        at += page_r;
+        if (at >= p.c.page_size) {
+          at -= p.c.page_size;
+          ++idx;
+        }
       }
     };
     PrefillRaw<D> raw[2];                          // loaded one step before it is converted
@@ -671,7 +781,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         warp_arrive(&bars[kBarKFull + s], lane);
         alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit));
         if (!alive) break;
-        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, seq.len - (t0 + j) * kPreKeys, pw, lane);
+        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, seq.len - (kBackwards ? t1 - 1 - j : t0 + j) * kPreKeys, pw, lane);
         fence_proxy_async_smem();
         warp_arrive(&bars[kBarVFull + s], lane);
       }
