@@ -29,7 +29,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // seen when it was set, and it is set again once a logit passes r + 14: weights
 // stay below 2^14 in fp16, and one that is 2^30 times smaller than the largest
 // still has a bit.  A finite start keeps "nothing seen yet" free of inf - inf, and
-// no logit lies below it.
+// no logit lies below it.  The kernels with capped or biased logits keep r at the largest
+// itself: such logits reach further (a cap is there because they do), and a row that passes
+// r + 14 costs its warp a step, while weights that are 2^14 times smaller than the
+// largest may lose bits of theirs (2^-25 of the largest at most).
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kRefBelow = 6.0f;
 constexpr float kRefSlack = 14.0f;

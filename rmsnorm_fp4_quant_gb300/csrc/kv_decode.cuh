@@ -353,9 +353,10 @@ kv_decode_kernel(const KvAttentionParams p) {
     // --- the ring: tile x of this warp is keys key0(x) ... + 15
     const int first_key = (w.skip + tile0) * kDecUnit + warp * 16;
     const int32_t* table = p.tables + static_cast<int64_t>(w.b) * p.max_pages;
-    // (MODE kMasked, kCapped: from the last tile to the first, as a bias makes logits grow towards
-    // a row's own place and every step would move its reference)
-    auto key_of = [&](int x) { return first_key + (MODE == kPlain ? x : n_units - 1 - x) * kDecUnit; };
+    // with a bias from the last tile to the first, as it makes logits grow towards a row's own place
+    // and every step would move its reference
+    const bool backwards = MODE != kPlain && p.slopes;
+    auto key_of = [&](int x) { return first_key + (backwards ? n_units - 1 - x : x) * kDecUnit; };
     // a row number counts slots of all pages and heads and fits 32 bits
     constexpr uint32_t kNoRow = 0xffffffffu;
     uint32_t row_of = kNoRow, row_next = kNoRow;
@@ -596,7 +597,7 @@ kv_decode_kernel(const KvAttentionParams p) {
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
-            const float r = ref_for(ref[n][e], m, MODE == kPlain ? fac[n][e] : 1.0f);
+            const float r = MODE == kPlain ? ref_for(ref[n][e], m, fac[n][e]) : fmaxf(ref[n][e], m);
             const float f = ex2(ref[n][e] - r);
             ref[n][e] = r;
             far |= MODE == kPlain && is_coarse(r);   // (a logit that is rounded needs no other code)

@@ -270,9 +270,9 @@ __device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim,
   }
   return sum2.x + sum2.y;
 }
-// The largest product of a row with a key that it sees.
-template <bool EDGE>
-__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, uint32_t have) {
+// The largest product of a row with a key that it sees (of keys `from` on: FROM).
+template <bool EDGE, bool FROM = false>
+__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, uint32_t have, int from = 0) {
   float m = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -286,8 +286,9 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim,
         float u = __uint_as_float(x[i + 2 * k]), v = __uint_as_float(x[i + 2 * k + 1]);
         if (EDGE) {
           const bool page = have >> (2 * c + i / 16) & 1u;
-          if (!page || key0 + 32 * c + i + 2 * k >= lim) u = -INFINITY;
-          if (!page || key0 + 32 * c + i + 2 * k + 1 >= lim) v = -INFINITY;
+          const int key = key0 + 32 * c + i + 2 * k;
+          if (!page || key >= lim || (FROM && key < from)) u = -INFINITY;
+          if (!page || key + 1 >= lim || (FROM && key + 1 < from)) v = -INFINITY;
         }
         y[k] = max3(y[k], u, v);
       }
@@ -303,10 +304,11 @@ struct PrefillLogits {
   int from, lim;
   __device__ __forceinline__ bool sees(int key, bool page) const { return page && key < lim && key >= from; }
 };
+// (away: the distance of key0, `key` of these behind it)
 template <int MODE>
-__device__ __forceinline__ float prefill_logit(uint32_t s, int key, bool page, const PrefillLogits& l) {
-  const float z = kv_logit<MODE>(__uint_as_float(s), l.fac, l.cap, l.slope, static_cast<float>(key) - l.own);
-  return l.sees(key, page) ? z : -INFINITY;
+__device__ __forceinline__ float prefill_logit(uint32_t s, int key0, int key, float away, bool page, const PrefillLogits& l) {
+  const float z = kv_logit<MODE>(__uint_as_float(s), l.fac, l.cap, l.slope, away + static_cast<float>(key));
+  return l.sees(key0 + key, page) ? z : -INFINITY;
 }
 // As prefill_weights above, logit by logit, each rounded before the reference is taken from it:
 // for steps on both sides of a row's own place, and for coarse references.
@@ -314,6 +316,7 @@ template <int MODE>
 __device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
                                                           float ref, uint32_t (&h)[64]) {
   float2 sum2 = make_float2(0.0f, 0.0f);
+  const float away = static_cast<float>(key0) - l.own;
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t x[16];
@@ -323,27 +326,34 @@ __device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0,
 #pragma unroll
     for (int i = 0; i < 16; i += 2) {
       float2 y;
-      y.x = ex2(__fsub_rn(prefill_logit<MODE>(x[i], key0 + 16 * c + i, page, l), ref));
-      y.y = ex2(__fsub_rn(prefill_logit<MODE>(x[i + 1], key0 + 16 * c + i + 1, page, l), ref));
+      y.x = ex2(__fsub_rn(prefill_logit<MODE>(x[i], key0, 16 * c + i, away, page, l), ref));
+      y.y = ex2(__fsub_rn(prefill_logit<MODE>(x[i + 1], key0, 16 * c + i + 1, away, page, l), ref));
       sum2 = __fadd2_rn(sum2, y);
       h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
     }
   }
   return sum2.x + sum2.y;
 }
+// The largest logit of a row's step; `products`: without biases, which is the largest product's.
 template <int MODE>
-__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l) {
+__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l, bool products) {
+  if (products) {
+    const float m = prefill_maximum<true, true>(ts, key0, l.lim, have, l.from);
+    return m > -INFINITY ? kv_logit<MODE>(m, l.fac, l.cap, 0.0f, 0.0f) : m;
+  }
   float m = -INFINITY;
+  const float away = static_cast<float>(key0) - l.own;
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
     uint32_t x[16];
     tmem_load_16cols_async(ts + 16 * c, x);
     tmem_load_wait(x);
     const bool page = have >> c & 1u;
+    const float at = away + static_cast<float>(16 * c);
 #pragma unroll
     for (int i = 0; i < 16; i += 2)
-      m = max3(m, prefill_logit<MODE>(x[i], key0 + 16 * c + i, page, l),
-               prefill_logit<MODE>(x[i + 1], key0 + 16 * c + i + 1, page, l));
+      m = max3(m, prefill_logit<MODE>(x[i], key0 + 16 * c, i, at, page, l),
+               prefill_logit<MODE>(x[i + 1], key0 + 16 * c, i + 1, at, page, l));
   }
   return m;
 }
@@ -473,11 +483,11 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   const int per = (max(0, all - skip) + splits - 1) / splits;
   const int t0 = min(all, skip + static_cast<int>(blockIdx.y) * per), t1 = min(all, t0 + per);
   const int all0 = (max(0, limit_of(last0)) + kPreKeys - 1) / kPreKeys;
-  // MODE kMasked, kCapped: from the last keys to the first, as a bias makes logits grow towards
-  // a row's own place and every step would move its reference; tile 0 then begins with keys
-  // that it may not see
-  constexpr bool kBackwards = MODE != kPlain;
-  const int n[2] = {kBackwards ? t1 - t0 : max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
+  // with a bias from the last keys to the first, as it makes logits grow towards a row's own
+  // place and every step would move its reference; tile 0 then begins with keys that it may
+  // not see
+  const bool backwards = MODE != kPlain && p.slopes;
+  const int n[2] = {backwards ? t1 - t0 : max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
   const int steps = max(n[0], n[1]);
 
   if (warp == 12) tmem_alloc(&tmem_slot, kPreTmemCols);
@@ -582,7 +592,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     float ref = kRefStart, sum = 0.0f;
     bool alive = true;
     for (int j = 0; j < n[tile]; ++j) {
-      const int key0 = (kBackwards ? t1 - 1 - j : t0 + j) * kPreKeys;
+      const int key0 = (backwards ? t1 - 1 - j : t0 + j) * kPreKeys;
       uint32_t have = 0xffu;                       // 16-key groups that have a page
       if (bad_pages) {
         uint32_t row_of, at_of;
@@ -613,10 +623,10 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
           if constexpr (MODE == kPlain)
             m = edge ? prefill_maximum<true>(ts, key0, lim, have) : prefill_maximum<false>(ts, key0, lim, have);
           else
-            m = prefill_maximum<MODE>(ts, key0, have, logits);
+            m = prefill_maximum<MODE>(ts, key0, have, logits, !p.slopes);
           float f = 1.0f;
           if (moved && m > -INFINITY) {
-            const float to_ref = ref_for(ref, m, MODE == kPlain ? fac : 1.0f);
+            const float to_ref = MODE == kPlain ? ref_for(ref, m, fac) : fmaxf(ref, m);
             f = ex2(ref - to_ref);
             ref = to_ref;
             sum *= f;
@@ -735,13 +745,13 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     // group `lane` (of 8) of the step after the one whose page is in page_of: page idx, place at;
     // a step of 128 keys is page_q pages and page_r places
     const int page_q = kPreKeys / p.c.page_size, page_r = kPreKeys - page_q * p.c.page_size;
-    int key = (kBackwards ? t1 - 1 : t0) * kPreKeys + 16 * (lane & 7);
+    int key = (backwards ? t1 - 1 : t0) * kPreKeys + 16 * (lane & 7);
     int idx = key / p.c.page_size, at = key - idx * p.c.page_size;
     int page_of, at_of;                            // the page's number is looked at a step later
     auto next_page = [&]() {
       at_of = at;
-      page_of = key < seq.len && (!kBackwards || key >= 0) ? prefill_page(p, b, idx) : -1;
-      if constexpr (kBackwards) {
+      page_of = key < seq.len && (!backwards || key >= 0) ? prefill_page(p, b, idx) : -1;
+      if (backwards) {
         key -= kPreKeys;
         idx -= page_q;
         at -= page_r;
@@ -781,7 +791,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         warp_arrive(&bars[kBarKFull + s], lane);
         alive = j < 2 || __all_sync(kFullMask, mbar_wait_bounded(&bars[kBarVEmpty + s], parity, wait_limit));
         if (!alive) break;
-        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, seq.len - (kBackwards ? t1 - 1 - j : t0 + j) * kPreKeys, pw, lane);
+        prefill_store_v<D>(raw[s], smem0 + S::kV + s * S::kTile, seq.len - (backwards ? t1 - 1 - j : t0 + j) * kPreKeys, pw, lane);
         fence_proxy_async_smem();
         warp_arrive(&bars[kBarVFull + s], lane);
       }
