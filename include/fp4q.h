@@ -512,7 +512,7 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
  *   j <= pos, or j < prefix_lens[b]        (causal; prefix_lens NULL: the first alone)
  *   j > pos - window                       (window > 0)
  *
- *   softcap        >= 0, finite.
+ *   softcap        >= 0, at most 2^20.
  *   alibi_slopes   [Hq] fp32 or NULL.
  *   window         >= 0; 0: none.  With causal only.  Pages that hold nothing but keys before the
  *                  first row's window are not read (fp4_kv_trim_nvfp4 gives them up).

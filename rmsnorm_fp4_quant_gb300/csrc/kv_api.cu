@@ -254,7 +254,7 @@ fp4_status_t fp4_attention_nvfp4_ex(const void* q, int64_t q_stride, const fp4_k
   if (!valid_dtype(dtype) || B < 0 || T < 0 || Hq <= 0 || max_pages < 0 || workspace_bytes < 0)
     return FP4_ERR_INVALID_ARG;
   if (!(sm_scale > 0.0f) || !std::isfinite(sm_scale)) return FP4_ERR_INVALID_ARG;
-  if (!(softcap >= 0.0f) || !std::isfinite(softcap) || window < 0 || (!causal && (window || prefix_lens)))
+  if (!(softcap >= 0.0f) || softcap > 1048576.0f || window < 0 || (!causal && (window || prefix_lens)))
     return FP4_ERR_INVALID_ARG;
   const fp4_status_t cs = check_cache_sizes(cache);
   if (cs != FP4_OK) return cs;

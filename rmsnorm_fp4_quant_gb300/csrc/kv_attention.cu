@@ -54,7 +54,7 @@ int64_t kv_attention_workspace_bound(int sms, int64_t B, int64_t T, int Hq, int 
 
 cudaError_t launch_kv_attention(int dtype, const KvAttentionParams& p, int pdl,
                                 cudaStream_t stream) {
-  return dtype == 0 ? launch_type<__nv_bfloat16, kPlain>(p, pdl, stream) : launch_type<__half, kPlain>(p, pdl, stream);
+  return launch_attention<kPlain, kPlain>(dtype, p, pdl, stream);
 }
 
 }  // namespace fp4q

@@ -5,7 +5,8 @@
 namespace fp4q {
 
 cudaError_t launch_kv_attention_capped(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream) {
-  return dtype == 0 ? launch_type<__nv_bfloat16, kCapped>(p, pdl, stream) : launch_type<__half, kCapped>(p, pdl, stream);
+  return p.slopes ? launch_attention<kCappedBiased, kCappedBiased>(dtype, p, pdl, stream)
+                  : launch_attention<kCapped, kCappedBiased>(dtype, p, pdl, stream);
 }
 
 }  // namespace fp4q

@@ -52,8 +52,12 @@ __device__ __forceinline__ float coarse_exponent(float product, float fac, float
 }
 
 // What a kernel does to the products: nothing but the causal mask; keys from a window's first
-// to a prefix's end too, and a bias; and a cap besides.
-enum KvLogits { kPlain = 0, kMasked = 1, kCapped = 2 };
+// to a prefix's end, too; with a bias; with a cap; with both.  The kernel of 256-row items has
+// one instance for each (their loops over the logits differ), the other one for kBiased and
+// kCappedBiased alone, which serve the calls without a bias, too.
+enum KvLogits { kPlain = 0, kMasked = 1, kBiased = 2, kCapped = 3, kCappedBiased = 4 };
+constexpr bool has_bias(int mode) { return mode == kBiased || mode == kCappedBiased; }
+constexpr bool has_cap(int mode) { return mode == kCapped || mode == kCappedBiased; }
 
 // Entries of the call's small arrays (0 for one outside: the debug build's checks).
 __device__ __forceinline__ int kv_len(const KvAttentionParams& p, int b) {
@@ -164,24 +168,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // A row's logit in units of log(2) from its product s and the distance to the key:
-//   kMasked   s fac - slope |away|
-//   kCapped   cap tanh(s fac / cap) - slope |away|, cap and slope in the same units; tanh(x) as
-//             1 - 2 / (1 + exp(2 x)): off by a few 2^-24 of the cap, where the hardware's own
-//             tanh would be off by 2^-11 of it.
-// fac is the product's factor, of kCapped times 2 log2(e) / cap for the exponential's argument.
+//   without a cap   s fac - slope |away|
+//   with one        cap tanh(s fac / cap) - slope |away|, cap and slope in the same units; tanh(x)
+//                   as 1 - 2 / (1 + exp(2 x)): off by a few 2^-24 of the cap, where the hardware's
+//                   own tanh would be off by 2^-11 of it.
+// fac is the product's factor, with a cap times 2 log2(e) / cap for the exponential's argument.
 template <int MODE>
 __device__ __forceinline__ float kv_logit(float s, float fac, float cap, float slope, float away) {
   float z;
-  if constexpr (MODE == kCapped)
+  if constexpr (has_cap(MODE))
     z = fmaf(-2.0f * cap, rcp(1.0f + ex2(s * fac)), cap);
   else
     z = __fmul_rn(s, fac);
-  return fmaf(-slope, fabsf(away), z);
+  return has_bias(MODE) ? fmaf(-slope, fabsf(away), z) : z;
 }
 // The factor from the one that turns a product into a logit in units of log(2).
 template <int MODE>
 __device__ __forceinline__ float kv_factor(const KvAttentionParams& p, float fac) {
-  return MODE == kCapped ? fac * __fdiv_rn(2.0f, p.softcap) : fac;
+  return has_cap(MODE) ? fac * __fdiv_rn(2.0f, p.softcap) : fac;
 }
 __device__ __forceinline__ float kv_slope(const KvAttentionParams& p, int hq) {
   return p.slopes && FP4Q_IN_RANGE(p, p.slopes + hq, 4, p.slopes, 4LL * p.Hq) ? kLog2e * __ldg(p.slopes + hq) : 0.0f;

@@ -1,5 +1,5 @@
 // kv_attention_launch.cuh - attention over the paged NVFP4 key/value cache: choice of
-// kernel and launch, for the kernels of one kind of logits (KvLogits).
+// kernel and launch.
 #pragma once
 
 #include <algorithm>
@@ -213,14 +213,20 @@ cudaError_t launch_prefill(const KvAttentionParams& p, int pdl, cudaStream_t str
   return cudaLaunchKernelEx(&cfg, kv_prefill_join_kernel<T, D>, p, splits);
 }
 
-template <typename T, int MODE>
+// PRE, DEC: the kinds of logits of the two kernels (KvLogits).
+template <typename T, int PRE, int DEC>
 cudaError_t launch_type(const KvAttentionParams& p, int pdl, cudaStream_t stream) {
   if (use_prefill(sm_count_current_device(), p.B, p.T, p.Hq, p.c.heads, p.c.D, keys_of(p)))
-    return p.c.D == 128 ? launch_prefill<T, 128, MODE>(p, pdl, stream) : launch_prefill<T, 64, MODE>(p, pdl, stream);
+    return p.c.D == 128 ? launch_prefill<T, 128, PRE>(p, pdl, stream) : launch_prefill<T, 64, PRE>(p, pdl, stream);
   const int nt = decode_tiles(p.B, p.T, p.group);
   if (p.c.D == 128)
-    return nt == 1 ? launch_decode<T, 128, 1, MODE>(p, pdl, stream) : launch_decode<T, 128, 2, MODE>(p, pdl, stream);
-  return nt == 1 ? launch_decode<T, 64, 1, MODE>(p, pdl, stream) : launch_decode<T, 64, 2, MODE>(p, pdl, stream);
+    return nt == 1 ? launch_decode<T, 128, 1, DEC>(p, pdl, stream) : launch_decode<T, 128, 2, DEC>(p, pdl, stream);
+  return nt == 1 ? launch_decode<T, 64, 1, DEC>(p, pdl, stream) : launch_decode<T, 64, 2, DEC>(p, pdl, stream);
+}
+// dtype 0 = bf16, 1 = fp16.
+template <int PRE, int DEC>
+cudaError_t launch_attention(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream) {
+  return dtype == 0 ? launch_type<__nv_bfloat16, PRE, DEC>(p, pdl, stream) : launch_type<__half, PRE, DEC>(p, pdl, stream);
 }
 
 }  // namespace

@@ -9,7 +9,8 @@ cudaError_t launch_kv_attention_capped(int dtype, const KvAttentionParams& p, in
 
 cudaError_t launch_kv_attention_masked(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream) {
   if (p.softcap > 0.0f) return launch_kv_attention_capped(dtype, p, pdl, stream);
-  return dtype == 0 ? launch_type<__nv_bfloat16, kMasked>(p, pdl, stream) : launch_type<__half, kMasked>(p, pdl, stream);
+  return p.slopes ? launch_attention<kBiased, kBiased>(dtype, p, pdl, stream)
+                  : launch_attention<kMasked, kBiased>(dtype, p, pdl, stream);
 }
 
 }  // namespace fp4q

@@ -478,7 +478,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     // a reference of the warp's rows is_coarse: its steps take the masked steps' code, where
     // the product is rounded before the reference is taken from it
     bool coarse = false;
-    [[maybe_unused]] const float cap = MODE == kCapped ? kLog2e * p.softcap : 0.0f;
+    [[maybe_unused]] const float cap = has_cap(MODE) ? kLog2e * p.softcap : 0.0f;
     // one step, whose slots of the ring are constants
     auto work = [&](int step, auto phase) {
       constexpr int kPhase = decltype(phase)::value;

@@ -232,8 +232,9 @@ __device__ __forceinline__ void prefill_store_v(const PrefillRaw<D>& r, uint32_t
 // One row's weights of a step: S from tensor memory, 16 columns being read while 16
 // are worked on, p = 2^(fac s - ref) in fp32 summed and in fp16 packed.  Keys that the
 // row does not see, and keys of 16-key groups without a page (bits of `have`), get 0.
-template <bool EDGE>
-__device__ __forceinline__ float2 prefill_weights_16(const uint32_t (&x)[16], int c, int key0, int lim,
+// FROM: and keys before `from`.
+template <bool EDGE, bool FROM>
+__device__ __forceinline__ float2 prefill_weights_16(const uint32_t (&x)[16], int c, int key0, int lim, int from,
                                                      uint32_t have, float2 fac2, float2 ref2, float2 sum2,
                                                      uint32_t (&h)[64]) {
 #pragma unroll
@@ -241,8 +242,9 @@ __device__ __forceinline__ float2 prefill_weights_16(const uint32_t (&x)[16], in
     float2 y = __ffma2_rn(make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1])), fac2, ref2);
     if (EDGE) {
       const bool page = have >> c & 1u;
-      if (!page || key0 + 16 * c + i >= lim) y.x = -INFINITY;
-      if (!page || key0 + 16 * c + i + 1 >= lim) y.y = -INFINITY;
+      const int key = key0 + 16 * c + i;
+      if (!page || key >= lim || (FROM && key < from)) y.x = -INFINITY;
+      if (!page || key + 1 >= lim || (FROM && key + 1 < from)) y.y = -INFINITY;
     }
     y.x = ex2(y.x);
     y.y = ex2(y.y);
@@ -251,8 +253,8 @@ __device__ __forceinline__ float2 prefill_weights_16(const uint32_t (&x)[16], in
   }
   return sum2;
 }
-template <bool EDGE>
-__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim, uint32_t have, float fac,
+template <bool EDGE, bool FROM>
+__device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim, int from, uint32_t have, float fac,
                                                  float ref, uint32_t (&h)[64]) {
   const float2 fac2 = make_float2(fac, fac), ref2 = make_float2(-ref, -ref);
   float2 sum2 = make_float2(0.0f, 0.0f);
@@ -262,17 +264,17 @@ __device__ __forceinline__ float prefill_weights(uint32_t ts, int key0, int lim,
 #pragma unroll
   for (int c = 0; c < 8; c += 2) {
     tmem_load_16cols_async(ts + 16 * c + 16, b);
-    sum2 = prefill_weights_16<EDGE>(a, c, key0, lim, have, fac2, ref2, sum2, h);
+    sum2 = prefill_weights_16<EDGE, FROM>(a, c, key0, lim, from, have, fac2, ref2, sum2, h);
     tmem_load_wait(b);
     if (c < 6) tmem_load_16cols_async(ts + 16 * c + 32, a);
-    sum2 = prefill_weights_16<EDGE>(b, c + 1, key0, lim, have, fac2, ref2, sum2, h);
+    sum2 = prefill_weights_16<EDGE, FROM>(b, c + 1, key0, lim, from, have, fac2, ref2, sum2, h);
     if (c < 6) tmem_load_wait(a);
   }
   return sum2.x + sum2.y;
 }
 // The largest product of a row with a key that it sees (of keys `from` on: FROM).
-template <bool EDGE, bool FROM = false>
-__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, uint32_t have, int from = 0) {
+template <bool EDGE, bool FROM>
+__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim, int from, uint32_t have) {
   float m = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 4; ++c) {
@@ -297,7 +299,7 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim,
   return m;
 }
 
-// What a row needs to turn products into logits (MODE kMasked, kCapped): kv_logit's arguments,
+// What a row needs to turn products into logits (has_bias, has_cap): kv_logit's arguments,
 // its own place, and the keys [from, lim) that it sees.
 struct PrefillLogits {
   float fac, cap, slope, own;
@@ -334,13 +336,9 @@ __device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0,
   }
   return sum2.x + sum2.y;
 }
-// The largest logit of a row's step; `products`: without biases, which is the largest product's.
+// The largest logit of a row's step, by logit, too.
 template <int MODE>
-__device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l, bool products) {
-  if (products) {
-    const float m = prefill_maximum<true, true>(ts, key0, l.lim, have, l.from);
-    return m > -INFINITY ? kv_logit<MODE>(m, l.fac, l.cap, 0.0f, 0.0f) : m;
-  }
+__device__ __forceinline__ float prefill_maximum_by_logit(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l) {
   float m = -INFINITY;
   const float away = static_cast<float>(key0) - l.own;
 #pragma unroll 1
@@ -362,46 +360,57 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, uint32_t
 // taken in), `grow` what it grows by from key to key.  Pairs of floats.  The cap's reciprocals
 // come four at a time from one, of their product: its arguments are held to 2^30, where tanh is 1
 // to the last bit, and special functions bound the step (three a logit, 2.25 so).
-template <int MODE, bool EDGE, bool BIAS>
+// Logits i .. i + 3 of x, the keys from key0 on; t and tb are the line at the two pairs.
+template <int MODE, bool EDGE>
+__device__ __forceinline__ void prefill_line_4(const uint32_t (&x)[16], int i, int key0, bool page, const PrefillLogits& l,
+                                               float2 t, float2 tb, float2& y, float2& z) {
+  const float2 fac2 = make_float2(l.fac, l.fac);
+  const float2 cap2 = make_float2(-2.0f * l.cap, -2.0f * l.cap), one2 = make_float2(1.0f, 1.0f);
+  float2 a = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
+  float2 b = make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
+  bool seen[4] = {true, true, true, true};
+  if (EDGE) {
+#pragma unroll
+    for (int k = 0; k < 4; ++k) seen[k] = l.sees(key0 + i + k, page);
+    if (has_cap(MODE)) {                           // what is in the other keys' place must not meet theirs
+      a = make_float2(seen[0] ? a.x : 0.0f, seen[1] ? a.y : 0.0f);
+      b = make_float2(seen[2] ? b.x : 0.0f, seen[3] ? b.y : 0.0f);
+    }
+  }
+  if constexpr (has_cap(MODE)) {
+    const float2 u = __fmul2_rn(a, fac2), v = __fmul2_rn(b, fac2);
+    const float2 d = __fadd2_rn(make_float2(ex2(min_nan(u.x, 30.0f)), ex2(min_nan(u.y, 30.0f))), one2);
+    const float2 e = __fadd2_rn(make_float2(ex2(min_nan(v.x, 30.0f)), ex2(min_nan(v.y, 30.0f))), one2);
+    const float2 q = __fmul2_rn(make_float2(d.x, e.x), make_float2(d.y, e.y));   // d.x d.y, e.x e.y
+    const float r = rcp(q.x * q.y);
+    const float2 w = __fmul2_rn(make_float2(r, r), make_float2(q.y, q.x));       // 1 / (d.x d.y), 1 / (e.x e.y)
+    y = __ffma2_rn(__fmul2_rn(make_float2(w.x, w.x), make_float2(d.y, d.x)), cap2, t);
+    z = __ffma2_rn(__fmul2_rn(make_float2(w.y, w.y), make_float2(e.y, e.x)), cap2, tb);
+  } else {
+    y = __ffma2_rn(a, fac2, t);
+    z = __ffma2_rn(b, fac2, tb);
+  }
+  if (EDGE) {
+    y = make_float2(seen[0] ? y.x : -INFINITY, seen[1] ? y.y : -INFINITY);
+    z = make_float2(seen[2] ? z.x : -INFINITY, seen[3] ? z.y : -INFINITY);
+  }
+}
+template <int MODE>
+__device__ __forceinline__ float2 prefill_line_start(int c, float base, float grow) {
+  return has_bias(MODE) ? make_float2(fmaf(16.0f * c, grow, base), fmaf(16.0f * c + 1.0f, grow, base))
+                        : make_float2(base, base);
+}
+template <int MODE, bool EDGE>
 __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c, int key0, uint32_t have,
                                                   const PrefillLogits& l, float base, float grow, float2 sum2,
                                                   uint32_t (&h)[64]) {
-  const float2 fac2 = make_float2(l.fac, l.fac), grow2 = make_float2(2.0f * grow, 2.0f * grow);
-  const float2 cap2 = make_float2(-2.0f * l.cap, -2.0f * l.cap), one2 = make_float2(1.0f, 1.0f);
-  float2 t = BIAS ? make_float2(fmaf(16.0f * c, grow, base), fmaf(16.0f * c + 1.0f, grow, base)) : make_float2(base, base);
+  const float2 grow2 = make_float2(2.0f * grow, 2.0f * grow);
+  float2 t = prefill_line_start<MODE>(c, base, grow);
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
-    float2 a = make_float2(__uint_as_float(x[i]), __uint_as_float(x[i + 1]));
-    float2 b = make_float2(__uint_as_float(x[i + 2]), __uint_as_float(x[i + 3]));
-    bool seen[4] = {true, true, true, true};
-    if (EDGE) {
-      const bool page = have >> c & 1u;
-#pragma unroll
-      for (int k = 0; k < 4; ++k) seen[k] = l.sees(key0 + 16 * c + i + k, page);
-      if (MODE == kCapped) {                       // what is in the other keys' place must not meet theirs
-        a = make_float2(seen[0] ? a.x : 0.0f, seen[1] ? a.y : 0.0f);
-        b = make_float2(seen[2] ? b.x : 0.0f, seen[3] ? b.y : 0.0f);
-      }
-    }
-    const float2 tb = BIAS ? __fadd2_rn(t, grow2) : t;
+    const float2 tb = has_bias(MODE) ? __fadd2_rn(t, grow2) : t;
     float2 y, z;
-    if constexpr (MODE == kCapped) {
-      const float2 u = __fmul2_rn(a, fac2), v = __fmul2_rn(b, fac2);
-      const float2 d = __fadd2_rn(make_float2(ex2(min_nan(u.x, 30.0f)), ex2(min_nan(u.y, 30.0f))), one2);
-      const float2 e = __fadd2_rn(make_float2(ex2(min_nan(v.x, 30.0f)), ex2(min_nan(v.y, 30.0f))), one2);
-      const float2 q = __fmul2_rn(make_float2(d.x, e.x), make_float2(d.y, e.y));   // d.x d.y, e.x e.y
-      const float r = rcp(q.x * q.y);
-      const float2 w = __fmul2_rn(make_float2(r, r), make_float2(q.y, q.x));       // 1 / (d.x d.y), 1 / (e.x e.y)
-      y = __ffma2_rn(__fmul2_rn(make_float2(w.x, w.x), make_float2(d.y, d.x)), cap2, t);
-      z = __ffma2_rn(__fmul2_rn(make_float2(w.y, w.y), make_float2(e.y, e.x)), cap2, tb);
-    } else {
-      y = __ffma2_rn(a, fac2, t);
-      z = __ffma2_rn(b, fac2, tb);
-    }
-    if (EDGE) {
-      y = make_float2(seen[0] ? y.x : -INFINITY, seen[1] ? y.y : -INFINITY);
-      z = make_float2(seen[2] ? z.x : -INFINITY, seen[3] ? z.y : -INFINITY);
-    }
+    prefill_line_4<MODE, EDGE>(x, i, key0 + 16 * c, have >> c & 1u, l, t, tb, y, z);
     y.x = ex2(y.x);
     y.y = ex2(y.y);
     z.x = ex2(z.x);
@@ -410,11 +419,34 @@ __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c
     sum2 = __fadd2_rn(sum2, z);
     h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
     h[8 * c + i / 2 + 1] = pack_f16x2(z.x, z.y);
-    if (BIAS) t = __fadd2_rn(tb, grow2);
+    if (has_bias(MODE)) t = __fadd2_rn(tb, grow2);
   }
   return sum2;
 }
-template <int MODE, bool EDGE, bool BIAS>
+// The largest logit of a row's step (base without the reference).
+template <int MODE>
+__device__ __forceinline__ float prefill_maximum_line(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
+                                                      float base, float grow) {
+  const float2 grow2 = make_float2(2.0f * grow, 2.0f * grow);
+  float m = -INFINITY;
+#pragma unroll 1
+  for (int c = 0; c < 8; ++c) {
+    uint32_t x[16];
+    tmem_load_16cols_async(ts + 16 * c, x);
+    tmem_load_wait(x);
+    float2 t = prefill_line_start<MODE>(c, base, grow);
+#pragma unroll
+    for (int i = 0; i < 16; i += 4) {
+      const float2 tb = __fadd2_rn(t, grow2);
+      float2 y, z;
+      prefill_line_4<MODE, true>(x, i, key0 + 16 * c, have >> c & 1u, l, t, tb, y, z);
+      m = max3(max3(m, y.x, y.y), z.x, z.y);
+      t = __fadd2_rn(tb, grow2);
+    }
+  }
+  return m;
+}
+template <int MODE, bool EDGE>
 __device__ __forceinline__ float prefill_weights_line(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
                                                       float base, float grow, uint32_t (&h)[64]) {
   float2 sum2 = make_float2(0.0f, 0.0f);
@@ -424,10 +456,10 @@ __device__ __forceinline__ float prefill_weights_line(uint32_t ts, int key0, uin
 #pragma unroll
   for (int c = 0; c < 8; c += 2) {
     tmem_load_16cols_async(ts + 16 * c + 16, b);
-    sum2 = prefill_line_16<MODE, EDGE, BIAS>(a, c, key0, have, l, base, grow, sum2, h);
+    sum2 = prefill_line_16<MODE, EDGE>(a, c, key0, have, l, base, grow, sum2, h);
     tmem_load_wait(b);
     if (c < 6) tmem_load_16cols_async(ts + 16 * c + 32, a);
-    sum2 = prefill_line_16<MODE, EDGE, BIAS>(b, c + 1, key0, have, l, base, grow, sum2, h);
+    sum2 = prefill_line_16<MODE, EDGE>(b, c + 1, key0, have, l, base, grow, sum2, h);
     if (c < 6) tmem_load_wait(a);
   }
   return sum2.x + sum2.y;
@@ -486,7 +518,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
   // with a bias from the last keys to the first, as it makes logits grow towards a row's own
   // place and every step would move its reference; tile 0 then begins with keys that it may
   // not see
-  const bool backwards = MODE != kPlain && p.slopes;
+  constexpr bool backwards = has_bias(MODE);
   const int n[2] = {backwards ? t1 - t0 : max(0, min(t1, all0) - t0), r0 + 128 < rows ? t1 - t0 : 0};
   const int steps = max(n[0], n[1]);
 
@@ -581,13 +613,18 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     [[maybe_unused]] int from_hi = 0;            // largest first key of the warp's rows
     [[maybe_unused]] float own_lo = 0.0f, own_hi = 0.0f;   // the rows' own places
     [[maybe_unused]] PrefillLogits logits;
-    if constexpr (MODE != kPlain) {
-      logits = PrefillLogits{fac, MODE == kCapped ? kLog2e * p.softcap : 0.0f, ok ? kv_slope(p, hq) : 0.0f,
-                             static_cast<float>(seen.off + tok), ok ? seen.first(tok) : 0, lim};
-      from_hi = __reduce_max_sync(kFullMask, logits.from);
+    const int from = ok ? seen.first(tok) : 0;   // (0 of kPlain)
+    if constexpr (MODE != kPlain) from_hi = __reduce_max_sync(kFullMask, from);
+    if constexpr (has_bias(MODE) || has_cap(MODE))
+      logits = PrefillLogits{fac, has_cap(MODE) ? kLog2e * p.softcap : 0.0f,
+                             has_bias(MODE) && ok ? kv_slope(p, hq) : 0.0f, static_cast<float>(seen.off + tok), from, lim};
+    if constexpr (has_bias(MODE)) {
       own_lo = static_cast<float>(__reduce_min_sync(kFullMask, ok ? seen.off + tok : INT32_MAX / 2));
       own_hi = static_cast<float>(__reduce_max_sync(kFullMask, ok ? seen.off + tok : INT32_MIN / 2));
     }
+    // a straight line of logits (prefill_weights_line) rather than products times a factor; a
+    // first key that is not 0
+    constexpr bool kLines = has_bias(MODE) || has_cap(MODE), kFrom = MODE != kPlain;
     constexpr int kCoarseRows = INT32_MIN;       // in lim_lo's place: a row's reference is_coarse, or was
     float ref = kRefStart, sum = 0.0f;
     bool alive = true;
@@ -610,55 +647,66 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       // had a coarse reference begins every step so, and rounds S times the factor in place
       // after it: the exponents' code is the usual one, with a factor of 1 (other code for
       // such rows, or two roundings in the masked steps', made every call 1 to 2 % slower)
+      // the side of the rows' own places that the step lies on (keys behind them that no row sees
+      // do not count)
+      [[maybe_unused]] bool line = true;
+      [[maybe_unused]] float grow = 0.0f;
+      if constexpr (has_bias(MODE)) {
+        const bool left = key0 + kPreKeys - 1 <= own_lo || (seen.causal && key0 >= seen.prefix);
+        line = left || key0 >= own_hi;
+        grow = left ? logits.slope : -logits.slope;
+      }
       uint32_t h[64];
       float step_sum;
       bool moved = j == 0 || lim_lo == kCoarseRows;
       if constexpr (MODE != kPlain)                // a row's first keys may come later
-        moved = __any_sync(kFullMask, j == 0 || (ref == kRefStart && key0 < lim && key0 + kPreKeys > logits.from));
+        moved = lim_lo == kCoarseRows || __any_sync(kFullMask, ref == kRefStart && key0 < lim && key0 + kPreKeys > from);
       bool last = moved;
+      const bool blind = kFrom && !__any_sync(kFullMask, key0 < lim && key0 + kPreKeys > from);
+      if (blind) {                                 // no row of the warp sees a key of the step
+        step_sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 64; ++i) h[i] = 0;
+      }
 #pragma unroll 1
-      for (;;) {
+      while (!blind) {
         if (last) {
           float m;
-          if constexpr (MODE == kPlain)
-            m = edge ? prefill_maximum<true>(ts, key0, lim, have) : prefill_maximum<false>(ts, key0, lim, have);
-          else
-            m = prefill_maximum<MODE>(ts, key0, have, logits, !p.slopes);
+          if constexpr (has_bias(MODE)) {
+            m = line ? prefill_maximum_line<MODE>(ts, key0, have, logits,
+                                                  fmaf(grow, static_cast<float>(key0) - logits.own, logits.cap), grow)
+                     : prefill_maximum_by_logit<MODE>(ts, key0, have, logits);
+          } else {
+            m = edge ? prefill_maximum<true, kFrom>(ts, key0, lim, from, have)
+                     : prefill_maximum<false, kFrom>(ts, key0, lim, from, have);
+            if (has_cap(MODE) && m > -INFINITY) m = kv_logit<MODE>(m, fac, logits.cap, 0.0f, 0.0f);
+          }
           float f = 1.0f;
           if (moved && m > -INFINITY) {
-            const float to_ref = MODE == kPlain ? ref_for(ref, m, fac) : fmaxf(ref, m);
+            const float to_ref = kLines ? fmaxf(ref, m) : ref_for(ref, m, fac);
             f = ex2(ref - to_ref);
             ref = to_ref;
             sum *= f;
           }
           if (j > 0) prefill_scale(to, D / 32, f);
-          // (a logit that is rounded before the reference is taken from it needs none of this)
-          if (MODE == kPlain && (lim_lo == kCoarseRows || __any_sync(kFullMask, is_coarse(ref)))) {
+          if (!kLines && (lim_lo == kCoarseRows || __any_sync(kFullMask, is_coarse(ref)))) {
             lim_lo = kCoarseRows;
             prefill_scale(ts, kPreKeys / 32, fac);
             tmem_store_wait();
           }
         }
-        if constexpr (MODE == kPlain) {
+        if constexpr (!kLines) {
           const float f = lim_lo == kCoarseRows ? 1.0f : fac;
-          step_sum = edge ? prefill_weights<true>(ts, key0, lim, have, f, ref, h)
-                          : prefill_weights<false>(ts, key0, lim, have, f, ref, h);
+          step_sum = edge ? prefill_weights<true, kFrom>(ts, key0, lim, from, have, f, ref, h)
+                          : prefill_weights<false, kFrom>(ts, key0, lim, from, have, f, ref, h);
         } else {
-          // the side of the rows' own places that the step lies on (keys behind them that no
-          // row sees do not count)
-          const bool left = !p.slopes || key0 + kPreKeys - 1 <= own_lo || (seen.causal && key0 >= seen.prefix);
-          const bool line = left || key0 >= own_hi;
-          if (!line || __any_sync(kFullMask, is_coarse(ref))) {
+          if (has_bias(MODE) && (!line || __any_sync(kFullMask, is_coarse(ref)))) {
             step_sum = prefill_weights_by_logit<MODE>(ts, key0, have, logits, ref, h);
           } else {
-            const float grow = left ? logits.slope : -logits.slope;
-            const float base = fmaf(grow, static_cast<float>(key0) - logits.own, logits.cap - ref);
-            if (p.slopes)
-              step_sum = edge ? prefill_weights_line<MODE, true, true>(ts, key0, have, logits, base, grow, h)
-                              : prefill_weights_line<MODE, false, true>(ts, key0, have, logits, base, grow, h);
-            else
-              step_sum = edge ? prefill_weights_line<MODE, true, false>(ts, key0, have, logits, base, grow, h)
-                              : prefill_weights_line<MODE, false, false>(ts, key0, have, logits, base, grow, h);
+            const float base = has_bias(MODE) ? fmaf(grow, static_cast<float>(key0) - logits.own, logits.cap - ref)
+                                              : logits.cap - ref;
+            step_sum = edge ? prefill_weights_line<MODE, true>(ts, key0, have, logits, base, grow, h)
+                            : prefill_weights_line<MODE, false>(ts, key0, have, logits, base, grow, h);
           }
         }
         if (last) break;
