@@ -581,7 +581,8 @@ FP4Q_API fp4_status_t fp4_attention_launch_shape(int64_t B, int64_t T, int64_t H
  *   tables, max_pages, seq_lens  [B, max_pages] and [B] int32: the old sequences.  All of them end
  *                  with the call; one goes on as itself by being a child's parent.
  *   parents        [N] int32: the old sequence that child i continues; outside [0, B) (beams that have
- *                  no candidate: -1): the child is empty.  NULL: child i continues sequence i (N == B).
+ *                  no candidate: -1): the child is empty.  NULL: child i continues sequence i (N == B, or
+ *                  N == 0: all of them end).
  *   new_lens, new_tokens  [N] int32, or NULL: tokens that child i is about to append, at most (NULL:
  *                  exactly) new_tokens; 0 for an empty child.
  *   out_tables, out_seq_lens  [N, max_pages] and [N] int32: the children, with room for their new

@@ -87,16 +87,24 @@ class AttentionResult:
     logit: np.ndarray      # [T, Hq] largest sum of |scale q k| over the row's keys
     keys: np.ndarray       # [T] keys the row sees
     rows: np.ndarray       # [T] bool: rows of a sequence
+    bias: np.ndarray       # [T, Hq] sum of p |bias|, and
+    bias_weight: np.ndarray  # [T, Hq, D] sum of p |bias| |v|: what errors relative to a bias scale with
+    largest: np.ndarray    # [T, Hq, D] largest |v| that the row sees
 
 
-def attention(q, cache, tables, seq_lens, cu=None, causal=True, sm_scale=1.0, k_gs=1.0, v_gs=1.0):
+def attention(q, cache, tables, seq_lens, cu=None, causal=True, sm_scale=1.0, k_gs=1.0, v_gs=1.0,
+              softcap=0.0, slopes=None, window=0, prefix=None):
+    """Row i of a sequence's n_q stands at place len - n_q + i.  softcap: logits x become
+    softcap * tanh(x / softcap); slopes [Hq]: slope * distance is taken off; window, prefix [B]:
+    with causal, the latest `window` keys up to the row's place, and the first prefix[b]."""
     q = np.asarray(q, np.float64)
     T, Hq, D = q.shape
     pages, heads, page, _ = cache[0].shape
     B = len(seq_lens)
     cu = np.arange(B + 1) if cu is None else np.asarray(cu)
     res = AttentionResult(np.full((T, Hq, D), np.nan), np.full((T, Hq), np.nan), np.zeros((T, Hq, D)),
-                          np.zeros((T, Hq)), np.zeros(T, np.int64), np.zeros(T, bool))
+                          np.zeros((T, Hq)), np.zeros(T, np.int64), np.zeros(T, bool), np.zeros((T, Hq)),
+                          np.zeros((T, Hq, D)), np.zeros((T, Hq, D)))
     for b in range(B):
         n_q = int(cu[b + 1] - cu[b])
         n = int(min(max(seq_lens[b], 0), tables.shape[1] * page))
@@ -110,7 +118,13 @@ def attention(q, cache, tables, seq_lens, cu=None, causal=True, sm_scale=1.0, k_
         k[~ok], v[~ok] = 0.0, 0.0
         for i in range(n_q):
             t = int(cu[b]) + i
-            seen = ok & (j <= (n - n_q + i if causal else n - 1))
+            place = n - n_q + i
+            seen = j <= (place if causal else n - 1)
+            if prefix is not None:
+                seen |= j < prefix[b]
+            if window:
+                seen &= j > place - window
+            seen &= ok
             res.rows[t], res.keys[t] = True, seen.sum()
             for h in range(Hq):
                 kk, vv = k[seen, h // (Hq // heads)], v[seen, h // (Hq // heads)]
@@ -118,10 +132,16 @@ def attention(q, cache, tables, seq_lens, cu=None, causal=True, sm_scale=1.0, k_
                     res.out[t, h], res.lse[t, h] = 0.0, -np.inf
                     continue
                 s = sm_scale * (kk @ q[t, h])
+                if softcap:
+                    s = softcap * np.tanh(s / softcap)
+                bias = np.zeros(len(s)) if slopes is None else float(slopes[h]) * np.abs(place - j[seen])
+                s = s - bias
                 top = s.max()
                 p = np.exp(s - top)
                 res.lse[t, h] = top + np.log(p.sum())
                 p /= p.sum()
                 res.out[t, h], res.weight[t, h] = p @ vv, p @ np.abs(vv)
+                res.bias[t, h], res.bias_weight[t, h] = p @ bias, (p * bias) @ np.abs(vv)
+                res.largest[t, h] = np.abs(vv).max(0)
                 res.logit[t, h] = sm_scale * (np.abs(kk) @ np.abs(q[t, h])).max()
     return res

@@ -348,7 +348,7 @@ fp4_status_t fp4_kv_fork_nvfp4(const fp4_kv_cache_t* cache, const int32_t* refs,
   if (B < 0 || N < 0 || max_pages < 0 || new_tokens < 0 || workspace_bytes < 0) return FP4_ERR_INVALID_ARG;
   const fp4_status_t cs = check_cache_sizes(cache);
   if (cs != FP4_OK) return cs;
-  if (!parents && N != B) return FP4_ERR_INVALID_ARG;
+  if (!parents && N && N != B) return FP4_ERR_INVALID_ARG;
   if (!pages_in_32_bits(*cache, B, max_pages) || !pages_in_32_bits(*cache, N, max_pages) ||
       new_tokens > INT32_MAX / 4 || (new_tokens && N > INT32_MAX / new_tokens))
     return FP4_ERR_UNSUPPORTED_SHAPE;

@@ -356,7 +356,7 @@ __device__ __forceinline__ float prefill_maximum_by_logit(uint32_t ts, int key0,
   return m;
 }
 // The same where the step lies on one side of the row's own place, so that the bias is a
-// straight line: `base` is its value at the step's first key (with the reference, and the cap,
+// straight line: `base` is its value at the row's own place (with the reference, and the cap,
 // taken in), `grow` what it grows by from key to key.  Pairs of floats.  The cap's reciprocals
 // come two at a time from one, of their product, whose factors are held to 2^60, where tanh is
 // long 1 to the last bit (a prompt of 4096, 32 heads of 128: 221 us; one for each 235, one for four
@@ -401,17 +401,20 @@ __device__ __forceinline__ uint32_t prefill_bits(const PrefillLogits& l, int key
   const int lo = min(max(l.from - key, 0), 16), hi = min(max(l.lim - key, lo), 16);
   return page ? (1u << hi) - (1u << lo) : 0u;
 }
+// The line at keys 16 c and 16 c + 1 of the step, whose first key lies `away` from the row's own
+// place: begun anew for every 16 keys, so that roundings are of the size of these keys' biases.
 template <int MODE>
-__device__ __forceinline__ float2 prefill_line_start(int c, float base, float grow) {
-  return has_bias(MODE) ? make_float2(fmaf(16.0f * c, grow, base), fmaf(16.0f * c + 1.0f, grow, base))
+__device__ __forceinline__ float2 prefill_line_start(int c, float base, float away, float grow) {
+  return has_bias(MODE) ? make_float2(fmaf(grow, away + 16.0f * c, base), fmaf(grow, away + (16.0f * c + 1.0f), base))
                         : make_float2(base, base);
 }
 template <int MODE, bool EDGE>
 __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c, int key0, uint32_t have,
-                                                  const PrefillLogits& l, float base, float grow, float2 sum2,
+                                                  const PrefillLogits& l, float base, float away, float grow,
+                                                  float2 sum2,
                                                   uint32_t (&h)[64]) {
   const float2 grow2 = make_float2(2.0f * grow, 2.0f * grow);
-  float2 t = prefill_line_start<MODE>(c, base, grow);
+  float2 t = prefill_line_start<MODE>(c, base, away, grow);
   const uint32_t bits = EDGE ? prefill_bits(l, key0 + 16 * c, have >> c & 1u) : 0u;
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
@@ -432,7 +435,7 @@ __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c
 // The largest logit of a row's step (base without the reference).
 template <int MODE>
 __device__ __forceinline__ float prefill_maximum_line(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
-                                                      float base, float grow) {
+                                                      float base, float away, float grow) {
   const float2 grow2 = make_float2(2.0f * grow, 2.0f * grow);
   float m = -INFINITY;
 #pragma unroll 1
@@ -440,7 +443,7 @@ __device__ __forceinline__ float prefill_maximum_line(uint32_t ts, int key0, uin
     uint32_t x[16];
     tmem_load_16cols_async(ts + 16 * c, x);
     tmem_load_wait(x);
-    float2 t = prefill_line_start<MODE>(c, base, grow);
+    float2 t = prefill_line_start<MODE>(c, base, away, grow);
     const uint32_t bits = prefill_bits(l, key0 + 16 * c, have >> c & 1u);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
@@ -455,7 +458,7 @@ __device__ __forceinline__ float prefill_maximum_line(uint32_t ts, int key0, uin
 }
 template <int MODE, bool EDGE>
 __device__ __forceinline__ float prefill_weights_line(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
-                                                      float base, float grow, uint32_t (&h)[64]) {
+                                                      float base, float away, float grow, uint32_t (&h)[64]) {
   float2 sum2 = make_float2(0.0f, 0.0f);
   uint32_t a[16], b[16];
   tmem_load_16cols_async(ts, a);
@@ -463,10 +466,10 @@ __device__ __forceinline__ float prefill_weights_line(uint32_t ts, int key0, uin
 #pragma unroll
   for (int c = 0; c < 8; c += 2) {
     tmem_load_16cols_async(ts + 16 * c + 16, b);
-    sum2 = prefill_line_16<MODE, EDGE>(a, c, key0, have, l, base, grow, sum2, h);
+    sum2 = prefill_line_16<MODE, EDGE>(a, c, key0, have, l, base, away, grow, sum2, h);
     tmem_load_wait(b);
     if (c < 6) tmem_load_16cols_async(ts + 16 * c + 32, a);
-    sum2 = prefill_line_16<MODE, EDGE>(b, c + 1, key0, have, l, base, grow, sum2, h);
+    sum2 = prefill_line_16<MODE, EDGE>(b, c + 1, key0, have, l, base, away, grow, sum2, h);
     if (c < 6) tmem_load_wait(a);
   }
   return sum2.x + sum2.y;
@@ -657,11 +660,12 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       // the side of the rows' own places that the step lies on (keys behind them that no row sees
       // do not count)
       [[maybe_unused]] bool line = true;
-      [[maybe_unused]] float grow = 0.0f;
+      [[maybe_unused]] float grow = 0.0f, away = 0.0f;
       if constexpr (has_bias(MODE)) {
         const bool left = key0 + kPreKeys - 1 <= own_lo || (seen.causal && key0 >= seen.prefix);
         line = left || key0 >= own_hi;
         grow = left ? logits.slope : -logits.slope;
+        away = static_cast<float>(key0) - logits.own;
       }
       uint32_t h[64];
       float step_sum;
@@ -680,8 +684,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         if (last) {
           float m;
           if constexpr (has_bias(MODE)) {
-            m = line ? prefill_maximum_line<MODE>(ts, key0, have, logits,
-                                                  fmaf(grow, static_cast<float>(key0) - logits.own, logits.cap), grow)
+            m = line ? prefill_maximum_line<MODE>(ts, key0, have, logits, logits.cap, away, grow)
                      : prefill_maximum_by_logit<MODE>(ts, key0, have, logits);
           } else {
             m = edge ? prefill_maximum<true, kFrom>(ts, key0, lim, from, have)
@@ -710,10 +713,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
           if (has_bias(MODE) && (!line || __any_sync(kFullMask, is_coarse(ref)))) {
             step_sum = prefill_weights_by_logit<MODE>(ts, key0, have, logits, ref, h);
           } else {
-            const float base = has_bias(MODE) ? fmaf(grow, static_cast<float>(key0) - logits.own, logits.cap - ref)
-                                              : logits.cap - ref;
-            step_sum = edge ? prefill_weights_line<MODE, true>(ts, key0, have, logits, base, grow, h)
-                            : prefill_weights_line<MODE, false>(ts, key0, have, logits, base, grow, h);
+            const float base = logits.cap - ref;
+            step_sum = edge ? prefill_weights_line<MODE, true>(ts, key0, have, logits, base, away, grow, h)
+                            : prefill_weights_line<MODE, false>(ts, key0, have, logits, base, away, grow, h);
           }
         }
         if (last) break;
