@@ -636,7 +636,9 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     // first key that is not 0
     constexpr bool kLines = has_bias(MODE) || has_cap(MODE), kFrom = MODE != kPlain;
     constexpr int kCoarseRows = INT32_MIN;       // in lim_lo's place: a row's reference is_coarse, or was
-    float ref = kRefStart, sum = 0.0f;
+    // (places behind the last row take part in steps without an edge: they need a reference,
+    // which they would not find in the masked steps)
+    float ref = MODE == kPlain || ok ? kRefStart : 0.0f, sum = 0.0f;
     bool alive = true;
     for (int j = 0; j < n[tile]; ++j) {
       const int key0 = (backwards ? t1 - 1 - j : t0 + j) * kPreKeys;
