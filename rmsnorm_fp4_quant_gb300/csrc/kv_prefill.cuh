@@ -401,26 +401,25 @@ __device__ __forceinline__ uint32_t prefill_bits(const PrefillLogits& l, int key
   const int lo = min(max(l.from - key, 0), 16), hi = min(max(l.lim - key, lo), 16);
   return page ? (1u << hi) - (1u << lo) : 0u;
 }
-// The line at keys 16 c and 16 c + 1 of the step, whose first key lies `away` from the row's own
-// place: begun anew for every 16 keys, so that roundings are of the size of these keys' biases.
+// The line at keys i and i + 1 of 16, from its value `start` at the first of these (begun anew for
+// every 16 keys, so that its roundings are of the size of these keys' biases).
 template <int MODE>
-__device__ __forceinline__ float2 prefill_line_start(int c, float base, float away, float grow) {
-  return has_bias(MODE) ? make_float2(fmaf(grow, away + 16.0f * c, base), fmaf(grow, away + (16.0f * c + 1.0f), base))
-                        : make_float2(base, base);
+__device__ __forceinline__ float2 prefill_line_at(float start, float grow, int i) {
+  return has_bias(MODE) ? make_float2(fmaf(grow, static_cast<float>(i), start), fmaf(grow, static_cast<float>(i + 1), start))
+                        : make_float2(start, start);
 }
 template <int MODE, bool EDGE>
 __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c, int key0, uint32_t have,
                                                   const PrefillLogits& l, float base, float away, float grow,
                                                   float2 sum2,
                                                   uint32_t (&h)[64]) {
-  const float2 grow2 = make_float2(2.0f * grow, 2.0f * grow);
-  float2 t = prefill_line_start<MODE>(c, base, away, grow);
+  const float start = has_bias(MODE) ? fmaf(grow, away + 16.0f * c, base) : base;
   const uint32_t bits = EDGE ? prefill_bits(l, key0 + 16 * c, have >> c & 1u) : 0u;
 #pragma unroll
   for (int i = 0; i < 16; i += 4) {
-    const float2 tb = has_bias(MODE) ? __fadd2_rn(t, grow2) : t;
     float2 y, z;
-    prefill_line_4<MODE, EDGE>(x, i, key0 + 16 * c, have >> c & 1u, bits, l, t, tb, y, z);
+    prefill_line_4<MODE, EDGE>(x, i, key0 + 16 * c, have >> c & 1u, bits, l, prefill_line_at<MODE>(start, grow, i),
+                               prefill_line_at<MODE>(start, grow, i + 2), y, z);
     y.x = ex2(y.x);
     y.y = ex2(y.y);
     z.x = ex2(z.x);
@@ -428,7 +427,6 @@ __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c
     sum2 = __fadd2_rn(sum2, __fadd2_rn(y, z));
     h[8 * c + i / 2] = pack_f16x2(y.x, y.y);
     h[8 * c + i / 2 + 1] = pack_f16x2(z.x, z.y);
-    if (has_bias(MODE)) t = __fadd2_rn(tb, grow2);
   }
   return sum2;
 }
@@ -436,22 +434,20 @@ __device__ __forceinline__ float2 prefill_line_16(const uint32_t (&x)[16], int c
 template <int MODE>
 __device__ __forceinline__ float prefill_maximum_line(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
                                                       float base, float away, float grow) {
-  const float2 grow2 = make_float2(2.0f * grow, 2.0f * grow);
   float m = -INFINITY;
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
     uint32_t x[16];
     tmem_load_16cols_async(ts + 16 * c, x);
     tmem_load_wait(x);
-    float2 t = prefill_line_start<MODE>(c, base, away, grow);
+    const float start = fmaf(grow, away + 16.0f * c, base);
     const uint32_t bits = prefill_bits(l, key0 + 16 * c, have >> c & 1u);
 #pragma unroll
     for (int i = 0; i < 16; i += 4) {
-      const float2 tb = __fadd2_rn(t, grow2);
       float2 y, z;
-      prefill_line_4<MODE, true>(x, i, key0 + 16 * c, have >> c & 1u, bits, l, t, tb, y, z);
+      prefill_line_4<MODE, true>(x, i, key0 + 16 * c, have >> c & 1u, bits, l, prefill_line_at<MODE>(start, grow, i),
+                                 prefill_line_at<MODE>(start, grow, i + 2), y, z);
       m = max3(max3(m, y.x, y.y), z.x, z.y);
-      t = __fadd2_rn(tb, grow2);
     }
   }
   return m;

@@ -7,9 +7,9 @@ L = largest sum of |scale q k|, b = sum of p |bias|, bw = sum of p |bias| |v|, V
     the cap's tanh does not make that larger; the cap's own steps (an exponential, 2^-22, a
     reciprocal of a product, 2^-23 and five roundings of 2^-24, times twice the cap, and the last
     sum) add 2^-20 * cap: e_s in all;
-  * a bias, its line's start (with the reference in it, which is a logit of the row) and seven
-    steps along the line, which begins anew for every 16 keys, are roundings of 2^-24 each of
-    at most |bias| + 16 |slope| + |lse| + L + cap: 2^-20 of that for every key;
+  * a bias, the start of its line (with the reference in it, which is a logit of the row; it begins
+    anew for every 16 keys) and its value there are a few roundings of 2^-24 each of at most
+    |bias| + 16 |slope| + |lse| + L + cap: 2^-20 of that for every key is more than these;
   * p is off by the factor exp of these, and so is the sum: 2 e_s w + 2^-20 (bw + b |out|) + ...;
   * each p is rounded to 11 bits for the product with v, and where it is 2^14 times smaller than
     the largest, to 2^-25 of that: 2^-11 w + n 2^-25 V;
