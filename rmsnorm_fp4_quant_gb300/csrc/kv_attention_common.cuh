@@ -182,10 +182,11 @@ __device__ __forceinline__ float kv_logit(float s, float fac, float cap, float s
     z = __fmul_rn(s, fac);
   return has_bias(MODE) ? fmaf(-slope, fabsf(away), z) : z;
 }
-// The factor from the one that turns a product into a logit in units of log(2).
+// The factor from the one that turns a product into a logit in units of log(2) (a number: a
+// product of 0 stays one).
 template <int MODE>
 __device__ __forceinline__ float kv_factor(const KvAttentionParams& p, float fac) {
-  return has_cap(MODE) ? fac * __fdiv_rn(2.0f, p.softcap) : fac;
+  return has_cap(MODE) ? fminf(fac * __fdiv_rn(2.0f, p.softcap), 3.402823466e38f) : fac;
 }
 __device__ __forceinline__ float kv_slope(const KvAttentionParams& p, int hq) {
   return p.slopes && FP4Q_IN_RANGE(p, p.slopes + hq, 4, p.slopes, 4LL * p.Hq) ? kLog2e * __ldg(p.slopes + hq) : 0.0f;

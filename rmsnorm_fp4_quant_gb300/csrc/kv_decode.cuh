@@ -331,7 +331,8 @@ kv_decode_kernel(const KvAttentionParams p) {
     const KvSeen<MODE> seen(p, w.s, w.b);
     int lim[NT][2];
     [[maybe_unused]] int from[NT][2];            // first visible keys
-    [[maybe_unused]] float slope[NT][2], own[NT][2];   // of the distance to the token's own place
+    [[maybe_unused]] float slope[NT][2];         // of the distance to the token's own place
+    [[maybe_unused]] int own[NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -341,7 +342,7 @@ kv_decode_kernel(const KvAttentionParams p) {
         lim[n][e] = rc < rows ? seen.limit(tok) : w.s.len;
         if constexpr (MODE != kPlain) {
           from[n][e] = rc < rows ? seen.first(tok) : 0;
-          own[n][e] = static_cast<float>(off + tok);
+          own[n][e] = off + tok;
           slope[n][e] = rc < rows ? kv_slope(p, kvh * p.group + rc - tok * p.group) : 0.0f;
         }
       }
@@ -549,7 +550,7 @@ kv_decode_kernel(const KvAttentionParams p) {
             if constexpr (MODE == kPlain) {
               y[j][n][e] = fmaf(s[j][n][e], fac[n][e & 1], -ref[n][e & 1]);
             } else {                             // the logit itself in the product's place, rounded once
-              const float away = static_cast<float>(key0[j] + row_k + (e & 2)) - own[n][e & 1];
+              const float away = static_cast<float>(key0[j] - own[n][e & 1]) + static_cast<float>(row_k + (e & 2));
               s[j][n][e] = kv_logit<MODE>(s[j][n][e], fac[n][e & 1], cap, slope[n][e & 1], away);
               y[j][n][e] = __fsub_rn(s[j][n][e], ref[n][e & 1]);
             }

@@ -302,8 +302,8 @@ __device__ __forceinline__ float prefill_maximum(uint32_t ts, int key0, int lim,
 // What a row needs to turn products into logits (has_bias, has_cap): kv_logit's arguments,
 // its own place, and the keys [from, lim) that it sees.
 struct PrefillLogits {
-  float fac, cap, slope, own;
-  int from, lim;
+  float fac, cap, slope;
+  int own, from, lim;
   __device__ __forceinline__ bool sees(int key, bool page) const { return page && key < lim && key >= from; }
 };
 // (away: the distance of key0, `key` of these behind it)
@@ -318,7 +318,7 @@ template <int MODE>
 __device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
                                                           float ref, uint32_t (&h)[64]) {
   float2 sum2 = make_float2(0.0f, 0.0f);
-  const float away = static_cast<float>(key0) - l.own;
+  const float away = static_cast<float>(key0 - l.own);
 #pragma unroll
   for (int c = 0; c < 8; ++c) {
     uint32_t x[16];
@@ -340,7 +340,7 @@ __device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0,
 template <int MODE>
 __device__ __forceinline__ float prefill_maximum_by_logit(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l) {
   float m = -INFINITY;
-  const float away = static_cast<float>(key0) - l.own;
+  const float away = static_cast<float>(key0 - l.own);
 #pragma unroll 1
   for (int c = 0; c < 8; ++c) {
     uint32_t x[16];
@@ -617,16 +617,16 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     int lim_lo = ok ? lim : INT32_MAX;           // smallest of the warp's rows
     lim_lo = __reduce_min_sync(kFullMask, lim_lo);
     [[maybe_unused]] int from_hi = 0;            // largest first key of the warp's rows
-    [[maybe_unused]] float own_lo = 0.0f, own_hi = 0.0f;   // the rows' own places
+    [[maybe_unused]] int own_lo = 0, own_hi = 0; // the rows' own places
     [[maybe_unused]] PrefillLogits logits;
     const int from = ok ? seen.first(tok) : 0;   // (0 of kPlain)
     if constexpr (MODE != kPlain) from_hi = __reduce_max_sync(kFullMask, from);
     if constexpr (has_bias(MODE) || has_cap(MODE))
       logits = PrefillLogits{fac, has_cap(MODE) ? kLog2e * p.softcap : 0.0f,
-                             has_bias(MODE) && ok ? kv_slope(p, hq) : 0.0f, static_cast<float>(seen.off + tok), from, lim};
+                             has_bias(MODE) && ok ? kv_slope(p, hq) : 0.0f, seen.off + tok, from, lim};
     if constexpr (has_bias(MODE)) {
-      own_lo = static_cast<float>(__reduce_min_sync(kFullMask, ok ? seen.off + tok : INT32_MAX / 2));
-      own_hi = static_cast<float>(__reduce_max_sync(kFullMask, ok ? seen.off + tok : INT32_MIN / 2));
+      own_lo = __reduce_min_sync(kFullMask, ok ? seen.off + tok : INT32_MAX);
+      own_hi = __reduce_max_sync(kFullMask, ok ? seen.off + tok : INT32_MIN);
     }
     // a straight line of logits (prefill_weights_line) rather than products times a factor; a
     // first key that is not 0
@@ -663,7 +663,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
         const bool left = key0 + kPreKeys - 1 <= own_lo || (seen.causal && key0 >= seen.prefix);
         line = left || key0 >= own_hi;
         grow = left ? logits.slope : -logits.slope;
-        away = static_cast<float>(key0) - logits.own;
+        away = static_cast<float>(key0 - logits.own);
       }
       uint32_t h[64];
       float step_sum;

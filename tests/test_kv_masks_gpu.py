@@ -200,6 +200,15 @@ def test_caps_of_any_size(size, cap, T):
     check(q, cache, tables, [300], [0, T], "fp16", cap=cap)
 
 
+@pytest.mark.parametrize("T", [1, 200])
+def test_tiny_caps_and_huge_queries(T):
+    """Where the product's factor leaves fp32: every logit meets the cap, products of 0 stay 0."""
+    cache, tables = fill_sequences([200], 1, 64, 16, seed=5)
+    q = queries(T, 4, 64, "bf16", 7, size=1e30)
+    q[0, 1] = 0
+    check(q, cache, tables, [200], [0, T], "bf16", cap=1e-30, shapes=False)
+
+
 def test_large_logits_with_windows_and_biases():
     """References beyond 2^22, where products are rounded before a reference is taken from them."""
     cache, tables = fill_sequences([200, 77], 1, 64, 16, seed=6)

@@ -157,6 +157,25 @@ def test_everything_ends():
     check_fork(1, 64, 16, refs, tables, lens, [-1, -1], 1)
 
 
+def test_nothing_to_do():
+    """No sequences, no children, no room in a table."""
+    z = lambda *s: np.zeros(s, np.int64)                                     # noqa: E731
+    check_fork(1, 64, 16, z(5), z(0, 3), z(0), [-1, 0], 1)
+    check_fork(1, 64, 16, z(5), z(2, 0), z(2), [1, 0], 2)
+    check_fork(1, 64, 16, z(5), z(0, 3), z(0), None, 1)
+    check_fork(1, 64, 16, np.array([0, 1, 0]), np.array([[1]]), np.array([16]), [0], 0)
+    for refs, tables, lens in ((z(4), z(0, 3), z(0)), (np.array([0, 2, 0]), z(1, 0), z(1))):
+        cache = [torch.from_numpy(x).cuda() for x in random_cache(len(refs), 1, 16, 64, 1)]
+        got = fq.kv_trim_nvfp4(cache, dev(refs), dev(tables), dev(lens))
+        for a, b in zip(got, opg.trim(16, refs, tables, lens)):
+            same("trim", a, b)
+        want = opg.compact([x.cpu().numpy() for x in cache], refs, tables, lens)
+        got = fq.kv_compact_nvfp4(cache, dev(refs), dev(tables), dev(lens))
+        for a, b in zip(got[:3], want):
+            same("compact", a, b)
+        assert got[3].item() == want[3]
+
+
 def test_many_pages():
     """Pages enough for every size of the plan, free ones at the end of the pool."""
     for pages in (3000, 40000, 300000):
