@@ -33,18 +33,10 @@ constexpr int kStatusNoPages = 6;             // FP4_ERR_NO_PAGES of the C ABI
 // header; per page two lists; per child its state and its copy.
 enum : int { kWsFree = 0, kWsWanted = kPlanMostWarps, kWsHeader = 2 * kPlanMostWarps, kWsPages = kWsHeader + 32 };
 enum : int { kHeadMoves = 0 };
-struct Child {
-  int parent;     // -1: none
-  int had;        // cached tokens before,
-  int grown;      // and after
-  int wants;      // pages to take; kCopies on top if the first one is a copy of the last page
-};
+// Per child four ints: its parent (-1: none), tokens before and after, pages to take, with kCopies
+// on top if the first of these is a copy of its last page; and four of that copy: from, to (< 0:
+// none), groups of 16 tokens.
 constexpr int kCopies = 1 << 30;
-struct PageCopy {
-  int src, dst;   // dst < 0: nothing to copy
-  int groups;     // of 16 tokens
-  int pad;
-};
 __host__ __device__ inline int64_t ws_children(int64_t pages) { return kWsPages + (2 * pages + 3) / 4 * 4; }
 __host__ __device__ inline int64_t ws_copies(int64_t pages, int64_t N) { return ws_children(pages) + 4 * N; }
 
@@ -133,93 +125,130 @@ __device__ __forceinline__ int counts_before(const KvPagesParams& p, const PlanP
 // the children's to pages that they share added, the first child of every last page that is to be
 // written noted; (3) such a page stays with its first child if nobody else holds it; pages
 // wanted and free counted; (4) free pages listed, lowest first; (5) taken, child by child.
+// What a phase reads comes from L2, a microsecond's part at a time, so a thread asks for several
+// table entries at once, children are kept in every CTA's shared memory and what a warp has found
+// out stays in its registers (512 children of 65 pages each: 25 -> 19 us with the copies).
+constexpr int kPlanChildren = 2048;             // children in shared memory; further ones in the workspace
+constexpr int kPlanBatch = 4;                   // table entries of a thread on their way
+constexpr int kPlanMasks = 8;                   // times 32 pages of a warp whose free ones it remembers
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const KvPagesParams p) {
+  __shared__ int4 near_children[kPlanChildren];
   const PlanPlace w = plan_place(p.c.num_pages);
   const int64_t heirs = kWsPages, free_list = kWsPages + p.c.num_pages;
   const int64_t children = ws_children(p.c.num_pages), copies = ws_copies(p.c.num_pages, p.N);
+  const int most = static_cast<int>(p.max_pages);
   griddep_wait();
   griddep_launch_dependents();
   for (int64_t i = w.thread; i < p.c.num_pages; i += w.threads) {
     set_out_ref(p, i, page_ref(p, i));
     ws_store(p, heirs + i, kNoChild);
   }
-  const int room = static_cast<int>(p.max_pages) * p.c.page_size;
+  const int room = most * p.c.page_size;
   bool short_of = false;
-  for (int i = w.thread; i < p.N; i += w.threads) {
+  auto look_up = [&](int i) {
     int parent = i;
     if (p.parents) parent = FP4Q_IN_RANGE(p, p.parents + i, 4, p.parents, 4LL * p.N) ? __ldg(p.parents + i) : -1;
-    Child c{-1, 0, 0, 0};
+    int4 c = make_int4(-1, 0, 0, 0);                         // parent, tokens before and after, (pages wanted)
     if (parent >= 0 && parent < p.B) {
-      c.parent = parent;
-      c.had = tokens_of(p, parent);
+      c.x = parent;
+      c.y = tokens_of(p, parent);
       int more = p.new_tokens;
       if (p.new_lens)
         more = FP4Q_IN_RANGE(p, p.new_lens + i, 4, p.new_lens, 4LL * p.N) ? min(max(__ldg(p.new_lens + i), 0), more) : 0;
-      c.grown = static_cast<int>(min(static_cast<int64_t>(c.had) + more, static_cast<int64_t>(room)));
-      short_of |= c.grown < static_cast<int64_t>(c.had) + more;
+      c.z = static_cast<int>(min(static_cast<int64_t>(c.y) + more, static_cast<int64_t>(room)));
+      short_of |= c.z < static_cast<int64_t>(c.y) + more;
     }
-    ws_store4(p, children + 4LL * i, make_int4(c.parent, c.had, c.grown, 0));
-    if (FP4Q_IN_RANGE(p, p.out_lens + i, 4, p.out_lens, 4LL * p.N)) p.out_lens[i] = c.grown;
-  }
+    return c;
+  };
+  for (int i = threadIdx.x; i < min(p.N, kPlanChildren); i += kPlanThreads) near_children[i] = look_up(i);
+  for (int i = kPlanChildren + w.thread; i < p.N; i += w.threads) ws_store4(p, children + 4LL * i, look_up(i));
   plan_sync();
 
-  auto child = [&](int i) {
-    const int4 v = ws_load4(p, children + 4LL * i);
-    return Child{v.x, v.y, v.z, v.w};
-  };
-  const int64_t old_entries = p.B * p.max_pages, new_entries = p.N * p.max_pages;
-  for (int64_t e = w.thread; e < old_entries; e += w.threads) {
-    const int b = static_cast<int>(e / p.max_pages);
-    const int64_t idx = e - b * p.max_pages;
-    if (idx >= pages_of(p, tokens_of(p, b))) continue;
-    const int page = old_entry(p, b, idx);
-    if (is_page(p, page)) add_out_ref(p, page, -1);
-  }
-  for (int64_t e = w.thread; e < new_entries; e += w.threads) {
-    const int i = static_cast<int>(e / p.max_pages);
-    const int64_t idx = e - i * p.max_pages;
-    const Child c = child(i);
-    int page = -1;
-    if (idx < pages_of(p, c.had)) {
-      page = old_entry(p, c.parent, idx);
-      if (is_page(p, page)) {
-        // a page that is to be written goes to one child
-        if (idx * p.c.page_size + p.c.page_size > c.had && c.grown > c.had) {
-          if (FP4Q_IN_RANGE(p, p.ws + heirs + page, 4, p.ws, 4LL * p.ws_ints)) atomicMin(p.ws + heirs + page, i);
-        } else {
-          add_out_ref(p, page, 1);
-        }
-      }
+  auto child = [&](int i) { return i < kPlanChildren ? near_children[i] : ws_load4(p, children + 4LL * i); };
+  const int old_entries = p.B * most, new_entries = p.N * most;
+  for (int e0 = w.thread; e0 < old_entries; e0 += kPlanBatch * w.threads) {
+    int page[kPlanBatch];
+#pragma unroll
+    for (int k = 0; k < kPlanBatch; ++k) {
+      const int64_t e = e0 + static_cast<int64_t>(k) * w.threads;
+      const int b = static_cast<int>(e) / most, idx = static_cast<int>(e) - b * most;
+      page[k] = e < old_entries && idx < pages_of(p, tokens_of(p, b)) ? old_entry(p, b, idx) : -1;
     }
-    set_entry(p, p.N, e, page);
+#pragma unroll
+    for (int k = 0; k < kPlanBatch; ++k)
+      if (is_page(p, page[k])) add_out_ref(p, page[k], -1);
+  }
+  for (int e0 = w.thread; e0 < new_entries; e0 += kPlanBatch * w.threads) {
+    int page[kPlanBatch], of[kPlanBatch];
+    bool last[kPlanBatch];
+#pragma unroll
+    for (int k = 0; k < kPlanBatch; ++k) {
+      const int64_t e = e0 + static_cast<int64_t>(k) * w.threads;
+      const int i = static_cast<int>(e) / most, idx = static_cast<int>(e) - i * most;
+      page[k] = -1;
+      of[k] = i;
+      last[k] = false;
+      if (e >= new_entries) continue;
+      const int4 c = child(i);
+      if (idx < pages_of(p, c.y)) page[k] = old_entry(p, c.x, idx);
+      // a page that is to be written goes to one child
+      last[k] = static_cast<int64_t>(idx) * p.c.page_size + p.c.page_size > c.y && c.z > c.y;
+    }
+#pragma unroll
+    for (int k = 0; k < kPlanBatch; ++k) {
+      const int64_t e = e0 + static_cast<int64_t>(k) * w.threads;
+      if (e >= new_entries) continue;
+      set_entry(p, p.N, e, page[k]);
+      if (!is_page(p, page[k])) continue;
+      if (!last[k])
+        add_out_ref(p, page[k], 1);
+      else if (FP4Q_IN_RANGE(p, p.ws + heirs + page[k], 4, p.ws, 4LL * p.ws_ints))
+        atomicMin(p.ws + heirs + page[k], of[k]);
+    }
   }
   plan_sync();
 
   // free: held by nobody, and not about to stay with its first child
   auto is_free = [&](int64_t page) { return out_ref(p, page) <= 0 && ws_load(p, heirs + page) == kNoChild; };
+  uint32_t masks[kPlanMasks];                              // free pages of the warp's first ones
+  int free = 0;
+  {
+    bool here[kPlanMasks];
+#pragma unroll
+    for (int k = 0; k < kPlanMasks; ++k) here[k] = w.page0 + 32 * k + w.lane < w.page1 && is_free(w.page0 + 32 * k + w.lane);
+#pragma unroll
+    for (int k = 0; k < kPlanMasks; ++k) {
+      masks[k] = __ballot_sync(kAll, here[k]);
+      free += __popc(masks[k]);
+    }
+  }
+  for (int64_t i = w.page0 + 32 * kPlanMasks; i < w.page1; i += 32)
+    free += __popc(__ballot_sync(kAll, i + w.lane < w.page1 && is_free(i + w.lane)));
   const int run = (p.N + w.warps - 1) / w.warps;           // children of a warp
-  const int child0 = min(static_cast<int64_t>(p.N), static_cast<int64_t>(w.warp) * run);
+  const int child0 = static_cast<int>(min(static_cast<int64_t>(p.N), static_cast<int64_t>(w.warp) * run));
   const int child1 = min(p.N, child0 + run);
   int wanted = 0;
+  int4 first_child = make_int4(-1, 0, 0, 0);               // the lane's, with what it wants
   for (int i = child0 + w.lane; i < child1; i += 32) {
-    const Child c = child(i);
-    const int used = pages_of(p, c.had);
-    int wants = pages_of(p, c.grown) - used;
-    const bool part = c.had % p.c.page_size != 0 && c.grown > c.had;
-    const int last = part ? old_entry(p, c.parent, used - 1) : -1;
-    bool copy = false;
+    int4 c = child(i);
+    const int used = pages_of(p, c.y);
+    int wants = pages_of(p, c.z) - used;
+    const bool part = c.y % p.c.page_size != 0 && c.z > c.y;
+    const int last = part ? old_entry(p, c.x, used - 1) : -1;
     if (is_page(p, last)) {
-      copy = ws_load(p, heirs + last) != i || out_ref(p, last) > 0;
-      if (!copy) set_out_ref(p, last, 1);                  // no other child reads or writes it
+      const int heir = ws_load(p, heirs + last), held = out_ref(p, last);
+      if (heir != i || held > 0)
+        wants = (wants + 1) | kCopies;
+      else
+        set_out_ref(p, last, 1);                           // no other child reads or writes it
     }
-    if (FP4Q_IN_RANGE(p, p.ws + children + 4LL * i + 3, 4, p.ws, 4LL * p.ws_ints))
-      __stcg(p.ws + children + 4LL * i + 3, copy ? (wants + 1) | kCopies : wants);
-    wanted += wants + copy;
+    c.w = wants;
+    ws_store4(p, children + 4LL * i, c);
+    if (FP4Q_IN_RANGE(p, p.out_lens + i, 4, p.out_lens, 4LL * p.N)) p.out_lens[i] = c.z;
+    if (i - child0 < 32) first_child = c;
+    wanted += wants & ~kCopies;
   }
   wanted = __reduce_add_sync(kAll, wanted);
-  int free = 0;
-  for (int64_t i = w.page0; i < w.page1; i += 32)
-    free += __popc(__ballot_sync(kAll, i + w.lane < w.page1 && is_free(i + w.lane)));
   if (w.lane == 0) {
     ws_store(p, kWsFree + w.warp, free);
     ws_store(p, kWsWanted + w.warp, wanted);
@@ -229,52 +258,46 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const KvPage
   int all_free, all_wanted;
   int rank = counts_before(p, w, kWsFree, all_free);
   const int first_wanted = counts_before(p, w, kWsWanted, all_wanted);
-  for (int64_t i = w.page0; i < w.page1; i += 32) {
-    const bool here = i + w.lane < w.page1 && is_free(i + w.lane);
-    const uint32_t who = __ballot_sync(kAll, here);
+  auto list = [&](int64_t page, uint32_t who) {            // 32 pages from `page` on
     const int r = rank + __popc(who & ((1u << w.lane) - 1));
-    if (here) {
-      if (r < all_wanted) ws_store(p, free_list + r, static_cast<int>(i) + w.lane);
-      if (out_ref(p, i + w.lane) < 0) set_out_ref(p, i + w.lane, 0);
+    if (who >> w.lane & 1u) {
+      if (r < all_wanted) ws_store(p, free_list + r, static_cast<int>(page) + w.lane);
+      set_out_ref(p, page + w.lane, 0);
     }
     rank += __popc(who);
-  }
+  };
+#pragma unroll
+  for (int k = 0; k < kPlanMasks; ++k)
+    if (masks[k]) list(w.page0 + 32 * k, masks[k]);
+  for (int64_t i = w.page0 + 32 * kPlanMasks; i < w.page1; i += 32)
+    list(i, __ballot_sync(kAll, i + w.lane < w.page1 && is_free(i + w.lane)));
   short_of |= all_wanted > all_free;
   plan_sync();
 
   int at = first_wanted;
   for (int i0 = child0; i0 < child1; i0 += 32) {
     // 32 children: where each one's pages begin in the list
-    const Child mine = i0 + w.lane < child1 ? child(i0 + w.lane) : Child{-1, 0, 0, 0};
-    const int mine_wants = mine.wants & ~kCopies;
-    int incl = mine_wants;
+    const int4 none = make_int4(-1, 0, 0, 0);
+    const int4 mine = i0 == child0 ? first_child : i0 + w.lane < child1 ? ws_load4(p, children + 4LL * (i0 + w.lane)) : none;
+    int incl = mine.w & ~kCopies;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int up = __shfl_up_sync(kAll, incl, o);
       if (w.lane >= o) incl += up;
     }
-    PageCopy copy{-1, -1, 0, 0};
     for (int j = 0; j < min(32, child1 - i0); ++j) {
-      const int had = __shfl_sync(kAll, mine.had, j), parent = __shfl_sync(kAll, mine.parent, j);
-      const int wants = __shfl_sync(kAll, mine.wants, j), n = wants & ~kCopies;
+      const int parent = __shfl_sync(kAll, mine.x, j), had = __shfl_sync(kAll, mine.y, j);
+      const int wants = __shfl_sync(kAll, mine.w, j), n = wants & ~kCopies;
       const int from = at + __shfl_sync(kAll, incl, j) - n;
-      const int64_t first = pages_of(p, had) - (wants & kCopies ? 1 : 0);
+      const int first = pages_of(p, had) - (wants & kCopies ? 1 : 0);
+      int4 copy = make_int4(-1, -1, 0, 0);
       for (int x = w.lane; x < n; x += 32) {
         const int page = from + x < all_free ? ws_load(p, free_list + from + x) : -1;
-        const int64_t entry = (i0 + j) * p.max_pages + first + x;
-        if (x == 0 && (wants & kCopies)) {
-          copy.src = old_entry(p, parent, first);
-          copy.dst = page;
-          copy.groups = (had % p.c.page_size + 15) / 16;
-        }
-        set_entry(p, p.N, entry, page);
+        if (x == 0 && (wants & kCopies)) copy = make_int4(old_entry(p, parent, first), page, (had % p.c.page_size + 15) / 16, 0);
+        set_entry(p, p.N, static_cast<int64_t>(i0 + j) * most + first + x, page);
         if (page >= 0) set_out_ref(p, page, 1);
       }
-      // lane 0 holds the copy of child j: stored from there
-      if (w.lane == 0) {
-        ws_store4(p, copies + 4LL * (i0 + j), wants & kCopies ? make_int4(copy.src, copy.dst, copy.groups, 0)
-                                                             : make_int4(-1, -1, 0, 0));
-      }
+      if (w.lane == 0) ws_store4(p, copies + 4LL * (i0 + j), copy);
     }
     at += __shfl_sync(kAll, incl, 31);
   }
