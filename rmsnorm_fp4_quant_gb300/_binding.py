@@ -1128,6 +1128,19 @@ def beam_select(logits, scores, take: Optional[int] = None, finished=None, end_t
     return tuple(out)
 
 
+@functools.lru_cache(maxsize=256)
+def _pages_workspace(L, pages, N) -> int:
+    return max(L.fp4_kv_pages_workspace_bytes(pages, N), 0)
+
+
+def _i32_ptr(t, name, dev, i32, shape):
+    """_dense_ptr of an int32 tensor; what is right costs no further call (host time is what small
+    page calls take)."""
+    if t.dtype is i32 and t.shape == shape and t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr()
+    return _dense_ptr(t, name, dev, i32, shape)
+
+
 def _page_state(torch, cache, refs, tables, seq_lens):
     """(fp4_kv_cache_t, device, B, max_pages, addresses of refs, tables and seq_lens)."""
     struct, dev, _, _ = _kv_struct(torch, cache, None, None)
@@ -1135,8 +1148,8 @@ def _page_state(torch, cache, refs, tables, seq_lens):
     if tables.dim() != 2:
         raise ValueError("tables must be (B, max_pages)")
     B, most = tables.shape
-    return (struct, dev, B, most, _dense_ptr(refs, "refs", dev, i32, (struct.num_pages,)),
-            _dense_ptr(tables, "tables", dev, i32, (B, most)), _dense_ptr(seq_lens, "seq_lens", dev, i32, (B,)))
+    return (struct, dev, B, most, _i32_ptr(refs, "refs", dev, i32, (struct.num_pages,)),
+            _i32_ptr(tables, "tables", dev, i32, (B, most)), _i32_ptr(seq_lens, "seq_lens", dev, i32, (B,)))
 
 
 def kv_fork_nvfp4(cache, refs, tables, seq_lens, parents=None, new_tokens: int = 1, new_lens=None,
@@ -1166,10 +1179,10 @@ def kv_fork_nvfp4(cache, refs, tables, seq_lens, parents=None, new_tokens: int =
         if parents.dim() != 1:
             raise ValueError("parents must be (N,)")
         N = parents.shape[0]
-        par = _dense_ptr(parents, "parents", dev, i32, (N,))
+        par = _i32_ptr(parents, "parents", dev, i32, (N,))
     if new_tokens < 0:
         raise ValueError("new_tokens must not be negative")
-    more = _dense_ptr(new_lens, "new_lens", dev, i32, (N,)) if new_lens is not None else 0
+    more = _i32_ptr(new_lens, "new_lens", dev, i32, (N,)) if new_lens is not None else 0
     if out_tables is None or out_seq_lens is None or out_refs is None or out_slots is None:
         with _on(stream):
             if out_tables is None:
@@ -1180,17 +1193,16 @@ def kv_fork_nvfp4(cache, refs, tables, seq_lens, parents=None, new_tokens: int =
                 out_refs = torch.empty_like(refs)
             if out_slots is None:
                 out_slots = torch.empty(N, new_tokens, dtype=torch.int64, device=tables.device)
-    o_t = _dense_ptr(out_tables, "out_tables", dev, i32, (N, most))
-    o_l = _dense_ptr(out_seq_lens, "out_seq_lens", dev, i32, (N,))
-    o_r = _dense_ptr(out_refs, "out_refs", dev, i32, (struct.num_pages,))
+    o_t = _i32_ptr(out_tables, "out_tables", dev, i32, (N, most))
+    o_l = _i32_ptr(out_seq_lens, "out_seq_lens", dev, i32, (N,))
+    o_r = _i32_ptr(out_refs, "out_refs", dev, i32, (struct.num_pages,))
     o_s = _dense_ptr(out_slots, "out_slots", dev, torch.int64, (N, new_tokens))
     if status is not None:
         _same_device(dev, "status", status)
     status_ptr = _status_ptr(status)
     L = lib()
     handle = _kv_stream(torch, stream, dev)
-    size = max(L.fp4_kv_pages_workspace_bytes(struct.num_pages, N), 0)
-    with _Workspace(torch, workspace, size, dev, handle, stream) as ws:
+    with _Workspace(torch, workspace, _pages_workspace(L, struct.num_pages, N), dev, handle, stream) as ws:
         st = L.fp4_kv_fork_nvfp4(struct, r, t, most, l, B, par or None, more or None, N, new_tokens, o_t, o_l,
                                  o_r, o_s, ws.ptr, ws.size, status_ptr or None, 1 if pdl else 0, handle)
     if st != 0:
@@ -1210,17 +1222,17 @@ def kv_trim_nvfp4(cache, refs, tables, seq_lens, first=None, end=None, out_table
     torch = _torch()
     struct, dev, B, most, r, t, l = _page_state(torch, cache, refs, tables, seq_lens)
     i32 = torch.int32
-    f = _dense_ptr(first, "first", dev, i32, (B,)) if first is not None else 0
-    e = _dense_ptr(end, "end", dev, i32, (B,)) if end is not None else 0
+    f = _i32_ptr(first, "first", dev, i32, (B,)) if first is not None else 0
+    e = _i32_ptr(end, "end", dev, i32, (B,)) if end is not None else 0
     if out_tables is None or out_seq_lens is None or out_refs is None:
         with _on(stream):
             out_tables = torch.empty_like(tables) if out_tables is None else out_tables
             out_seq_lens = torch.empty_like(seq_lens) if out_seq_lens is None else out_seq_lens
             out_refs = torch.empty_like(refs) if out_refs is None else out_refs
     st = lib().fp4_kv_trim_nvfp4(struct, r, t, most, l, B, f or None, e or None,
-                                 _dense_ptr(out_tables, "out_tables", dev, i32, (B, most)),
-                                 _dense_ptr(out_seq_lens, "out_seq_lens", dev, i32, (B,)),
-                                 _dense_ptr(out_refs, "out_refs", dev, i32, (struct.num_pages,)),
+                                 _i32_ptr(out_tables, "out_tables", dev, i32, (B, most)),
+                                 _i32_ptr(out_seq_lens, "out_seq_lens", dev, i32, (B,)),
+                                 _i32_ptr(out_refs, "out_refs", dev, i32, (struct.num_pages,)),
                                  1 if pdl else 0, _kv_stream(torch, stream, dev))
     if st != 0:
         raise Fp4Error(st, "fp4_kv_trim_nvfp4")
@@ -1242,13 +1254,13 @@ def kv_compact_nvfp4(cache, refs, tables, seq_lens, out_tables=None, out_refs=No
             out_refs = torch.empty_like(refs) if out_refs is None else out_refs
             out_map = torch.empty_like(refs) if out_map is None else out_map
             out_live = torch.empty(1, dtype=i32, device=refs.device) if out_live is None else out_live
-    o_t = _dense_ptr(out_tables, "out_tables", dev, i32, (B, most))
-    o_r = _dense_ptr(out_refs, "out_refs", dev, i32, (pages,))
-    o_m = _dense_ptr(out_map, "out_map", dev, i32, (pages,))
-    o_n = _dense_ptr(out_live, "out_live", dev, i32, (1,))
+    o_t = _i32_ptr(out_tables, "out_tables", dev, i32, (B, most))
+    o_r = _i32_ptr(out_refs, "out_refs", dev, i32, (pages,))
+    o_m = _i32_ptr(out_map, "out_map", dev, i32, (pages,))
+    o_n = _i32_ptr(out_live, "out_live", dev, i32, (1,))
     L = lib()
     handle = _kv_stream(torch, stream, dev)
-    with _Workspace(torch, workspace, max(L.fp4_kv_pages_workspace_bytes(pages, 0), 0), dev, handle, stream) as ws:
+    with _Workspace(torch, workspace, _pages_workspace(L, pages, 0), dev, handle, stream) as ws:
         st = L.fp4_kv_compact_nvfp4(struct, r, t, most, l, B, o_t, o_r, o_m, o_n, ws.ptr, ws.size,
                                     1 if pdl else 0, handle)
     if st != 0:

@@ -121,6 +121,44 @@ __device__ __forceinline__ int counts_before(const KvPagesParams& p, const PlanP
 }
 
 // --- fork -----------------------------------------------------------------------
+__device__ __forceinline__ void copy16(const KvPagesParams& p, uint8_t* base, int64_t src, int64_t dst, long long extent) {
+  if (FP4Q_IN_RANGE(p, base + src, 16, base, extent) && FP4Q_IN_RANGE(p, base + dst, 16, base, extent))
+    *reinterpret_cast<uint4*>(base + dst) = *reinterpret_cast<const uint4*>(base + src);
+}
+// The tokens of a last page that a child has copied, one head: by threads tid, tid + threads ...
+__device__ __forceinline__ void fork_copy(const KvPagesParams& p, const int4& m, int head, int tid, int threads) {
+  const int src = m.x, dst = m.y, groups = m.z;
+  if (dst < 0) return;
+  const int D = p.c.D, page = p.c.page_size;
+  const long long codes = kv_packed_extent(p.c), scales = kv_sf_extent(p.c);
+  const int64_t a = static_cast<int64_t>(src) * p.c.heads + head, b = static_cast<int64_t>(dst) * p.c.heads + head;
+  const int64_t page_codes = static_cast<int64_t>(page) * (D / 2), page_sf = static_cast<int64_t>(page) * (D / 16);
+  for (int x = tid; x < groups * (D / 2); x += threads) {            // 16 bytes of 16 tokens' D / 2 each
+    copy16(p, p.c.k_packed, a * page_codes + 16 * x, b * page_codes + 16 * x, codes);
+    copy16(p, p.c.v_packed, a * page_codes + 16 * x, b * page_codes + 16 * x, codes);
+  }
+  for (int x = tid; x < groups * (D / 16); x += threads) {
+    copy16(p, p.c.k_sf, a * page_sf + 16 * x, b * page_sf + 16 * x, scales);
+    const int block = x / groups, g = x - block * groups;            // the values' scales: tokens side by side
+    const int64_t o = static_cast<int64_t>(block) * page + 16 * g;
+    copy16(p, p.c.v_sf, a * page_sf + o, b * page_sf + o, scales);
+  }
+}
+// The slots of a child's new tokens.
+__device__ __forceinline__ void fork_slots(const KvPagesParams& p, int i, int had, int grown, int tid, int threads) {
+  for (int x = tid; x < p.new_tokens; x += threads) {
+    const int64_t pos = static_cast<int64_t>(had) + x;
+    int64_t slot = -1;
+    if (pos < grown) {
+      const int32_t* e = p.out_tables + i * p.max_pages + pos / p.c.page_size;
+      const int page = FP4Q_IN_RANGE(p, e, 4, p.out_tables, 4LL * p.N * p.max_pages) ? __ldcg(e) : -1;
+      if (is_page(p, page)) slot = static_cast<int64_t>(page) * p.c.page_size + pos % p.c.page_size;
+    }
+    int64_t* out = p.out_slots + static_cast<int64_t>(i) * p.new_tokens + x;
+    if (FP4Q_IN_RANGE(p, out, 8, p.out_slots, 8LL * p.N * p.new_tokens)) *out = slot;
+  }
+}
+
 // Phases: (1) counts copied, children's lengths; (2) the old sequences' references dropped,
 // the children's to pages that they share added, the first child of every last page that is to be
 // written noted; (3) such a page stays with its first child if nobody else holds it; pages
@@ -131,6 +169,8 @@ __device__ __forceinline__ int counts_before(const KvPagesParams& p, const PlanP
 constexpr int kPlanChildren = 2048;             // children in shared memory; further ones in the workspace
 constexpr int kPlanBatch = 4;                   // table entries of a thread on their way
 constexpr int kPlanMasks = 8;                   // times 32 pages of a warp whose free ones it remembers
+// COPY: the plan's CTAs make the copies and slots themselves.
+template <bool COPY>
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const KvPagesParams p) {
   __shared__ int4 near_children[kPlanChildren];
   const PlanPlace w = plan_place(p.c.num_pages);
@@ -302,50 +342,32 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const KvPage
     at += __shfl_sync(kAll, incl, 31);
   }
   if (p.status && __any_sync(kAll, short_of) && w.lane == 0) atomicExch(p.status, kStatusNoPages);
+  if constexpr (COPY) {
+    plan_sync();
+    for (int x = w.warp; x < p.N * p.c.heads; x += w.warps) {
+      const int i = x / p.c.heads, head = x - i * p.c.heads;
+      const int4 m = ws_load4(p, copies + 4LL * i);
+      if (head == 0) {
+        const int4 c = ws_load4(p, children + 4LL * i);
+        fork_slots(p, i, c.y, c.z, w.lane, 32);
+      }
+      fork_copy(p, m, head, w.lane, 32);
+    }
+  }
 }
 
-__device__ __forceinline__ void copy16(const KvPagesParams& p, uint8_t* base, int64_t src, int64_t dst, long long extent) {
-  if (FP4Q_IN_RANGE(p, base + src, 16, base, extent) && FP4Q_IN_RANGE(p, base + dst, 16, base, extent))
-    *reinterpret_cast<uint4*>(base + dst) = *reinterpret_cast<const uint4*>(base + src);
-}
-
-// The tokens of a last page that a child has copied, a head per CTA, and the child's slots.
+// The rest of a larger fork: pages, a head per CTA, and slots.
 constexpr int kForkThreads = 128;
 __global__ void __launch_bounds__(kForkThreads) kv_fork_copy_kernel(const KvPagesParams p) {
   const int i = blockIdx.x, head = blockIdx.y, tid = threadIdx.x;
   griddep_wait();
   griddep_launch_dependents();
+  const int4 m = ws_load4(p, ws_copies(p.c.num_pages, p.N) + 4LL * i);
   if (head == 0 && p.new_tokens > 0) {
     const int4 c = ws_load4(p, ws_children(p.c.num_pages) + 4LL * i);
-    for (int x = tid; x < p.new_tokens; x += kForkThreads) {
-      const int64_t pos = static_cast<int64_t>(c.y) + x;
-      int64_t slot = -1;
-      if (pos < c.z) {
-        const int32_t* e = p.out_tables + i * p.max_pages + pos / p.c.page_size;
-        const int page = FP4Q_IN_RANGE(p, e, 4, p.out_tables, 4LL * p.N * p.max_pages) ? *e : -1;
-        if (is_page(p, page)) slot = static_cast<int64_t>(page) * p.c.page_size + pos % p.c.page_size;
-      }
-      int64_t* out = p.out_slots + static_cast<int64_t>(i) * p.new_tokens + x;
-      if (FP4Q_IN_RANGE(p, out, 8, p.out_slots, 8LL * p.N * p.new_tokens)) *out = slot;
-    }
+    fork_slots(p, i, c.y, c.z, tid, kForkThreads);
   }
-  const int4 m = ws_load4(p, ws_copies(p.c.num_pages, p.N) + 4LL * i);
-  const int src = m.x, dst = m.y, groups = m.z;
-  if (dst < 0) return;
-  const int D = p.c.D, page = p.c.page_size;
-  const long long codes = kv_packed_extent(p.c), scales = kv_sf_extent(p.c);
-  const int64_t a = static_cast<int64_t>(src) * p.c.heads + head, b = static_cast<int64_t>(dst) * p.c.heads + head;
-  const int64_t page_codes = static_cast<int64_t>(page) * (D / 2), page_sf = static_cast<int64_t>(page) * (D / 16);
-  for (int x = tid; x < groups * (D / 2); x += kForkThreads) {       // 16 bytes of 16 tokens' D / 2 each
-    copy16(p, p.c.k_packed, a * page_codes + 16 * x, b * page_codes + 16 * x, codes);
-    copy16(p, p.c.v_packed, a * page_codes + 16 * x, b * page_codes + 16 * x, codes);
-  }
-  for (int x = tid; x < groups * (D / 16); x += kForkThreads) {
-    copy16(p, p.c.k_sf, a * page_sf + 16 * x, b * page_sf + 16 * x, scales);
-    const int block = x / groups, g = x - block * groups;            // the values' scales: tokens side by side
-    const int64_t o = static_cast<int64_t>(block) * page + 16 * g;
-    copy16(p, p.c.v_sf, a * page_sf + o, b * page_sf + o, scales);
-  }
+  fork_copy(p, m, head, tid, kForkThreads);
 }
 
 // --- trim -----------------------------------------------------------------------
@@ -496,18 +518,19 @@ unsigned plan_ctas(int64_t work) { return work <= 4 * kPlanThreads ? 1 : work <=
 cudaError_t launch_plan(void (*kernel)(KvPagesParams), unsigned ctas, const KvPagesParams& p, int pdl,
                         cudaStream_t stream) {
   cudaLaunchAttribute attr[2];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = ctas;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
-  attr[1].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-  attr[1].val.programmaticStreamSerializationAllowed = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = pdl ? 1 : 0;
+  attr[1].id = cudaLaunchAttributeClusterDimension;
+  attr[1].val.clusterDim.x = ctas;
+  attr[1].val.clusterDim.y = 1;
+  attr[1].val.clusterDim.z = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(ctas);
   cfg.blockDim = dim3(kPlanThreads);
   cfg.stream = stream;
-  cfg.attrs = attr;
-  cfg.numAttrs = pdl ? 2 : 1;
+  // (a CTA alone is a cluster of its own without being told so)
+  cfg.attrs = ctas > 1 || pdl ? attr : nullptr;
+  cfg.numAttrs = ctas > 1 ? 2 : pdl ? 1 : 0;
   return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 cudaError_t launch_after(void (*kernel)(KvPagesParams), dim3 grid, int threads, const KvPagesParams& p,
@@ -528,9 +551,17 @@ cudaError_t launch_after(void (*kernel)(KvPagesParams), dim3 grid, int threads, 
 
 int64_t kv_pages_workspace(int64_t num_pages, int64_t N) { return ws_copies(num_pages, N) + 4 * N; }
 
+// A fork whose plan is one CTA and whose copies (a page a child at most) are no more than this
+// makes them there: 4 children of 16-token pages 18.2 -> 14.4 us; with 0.7 MB one CTA takes 20 us
+// for what 140 do in 4.
+constexpr int64_t kForkOwnCopies = 64 << 10;
+
 cudaError_t launch_kv_fork(const KvPagesParams& p, int pdl, cudaStream_t stream) {
-  const cudaError_t e = launch_plan(kv_fork_plan_kernel, plan_ctas(p.c.num_pages + (p.B + static_cast<int64_t>(p.N)) * p.max_pages),
-                                    p, pdl, stream);
+  const unsigned ctas = plan_ctas(p.c.num_pages + (p.B + static_cast<int64_t>(p.N)) * p.max_pages);
+  const int64_t page_bytes = 18LL * p.c.heads * p.c.page_size * p.c.D / 16;
+  if (ctas == 1 && p.N * page_bytes <= kForkOwnCopies && static_cast<int64_t>(p.N) * p.new_tokens <= 4096)
+    return launch_plan(kv_fork_plan_kernel<true>, ctas, p, pdl, stream);
+  const cudaError_t e = launch_plan(kv_fork_plan_kernel<false>, ctas, p, pdl, stream);
   if (e != cudaSuccess || p.N == 0) return e;
   return launch_after(kv_fork_copy_kernel, dim3(static_cast<unsigned>(p.N), static_cast<unsigned>(p.c.heads)),
                       kForkThreads, p, stream);
