@@ -23,6 +23,10 @@
 // reference r and the sum l, fp32) in the workspace and a second, small
 // kernel joins the parts in order.
 //
+// With a window, an item's units begin with the first that one of its sequence's rows sees.  A
+// cap and a bias are taken in place of the product (MODE, KvLogits): 16 sequences of 12-16 K tokens,
+// 40 query and 8 key/value heads of 128, 58 us without, 62 with a bias, 64 with a cap.
+//
 // A CTA is 4 warps, each with its own 16 keys of a unit, its own r, l and O, and
 // its own ring of tiles in shared memory that cp.async fills ahead (a tile: 16
 // keys' codes and scales, 18 D bytes); no barrier in the loop.

@@ -165,14 +165,16 @@ __device__ __forceinline__ void fork_slots(const KvPagesParams& p, int i, int ha
 // wanted and free counted; (4) free pages listed, lowest first; (5) taken, child by child.
 // What a phase reads comes from L2, a microsecond's part at a time, so a thread asks for several
 // table entries at once, children are kept in every CTA's shared memory and what a warp has found
-// out stays in its registers (512 children of 65 pages each: 25 -> 19 us with the copies).
+// out stays in its registers (512 children of 65 pages each: the plan takes 16.5 us, 21
+// with an entry a thread at a time and all counts by atomics).
 constexpr int kPlanChildren = 2048;             // children in shared memory; further ones in the workspace
-constexpr int kPlanBatch = 4;                   // table entries of a thread on their way
 constexpr int kPlanMasks = 8;                   // times 32 pages of a warp whose free ones it remembers
 // COPY: the plan's CTAs make the copies and slots themselves.
 template <bool COPY>
 __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const KvPagesParams p) {
   __shared__ int4 near_children[kPlanChildren];
+  __shared__ int kids[kPlanChildren];            // of an old sequence: children, and 2^16 times those that grow
+  const bool counted = p.N <= kPlanChildren && p.B <= kPlanChildren;
   const PlanPlace w = plan_place(p.c.num_pages);
   const int64_t heirs = kWsPages, free_list = kWsPages + p.c.num_pages;
   const int64_t children = ws_children(p.c.num_pages), copies = ws_copies(p.c.num_pages, p.N);
@@ -200,50 +202,57 @@ __global__ void __launch_bounds__(kPlanThreads) kv_fork_plan_kernel(const KvPage
     }
     return c;
   };
-  for (int i = threadIdx.x; i < min(p.N, kPlanChildren); i += kPlanThreads) near_children[i] = look_up(i);
+  if (counted) {
+    for (int b = threadIdx.x; b < p.B; b += kPlanThreads) kids[b] = 0;
+    __syncthreads();
+  }
+  for (int i = threadIdx.x; i < min(p.N, kPlanChildren); i += kPlanThreads) {
+    const int4 c = look_up(i);
+    near_children[i] = c;
+    if (counted && c.x >= 0) atomicAdd(&kids[c.x], c.z > c.y ? 65537 : 1);
+  }
   for (int i = kPlanChildren + w.thread; i < p.N; i += w.threads) ws_store4(p, children + 4LL * i, look_up(i));
   plan_sync();
 
   auto child = [&](int i) { return i < kPlanChildren ? near_children[i] : ws_load4(p, children + 4LL * i); };
-  const int old_entries = p.B * most, new_entries = p.N * most;
-  for (int e0 = w.thread; e0 < old_entries; e0 += kPlanBatch * w.threads) {
-    int page[kPlanBatch];
+  // a warp takes 128 entries of a row: what the row decides is looked up once for them
+  const int pages = static_cast<int>(p.c.num_pages);
+  const int segs = (most + 127) / 128;
+  for (int u = w.warp; u < p.B * segs; u += w.warps) {
+    const int b = u / segs, from = (u - b * segs) * 128 + w.lane;
+    const int len = tokens_of(p, b), used = pages_of(p, len);
+    // what the sequence gives up, and, where they were counted, what its children take on; a last
+    // page that is not full is taken on by those that do not write it
+    const int all = counted ? (kids[b] & 0xffff) - 1 : -1, last = counted ? all - (kids[b] >> 16) : -1;
+    int page[4];
 #pragma unroll
-    for (int k = 0; k < kPlanBatch; ++k) {
-      const int64_t e = e0 + static_cast<int64_t>(k) * w.threads;
-      const int b = static_cast<int>(e) / most, idx = static_cast<int>(e) - b * most;
-      page[k] = e < old_entries && idx < pages_of(p, tokens_of(p, b)) ? old_entry(p, b, idx) : -1;
+    for (int k = 0; k < 4; ++k) page[k] = from + 32 * k < used ? old_entry(p, b, from + 32 * k) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int by = from + 32 * k == used - 1 && len % p.c.page_size ? last : all;
+      if (by && page[k] >= 0 && page[k] < pages) add_out_ref(p, page[k], by);
     }
-#pragma unroll
-    for (int k = 0; k < kPlanBatch; ++k)
-      if (is_page(p, page[k])) add_out_ref(p, page[k], -1);
   }
-  for (int e0 = w.thread; e0 < new_entries; e0 += kPlanBatch * w.threads) {
-    int page[kPlanBatch], of[kPlanBatch];
-    bool last[kPlanBatch];
+  for (int u = w.warp; u < p.N * segs; u += w.warps) {
+    const int i = u / segs, from = (u - i * segs) * 128 + w.lane;
+    const int4 c = child(i);
+    const int used = pages_of(p, c.y);
+    // a page that is to be written goes to one child
+    const int written = c.z > c.y && c.y % p.c.page_size ? used - 1 : -1;
+    int page[4];
 #pragma unroll
-    for (int k = 0; k < kPlanBatch; ++k) {
-      const int64_t e = e0 + static_cast<int64_t>(k) * w.threads;
-      const int i = static_cast<int>(e) / most, idx = static_cast<int>(e) - i * most;
-      page[k] = -1;
-      of[k] = i;
-      last[k] = false;
-      if (e >= new_entries) continue;
-      const int4 c = child(i);
-      if (idx < pages_of(p, c.y)) page[k] = old_entry(p, c.x, idx);
-      // a page that is to be written goes to one child
-      last[k] = static_cast<int64_t>(idx) * p.c.page_size + p.c.page_size > c.y && c.z > c.y;
-    }
+    for (int k = 0; k < 4; ++k) page[k] = from + 32 * k < used ? old_entry(p, c.x, from + 32 * k) : -1;
 #pragma unroll
-    for (int k = 0; k < kPlanBatch; ++k) {
-      const int64_t e = e0 + static_cast<int64_t>(k) * w.threads;
-      if (e >= new_entries) continue;
-      set_entry(p, p.N, e, page[k]);
-      if (!is_page(p, page[k])) continue;
-      if (!last[k])
-        add_out_ref(p, page[k], 1);
-      else if (FP4Q_IN_RANGE(p, p.ws + heirs + page[k], 4, p.ws, 4LL * p.ws_ints))
-        atomicMin(p.ws + heirs + page[k], of[k]);
+    for (int k = 0; k < 4; ++k) {
+      const int idx = from + 32 * k;
+      if (idx >= most) continue;
+      set_entry(p, p.N, static_cast<int64_t>(i) * most + idx, page[k]);
+      if (page[k] < 0 || page[k] >= pages) continue;
+      if (idx != written) {
+        if (!counted) add_out_ref(p, page[k], 1);
+      } else if (FP4Q_IN_RANGE(p, p.ws + heirs + page[k], 4, p.ws, 4LL * p.ws_ints)) {
+        atomicMin(p.ws + heirs + page[k], i);
+      }
     }
   }
   plan_sync();
@@ -390,19 +399,26 @@ __global__ void __launch_bounds__(kPlanThreads) kv_trim_kernel(const KvPagesPara
     range(b, first, end);
     if (FP4Q_IN_RANGE(p, p.out_lens + b, 4, p.out_lens, 4LL * p.B)) p.out_lens[b] = end;
   }
-  const int64_t entries = p.B * p.max_pages;
-  for (int64_t e = w.thread; e < entries; e += w.threads) {
-    const int b = static_cast<int>(e / p.max_pages);
-    const int64_t idx = e - b * p.max_pages;
+  const int most = static_cast<int>(p.max_pages), segs = (most + 127) / 128;
+  for (int u = w.warp; u < p.B * segs; u += w.warps) {     // a warp takes 128 entries of a row
+    const int b = u / segs, from = (u - b * segs) * 128 + w.lane;
     int first, end;
-    const int n = range(b, first, end);
-    int page = idx < pages_of(p, n) ? old_entry(p, b, idx) : -1;
-    if (!is_page(p, page)) page = -1;
-    if (page >= 0 && (idx < first / p.c.page_size || idx >= pages_of(p, end))) {
-      add_out_ref(p, page, -1);
-      page = -1;
+    const int used = pages_of(p, range(b, first, end));
+    const int keep0 = first / p.c.page_size, keep1 = pages_of(p, end);
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = from + 32 * k < used ? old_entry(p, b, from + 32 * k) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int idx = from + 32 * k;
+      if (idx >= most) continue;
+      if (!is_page(p, page[k])) page[k] = -1;
+      if (page[k] >= 0 && (idx < keep0 || idx >= keep1)) {
+        add_out_ref(p, page[k], -1);
+        page[k] = -1;
+      }
+      set_entry(p, p.B, static_cast<int64_t>(b) * most + idx, page[k]);
     }
-    set_entry(p, p.B, e, page);
   }
 }
 
@@ -457,16 +473,21 @@ __global__ void __launch_bounds__(kPlanThreads) kv_compact_plan_kernel(const KvP
   }
   plan_sync();
 
-  const int64_t entries = p.B * p.max_pages;
-  for (int64_t e = w.thread; e < entries; e += w.threads) {
-    const int b = static_cast<int>(e / p.max_pages);
-    const int64_t idx = e - b * p.max_pages;
-    int page = idx < pages_of(p, tokens_of(p, b)) ? old_entry(p, b, idx) : -1;
-    if (is_page(p, page))
-      page = FP4Q_IN_RANGE(p, p.out_map + page, 4, p.out_map, 4LL * p.c.num_pages) ? __ldcg(p.out_map + page) : -1;
-    else
-      page = -1;
-    set_entry(p, p.B, e, page);
+  const int most = static_cast<int>(p.max_pages), segs = (most + 127) / 128;
+  for (int u = w.warp; u < p.B * segs; u += w.warps) {     // a warp takes 128 entries of a row
+    const int b = u / segs, from = (u - b * segs) * 128 + w.lane;
+    const int used = pages_of(p, tokens_of(p, b));
+    int page[4];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) page[k] = from + 32 * k < used ? old_entry(p, b, from + 32 * k) : -1;
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool here = is_page(p, page[k]) && FP4Q_IN_RANGE(p, p.out_map + page[k], 4, p.out_map, 4LL * p.c.num_pages);
+      page[k] = here ? __ldcg(p.out_map + page[k]) : -1;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+      if (from + 32 * k < most) set_entry(p, p.B, static_cast<int64_t>(b) * most + from + 32 * k, page[k]);
   }
 }
 

@@ -33,6 +33,15 @@
 // the tensor cores' full rate, no less would; two tiles per CTA fill tensor
 // memory (512 columns at D = 128) and share every conversion.
 //
+// Windows, prefixes, biases and caps (MODE, KvLogits).  A row sees a run of keys, [first, limit),
+// and an item takes the steps that one of its rows has keys in.  A window or a prefix alone only
+// changes the masks.  A bias is a straight line on either side of a row's own place: one
+// more multiply-add a pair of keys (a prompt of 4096, 32 heads of 128, logits of deviation 2: 163 us,
+// 126 without), and the keys are taken from the last to the first.  A cap is three special
+// functions instead of one, two reciprocals in one of them (213 us; logits of deviation 9: 229, of
+// which the maximum moves more often, 181 without a cap): 13 instructions a logit, against 8, bound
+// these steps (an exponential in polynomials instead of the special function: 238 and more).
+//
 // Every wait is bounded.  A role whose wait runs out stops and the others' waits
 // run out after it; the rows not finished by then are written as NaN, the status
 // word (if any) set, and tensor memory freed once the products issued so far have

@@ -102,6 +102,8 @@ FORKS = [
     (130, 900, 32, 257, 1, 1, 64, 400),
     (6, 40000, 16, 17, 1, 1, 64, 30),
     (3, 50, 16, 1100, 1, 1, 64, 1200),
+    (5, 40, 16, 3000, 1, 1, 64, 3100),                          # more children than shared memory keeps,
+    (2200, 30, 16, 2200, 1, 1, 64, 2300),                       # and more sequences
 ]
 
 
