@@ -75,6 +75,7 @@ from ._binding import (  # noqa: F401
     fp4_kv_fork_nvfp4,
     fp4_kv_gather_nvfp4,
     fp4_kv_pages_workspace_bytes,
+    fp4_kv_read_status,
     fp4_kv_trim_nvfp4,
     kv_append_nvfp4,
     kv_cache_nvfp4,

@@ -160,6 +160,10 @@ def _open(path: str, how: str) -> ctypes.CDLL:
     L.fp4_kv_trim_nvfp4.restype = ci
     L.fp4_kv_compact_nvfp4.argtypes = [cp, vp, vp, i64, vp, i64, vp, vp, vp, vp, vp, i64, ci, vp]
     L.fp4_kv_compact_nvfp4.restype = ci
+    L.fp4_kv_read_status.argtypes = [vp, vp]
+    L.fp4_kv_read_status.restype = ci
+    L.fp4_kv_status_string.argtypes = [ci]
+    L.fp4_kv_status_string.restype = ctypes.c_char_p
     L.fp4_kv_pages_workspace_bytes.argtypes = [i64, i64]
     L.fp4_kv_pages_workspace_bytes.restype = i64
     L.fp4_beam_select.argtypes = [vp, i64, ci, vp, vp, i64, i64, i64, i64, i64, vp, vp, vp, vp, vp,
@@ -372,6 +376,10 @@ def fp4_beam_select_workspace_bytes(B: int, K: int, V: int, n: int, dtype: int) 
     return lib().fp4_beam_select_workspace_bytes(B, K, V, n, dtype)
 
 
+def fp4_kv_read_status(status_ptr: int, stream: int) -> int:
+    return lib().fp4_kv_read_status(status_ptr or None, stream or None)
+
+
 def fp4_read_device_status(status_ptr: int, stream: int) -> int:
     return lib().fp4_read_device_status(status_ptr or None, stream or None)
 
@@ -391,7 +399,7 @@ def fp4_sf_size_bytes(M: int, H: int, fmt: int, layout: int) -> int:
 
 
 def fp4_status_string(status: int) -> str:
-    return lib().fp4_status_string(status).decode()
+    return lib().fp4_kv_status_string(status).decode()     # (the same, and FP4_ERR_NO_PAGES)
 
 
 def fp4_last_cuda_error() -> int:
@@ -524,9 +532,9 @@ def _status_ptr(status) -> int:
 def read_device_status(status, stream=None) -> int:
     """Synchronises the stream and returns the device status word as a status
     code (FP4_OK, FP4_ERR_TIMEOUT or FP4_ERR_NO_PAGES)."""
-    st = fp4_read_device_status(_status_ptr(status), _stream_handle(stream))
+    st = fp4_kv_read_status(_status_ptr(status), _stream_handle(stream))
     if st not in (FP4_OK, FP4_ERR_TIMEOUT, FP4_ERR_NO_PAGES):
-        raise Fp4Error(st, "fp4_read_device_status")
+        raise Fp4Error(st, "fp4_kv_read_status")
     return st
 
 
@@ -1061,7 +1069,7 @@ def _current(torch, t, name):
 
 
 @functools.lru_cache(maxsize=256)
-def _beam_workspace(L, B, K, V, n, dt) -> int:
+def _beam_workspace(L, dev, B, K, V, n, dt) -> int:
     return max(L.fp4_beam_select_workspace_bytes(B, K, V, n, dt), 0)
 
 
@@ -1120,7 +1128,7 @@ def beam_select(logits, scores, take: Optional[int] = None, finished=None, end_t
     o_f = _dense_ptr(out[3], "out[3]", dev, torch.bool, shape) if finished is not None else 0
     L = lib()
     handle = _kv_stream(torch, stream, dev)
-    with _Workspace(torch, workspace, _beam_workspace(L, B, K, V, n, dt), dev, handle, stream) as ws:
+    with _Workspace(torch, workspace, _beam_workspace(L, dev, B, K, V, n, dt), dev, handle, stream) as ws:
         st = L.fp4_beam_select(logits.data_ptr(), sk, dt, score_ptr, done or None, end_token, B, K, V, n,
                                o_s, o_p, o_t, o_f or None, ws.ptr, ws.size, 1 if pdl else 0, handle)
     if st != 0:

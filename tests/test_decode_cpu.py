@@ -186,3 +186,11 @@ def test_tensor_calls_refuse_cpu_tensors():
     for call in (fq.kv_fork_nvfp4, fq.kv_trim_nvfp4, fq.kv_compact_nvfp4):
         with pytest.raises(ValueError):
             call(c, i, i[None], i[:1])
+
+
+def test_statuses_of_the_pages_are_read_with_their_own_call():
+    assert fq.fp4_kv_read_status(0, 0) == fq.FP4_ERR_INVALID_ARG
+    assert fq.fp4_kv_read_status(0x10002, 0) == fq.FP4_ERR_INVALID_ARG
+    # every other status has the name that it has everywhere
+    for status in (0, 1, 2, 3, 4, 5, 99):
+        assert fq.lib().fp4_kv_status_string(status) == fq.lib().fp4_status_string(status)
