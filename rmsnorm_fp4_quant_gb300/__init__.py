@@ -21,9 +21,13 @@ operands, any K that is a multiple of 32), with ``fp4_gemm_variant`` and
 The paged key/value cache holds attention's keys and values in the same NVFP4
 blocks: ``kv_cache_nvfp4`` makes one, ``kv_append_nvfp4`` rotates queries and keys
 and stores the tokens, ``kv_gather_nvfp4`` reads slots back and
-``attention_nvfp4`` attends over the cached sequences of a batch.
+``attention_nvfp4`` attends over the cached sequences of a batch (with capped logits,
+distance biases, windows and prefixes where asked).  Between two tokens ``beam_select``
+takes the best continuations of every beam search, ``kv_fork_nvfp4`` continues
+sequences by their children, ``kv_trim_nvfp4`` gives up tokens and ``kv_compact_nvfp4``
+moves the pages that are held together.
 Kernels that wait on asynchronous copies bound every wait; a call given a
-device ``status`` word learns of a wait that ran out (``read_device_status``).
+device ``status`` word learns of a wait that ran out, or of pages that did (``read_device_status``).
 """
 from ._binding import (  # noqa: F401
     FP4_DT_BF16,
