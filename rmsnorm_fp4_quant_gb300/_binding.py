@@ -1118,7 +1118,7 @@ def beam_select(logits, scores, take: Optional[int] = None, finished=None, end_t
     if out is None:
         with _on(stream):
             out = [torch.empty(B, n, dtype=t, device=logits.device)
-                   for t in (torch.float32, torch.int32, torch.int32) + ((torch.bool,) if done else ())]
+                   for t in (torch.float32, torch.int32, torch.int32) + ((torch.bool,) if finished is not None else ())]
     elif len(out) != (4 if finished is not None else 3):
         raise ValueError("out must be (scores, parents, tokens), and finished with finished")
     shape = (B, n)

@@ -200,6 +200,13 @@ def test_offsets_beyond_32_bits():
     assert abs(s[0, 0].item() - (-1 + 9 - total)) < 2e-3          # (65536 sums of a part's 32768 groups: 2^-24 each)
 
 
+def test_an_empty_batch():
+    for done in (None, torch.zeros(0, 4, dtype=torch.bool, device="cuda")):
+        got = fq.beam_select(torch.zeros(0, 4, 100, device="cuda"), torch.zeros(0, 4, device="cuda"), take=3, finished=done)
+        torch.cuda.synchronize()
+        assert len(got) == (3 if done is None else 4) and all(t.shape == (0, 3) for t in got)
+
+
 def test_refusals():
     x, scores, done = inputs(2, 3, 100, "bf16", seed=1, finished=True)
     dx, ds, dd = x.cuda(), scores.cuda(), done.cuda()
