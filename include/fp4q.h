@@ -670,7 +670,8 @@ FP4Q_API int64_t fp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t N);
  *   scores         [B, K] fp32.  A beam whose score is not finite has no candidates (dead beams, and
  *                  all but one at the start: -infinity), nor has one with a logit that is NaN or
  *                  above 2^125.  A logit of at most -2^125 (a mask of -infinity or of the type's lowest
- *                  value) is no candidate and adds nothing to the sum.
+ *                  value) is no candidate and adds nothing to the sum.  Between these they may lie
+ *                  anywhere: tokens filled with -1e10 or -1e30, rows that are all as far from 0.
  *   finished       [B, K] bytes or NULL: a beam with a nonzero byte has ended; its one candidate
  *                  is end_token with its score as it is, whatever its logits are.
  *   end_token      in [0, V).

@@ -9,14 +9,19 @@ import numpy as np
 LOWEST = -2.0 ** 125          # logits up to here are no candidates and add nothing to a sum
 
 
-def log_sum(x) -> float:
-    """log(sum(exp(x))) of one row; NaN where the row has no candidates."""
+def sum_against_largest(x):
+    """(largest, log(sum(exp(x - largest)))) of one row; NaN where the row has no candidates."""
     x = np.asarray(x, np.float64)
     x = np.where(x <= LOWEST, -np.inf, x)
     if np.any(np.isnan(x)) or np.any(x > -LOWEST) or not np.any(x > -np.inf):
-        return np.nan
+        return np.nan, np.nan
     top = x.max()
-    return float(top + np.log(np.exp(x - top).sum()))
+    return float(top), float(np.log(np.exp(x - top).sum()))
+
+
+def log_sum(x) -> float:
+    """log(sum(exp(x))) of one row; NaN where the row has no candidates."""
+    return float(sum(sum_against_largest(x)))
 
 
 def select(logits, scores, n, finished=None, end_token=0):
@@ -37,12 +42,12 @@ def select(logits, scores, n, finished=None, end_token=0):
             if finished is not None and finished[b, k]:
                 cand.append((s, k, 0, end_token))
                 continue
-            total = log_sum(logits[b, k])
+            top, total = sum_against_largest(logits[b, k])
             if np.isnan(total):
                 continue
             row = logits[b, k]
             order = np.lexsort((np.arange(V), -row))[: n + 1]
-            cand += [(s + (row[v] - total), k, i, int(v)) for i, v in enumerate(order) if row[v] > LOWEST]
+            cand += [(s + ((row[v] - top) - total), k, i, int(v)) for i, v in enumerate(order) if row[v] > LOWEST]
         cand.sort(key=lambda c: (-c[0], c[1], c[2]))
         for i, (s, k, _, v) in enumerate(cand[:n]):
             out[0][b, i], out[1][b, i], out[2][b, i] = s, b * K + k, v
