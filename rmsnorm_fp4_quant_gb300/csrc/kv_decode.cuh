@@ -353,6 +353,7 @@ kv_decode_kernel(const KvAttentionParams p) {
     const int last = min(r0 + ROWS, rows) - 1;
     const int lim_lo = MODE != kPlain ? seen.limit(r0 / p.group) : p.causal ? off + r0 / p.group + 1 : w.s.len;
     const int lim_hi = MODE != kPlain ? seen.limit(last / p.group) : p.causal ? off + last / p.group + 1 : w.s.len;
+    const int from_lo = MODE != kPlain ? seen.first(r0 / p.group) : 0;
     const int from_hi = MODE != kPlain ? seen.first(last / p.group) : 0;
 
     // --- the ring: tile x of this warp is keys key0(x) ... + 15
@@ -369,7 +370,9 @@ kv_decode_kernel(const KvAttentionParams p) {
     auto look_up = [&](int x, uint32_t& row, int& at) {      // tile x + lane
       const int key = key_of(x + lane);
       row = kNoRow;
-      if (x + lane < n_units && key < lim_hi) {
+      // (keys before a window may be in pages that have been given up: they have no row here,
+      // and their values are zeros)
+      if (x + lane < n_units && key < lim_hi && (MODE == kPlain || key + 16 > from_lo)) {
         const int idx = key / p.c.page_size;
         int page = -1;
         if (FP4Q_IN_RANGE(p, table + idx, 4, p.tables, 4LL * p.B * p.max_pages)) page = __ldg(table + idx);

@@ -815,7 +815,8 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
     int page_of, at_of;                            // the page's number is looked at a step later
     auto next_page = [&]() {
       at_of = at;
-      page_of = key < seq.len && (!backwards || key >= 0) ? prefill_page(p, b, idx) : -1;
+      // (16 keys before a window may be in a page that has been given up: zeros stand for them)
+      page_of = key < seq.len && (MODE == kPlain || key + 16 > from_key) ? prefill_page(p, b, idx) : -1;
       if (backwards) {
         key -= kPreKeys;
         idx -= page_q;
