@@ -117,8 +117,8 @@ KERNEL_SOURCES = {
     # the key/value cache: captures only, no workload of this benchmark
     "kv": ("async_copy.cuh", "debug_checks.h", "fp4q_device.cuh", "fp4q_launch.h",
            "fused_common.cuh", "kv_attention.cu", "kv_attention_capped.cu", "kv_attention_common.cuh",
-           "kv_attention_launch.cuh", "kv_attention_masked.cu", "kv_cache.cu", "kv_decode.cuh",
-           "kv_launch.h", "kv_prefill.cuh", "kv_tcgen05.cuh", "tcgen05.cuh"),
+           "kv_attention_launch.cuh", "kv_attention_masked.cu", "kv_attention_wide_cap.cu", "kv_cache.cu",
+           "kv_decode.cuh", "kv_launch.h", "kv_prefill.cuh", "kv_tcgen05.cuh", "tcgen05.cuh"),
     "kv_pages": ("async_copy.cuh", "debug_checks.h", "fp4q_launch.h", "kv_launch.h", "kv_pages.cu"),
     "beam": ("async_copy.cuh", "beam_launch.h", "beam_select.cu", "debug_checks.h", "fp4q_device.cuh",
              "fp4q_launch.h", "fused_common.cuh"),

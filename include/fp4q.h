@@ -520,7 +520,8 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
  *   workspace      fp4_attention_workspace_bytes for max_keys, with a window for
  *                  min(max_keys, window + ceil(T / B) + 63) (or _bound's).
  * Logits are fp32, rounded once after each of the steps above; the cap's is off by a few 2^-24
- * of softcap.  Other arguments, and what is rounded, as above.
+ * of softcap, or, with a softcap above 256, by 2^-19 of itself at most (prompts then take up to three
+ * times as long).  Other arguments, and what is rounded, as above.
  */
 FP4Q_API fp4_status_t fp4_attention_nvfp4_ex(const void* q, int64_t q_stride,
                                              const fp4_kv_cache_t* cache,

@@ -4,7 +4,11 @@
 
 namespace fp4q {
 
+// (kv_attention_wide_cap.cu)
+cudaError_t launch_kv_attention_wide_cap(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream);
+
 cudaError_t launch_kv_attention_capped(int dtype, const KvAttentionParams& p, int pdl, cudaStream_t stream) {
+  if (p.softcap > kWideCap) return launch_kv_attention_wide_cap(dtype, p, pdl, stream);
   return p.slopes ? launch_attention<kCappedBiased, kCappedBiased>(dtype, p, pdl, stream)
                   : launch_attention<kCapped, kCappedBiased>(dtype, p, pdl, stream);
 }

@@ -52,12 +52,16 @@ __device__ __forceinline__ float coarse_exponent(float product, float fac, float
 }
 
 // What a kernel does to the products: nothing but the causal mask; keys from a window's first
-// to a prefix's end, too; with a bias; with a cap; with both.  The kernel of 256-row items has
-// one instance for each (their loops over the logits differ), the other one for kBiased and
-// kCappedBiased alone, which serve the calls without a bias, too.
-enum KvLogits { kPlain = 0, kMasked = 1, kBiased = 2, kCapped = 3, kCappedBiased = 4 };
-constexpr bool has_bias(int mode) { return mode == kBiased || mode == kCappedBiased; }
-constexpr bool has_cap(int mode) { return mode == kCapped || mode == kCappedBiased; }
+// to a prefix's end, too; with a bias; with a cap; with both; with a cap above kWideCap, bias or not.
+// The kernel of 256-row items has one instance for each (their loops over the logits differ), the
+// other one for kBiased, kCappedBiased and kWideCapBiased alone, which serve the calls without a
+// bias, too.
+enum KvLogits { kPlain = 0, kMasked = 1, kBiased = 2, kCapped = 3, kCappedBiased = 4, kWideCapBiased = 5 };
+constexpr bool has_wide_cap(int mode) { return mode == kWideCapBiased; }
+constexpr bool has_bias(int mode) { return mode == kBiased || mode == kCappedBiased || has_wide_cap(mode); }
+constexpr bool has_cap(int mode) { return mode == kCapped || mode == kCappedBiased || has_wide_cap(mode); }
+// Caps above this take capped_wide, whose error goes by the logit and not by the cap
+constexpr float kWideCap = 256.0f;
 
 // Entries of the call's small arrays (0 for one outside: the debug build's checks).
 __device__ __forceinline__ int kv_len(const KvAttentionParams& p, int b) {
@@ -171,22 +175,34 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 //   without a cap   s fac - slope |away|
 //   with one        cap tanh(s fac / cap) - slope |away|, cap and slope in the same units; tanh(x)
 //                   as 1 - 2 / (1 + exp(2 x)): off by a few 2^-24 of the cap, where the hardware's
-//                   own tanh would be off by 2^-11 of it.
+//                   own tanh would be off by 2^-11 of it.  A wide cap: capped_wide.
 // fac is the product's factor, with a cap times 2 log2(e) / cap for the exponential's argument.
+__device__ __forceinline__ float capped_wide(float x, float cap);
 template <int MODE>
 __device__ __forceinline__ float kv_logit(float s, float fac, float cap, float slope, float away) {
   float z;
-  if constexpr (has_cap(MODE))
+  if constexpr (has_wide_cap(MODE))
+    z = capped_wide(__fmul_rn(s, fac), cap);
+  else if constexpr (has_cap(MODE))
     z = fmaf(-2.0f * cap, rcp(1.0f + ex2(s * fac)), cap);
   else
     z = __fmul_rn(s, fac);
   return has_bias(MODE) ? fmaf(-slope, fabsf(away), z) : z;
 }
+// cap tanh(x / cap) for caps that most logits lie far below, where a few 2^-24 of the cap would be
+// much of a logit (at 2^20 tenths): below a quarter of the cap by tanh's series about 0, whose terms
+// from the 11th power on are less than 2^-26 of it, above by the exponential, whose error is
+// 2^-21.3 of the cap at most and so 2^-19 of the result.
+__device__ __forceinline__ float capped_wide(float x, float cap) {
+  const float t = x * rcp(cap), tt = t * t;
+  const float series = fmaf(tt, fmaf(tt, fmaf(tt, 62.0f / 2835, -17.0f / 315), 2.0f / 15), -1.0f / 3);
+  return fabsf(t) < 0.25f ? fmaf(x, tt * series, x) : fmaf(-2.0f * cap, rcp(1.0f + ex2(2.0f * kLog2e * t)), cap);
+}
 // The factor from the one that turns a product into a logit in units of log(2) (a number: a
 // product of 0 stays one).
 template <int MODE>
 __device__ __forceinline__ float kv_factor(const KvAttentionParams& p, float fac) {
-  return has_cap(MODE) ? fminf(fac * __fdiv_rn(2.0f, p.softcap), 3.402823466e38f) : fac;
+  return has_cap(MODE) && !has_wide_cap(MODE) ? fminf(fac * __fdiv_rn(2.0f, p.softcap), 3.402823466e38f) : fac;
 }
 __device__ __forceinline__ float kv_slope(const KvAttentionParams& p, int hq) {
   return p.slopes && FP4Q_IN_RANGE(p, p.slopes + hq, 4, p.slopes, 4LL * p.Hq) ? kLog2e * __ldg(p.slopes + hq) : 0.0f;

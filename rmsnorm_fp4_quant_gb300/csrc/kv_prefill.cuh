@@ -323,7 +323,7 @@ __device__ __forceinline__ float prefill_logit(uint32_t s, int key0, int key, fl
   return l.sees(key0 + key, page) ? z : -INFINITY;
 }
 // As prefill_weights above, logit by logit, each rounded before the reference is taken from it:
-// for steps on both sides of a row's own place, and for coarse references.
+// for steps on both sides of a row's own place, for coarse references, and for wide caps.
 template <int MODE>
 __device__ __forceinline__ float prefill_weights_by_logit(uint32_t ts, int key0, uint32_t have, const PrefillLogits& l,
                                                           float ref, uint32_t (&h)[64]) {
@@ -671,7 +671,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
       [[maybe_unused]] float grow = 0.0f, away = 0.0f;
       if constexpr (has_bias(MODE)) {
         const bool left = key0 + kPreKeys - 1 <= own_lo || (seen.causal && key0 >= seen.prefix);
-        line = left || key0 >= own_hi;
+        line = !has_wide_cap(MODE) && (left || key0 >= own_hi);
         grow = left ? logits.slope : -logits.slope;
         away = static_cast<float>(key0 - logits.own);
       }
@@ -718,7 +718,7 @@ __global__ void __launch_bounds__(kPreThreads, 1) kv_prefill_kernel(const KvAtte
           step_sum = edge ? prefill_weights<true, kFrom>(ts, key0, lim, from, have, f, ref, h)
                           : prefill_weights<false, kFrom>(ts, key0, lim, from, have, f, ref, h);
         } else {
-          if (has_bias(MODE) && (!line || __any_sync(kFullMask, is_coarse(ref)))) {
+          if (has_wide_cap(MODE) || (has_bias(MODE) && (!line || __any_sync(kFullMask, is_coarse(ref))))) {
             step_sum = prefill_weights_by_logit<MODE>(ts, key0, have, logits, ref, h);
           } else {
             const float base = logits.cap - ref;
