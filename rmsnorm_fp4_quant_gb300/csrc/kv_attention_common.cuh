@@ -60,7 +60,7 @@ enum KvLogits { kPlain = 0, kMasked = 1, kBiased = 2, kCapped = 3, kCappedBiased
 constexpr bool has_wide_cap(int mode) { return mode == kWideCapBiased; }
 constexpr bool has_bias(int mode) { return mode == kBiased || mode == kCappedBiased || has_wide_cap(mode); }
 constexpr bool has_cap(int mode) { return mode == kCapped || mode == kCappedBiased || has_wide_cap(mode); }
-// Caps above this take capped_wide, whose error goes by the logit and not by the cap
+// Caps above this take capped_wide, whose error goes by the logit and not by the cap.
 constexpr float kWideCap = 256.0f;
 
 // Entries of the call's small arrays (0 for one outside: the debug build's checks).
