@@ -480,7 +480,8 @@ FP4Q_API fp4_status_t fp4_kv_gather_nvfp4(const fp4_kv_cache_t* cache, const int
  * Lengths and tables are read on the device, so a captured call follows them.
  * Rows that a kernel gave up on (a bounded wait ran out: status) are NaN, lse too.
  * Logits, references, sums and accumulators are fp32.  Two things are rounded to 16
- * bits on the way: each weight exp(..) to fp16's 11 bits (relative 2^-11) before it is
+ * bits on the way: each weight exp(..) to fp16's 11 bits (relative 2^-11; one that is 2^20 times
+ * smaller than the row's largest to 2^-31 of that) before it is
  * multiplied with v, while the sum takes it unrounded; and each query element, scaled
  * by a power of two, by at most 2^-39 of its row's largest (most elements by nothing).
  * Keys and values are exact.  One kernel serves a call, chosen by the average number of
@@ -521,7 +522,9 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
  *                  min(max_keys, window + ceil(T / B) + 63) (or _bound's).
  * Logits are fp32, rounded once after each of the steps above; the cap's is off by a few 2^-24
  * of softcap, or, with a softcap above 256, by 2^-19 of itself at most (prompts then take up to three
- * times as long).  Other arguments, and what is rounded, as above.
+ * times as long).  What is rounded to 16 bits is as above, but that calls of many rows with a cap or a
+ * bias round a weight that is 2^14 times smaller than the row's largest to 2^-25 of that.
+ * Other arguments as above.
  */
 FP4Q_API fp4_status_t fp4_attention_nvfp4_ex(const void* q, int64_t q_stride,
                                              const fp4_kv_cache_t* cache,

@@ -29,9 +29,10 @@ constexpr float kLn2 = 0.6931471805599453f;
 // seen when it was set, and it is set again once a logit passes r + 14: weights
 // stay below 2^14 in fp16, and one that is 2^30 times smaller than the largest
 // still has a bit.  A finite start keeps "nothing seen yet" free of inf - inf, and
-// no logit lies below it.  The kernels with capped or biased logits keep r at the largest
-// itself: such logits reach further (a cap is there because they do), and a row that passes
-// r + 14 costs its warp a step, while weights that are 2^14 times smaller than the
+// no logit lies below it.  The kernel of 256-row items keeps r at the largest itself where
+// logits are capped or biased: such logits reach further (a cap is there because they do), and
+// a row that passes r + 14 costs its warp a step (a prompt of 4096 with a cap of 50, 32 heads of
+// 128: 284 us, 330 with r 6 below), while weights that are 2^14 times smaller than the
 // largest may lose bits of theirs (2^-25 of the largest at most).
 constexpr float kRefStart = -3.402823466e38f;
 constexpr float kRefBelow = 6.0f;
@@ -60,7 +61,10 @@ enum KvLogits { kPlain = 0, kMasked = 1, kBiased = 2, kCapped = 3, kCappedBiased
 constexpr bool has_wide_cap(int mode) { return mode == kWideCapBiased; }
 constexpr bool has_bias(int mode) { return mode == kBiased || mode == kCappedBiased || has_wide_cap(mode); }
 constexpr bool has_cap(int mode) { return mode == kCapped || mode == kCappedBiased || has_wide_cap(mode); }
-// Caps above this take capped_wide, whose error goes by the logit and not by the cap.
+// Caps above this take capped_wide, whose error goes by the logit and not by the cap: lse of a
+// prompt of 200 with small logits is off by 9e-6 at a cap of 128 without it, by 2e-6 at 256 and
+// 1e-6 at 1000 and 2^20 with it.  A prompt of 4096, 32 heads of 128, logits of deviation 9, takes
+// 306 us with a cap of 128 and 955 with capped_wide.
 constexpr float kWideCap = 256.0f;
 
 // Entries of the call's small arrays (0 for one outside: the debug build's checks).

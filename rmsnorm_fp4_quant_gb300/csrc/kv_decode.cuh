@@ -25,7 +25,8 @@
 //
 // With a window, an item's units begin with the first that one of its sequence's rows sees.  A
 // cap and a bias are taken in place of the product (MODE, KvLogits): 16 sequences of 12-16 K tokens,
-// 40 query and 8 key/value heads of 128, 58 us without, 62 with a bias, 64 with a cap.
+// 40 query and 8 key/value heads of 128, 58.4 us without, 59.3 with a bias, 61.0 with a cap, 64.7 with
+// one above kWideCap.
 //
 // A CTA is 4 warps, each with its own 16 keys of a unit, its own r, l and O, and
 // its own ring of tiles in shared memory that cp.async fills ahead (a tile: 16
@@ -605,7 +606,8 @@ kv_decode_kernel(const KvAttentionParams p) {
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 4));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 8));
             m = fmaxf(m, __shfl_xor_sync(kFullMask, m, 16));
-            const float r = MODE == kPlain ? ref_for(ref[n][e], m, fac[n][e]) : fmaxf(ref[n][e], m);
+            // (a logit that is rounded already stands for its product, with a factor of 1)
+            const float r = ref_for(ref[n][e], m, MODE == kPlain ? fac[n][e] : 1.0f);
             const float f = ex2(ref[n][e] - r);
             ref[n][e] = r;
             far |= MODE == kPlain && is_coarse(r);   // (a logit that is rounded needs no other code)

@@ -71,7 +71,7 @@ struct KvAttentionParams {
   int group;           // Hq / heads
   float sm_scale;
   int causal;
-  float softcap;         // 0: none (this and the three below: kernels with MASKED or more)
+  float softcap;         // 0: none (this and the three below: kinds of logits other than kPlain)
   const float* slopes;   // [Hq] or null
   int window;            // 0: none
   const int32_t* prefix; // [B] or null

@@ -38,10 +38,12 @@
 // changes the masks.  A bias is a straight line on either side of a row's own place: one
 // more multiply-add a pair of keys (a prompt of 4096, 32 heads of 128, logits of deviation 2: 163 us,
 // 126 without), and the keys are taken from the last to the first.  A cap is three special
-// functions instead of one, two reciprocals in one of them (213 us; logits of deviation 9: 229, of
-// which the maximum moves more often, 181 without a cap): 13 instructions a logit (114 million
-// warp instructions, all roles', over 8.65 million warps of logits) bound these steps (an
-// exponential in polynomials instead of the special function: 238 us and more, where it was 213).
+// functions instead of one, two reciprocals in one of them (with logits of deviation 9 230 us): 13.2
+// instructions a logit (114 million warp instructions, all roles', over 8.65 million warps of
+// logits) where there are 7.7 without, at the same share of the issue slots (43 and 44 %).  No unit is
+// near its limit (tensor pipe 25 %, special functions 32 %): two softmax warps per scheduler wait for
+// one result after the other.  An exponential in polynomials instead of the special function made
+// the calls 12 % slower and more.
 //
 // Every wait is bounded.  A role whose wait runs out stops and the others' waits
 // run out after it; the rows not finished by then are written as NaN, the status
@@ -369,8 +371,8 @@ __device__ __forceinline__ float prefill_maximum_by_logit(uint32_t ts, int key0,
 // straight line: `base` is its value at the row's own place (with the reference, and the cap,
 // taken in), `grow` what it grows by from key to key.  Pairs of floats.  The cap's reciprocals
 // come two at a time from one, of their product, whose factors are held to 2^60, where tanh is
-// long 1 to the last bit (a prompt of 4096, 32 heads of 128: 221 us; one for each 235, one for four
-// 239, whose chains are longer; special functions alone would take 160).
+// long 1 to the last bit (when it was chosen, a prompt of 4096, 32 heads of 128, took 221 us so, 235
+// with one for each and 239 with one for four, whose chains are longer).
 // Logits i .. i + 3 of x, the keys from `key` on; t and tb are the line at the two pairs.  EDGE:
 // keys that the row does not see (by prefill_bits where there is a bias, 5 % faster, by
 // comparisons where there is only a cap, 5 % faster again: registers) are -infinity.
