@@ -617,9 +617,11 @@ FP4Q_API fp4_status_t fp4_kv_fork_nvfp4(const fp4_kv_cache_t* cache, const int32
  * fp4_kv_trim_nvfp4 - sequences give up tokens: those that end, drafted tokens that were not
  * taken, what lies behind a window.
  *
- *   first, end     [B] int32, or NULL (0; the length): tokens first .. end - 1 stay.  Pages that hold
- *                  none of them are given up: out_tables has -1 there and everywhere behind the
- *                  sequence's pages (and for an entry that holds no page).
+ *   first, end     [B] int32, or NULL (0; the length): tokens first .. end - 1 stay.  Pages that end
+ *                  before place `first` and pages that begin at place `end` or behind it are given up:
+ *                  out_tables has -1 there and everywhere behind the sequence's pages (and for an
+ *                  entry that holds no page).  A page that both places lie in stays, and so it does
+ *                  where no token does (first >= end): the next token goes there.
  *   out_seq_lens   [B] int32: min(end, length), not changed by first.
  *   out_refs       [num_pages] int32.
  * Other arguments as above.  Only the sizes of `cache` count; no page is read or written.

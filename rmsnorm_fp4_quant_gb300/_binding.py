@@ -1220,12 +1220,13 @@ def kv_fork_nvfp4(cache, refs, tables, seq_lens, parents=None, new_tokens: int =
 
 def kv_trim_nvfp4(cache, refs, tables, seq_lens, first=None, end=None, out_tables=None, out_seq_lens=None,
                   out_refs=None, pdl: bool = False, stream=None):
-    """Sequences keep tokens first .. end - 1 and give up the pages that hold none of them;
+    """Sequences keep tokens first .. end - 1 and give up the pages before and behind these;
     returns (tables, seq_lens, refs).
 
     first, end: (B,) int32 or None (0; the length): end 0 for a sequence that has ended, less
     than its length where drafted tokens were not taken, first behind 0 where a window has
-    moved on.  Given-up pages are -1 in tables; seq_lens are min(end, length), as keys keep
+    moved on.  A page that first and end both lie in stays (the next token goes there, also where
+    first = end keeps none).  Given-up pages are -1 in tables; seq_lens are min(end, length), as keys keep
     their places.  Other arguments as in kv_fork_nvfp4; of the cache only the sizes count."""
     torch = _torch()
     struct, dev, B, most, r, t, l = _page_state(torch, cache, refs, tables, seq_lens)
