@@ -966,8 +966,8 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     if extra:
         slopes = _dense_ptr(alibi_slopes, "alibi_slopes", dev, torch.float32, (hq,)) if alibi_slopes is not None else None
         prefix = _dense_ptr(prefix_lens, "prefix_lens", dev, i32, (B,)) if prefix_lens is not None else None
-        if softcap is not None and not softcap > 0:
-            raise ValueError("softcap must be positive")
+        if softcap is not None and not ctypes.c_float(softcap).value > 0:
+            raise ValueError("softcap must be positive (in fp32, where 0 is no cap at all)")
         if window is not None:
             if window <= 0:
                 raise ValueError("window must be positive")

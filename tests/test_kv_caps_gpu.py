@@ -59,6 +59,15 @@ def test_wide_caps_with_the_rest(lens, q_lens, slopes, window, prefix):
           slopes_of(6) if slopes else None, window, [n // 3 for n in lens] if prefix else None)
 
 
+def test_a_cap_below_fp32s_numbers_is_refused():
+    """It is 0 in fp32, which the C call takes for no cap at all."""
+    cache, tables = fill_sequences([30], 1, 64, 16, seed=47)
+    dev = [torch.from_numpy(c).cuda() for c in cache]
+    t, l = torch.from_numpy(tables.astype(np.int32)).cuda(), torch.tensor([30], dtype=torch.int32, device="cuda")
+    with pytest.raises(ValueError):
+        fq.attention_nvfp4(queries(1, 2, 64, "bf16", 48).cuda(), dev, t, l, softcap=1e-46)
+
+
 @pytest.mark.parametrize("T", [1, 200])
 def test_a_cap_far_above_the_logits_changes_nothing(T):
     """Logits x of up to some 30: x - cap tanh(x / cap) = x^3 / (3 cap^2) is below 2^-26 of that."""
