@@ -91,7 +91,7 @@ typedef enum {
  * there.  The library never clears it (and writes nothing else to it, but
  * FP4_ERR_NO_PAGES in fp4_kv_fork_nvfp4):
  * zero it before the call, synchronise, and read it (fp4_read_device_status
- * does the last two; fp4_kv_read_status where a fork may have written it).  What a timed-out call leaves behind:
+ * does the last two).  What a timed-out call leaves behind:
  *   fused op: every scale byte of the rows the CTA did not finish is 0xFF
  *             (NaN in E4M3 and in UE8M0); their codes, residual rows and y
  *             rows are unspecified (the residual row may be the old value);
@@ -653,7 +653,7 @@ FP4Q_API fp4_status_t fp4_kv_compact_nvfp4(const fp4_kv_cache_t* cache, const in
                                            void* workspace, int64_t workspace_bytes, int pdl,
                                            fp4q_stream_t stream);
 
-/* fp4_read_device_status and fp4_status_string, which know FP4_ERR_NO_PAGES too. */
+/* fp4_read_device_status and fp4_status_string under the names that cache programs use. */
 FP4Q_API fp4_status_t fp4_kv_read_status(const int32_t* status, fp4q_stream_t stream);
 FP4Q_API const char* fp4_kv_status_string(fp4_status_t status);
 
@@ -707,8 +707,8 @@ FP4Q_API int64_t fp4_beam_select_workspace_bytes(int64_t B, int64_t K, int64_t V
 
 /*
  * fp4_read_device_status - synchronises `stream`, then copies the device
- * status word back and returns it as a status: FP4_OK (0) or FP4_ERR_TIMEOUT;
- * FP4_ERR_INVALID_ARG for a NULL or misaligned pointer or a value that is no
+ * status word back and returns it as a status: FP4_OK (0), FP4_ERR_TIMEOUT or
+ * FP4_ERR_NO_PAGES; FP4_ERR_INVALID_ARG for a NULL or misaligned pointer or a value that is no
  * status; FP4_ERR_CUDA if the synchronisation or the copy failed.  Blocks the
  * calling thread; not for use inside stream capture.
  */

@@ -399,7 +399,7 @@ def fp4_sf_size_bytes(M: int, H: int, fmt: int, layout: int) -> int:
 
 
 def fp4_status_string(status: int) -> str:
-    return lib().fp4_kv_status_string(status).decode()     # (the same, and FP4_ERR_NO_PAGES)
+    return lib().fp4_status_string(status).decode()
 
 
 def fp4_last_cuda_error() -> int:
@@ -532,9 +532,9 @@ def _status_ptr(status) -> int:
 def read_device_status(status, stream=None) -> int:
     """Synchronises the stream and returns the device status word as a status
     code (FP4_OK, FP4_ERR_TIMEOUT or FP4_ERR_NO_PAGES)."""
-    st = fp4_kv_read_status(_status_ptr(status), _stream_handle(stream))
+    st = fp4_read_device_status(_status_ptr(status), _stream_handle(stream))
     if st not in (FP4_OK, FP4_ERR_TIMEOUT, FP4_ERR_NO_PAGES):
-        raise Fp4Error(st, "fp4_kv_read_status")
+        raise Fp4Error(st, "fp4_read_device_status")
     return st
 
 

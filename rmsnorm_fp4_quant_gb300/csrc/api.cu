@@ -282,6 +282,7 @@ const char* fp4_status_string(fp4_status_t s) {
     case FP4_ERR_MISALIGNED: return "misaligned pointer";
     case FP4_ERR_CUDA: return "CUDA error";
     case FP4_ERR_TIMEOUT: return "a kernel gave up on a bounded wait (timeout)";
+    case FP4_ERR_NO_PAGES: return "no free page, or no room in a page table";
     default: return "unknown status";
   }
 }
@@ -536,7 +537,8 @@ fp4_status_t fp4_read_device_status(const int32_t* status, fp4q_stream_t stream)
   int32_t v = 0;
   if (e == cudaSuccess) e = cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost);
   if (e != cudaSuccess) return record_cuda_status(e);
-  return v == FP4_OK || v == FP4_ERR_TIMEOUT ? static_cast<fp4_status_t>(v) : FP4_ERR_INVALID_ARG;
+  return v == FP4_OK || v == FP4_ERR_TIMEOUT || v == FP4_ERR_NO_PAGES ? static_cast<fp4_status_t>(v)
+                                                                      : FP4_ERR_INVALID_ARG;
 }
 
 fp4_status_t fp4_dequant(const uint8_t* packed, const uint8_t* sf, int64_t M, int64_t H,

@@ -334,18 +334,10 @@ fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride, const fp4_kv_c
                                 workspace_bytes, status, pdl, stream);
 }
 
-const char* fp4_kv_status_string(fp4_status_t s) {
-  return s == FP4_ERR_NO_PAGES ? "no free page, or no room in a page table" : fp4_status_string(s);
-}
+const char* fp4_kv_status_string(fp4_status_t s) { return fp4_status_string(s); }
 
 fp4_status_t fp4_kv_read_status(const int32_t* status, fp4q_stream_t stream) {
-  if (!status || !abi_aligned(status, 4)) return FP4_ERR_INVALID_ARG;
-  cudaError_t e = cudaStreamSynchronize(reinterpret_cast<cudaStream_t>(stream));
-  int32_t v = 0;
-  if (e == cudaSuccess) e = cudaMemcpy(&v, status, sizeof(v), cudaMemcpyDeviceToHost);
-  if (e != cudaSuccess) return static_cast<fp4_status_t>(record_cuda_error(e));
-  return v == FP4_OK || v == FP4_ERR_TIMEOUT || v == FP4_ERR_NO_PAGES ? static_cast<fp4_status_t>(v)
-                                                                      : FP4_ERR_INVALID_ARG;
+  return fp4_read_device_status(status, stream);
 }
 
 int64_t fp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t N) {
