@@ -517,7 +517,8 @@ FP4Q_API fp4_status_t fp4_attention_nvfp4(const void* q, int64_t q_stride,
  *   alibi_slopes   [Hq] fp32 or NULL.
  *   window         >= 0; 0: none.  With causal only.  Pages that hold nothing but keys before the
  *                  first row's window are not read (fp4_kv_trim_nvfp4 gives them up).
- *   prefix_lens    [B] int32 or NULL (taken as clamped to [0, len]).  With causal only.
+ *   prefix_lens    [B] int32 or NULL (taken as clamped to [0, len]).  With causal only.  Of a prefix
+ *                  before a row's window the row sees nothing.
  *   workspace      fp4_attention_workspace_bytes for max_keys, with a window for
  *                  min(max_keys, window + ceil(T / B) + 63) (or _bound's).
  * Logits are fp32, rounded once after each of the steps above; the cap's is off by a few 2^-24

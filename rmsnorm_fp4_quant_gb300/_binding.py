@@ -934,11 +934,13 @@ def attention_nvfp4(q, cache, block_tables, seq_lens, cu_seqlens_q=None, causal:
     fp4_attention_workspace_bytes bytes (one for calls of several sizes:
     fp4_attention_workspace_bound), for one call at a time.
 
-    softcap: logits become softcap * tanh(logit / softcap).  alibi_slopes: (heads,) fp32; then
-    slope * distance between the row's place and the key's is taken off.  With causal:
-    window: a row sees the latest `window` of its keys only (pages before that may have
-    been given up: kv_trim_nvfp4); prefix_lens: (B,) int32, every row of the sequence
-    also sees its first prefix_lens[b] keys.  (A workspace of the exact size is then
+    softcap: logits become softcap * tanh(logit / softcap); at most 2^20, and prompts take up to
+    three times as long with one above 256.  alibi_slopes: (heads,) fp32; then slope * distance
+    between the row's place and the key's is taken off.  With causal:
+    window: a row sees no key that lies `window` or more places before its own (pages before
+    that may have been given up: kv_trim_nvfp4); prefix_lens: (B,) int32, rows also see keys
+    behind their own place among the sequence's first prefix_lens[b] (a window hides a prefix
+    that lies before it like any other keys).  (A workspace of the exact size is then
     that for min(max_keys, window + ceil(T / B) + 63) keys.)"""
     torch = _torch()
     struct, dev, heads, dim = _kv_struct(torch, cache, k_global_scale, v_global_scale)
