@@ -669,8 +669,8 @@ FP4Q_API int64_t fp4_kv_pages_workspace_bytes(int64_t num_pages, int64_t N);
  *   scores[b, k] + logits[b, k, v] - log(sum_v exp(logits[b, k, v]))
  *
  * in descending order.  Candidates of one beam are ordered by their logits,
- * equal ones by token, lowest first; of different beams by their scores (48 bits),
- * equal ones by beam.
+ * equal ones by token, lowest first; of different beams by their scores (48 bits, and none
+ * below a 64-bit number's steps), equal ones by beam.
  *
  *   logits, row_stride  [B * K, V] dtype (bf16, fp16 or fp32), row_stride elements between rows
  *                  (0: V); row b * K + k is beam k of entry b.  Any alignment that the type has.

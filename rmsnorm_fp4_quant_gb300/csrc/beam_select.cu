@@ -304,11 +304,16 @@ __device__ __forceinline__ float2 log_sum(float m, float2 s) {
   return l;
 }
 
-// s + (x - l) in order.
+// s + (x - l) in order, to the 53 bits of a 64-bit number: two floats can hold a large one and
+// what is left of a small one far below, by which tokens filled with -1e30 would be ordered by
+// their beams' scores where they are as far behind in all of them.
 __device__ __forceinline__ uint64_t pair_score(float x, float2 l, float s) {
   float2 v = two_sum(x, -l.x);
   v.y -= l.y;
   v = add_pairs(v, make_float2(s, 0.0f));
+  const float top = __uint_as_float(__float_as_uint(v.x) & 0x7f800000u);   // the power of two in it
+  const float step = top * 2.7939677e-9f;                                 // 1.5 * 2^-29: steps of 2^-52 of that
+  if (fabsf(v.y) < top * 9.3132257e-10f) v.y = __fsub_rn(__fadd_rn(v.y, step), step);
   return static_cast<uint64_t>(ordered(v.x)) << 32 | ordered(v.y);
 }
 

@@ -70,6 +70,26 @@ def test_a_vocabulary_of_a_few_tokens(dtype, fill):
     check(x, torch.tensor([[-2.0], [-3.0]]), 20)
 
 
+@pytest.mark.parametrize("fill", [-1e18, -1e20, -1e30])
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+def test_filled_tokens_of_several_beams_come_in_order(dtype, fill):
+    """Behind the tokens that are not filled all scores are the fill in 64 bits: lowest beam and
+    token first, whatever the beams' own scores are."""
+    x = torch.full((2, 3, 2003), fill, dtype=DT[dtype])
+    x[:, 0, 1000], x[:, 1, [5, 6]], x[0, 2, 2002] = 1.0, torch.tensor([3.0, 1.0], dtype=DT[dtype]), 2.0
+    scores = torch.tensor([[-9.0, -3.25, -1.5], [-2.0, -7.5, -float("inf")]])
+    finished = torch.zeros(2, 3, dtype=torch.bool)
+    total = scores.double()[..., None] + torch.log_softmax(x.double(), -1)
+    value, index = torch.sort(total.flatten(1), dim=1, descending=True, stable=True)
+    some = value[:, :40] > -float("inf")
+    parents = torch.where(some, index[:, :40] // 2003 + 3 * torch.arange(2)[:, None], -1)
+    tokens = torch.where(some, index[:, :40] % 2003, -1)
+    for kw in (dict(), dict(finished=finished.cuda(), end_token=7)):
+        got = fq.beam_select(x.cuda(), scores.cuda(), 40, **kw)
+        assert torch.equal(got[1].cpu().long(), parents) and torch.equal(got[2].cpu().long(), tokens)
+        assert torch.allclose(got[0].cpu().double(), value[:, :40], rtol=2.0 ** -23, atol=FAR_ERROR)
+
+
 FAR = [v for m in (1.25e7, 1e9, 2.0 ** 30, 2.0 ** 30 + 128, 1e10, 1e20, 1e30, 4e37) for v in (m, -m)]
 
 
